@@ -16,6 +16,10 @@ GDR_F32 = 0
 GDR_BF16 = 1
 GDR_DECAY_G = 0
 GDR_DECAY_LOG = 1
+GDR_ACT_NONE = 0
+GDR_ACT_SILU = 1
+CONV_MAX_TAPS = 8  # GDR_CONV_MAX_TAPS
+SCAN_MAX_STATES = 64  # GDR_SCAN_MAX_STATES
 
 # entry points declared in include/gdr.h, with their ctypes signatures
 _c_shape_p = None  # set below
@@ -35,7 +39,37 @@ class GdrShape(ctypes.Structure):
     ]
 
 
+class GdrConvShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "rows", "C", "K", "x_stride")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "wdtype", "act", "reserved")])
+
+
+class GdrScanShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "rows", "C", "N", "G", "u_stride",
+                                               "dt_stride", "z_stride", "b_stride", "c_stride")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "softplus")])
+
+
+class GdrNormShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "C", "G", "x_stride", "z_stride")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int32) for n in ("dtype", "wdtype", "center", "shared_weight",
+                                                 "act")])
+
+
 _vp = ctypes.c_void_p
+
+
+def _size_query(shape):
+    return (ctypes.c_int, [ctypes.POINTER(shape), ctypes.POINTER(ctypes.c_size_t)])
+
+
+def _call(shape, pointers, workspace=False):
+    """shape, data pointers (the workspace among them, then its bytes), stream."""
+    return (ctypes.c_int, [ctypes.POINTER(shape)] + [_vp] * pointers
+            + ([ctypes.c_size_t] if workspace else []) + [_vp])
+
+
 _SIGNATURES = {
     "gdr_num_chunks": (ctypes.c_int, [ctypes.POINTER(GdrShape), ctypes.POINTER(ctypes.c_int64)]),
     "gdr_checkpoint_bytes": (ctypes.c_int, [ctypes.POINTER(GdrShape), ctypes.POINTER(ctypes.c_size_t)]),
@@ -47,6 +81,17 @@ _SIGNATURES = {
     "gdr_backward": (ctypes.c_int, [ctypes.POINTER(GdrShape)] + [_vp] * 16
                      + [ctypes.c_size_t, _vp]),
     "gdr_set_launch_events": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int]),
+    "gdr_conv_forward": _call(GdrConvShape, 7),
+    "gdr_conv_backward_workspace_bytes": _size_query(GdrConvShape),
+    "gdr_conv_backward": _call(GdrConvShape, 12, workspace=True),
+    "gdr_scan_checkpoint_bytes": _size_query(GdrScanShape),
+    "gdr_scan_forward_workspace_bytes": _size_query(GdrScanShape),
+    "gdr_scan_backward_workspace_bytes": _size_query(GdrScanShape),
+    "gdr_scan_forward": _call(GdrScanShape, 14, workspace=True),
+    "gdr_scan_backward": _call(GdrScanShape, 22, workspace=True),
+    "gdr_norm_forward": _call(GdrNormShape, 6),
+    "gdr_norm_backward_workspace_bytes": _size_query(GdrNormShape),
+    "gdr_norm_backward": _call(GdrNormShape, 11, workspace=True),
     "gdr_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "gdr_version": (ctypes.c_char_p, []),
 }
@@ -161,3 +206,18 @@ def backward_raw(shape, q, k, g, beta, ckpt, dy, dS_T, dq, dk, dv, dg, dbeta,
     return load().gdr_backward(ctypes.byref(shape), *ptrs,
                                ctypes.c_size_t(int(workspace_bytes)),
                                _vp(stream or None))
+
+
+def size_of(query: str, shape) -> int:
+    """A size query of the convolution, scan or norm by its name."""
+    out = ctypes.c_size_t()
+    check(getattr(load(), query)(ctypes.byref(shape), ctypes.byref(out)), query)
+    return out.value
+
+
+def layer_raw(name: str, shape, pointers, stream, workspace_bytes=None) -> int:
+    """A convolution, scan or norm call by its name, with integer device
+    addresses (0 = NULL; the workspace last); returns the status."""
+    tail = () if workspace_bytes is None else (workspace_bytes,)
+    return getattr(load(), name)(ctypes.byref(shape), *[p or None for p in pointers], *tail,
+                                 stream or None)

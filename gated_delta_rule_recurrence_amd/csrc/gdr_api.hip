@@ -537,11 +537,16 @@ const char* gdr_strerror(int status) {
       return "the forward workspace this shape needs exceeds the no-allocation scratch";
     case GDR_ERR_BAD_COUNT:
       return "the launch-event count must be in [0, GDR_MAX_LAUNCH_EVENTS]";
+    case GDR_ERR_BAD_DIM:
+      return "a dimension of a convolution, scan or norm is outside its range";
+    case GDR_ERR_BAD_STRIDE: return "a row stride is below the row's width or above 2^31 - 1";
+    case GDR_ERR_BAD_ACT: return "act must be GDR_ACT_NONE or GDR_ACT_SILU, softplus 0 or 1";
+    case GDR_ERR_BAD_EPS: return "eps must be finite and >= 0";
   }
   return "unknown gdr status";
 }
 
-const char* gdr_version(void) { return "0.7.0"; }
+const char* gdr_version(void) { return "0.8.0"; }
 
 }  // extern "C"
 
@@ -551,6 +556,9 @@ void note_launch(hipStream_t s) {
   const int i = launch_count++;
   if (i < n_launch_events) (void)hipEventRecord(launch_events[i], s);
 }
+
+void begin_call() { launch_count = 0; }
+int finish_call(int status, void* stream) { return end_call(status, stream); }
 
 int device_cu_count() {
   static std::atomic<int> cache[64];

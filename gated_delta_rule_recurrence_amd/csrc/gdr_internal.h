@@ -130,6 +130,10 @@ int device_cu_count();
 // After each kernel launch: records the caller's next measurement event on s,
 // if gdr_set_launch_events has set one for this launch (include/gdr.h).
 void note_launch(hipStream_t s);
+// The same hook around a call: its first launch counts from 0, and its end
+// records the events that no launch took.
+void begin_call();
+int finish_call(int status, void* stream);
 hipError_t launch_bwd_chunk(const ChunkArgs& a, bool bf16, hipStream_t s);
 // The eight-wave chunk kernel for bf16 inputs (gdr_chunk_bf16.hip): whether it
 // takes the shape (Dk, Dv multiples of 8, 48 < Dk <= 256), and its launch.

@@ -1,0 +1,274 @@
+// Launch interface and shared device helpers of the layer operators beside
+// the gated delta rule: the short causal convolution, the selective state
+// space scan and the group norm (include/gdr.h states their formulas).
+#pragma once
+
+#include "gdr_device.h"
+#include "gdr_internal.h"
+
+namespace gdr {
+
+// The element types of activations and of weights (gdr_dtype) travel as
+// "is bf16" flags.
+struct ConvArgs {
+  int B, T, C, K;
+  int64_t rows, x_stride;
+  int act;            // 1: SiLU
+  int w_bf16;         // weight, bias and their gradients
+  const int32_t* spans;  // [B][2] or null
+  const void* x;
+  const void* w;      // [C][K]
+  const void* bias;   // [C] or null
+  const void* state;  // [B][K-1][C] or null (zeros)
+  void* y;
+  void* state_out;    // or null
+  // backward
+  const void* dy;
+  const void* dstate_out;  // or null
+  void* dx;
+  void* dw;
+  void* dbias;        // or null
+  void* dstate;       // or null
+  float* part;        // [parts][K+1][C]
+};
+// Steps a wave takes in the backward, and the partial sums that leaves.
+int conv_bwd_steps(int64_t B, int64_t T, int64_t C, bool bf16);
+int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C, bool bf16);
+hipError_t launch_conv_fwd(const ConvArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_conv_bwd(const ConvArgs& a, bool bf16, hipStream_t s);
+
+struct NormArgs {
+  int64_t rows, x_stride, z_stride;
+  int C, G, D;        // D = C / G
+  int act, center, shared;
+  int w_bf16;
+  float eps;
+  const void* x;
+  const void* w;      // [C], or [D] (shared); null: ones
+  const void* bias;   // as w; null: zeros
+  const void* z;      // gate or null
+  void* y;
+  float* stats;       // [rows][G][2]: mean, 1/sqrt(var + eps); may be null
+  // backward
+  const void* dy;
+  void* dx;
+  void* dw;
+  void* dbias;
+  void* dz;
+  float* part;        // [parts][2][period][D]
+};
+struct NormPlan {
+  int lanes, nv;      // lanes and vectors per lane of one group
+  bool vec;
+  int64_t period;     // groups after which the weight repeats for every lane
+  int64_t slabs;      // waves (blocks, for lanes > 64) that cover one period
+  int64_t parts;      // blocks per slab in the backward
+};
+bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool shared, bool bf16,
+               NormPlan* p);
+hipError_t launch_norm_fwd(const NormArgs& a, const NormPlan& p, bool bf16, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, const NormPlan& p, bool bf16, hipStream_t s);
+
+struct ScanArgs {
+  int B, T, C, N, G;
+  int64_t rows, u_stride, dt_stride, z_stride, b_stride, c_stride;
+  int softplus;
+  const int32_t* spans;
+  const void* u;
+  const void* dt;
+  const float* A;       // [C][N]
+  const void* Bm;       // [rows][G][N]
+  const void* Cm;
+  const float* D;       // [C] or null
+  const void* z;        // or null
+  const float* dt_bias; // [C] or null
+  const float* S0;      // [B][C][N] or null
+  void* y;
+  float* S_T;           // or null
+  float* ckpt;          // tile states (scan_tile_slots) or null
+  // chunked form (chunks > 1): the state (or adjoint) before every chunk and
+  // the summed steps of every chunk
+  int chunk;            // steps, a multiple of the tile
+  int chunks;           // of the longest sequence
+  float* edge;          // [slots][C][Np]
+  float* dsum;          // [slots][C]
+  // backward
+  const void* dy;
+  const float* dS_T;    // or null
+  void* du;
+  void* ddt;
+  float* dA;
+  void* dB;
+  void* dC;
+  float* dD;
+  void* dz;
+  float* ddt_bias;
+  float* dS0;           // or null
+  float* pA;            // [B * chunks][C][Np] partial dA
+  float* pD;            // [B * chunks][2][C] partial dD, ddt_bias
+  float* pB;            // [2][channel tiles][rows][G][N] partial dB, dC
+};
+// Padded states per channel, steps of one tile and channels of one block.
+int scan_padded(int64_t N);
+int scan_tile(int64_t N);
+int scan_channels();
+// Steps of one chunk (0: the whole sequence runs as one).
+int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, bool bwd);
+hipError_t launch_scan_fwd(const ScanArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_scan_bwd(const ScanArgs& a, bool bf16, hipStream_t s);
+
+// ---- device helpers ---------------------------------------------------------
+
+// Rows of sequence b, held inside [0, rows) and to T steps whatever spans
+// holds.
+struct Span {
+  int64_t first;
+  int len;
+};
+__device__ __forceinline__ Span span_of(const int32_t* spans, int b, int T, int64_t rows) {
+  if (spans == nullptr) return Span{(int64_t)b * T, T};
+  int64_t s = spans[2 * b], e = spans[2 * b + 1];
+  s = s < 0 ? 0 : (s > rows ? rows : s);
+  e = e > rows ? rows : e;
+  int64_t n = e - s;
+  n = n < 0 ? 0 : (n > T ? T : n);
+  return Span{s, (int)n};
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 1 / (1 + e^-x): the exponential overflows to inf for x < -88, whose
+// reciprocal is the 0 that is meant.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + exp2_hw(-kLog2e * x));
+}
+
+// act(x), and its derivative
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+__device__ __forceinline__ float dsilu(float x, float sg) { return sg * (1.f + x * (1.f - sg)); }
+
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(t) for t in (0, 1] is
+// log(w) t / (w - 1) with w = 1 + t as rounded: the rounding of w enters
+// numerator and denominator alike and cancels, so that small steps (t down
+// to the smallest float) keep their relative accuracy.  Also gives the
+// derivative, sigmoid(x).
+__device__ __forceinline__ float softplus(float x) {
+  const float t = exp2_hw(-kLog2e * fabsf(x));
+  const float w = 1.f + t, d = w - 1.f;
+  const float l = kLn2 * __builtin_amdgcn_logf(w) * t * __builtin_amdgcn_rcpf(d);
+  return fmaxf(x, 0.f) + (d == 0.f ? t : l);
+}
+
+// Loads V consecutive elements as floats; V = 1, or a 16-byte vector.
+template <typename T, int V>
+struct Pack {
+  T v[V];
+};
+template <>
+struct Pack<float, 4> {
+  float4 v;
+};
+template <>
+struct Pack<bf16, 8> {
+  uint4 v;
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+  Pack<T, V> r;
+  if constexpr (V == 1) {
+    r.v[0] = *p;
+  } else {
+    r = *reinterpret_cast<const Pack<T, V>*>(p);
+  }
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> zero_pack() {
+  Pack<T, V> r;
+  __builtin_memset(&r, 0, sizeof(r));
+  return r;
+}
+__device__ __forceinline__ void unpack(const Pack<float, 1>& p, float (&f)[1]) { f[0] = p.v[0]; }
+__device__ __forceinline__ void unpack(const Pack<bf16, 1>& p, float (&f)[1]) {
+  f[0] = to_f32(p.v[0]);
+}
+__device__ __forceinline__ void unpack(const Pack<float, 4>& p, float (&f)[4]) {
+  f[0] = p.v.x;
+  f[1] = p.v.y;
+  f[2] = p.v.z;
+  f[3] = p.v.w;
+}
+__device__ __forceinline__ void unpack(const Pack<bf16, 8>& p, float (&f)[8]) {
+  const uint32_t w[4] = {p.v.x, p.v.y, p.v.z, p.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+// Stores V floats, each rounded to nearest even.
+__device__ __forceinline__ void store_pack(float* p, const float (&f)[1]) { *p = f[0]; }
+__device__ __forceinline__ void store_pack(bf16* p, const float (&f)[1]) {
+  *p = from_f32<bf16>(f[0]);
+}
+__device__ __forceinline__ void store_pack(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = float4{f[0], f[1], f[2], f[3]};
+}
+__device__ __forceinline__ void store_pack(bf16* p, const float (&f)[8]) {
+  *reinterpret_cast<uint4*>(p) = uint4{cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3]),
+                                       cvt_pk_bf16(f[4], f[5]), cvt_pk_bf16(f[6], f[7])};
+}
+
+// A weight element of either type (loaded once per thread, so the branch is
+// of no account).
+__device__ __forceinline__ float ld_weight(const void* p, int64_t i, int is_bf16) {
+  return is_bf16 ? to_f32(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void st_weight(void* p, int64_t i, float x, int is_bf16) {
+  if (is_bf16)
+    static_cast<bf16*>(p)[i] = from_f32<bf16>(x);
+  else
+    static_cast<float*>(p)[i] = x;
+}
+
+// Sums over the rows of part[rows][width], 16 columns and 16 row lanes per
+// workgroup, in a fixed order: column c goes to store(c, sum).
+constexpr int kSumCols = 16;
+template <typename Store>
+__global__ __launch_bounds__(256) void column_sums(const float* __restrict__ part, int64_t rows,
+                                                   int64_t width, Store store) {
+  __shared__ float red[16][kSumCols + 1];
+  const int tc = threadIdx.x % kSumCols, tr = threadIdx.x / kSumCols;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + tc;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < width) {
+    int64_t r = tr;
+    for (; r + 48 < rows; r += 64)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += part[(r + 16 * k) * width + c];
+    for (; r < rows; r += 16) s[0] += part[r * width + c];
+  }
+  red[tr][tc] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (tr == 0 && c < width) {
+    float t = red[0][tc];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) t += red[k][tc];
+    store(c, t);
+  }
+}
+template <typename Store>
+hipError_t launch_column_sums(const float* part, int64_t rows, int64_t width, Store store,
+                              hipStream_t s) {
+  const int64_t blocks = (width + kSumCols - 1) / kSumCols;
+  hipLaunchKernelGGL((column_sums<Store>), dim3((unsigned)blocks), dim3(256), 0, s, part, rows,
+                     width, store);
+  const hipError_t e = hipGetLastError();
+  note_launch(s);
+  return e;
+}
+
+}  // namespace gdr

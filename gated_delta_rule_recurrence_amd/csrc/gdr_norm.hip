@@ -1,0 +1,427 @@
+// Group norm over channels-last rows on gfx950.  A group is D = C / G
+// neighbouring channels of one row:
+//   xh = (x - mu) r,  r = 1 / sqrt(mean((x - mu)^2) + eps)   (mu = 0: RMS)
+//   n = xh w + b;  y = act(n), or n act(z) with a gate z.
+// Backward, with mu and r from the forward:
+//   dn = dy act(z) (dy act'(n) without a gate),  dz = dy n act'(z),
+//   e = dn w,  dx = r (e - mean(e) - xh mean(e xh))   (mean(e): centred only)
+//   dw = sum over rows dn xh,  db = sum over rows dn.
+// Bound by HBM bytes: every tensor once.
+//
+// Mapping: LANES lanes own one group, each NV vectors of V channels, kept in
+// registers between the statistics and the output.  Groups of up to 64
+// vectors share a wave (LANES = 8 .. 64), wider ones take a whole workgroup.
+// A "slab" is what one wave (one workgroup, for LANES > 64) takes at a time:
+// consecutive groups of the flattened [rows * G] list.  In the backward a
+// slab position walks the list in steps of `period` groups, a multiple of G
+// (of anything, for a weight that every group shares), so that a lane meets
+// the same weights, and keeps them and the sums dw, db in registers, all the
+// way.
+#include "gdr_layer.h"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sum over the LANES lanes of a group, the same bits in every lane.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float x, float* red) {
+  if constexpr (LANES <= 64) {
+#pragma unroll
+    for (int m = 1; m < LANES; m <<= 1) x += __shfl_xor(x, m, 64);
+    return x;
+  } else {
+    constexpr int W = LANES / 64;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+    __syncthreads();  // the last sum has been read
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    float t = red[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) t += red[i];
+    return t;
+  }
+}
+
+template <typename T, int LANES, int NV, int V>
+struct Norm {
+  static constexpr int kBlock = LANES > 64 ? LANES : kThreads;
+  static constexpr int kUnits = LANES > 64 ? 1 : 64 / LANES;  // groups of one slab
+  static constexpr int kSlabs = LANES > 64 ? 1 : kThreads / 64;  // slabs of a workgroup at once
+
+  // channel of vector i of this lane inside its group
+  static __device__ __forceinline__ int at(int lane, int i) { return (i * LANES + lane) * V; }
+
+  static __device__ __forceinline__ void weights(const NormArgs& a, int lane, int g,
+                                                 float (&w)[NV][V], float (&b)[NV][V]) {
+    const int64_t base = a.shared ? 0 : (int64_t)g * a.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int d = at(lane, i) + v;
+        const bool ok = d < a.D;
+        w[i][v] = ok ? (a.w != nullptr ? ld_weight(a.w, base + d, a.w_bf16) : 1.f) : 0.f;
+        b[i][v] = ok && a.bias != nullptr ? ld_weight(a.bias, base + d, a.w_bf16) : 0.f;
+      }
+  }
+  // A group's channels of one tensor (zeros past the group's end).
+  static __device__ __forceinline__ void load(const void* p, int64_t off, int lane, int D, bool ok,
+                                              Pack<T, V> (&x)[NV]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      x[i] = ok && at(lane, i) < D ? load_pack<T, V>(static_cast<const T*>(p) + off + at(lane, i))
+                                   : zero_pack<T, V>();
+  }
+};
+
+template <typename T, int LANES, int NV, int V>
+__global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_fwd_kernel(NormArgs a,
+                                                                                   int64_t units) {
+  using P = Norm<T, LANES, NV, V>;
+  __shared__ float red[LANES > 64 ? LANES / 64 : 1];
+  const int lane = LANES > 64 ? threadIdx.x : threadIdx.x & (LANES - 1);
+  const int64_t unit = (int64_t)blockIdx.x * (P::kBlock / LANES) + threadIdx.x / LANES;
+  const bool ok = unit < units;
+  const uint32_t u32 = (uint32_t)(ok ? unit : 0);  // rows G fits in 31 bits
+  const int64_t row = u32 / (uint32_t)a.G;
+  const int g = (int)(u32 - (uint32_t)row * (uint32_t)a.G);
+  const int64_t xo = row * a.x_stride + (int64_t)g * a.D;
+  Pack<T, V> xr[NV], zr[NV];
+  P::load(a.x, xo, lane, a.D, ok, xr);
+  if (a.z != nullptr) P::load(a.z, row * a.z_stride + (int64_t)g * a.D, lane, a.D, ok, zr);
+  float w[NV][V], bias[NV][V];
+  P::weights(a, lane, g, w, bias);
+
+  float x[NV][V], mu = 0.f, s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) unpack(xr[i], x[i]);
+  const float inv = 1.f / (float)a.D;
+  if (a.center) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s += x[i][v];
+    mu = group_sum<LANES>(s, red) * inv;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[i][v] = P::at(lane, i) + v < a.D ? x[i][v] - mu : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) s = fmaf(x[i][v], x[i][v], s);
+  const float r = 1.f / sqrtf(fmaf(group_sum<LANES>(s, red), inv, a.eps));
+  if (!ok) return;
+  if (a.stats != nullptr && lane == 0) {
+    a.stats[2 * unit] = mu;
+    a.stats[2 * unit + 1] = r;
+  }
+  T* const y = static_cast<T*>(a.y) + row * a.C + (int64_t)g * a.D;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float o[V], z[V];
+    if (a.z != nullptr) unpack(zr[i], z);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float n = fmaf(x[i][v] * r, w[i][v], bias[i][v]);
+      const float in = a.z != nullptr ? z[v] : n;
+      o[v] = a.act ? silu(in) : in;
+      if (a.z != nullptr) o[v] *= n;
+    }
+    if (P::at(lane, i) < a.D) store_pack(y + P::at(lane, i), o);
+  }
+}
+
+template <typename T, int LANES, int NV, int V>
+__global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_bwd_kernel(
+    NormArgs a, int64_t units, int64_t period, int slabs) {
+  using P = Norm<T, LANES, NV, V>;
+  __shared__ float red[LANES > 64 ? LANES / 64 : 1];
+  const int lane = LANES > 64 ? threadIdx.x : threadIdx.x & (LANES - 1);
+  const int slab = blockIdx.x % slabs;
+  const int64_t part = blockIdx.x / slabs, parts = gridDim.x / slabs;  // shared: one slab
+  // this lane's place in the period, and its phase among the walkers of it
+  const int sub = LANES > 64 ? 0 : (threadIdx.x & 63) / LANES;
+  const int64_t place = (int64_t)slab * P::kUnits + sub;
+  const int64_t phase = part * P::kSlabs + (LANES > 64 ? 0 : threadIdx.x >> 6);
+  const int64_t step = period * parts * P::kSlabs;
+  const int g = (int)(place % a.G);
+  float w[NV][V], bias[NV][V], dw[NV][V], db[NV][V];
+  P::weights(a, lane, g, w, bias);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) dw[i][v] = db[i][v] = 0.f;
+  const float inv = 1.f / (float)a.D;
+
+  // every lane of a wave (workgroup, LANES > 64) makes the same number of
+  // turns: the first unit of the slab decides
+  for (int64_t base = period * phase + (int64_t)slab * P::kUnits; base < units; base += step) {
+    const int64_t unit = base + sub;
+    const bool ok = unit < units;
+    // rows G fits in 31 bits; a shared weight's period is no multiple of G
+    const uint32_t ur = (uint32_t)(ok ? unit : 0) / (uint32_t)a.G;
+    const int64_t row = ur;
+    const int64_t go = (int64_t)((uint32_t)(ok ? unit : 0) - ur * (uint32_t)a.G) * a.D;
+    Pack<T, V> xr[NV], zr[NV], dyr[NV];
+    P::load(a.x, row * a.x_stride + go, lane, a.D, ok, xr);
+    P::load(a.dy, row * a.C + go, lane, a.D, ok, dyr);
+    if (a.z != nullptr) P::load(a.z, row * a.z_stride + go, lane, a.D, ok, zr);
+    const float mu = ok ? a.stats[2 * unit] : 0.f, r = ok ? a.stats[2 * unit + 1] : 0.f;
+    float xh[NV][V], e[NV][V], se = 0.f, sx = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float dz[V], z[V], dy[V];
+      unpack(xr[i], xh[i]);
+      unpack(dyr[i], dy);
+      if (a.z != nullptr) unpack(zr[i], z);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool in = ok && P::at(lane, i) + v < a.D;
+        xh[i][v] = in ? (xh[i][v] - mu) * r : 0.f;
+        const float n = fmaf(xh[i][v], w[i][v], bias[i][v]);
+        float dn = dy[v];
+        if (a.z != nullptr) {
+          const float sg = a.act ? sigmoid(z[v]) : 1.f;
+          dz[v] = a.act ? dy[v] * n * dsilu(z[v], sg) : dy[v] * n;
+          dn *= z[v] * sg;
+        } else if (a.act) {
+          dn *= dsilu(n, sigmoid(n));
+        }
+        dn = in ? dn : 0.f;
+        dw[i][v] = fmaf(dn, xh[i][v], dw[i][v]);
+        db[i][v] += dn;
+        e[i][v] = dn * w[i][v];
+        se += e[i][v];
+        sx = fmaf(e[i][v], xh[i][v], sx);
+      }
+      if (a.z != nullptr && ok && P::at(lane, i) < a.D)
+        store_pack(static_cast<T*>(a.dz) + row * a.C + go + P::at(lane, i), dz);
+    }
+    sx = group_sum<LANES>(sx, red) * inv;
+    se = a.center ? group_sum<LANES>(se, red) * inv : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = r * (e[i][v] - se - xh[i][v] * sx);
+      if (ok && P::at(lane, i) < a.D)
+        store_pack(static_cast<T*>(a.dx) + row * a.C + go + P::at(lane, i), o);
+    }
+  }
+  if (a.dw == nullptr && a.dbias == nullptr) return;
+  // Sums over the workgroup's waves (and, for a shared weight, over a wave's
+  // groups), then part[part][2][period][D], or part[part][2][D] shared.
+  if constexpr (LANES <= 64) {
+    __shared__ float sum[P::kSlabs - 1][2][64];
+    const int q = threadIdx.x >> 6, wl = threadIdx.x & 63;
+    const int64_t width = a.shared ? a.D : period * a.D;
+    const int64_t base = a.shared ? 0 : place * a.D;
+    float* const p = a.part + part * 2 * width + base;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float s0 = dw[i][v], s1 = db[i][v];
+        if (a.shared)
+#pragma unroll
+          for (int m = LANES; m < 64; m <<= 1) {
+            s0 += __shfl_xor(s0, m, 64);
+            s1 += __shfl_xor(s1, m, 64);
+          }
+        __syncthreads();
+        if (q > 0) {
+          sum[q - 1][0][wl] = s0;
+          sum[q - 1][1][wl] = s1;
+        }
+        __syncthreads();
+        const int d = P::at(lane, i) + v;
+        if (q == 0 && d < a.D && (!a.shared || wl < LANES)) {
+#pragma unroll
+          for (int k = 0; k < P::kSlabs - 1; ++k) {
+            s0 += sum[k][0][wl];
+            s1 += sum[k][1][wl];
+          }
+          p[d] = s0;
+          p[width + d] = s1;
+        }
+      }
+  } else {
+    const int64_t width = a.shared ? a.D : period * a.D;
+    const int64_t base = a.shared ? 0 : place * a.D;
+    float* const p = a.part + part * 2 * width + base;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int d = P::at(lane, i) + v;
+        if (d < a.D) {
+          p[d] = dw[i][v];
+          p[width + d] = db[i][v];
+        }
+      }
+  }
+}
+
+// Column c of a partial row [2][reps][W]: the repeats of W (a period that
+// holds the weight's channels more than once) are further rows.
+struct NormSumStore {
+  void* dw;
+  void* dbias;
+  int64_t W;
+  int w_bf16;
+  __device__ void operator()(int64_t c, float x) const {
+    if (c < W) {
+      if (dw != nullptr) st_weight(dw, c, x, w_bf16);
+    } else if (dbias != nullptr) {
+      st_weight(dbias, c - W, x, w_bf16);
+    }
+  }
+};
+
+// Sums of part[parts][2][reps][W] to [2][W]: thread = column, 16 row lanes
+// over parts * reps.
+__global__ __launch_bounds__(256) void norm_sums(const float* __restrict__ part, int64_t parts,
+                                                 int64_t reps, NormSumStore store) {
+  __shared__ float red[16][kSumCols + 1];
+  const int tc = threadIdx.x % kSumCols, tr = threadIdx.x / kSumCols;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + tc;
+  float s = 0.f;
+  if (c < 2 * store.W) {
+    const int64_t half = c / store.W, d = c % store.W;
+    const float* const p = part + half * reps * store.W + d;
+    for (int64_t r = tr; r < parts * reps; r += 16)
+      s += p[(r / reps * 2 * reps + r % reps) * store.W];
+  }
+  red[tr][tc] = s;
+  __syncthreads();
+  if (tr == 0 && c < 2 * store.W) {
+    float t = red[0][tc];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) t += red[k][tc];
+    store(c, t);
+  }
+}
+
+template <typename T, int LANES, int NV, int V>
+hipError_t fwd(const NormArgs& a, const NormPlan&, hipStream_t s) {
+  using P = Norm<T, LANES, NV, V>;
+  const int64_t units = a.rows * a.G, per = P::kBlock / LANES;
+  hipLaunchKernelGGL((norm_fwd_kernel<T, LANES, NV, V>), dim3((unsigned)((units + per - 1) / per)),
+                     dim3(P::kBlock), 0, s, a, units);
+  const hipError_t e = hipGetLastError();
+  note_launch(s);
+  return e;
+}
+
+template <typename T, int LANES, int NV, int V>
+hipError_t bwd(const NormArgs& a, const NormPlan& p, hipStream_t s) {
+  using P = Norm<T, LANES, NV, V>;
+  hipLaunchKernelGGL((norm_bwd_kernel<T, LANES, NV, V>), dim3((unsigned)(p.slabs * p.parts)),
+                     dim3(P::kBlock), 0, s, a, a.rows * a.G, p.period, (int)p.slabs);
+  hipError_t e = hipGetLastError();
+  note_launch(s);
+  if (e != hipSuccess || (a.dw == nullptr && a.dbias == nullptr)) return e;
+  const int64_t W = a.shared ? a.D : a.C;
+  const int64_t reps = a.shared ? 1 : p.period / a.G;
+  hipLaunchKernelGGL(norm_sums, dim3((unsigned)((2 * W + kSumCols - 1) / kSumCols)), dim3(256), 0,
+                     s, a.part, p.parts, reps, NormSumStore{a.dw, a.dbias, W, a.w_bf16});
+  e = hipGetLastError();
+  note_launch(s);
+  return e;
+}
+
+template <typename T, bool BWD, int LANES, int NV, int V>
+hipError_t go(const NormArgs& a, const NormPlan& p, hipStream_t s) {
+  return BWD ? bwd<T, LANES, NV, V>(a, p, s) : fwd<T, LANES, NV, V>(a, p, s);
+}
+
+template <typename T, bool BWD, int NV, int V>
+hipError_t launch_lanes(const NormArgs& a, const NormPlan& p, hipStream_t s) {
+  if constexpr (NV == 1) {
+    if (p.lanes == 8) return go<T, BWD, 8, 1, V>(a, p, s);
+    if (p.lanes == 16) return go<T, BWD, 16, 1, V>(a, p, s);
+    if (p.lanes == 32) return go<T, BWD, 32, 1, V>(a, p, s);
+  }
+  if (p.lanes == 64) return go<T, BWD, 64, NV, V>(a, p, s);
+  if constexpr (NV * V >= 8)
+    if (p.lanes == 256) return go<T, BWD, 256, NV, V>(a, p, s);
+  if constexpr (NV * V == 16)
+    if (p.lanes == 512) return go<T, BWD, 512, NV, V>(a, p, s);
+  return hipErrorInvalidValue;
+}
+
+template <typename T, bool BWD, int V>
+hipError_t launch_v(const NormArgs& a, const NormPlan& p, hipStream_t s) {
+  switch (p.nv) {
+    case 1: return launch_lanes<T, BWD, 1, V>(a, p, s);
+    case 2: return launch_lanes<T, BWD, 2, V>(a, p, s);
+    case 4:
+      if constexpr (V <= 4) return launch_lanes<T, BWD, 4, V>(a, p, s);
+      break;
+    case 16:
+      if constexpr (V == 1) return launch_lanes<T, BWD, 16, V>(a, p, s);
+      break;
+  }
+  return hipErrorInvalidValue;
+}
+
+template <typename T, bool BWD>
+hipError_t launch(const NormArgs& a, const NormPlan& p, hipStream_t s) {
+  return p.vec ? launch_v<T, BWD, 16 / sizeof(T)>(a, p, s) : launch_v<T, BWD, 1>(a, p, s);
+}
+
+int64_t gcd64(int64_t a, int64_t b) { return b == 0 ? a : gcd64(b, a % b); }
+
+}  // namespace
+
+// Lanes and vectors of a group: at most 16 channels per lane (the backward
+// holds six values per channel), so groups of up to 1024 channels take (part
+// of) a wave and up to 8192 a workgroup.
+bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool shared, bool bf16,
+               NormPlan* p) {
+  const int64_t D = C / G, V = bf16 ? 8 : 4;
+  p->vec = D % V == 0 && xs % V == 0 && zs % V == 0;
+  const int64_t v = p->vec ? V : 1, n = (D + v - 1) / v;  // vectors of a group
+  const int most_nv = (int)(16 / v);
+  if (n <= 64) {
+    p->lanes = 8;
+    while (p->lanes < n) p->lanes *= 2;
+  } else if (n <= 64 * most_nv) {
+    p->lanes = 64;
+  } else {
+    p->lanes = 256;
+    while (p->lanes * most_nv < n) p->lanes *= 2;
+    if (p->lanes > 512) return false;
+  }
+  p->nv = 1;
+  while (p->lanes * p->nv < n) p->nv *= 2;
+  if (p->nv == 8 || (p->nv < most_nv && p->lanes > 256)) p->nv = most_nv;
+  const int64_t per = p->lanes > 64 ? 1 : 64 / p->lanes;
+  p->period = shared ? per : G / gcd64(G, per) * per;
+  p->slabs = p->period / per;
+  // about 2048 workgroups (of four waves; 512 of sixteen) in all, a part
+  // per workgroup of a slab, and no more parts than there are units for
+  const int64_t walkers = p->lanes > 64 ? 1 : kThreads / 64;
+  const int64_t want = p->lanes > 64 ? 512 : 2048;
+  const int64_t turns = (rows * G + p->period - 1) / p->period;
+  int64_t parts = (want + p->slabs - 1) / p->slabs;
+  const int64_t most = (turns + walkers - 1) / walkers;
+  if (parts > most) parts = most;
+  p->parts = parts < 1 ? 1 : parts;
+  return true;
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a, const NormPlan& p, bool is_bf16, hipStream_t s) {
+  return is_bf16 ? launch<bf16, false>(a, p, s) : launch<float, false>(a, p, s);
+}
+hipError_t launch_norm_bwd(const NormArgs& a, const NormPlan& p, bool is_bf16, hipStream_t s) {
+  return is_bf16 ? launch<bf16, true>(a, p, s) : launch<float, true>(a, p, s);
+}
+
+}  // namespace gdr

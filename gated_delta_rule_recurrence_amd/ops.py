@@ -200,3 +200,398 @@ def gated_delta_rule(q, k, v, g, beta, S0=None, chunk=DEFAULT_CHUNK, log_decay=F
     the log of the decay and its gradient is dL/d(log g); mask [B,T] marks
     identity steps with 0."""
     return GatedDeltaRule.apply(q, k, v, g, beta, S0, chunk, log_decay, mask)
+
+
+# ---- the operators around the recurrence ----------------------------------------
+#
+# Activations are rows: [B, T, ...] or, with spans, [rows, ...] (any leading
+# dimensions that collapse to one row stride, so slices of a wider projection
+# pass as they are).  spans is int32 [B, 2] on the device, the first row and
+# the row past the last of each sequence, ascending and disjoint; T is then
+# the longest sequence's length (by default the number of rows, which sizes
+# grid and workspace for that).  Rows of no sequence are neither read nor
+# written: buffers that a call allocates hold zeros there.
+
+_ACTS = {None: _lib.GDR_ACT_NONE, "none": _lib.GDR_ACT_NONE, "silu": _lib.GDR_ACT_SILU}
+
+
+def _act(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be None, 'none' or 'silu', got {act!r}")
+    return _ACTS[act]
+
+
+def _row_stride(name, t, tail, dtype, device, rows=None):
+    """Checks a tensor of rows whose last dimensions are `tail` and dense;
+    returns (rows, elements from one row to the next)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    k = len(tail)
+    shape, strides = t.shape, t.stride()
+    if len(shape) <= k or tuple(shape[-k:]) != tuple(tail):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected rows of {tuple(tail)}")
+    width = 1
+    for size, stride in zip(reversed(shape[-k:]), reversed(strides[-k:])):
+        if size != 1 and stride != width:
+            raise ValueError(f"{name}: a row's {tuple(tail)} elements must be contiguous")
+        width *= size
+    n, step = 1, 0
+    for size, stride in zip(reversed(shape[:-k]), reversed(strides[:-k])):
+        if size == 0:
+            n = 0
+            break
+        if size == 1:
+            continue
+        if n == 1:
+            step = stride
+        elif stride != step * n:
+            raise ValueError(f"{name}: the rows must lie at one stride (got strides {strides})")
+        n *= size
+    if n > 1 and step < width:
+        raise ValueError(f"{name}: the rows overlap (got strides {strides})")
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} has {n} rows, expected {rows}")
+    return n, (step if n > 1 else width)
+
+
+def _gpu(x):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("the rows must be a torch.Tensor")
+    if x.device.type != "cuda":
+        raise ValueError("the rows must be a GPU tensor (the library has no CPU path)")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    return x.device, x.dtype
+
+
+def _sequences(x, rows, tail, spans, T, device):
+    """(B, T) of rows x [..., *tail]."""
+    if spans is not None:
+        if spans.dim() != 2:
+            raise ValueError(f"spans has shape {tuple(spans.shape)}, expected (B, 2)")
+        _check_tensor("spans", spans, (spans.shape[0], 2), torch.int32, device)
+        return spans.shape[0], rows if T is None else int(T)
+    if T is None:
+        if x.dim() != len(tail) + 2:
+            raise ValueError("T is needed where the rows are not [B, T, ...]")
+        return x.shape[0], x.shape[1]
+    T = int(T)
+    if T < 0 or (rows % T if T else rows):
+        raise ValueError(f"{rows} rows are not sequences of {T}")
+    return (rows // T if T else 0), T
+
+
+def _weight_dtype(name, w):
+    if w.dtype not in _DTYPES:
+        raise ValueError(f"{name} has unsupported dtype {w.dtype}")
+    return w.dtype
+
+
+def _out(given, name, shape, dtype, device, spans):
+    if given is None:
+        make = torch.empty if spans is None else torch.zeros
+        return make(shape, dtype=dtype, device=device)
+    _check_tensor(name, given, shape, dtype, device)
+    return given
+
+
+def _scratch(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=device)
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return workspace
+
+
+def _launch(name, shape, tensors, device, workspace=None):
+    ptrs = [0 if t is None else t.data_ptr() for t in tensors]
+    nbytes = None
+    if workspace is not None:
+        ptrs.append(workspace.data_ptr())
+        nbytes = workspace.numel() * workspace.element_size()
+    if torch.cuda.current_device() == device.index:
+        status = _lib.layer_raw(name, shape, ptrs, _stream(device), nbytes)
+    else:  # a stream's kernels are launched with its device current
+        with torch.cuda.device(device):
+            status = _lib.layer_raw(name, shape, ptrs, _stream(device), nbytes)
+    _lib.check(status, name)
+
+
+def _conv_shape(x, weight, bias, state, spans, T, act):
+    dev, dt = _gpu(x)
+    C, K = weight.shape
+    wdt = _weight_dtype("weight", weight)
+    _check_tensor("weight", weight, (C, K), wdt, dev)
+    rows, xs = _row_stride("x", x, (C,), dt, dev)
+    B, T = _sequences(x, rows, (C,), spans, T, dev)
+    if bias is not None:
+        _check_tensor("bias", bias, (C,), wdt, dev)
+    if state is not None:
+        _check_tensor("state", state, (B, K - 1, C), dt, dev)
+    return _lib.GdrConvShape(B, T, rows, C, K, xs, _DTYPES[dt], _DTYPES[wdt], _act(act), 0)
+
+
+def gdr_conv_forward(x, weight, bias=None, state=None, *, act="silu", spans=None, T=None,
+                     out_state=True, y=None, state_out=None):
+    """Short causal convolution.  Returns (y, state_out or None).
+
+    x [B,T,C] (or rows, see above), weight [C,K], bias [C] or None, state
+    [B,K-1,C] (the inputs before each sequence) or None.  state_out may be
+    state (in place)."""
+    shape = _conv_shape(x, weight, bias, state, spans, T, act)
+    dev, dt = x.device, x.dtype
+    y = _out(y, "y", x.shape, dt, dev, spans)
+    if not out_state:
+        state_out = None
+    else:
+        state_out = _out(state_out, "state_out", (shape.B, shape.K - 1, shape.C), dt, dev, None)
+    _launch("gdr_conv_forward", shape, (x, weight, bias, state, spans, y, state_out), dev)
+    return y, state_out
+
+
+def gdr_conv_backward(x, weight, bias, state, dy, dstate_out=None, *, act="silu", spans=None,
+                      T=None, want_dstate=False, workspace=None):
+    """Returns (dx, dweight, dbias or None, dstate or None)."""
+    shape = _conv_shape(x, weight, bias, state, spans, T, act)
+    dev, dt = x.device, x.dtype
+    _check_tensor("dy", dy, x.shape, dt, dev)
+    window = (shape.B, shape.K - 1, shape.C)
+    if dstate_out is not None:
+        _check_tensor("dstate_out", dstate_out, window, dt, dev)
+    dx = _out(None, "dx", x.shape, dt, dev, spans)
+    make = torch.empty_like if shape.B > 0 else torch.zeros_like
+    dweight = make(weight)
+    dbias = None if bias is None else make(bias)
+    dstate = torch.empty(window, dtype=dt, device=dev) if want_dstate else None
+    workspace = _scratch(workspace, _lib.size_of("gdr_conv_backward_workspace_bytes", shape), dev)
+    _launch("gdr_conv_backward", shape, (x, weight, bias, state, spans, dy, dstate_out, dx,
+                                         dweight, dbias, dstate), dev, workspace)
+    return dx, dweight, dbias, dstate
+
+
+@dataclass
+class ScanSaved:
+    """What gdr_scan_forward leaves for gdr_scan_backward (opaque fp32
+    buffer), with the settings the backward must repeat."""
+
+    ckpt: torch.Tensor
+    spans: Optional[torch.Tensor]
+    T: int
+    softplus: bool
+
+
+def _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus):
+    dev, ty = _gpu(u)
+    f32 = torch.float32
+    if A.dim() != 2 or Bm.dim() < 3:
+        raise ValueError("A must be [C, N] and Bm, Cm [.., G, N]")
+    C, N = A.shape
+    G = Bm.shape[-2]
+    rows, us = _row_stride("u", u, (C,), ty, dev)
+    _, dts = _row_stride("dt", dt, (C,), ty, dev, rows)
+    _, bs = _row_stride("Bm", Bm, (G, N), ty, dev, rows)
+    _, cs = _row_stride("Cm", Cm, (G, N), ty, dev, rows)
+    zs = C if z is None else _row_stride("z", z, (C,), ty, dev, rows)[1]
+    _check_tensor("A", A, (C, N), f32, dev)
+    if D is not None:
+        _check_tensor("D", D, (C,), f32, dev)
+    if dt_bias is not None:
+        _check_tensor("dt_bias", dt_bias, (C,), f32, dev)
+    B, T = _sequences(u, rows, (C,), spans, T, dev)
+    return _lib.GdrScanShape(B, T, rows, C, N, G, us, dts, zs, bs, cs, _DTYPES[ty],
+                             1 if softplus else 0)
+
+
+def gdr_scan_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, softplus=True,
+                     spans=None, T=None, save=True, out_state=True, y=None, S_T=None, ckpt=None,
+                     workspace=None):
+    """Selective state space scan.  Returns (y, S_T or None, ScanSaved or None).
+
+    u, dt, z [B,T,C] (or rows, see above); A [C,N], D, dt_bias [C] fp32; Bm,
+    Cm [B,T,G,N]; S0 [B,C,N] fp32 or None.  S_T may be S0 (in place)."""
+    shape = _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus)
+    dev = u.device
+    states = (shape.B, shape.C, shape.N)
+    if S0 is not None:
+        _check_tensor("S0", S0, states, torch.float32, dev)
+    y = _out(y, "y", u.shape, u.dtype, dev, spans)
+    S_T = _out(S_T, "S_T", states, torch.float32, dev, None) if out_state else None
+    saved = None
+    if save:
+        nbytes = _lib.size_of("gdr_scan_checkpoint_bytes", shape)
+        if ckpt is None:
+            ckpt = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=dev)
+        if ckpt.numel() * ckpt.element_size() < nbytes:
+            raise ValueError("ckpt buffer too small")
+        saved = ScanSaved(ckpt, spans, shape.T, bool(softplus))
+    workspace = _scratch(workspace, _lib.size_of("gdr_scan_forward_workspace_bytes", shape), dev)
+    _launch("gdr_scan_forward", shape, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, spans, y, S_T,
+                                        ckpt if save else None), dev, workspace)
+    return y, S_T, saved
+
+
+def gdr_scan_backward(u, dt, A, Bm, Cm, D, z, dt_bias, saved: ScanSaved, dy, dS_T=None, *,
+                      want_dS0=True, workspace=None):
+    """Returns (du, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dS0); None where the
+    forward had no such input, and dS0 only where wanted."""
+    spans = saved.spans
+    shape = _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.T, saved.softplus)
+    dev, ty = u.device, u.dtype
+    states = (shape.B, shape.C, shape.N)
+    _check_tensor("dy", dy, u.shape, ty, dev)
+    if dS_T is not None:
+        _check_tensor("dS_T", dS_T, states, torch.float32, dev)
+    du, ddt, dB, dC = (_out(None, "", t.shape, ty, dev, spans) for t in (u, dt, Bm, Cm))
+    dz = None if z is None else _out(None, "", z.shape, ty, dev, spans)
+    make = torch.empty_like if shape.B > 0 else torch.zeros_like
+    dA = make(A)
+    dD, dbias = (None if t is None else make(t) for t in (D, dt_bias))
+    dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
+    workspace = _scratch(workspace, _lib.size_of("gdr_scan_backward_workspace_bytes", shape), dev)
+    _launch("gdr_scan_backward", shape, (u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.ckpt, dy,
+                                         dS_T, du, ddt, dA, dB, dC, dD, dz, dbias, dS0), dev,
+            workspace)
+    return du, ddt, dA, dB, dC, dD, dz, dbias, dS0
+
+
+def _norm_shape(x, weight, bias, z, groups, eps, center, act):
+    dev, dt = _gpu(x)
+    C = x.shape[-1]
+    if groups < 1 or C % groups:
+        raise ValueError(f"{C} channels are not {groups} groups")
+    wdt, shared = dt, False
+    for name, w in (("weight", weight), ("bias", bias)):
+        if w is None:
+            continue
+        wdt = _weight_dtype(name, w if weight is None else weight)
+        shared = w.numel() != C
+        width = C // groups if (w if weight is None else weight).numel() != C else C
+        _check_tensor(name, w, (width,), wdt, dev)
+    rows, xs = _row_stride("x", x, (C,), dt, dev)
+    zs = C
+    if z is not None:
+        if z.shape != x.shape:
+            raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(x.shape)}")
+        zs = _row_stride("z", z, (C,), dt, dev, rows)[1]
+    return _lib.GdrNormShape(rows, C, groups, xs, zs, eps, _DTYPES[dt], _DTYPES[wdt],
+                             1 if center else 0, 1 if shared else 0, _act(act))
+
+
+def gdr_norm_forward(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, center=False,
+                     act="silu", save=True, y=None, stats=None):
+    """Group norm of the last dimension, in `groups` groups.  Returns (y,
+    stats or None).  x, z [..., C]; weight, bias [C], or [C // groups] used by
+    every group.  The activation takes z where there is one, else the normed
+    rows."""
+    shape = _norm_shape(x, weight, bias, z, groups, eps, center, act)
+    dev = x.device
+    y = _out(y, "y", x.shape, x.dtype, dev, None)
+    if save:
+        stats = _out(stats, "stats", (shape.rows, shape.G, 2), torch.float32, dev, None)
+    else:
+        stats = None
+    _launch("gdr_norm_forward", shape, (x, weight, bias, z, y, stats), dev)
+    return y, stats
+
+
+def gdr_norm_backward(x, weight, bias, z, stats, dy, *, groups, center=False, act="silu",
+                      workspace=None):
+    """Returns (dx, dweight, dbias, dz); None where the forward had no such
+    input."""
+    shape = _norm_shape(x, weight, bias, z, groups, 0.0, center, act)
+    dev = x.device
+    _check_tensor("dy", dy, x.shape, x.dtype, dev)
+    _check_tensor("stats", stats, (shape.rows, shape.G, 2), torch.float32, dev)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dz = None if z is None else torch.empty(z.shape, dtype=x.dtype, device=dev)
+    dweight, dbias = (None if w is None else torch.empty_like(w) for w in (weight, bias))
+    if weight is None and bias is None:
+        nbytes = 0
+    else:
+        nbytes = _lib.size_of("gdr_norm_backward_workspace_bytes", shape)
+    workspace = _scratch(workspace, nbytes, dev)
+    _launch("gdr_norm_backward", shape, (x, weight, bias, z, stats, dy, dx, dweight, dbias, dz),
+            dev, workspace)
+    return dx, dweight, dbias, dz
+
+
+class CausalConv(torch.autograd.Function):
+    """y, state_out = causal_conv(x, weight, bias, state) with the library VJP."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, act, spans, T):
+        y, state_out = gdr_conv_forward(x, weight, bias, state, act=act, spans=spans, T=T)
+        ctx.settings = (act, T)
+        ctx.save_for_backward(x, weight, bias, state, spans)
+        return y, state_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dstate_out):
+        x, weight, bias, state, spans = ctx.saved_tensors
+        act, T = ctx.settings
+        dx, dw, db, ds = gdr_conv_backward(
+            x, weight, bias, state, dy.contiguous(), dstate_out.contiguous(), act=act, spans=spans,
+            T=T, want_dstate=state is not None)
+        return dx, dw, db, ds, None, None, None
+
+
+def causal_conv(x, weight, bias=None, state=None, *, act="silu", spans=None, T=None):
+    """Autograd-enabled short causal convolution: returns (y, state_out)."""
+    return CausalConv.apply(x, weight, bias, state, act, spans, T)
+
+
+class SelectiveScan(torch.autograd.Function):
+    """y, S_T = selective_scan(...) with the library VJP."""
+
+    @staticmethod
+    def forward(ctx, u, dt, A, Bm, Cm, D, z, dt_bias, S0, softplus, spans, T, save):
+        y, S_T, ctx.saved = gdr_scan_forward(u, dt, A, Bm, Cm, D, z, dt_bias, S0,
+                                             softplus=softplus, spans=spans, T=T, save=save)
+        ctx.has_S0 = S0 is not None
+        ctx.save_for_backward(u, dt, A, Bm, Cm, D, z, dt_bias)
+        return y, S_T
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dS_T):
+        grads = gdr_scan_backward(*ctx.saved_tensors, ctx.saved, dy.contiguous(),
+                                  dS_T.contiguous(), want_dS0=ctx.has_S0)
+        return (*grads, None, None, None, None)
+
+
+def selective_scan(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, softplus=True,
+                   spans=None, T=None):
+    """Autograd-enabled selective state space scan: returns (y, S_T).  The
+    states for the backward are saved only where a gradient is wanted."""
+    args = (u, dt, A, Bm, Cm, D, z, dt_bias, S0)
+    save = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args)
+    return SelectiveScan.apply(*args, softplus, spans, T, save)
+
+
+class GroupNorm(torch.autograd.Function):
+    """y = group_norm(x, weight, bias, z) with the library VJP."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, z, groups, eps, center, act):
+        y, stats = gdr_norm_forward(x, weight, bias, z, groups=groups, eps=eps, center=center,
+                                    act=act)
+        ctx.settings = dict(groups=groups, center=center, act=act)
+        ctx.save_for_backward(x, weight, bias, z, stats)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        dx, dw, db, dz = gdr_norm_backward(*ctx.saved_tensors, dy.contiguous(), **ctx.settings)
+        return dx, dw, db, dz, None, None, None, None
+
+
+def group_norm(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, center=False, act="silu"):
+    """Autograd-enabled group norm of the last dimension (see
+    gdr_norm_forward): returns y."""
+    return GroupNorm.apply(x, weight, bias, z, groups, eps, center, act)

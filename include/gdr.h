@@ -60,8 +60,15 @@ typedef enum {
   GDR_ERR_BAD_DECAY = -11,      /* decay is not GDR_DECAY_G or GDR_DECAY_LOG    */
   GDR_ERR_SCRATCH_LIMIT = -12,  /* gdr_forward_noalloc: the shape's forward
                                    workspace exceeds GDR_NOALLOC_SCRATCH_BYTES */
-  GDR_ERR_BAD_COUNT = -13       /* gdr_set_launch_events: n outside
+  GDR_ERR_BAD_COUNT = -13,      /* gdr_set_launch_events: n outside
                                    0 .. GDR_MAX_LAUNCH_EVENTS               */
+  GDR_ERR_BAD_DIM = -14,        /* a dimension of a gdr_conv_shape,
+                                   gdr_scan_shape or gdr_norm_shape outside
+                                   the range stated there                   */
+  GDR_ERR_BAD_STRIDE = -15,     /* a row stride below the row's width or
+                                   above 2^31 - 1                           */
+  GDR_ERR_BAD_ACT = -16,        /* act is not a gdr_act, or softplus not 0, 1 */
+  GDR_ERR_BAD_EPS = -17         /* eps negative, infinite or NaN             */
 } gdr_status;
 
 /* Size of the device-side scratch array behind gdr_forward_noalloc (128 MiB;
@@ -201,7 +208,7 @@ int gdr_backward(const gdr_shape* shape, const void* q, const void* k,
 /* Measurement hook, for callers that time the library's kernels one by one
  * (a profiler-free per-kernel breakdown; not needed to compute anything).
  * While n > 0, every gdr_forward, gdr_forward_noalloc and gdr_backward call
- * records events[i] on its stream right after launching its i-th kernel
+ * (and every forward and backward of the operators below) records events[i] on its stream right after launching its i-th kernel
  * (counted from 0 in each call; launches past the n-th record nothing) and,
  * when it succeeds, the events past its last launch at its end, so that each
  * event is recorded once per call.  The time between two consecutive events,
@@ -217,6 +224,144 @@ int gdr_backward(const gdr_shape* shape, const void* q, const void* k,
  * GDR_ERR_NULL_ARG (events, or one of its first n entries, is NULL, n > 0). */
 #define GDR_MAX_LAUNCH_EVENTS 8
 int gdr_set_launch_events(void* const* events, int n);
+
+/* ---------------------------------------------------------------------------
+ * The operators around the recurrence in a layer: the short causal
+ * convolution that makes its q, k, v, the selective state space scan (the
+ * sibling recurrence, with a diagonal state per channel) and the group norm
+ * with a gate behind it.  Ownership, streams, errors and determinism as
+ * above; every data pointer is 16-byte aligned.
+ *
+ * Rows.  Activations are rows [rows][width] of one element type; x, u, dt, z,
+ * B and C may be slices of wider rows (a *_stride field: elements from one
+ * row to the next, 0 means dense); every output and every gradient is dense.
+ *
+ * Sequences.  spans = NULL: B sequences of T rows each, one after another
+ * (rows = B T).  Else spans is a device array int32[B][2]: sequence b owns
+ * rows spans[b][0] <= row < spans[b][1], sequences ascending and disjoint
+ * (packed prompts, batches padded on either side); T is then the longest
+ * sequence's length, and steps past T are not taken.  Rows of no sequence
+ * are neither read nor written.  A sequence of no rows keeps its state.
+ * Spans outside 0 .. rows are cut to that range; ones that overlap give
+ * unspecified values.
+ * ------------------------------------------------------------------------- */
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_act; /* x, x / (1 + e^-x) */
+
+/* Causal convolution of K taps over the rows of each sequence, per channel:
+ *     s_t = bias[c] + sum_{j<K} weight[c][j] x_{t-(K-1)+j}[c];  y_t = act(s_t)
+ * with x before the sequence from state (the K - 1 inputs before it), or 0.
+ * 1 <= K <= GDR_CONV_MAX_TAPS, 1 <= C <= 2^20, B <= 65535, T and rows at most
+ * 2^30 - 1. */
+#define GDR_CONV_MAX_TAPS 8
+typedef struct {
+  int64_t B, T, rows, C, K;
+  int64_t x_stride;      /* 0 = C */
+  int32_t dtype, wdtype; /* gdr_dtype of the rows; of weight, bias and theirs */
+  int32_t act;           /* gdr_act */
+  int32_t reserved;
+} gdr_conv_shape;
+
+/*   in : x [rows][C], weight [C][K], bias [C] (NULL: 0), state [B][K-1][C]
+ *        (dtype; NULL: 0), spans (NULL: dense)
+ *   out: y [rows][C]; state_out [B][K-1][C]: the last K - 1 inputs of each
+ *        sequence, its state included (NULL: not written).  state_out may be
+ *        state (in place).
+ * Single tokens are calls with T = 1 that pass the state along. */
+int gdr_conv_forward(const gdr_conv_shape* shape, const void* x, const void* weight,
+                     const void* bias, const void* state, const int32_t* spans, void* y,
+                     void* state_out, void* stream);
+
+int gdr_conv_backward_workspace_bytes(const gdr_conv_shape* shape, size_t* out);
+
+/* VJP of gdr_conv_forward for <dy, y> + <dstate_out, state_out> (dstate_out
+ * NULL: 0).  dx [rows][C]; dweight [C][K], dbias [C] (NULL: not written), in
+ * wdtype, summed in fp32 in a fixed order; dstate [B][K-1][C] (NULL: not
+ * written; not the dstate_out buffer).  Nothing is saved by the forward:
+ * s_t is formed again from x. */
+int gdr_conv_backward(const gdr_conv_shape* shape, const void* x, const void* weight,
+                      const void* bias, const void* state, const int32_t* spans, const void* dy,
+                      const void* dstate_out, void* dx, void* dweight, void* dbias, void* dstate,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Selective state space scan: per sequence, channel c and state n, channel c
+ * reading group g = c / (C / G) of B and C, with fp32 states
+ *     delta_t = softplus(dt_t[c] + dt_bias[c])   (softplus = 0: the sum itself)
+ *     h_t[c][n] = exp(delta_t A[c][n]) h_{t-1}[c][n] + delta_t u_t[c] B_t[g][n]
+ *     y_t[c] = (sum_n C_t[g][n] h_t[c][n] + D[c] u_t[c]) * silu(z_t[c])
+ * 1 <= N <= GDR_SCAN_MAX_STATES, C a multiple of G, C <= 2^20, B <= 65535,
+ * T and rows at most 2^30 - 1. */
+#define GDR_SCAN_MAX_STATES 64
+typedef struct {
+  int64_t B, T, rows, C, N, G;
+  int64_t u_stride, dt_stride, z_stride; /* 0 = C */
+  int64_t b_stride, c_stride;            /* 0 = G N */
+  int32_t dtype;    /* gdr_dtype of u, dt, B, C, z, y and their gradients */
+  int32_t softplus; /* 0 or 1 */
+} gdr_scan_shape;
+
+/* Bytes of the save buffer (the states every 16 steps: 8 for N > 16, 4 for
+ * N > 32), and of the scratch buffers (0 where the sequences run unsplit). */
+int gdr_scan_checkpoint_bytes(const gdr_scan_shape* shape, size_t* out);
+int gdr_scan_forward_workspace_bytes(const gdr_scan_shape* shape, size_t* out);
+int gdr_scan_backward_workspace_bytes(const gdr_scan_shape* shape, size_t* out);
+
+/*   in : u, dt [rows][C]; A [C][N] fp32; Bm, Cm [rows][G][N]; D [C] fp32
+ *        (NULL: 0); z [rows][C] (NULL: no gate); dt_bias [C] fp32 (NULL: 0);
+ *        S0 [B][C][N] fp32 (NULL: 0); spans (NULL: dense)
+ *   out: y [rows][C]; S_T [B][C][N] fp32 (NULL: not written; may be S0);
+ *        ckpt: gdr_scan_checkpoint_bytes bytes (NULL: inference).
+ *   workspace: gdr_scan_forward_workspace_bytes bytes (NULL if 0).
+ * Single tokens are calls with T = 1 and S_T = S0. */
+int gdr_scan_forward(const gdr_scan_shape* shape, const void* u, const void* dt, const float* A,
+                     const void* Bm, const void* Cm, const float* D, const void* z,
+                     const float* dt_bias, const float* S0, const int32_t* spans, void* y,
+                     float* S_T, void* ckpt, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* VJP of gdr_scan_forward for <dy, y> + <dS_T, S_T> (dS_T NULL: 0), from the
+ * same inputs and the ckpt that call wrote (S0 is in it).  du, ddt, dz
+ * [rows][C], dB, dC [rows][G][N] in dtype; dA [C][N], dD [C], ddt_bias [C],
+ * dS0 [B][C][N] fp32.  dz is required with z; dD, ddt_bias and dS0 may be
+ * NULL.  Sums over rows, sequences and the channels of a group are formed in
+ * fp32 in a fixed order. */
+int gdr_scan_backward(const gdr_scan_shape* shape, const void* u, const void* dt, const float* A,
+                      const void* Bm, const void* Cm, const float* D, const void* z,
+                      const float* dt_bias, const int32_t* spans, const void* ckpt, const void* dy,
+                      const float* dS_T, void* du, void* ddt, float* dA, void* dB, void* dC,
+                      float* dD, void* dz, float* ddt_bias, float* dS0, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Group norm of rows [rows][C]: group g is channels g C/G .. of one row,
+ *     xh = (x - mu) / sqrt(mean((x - mu)^2) + eps),  mu = the group's mean
+ *     (center = 1) or 0 (center = 0, a root mean square norm)
+ *     n = xh weight + bias;  y = act(n) without z, n act(z) with a gate z.
+ * weight and bias are [C], or [C/G] used by every group (shared_weight).
+ * C a multiple of G, C/G <= 8192, C <= 2^20, rows <= 2^30 - 1,
+ * rows G <= 2^31 - 1. */
+typedef struct {
+  int64_t rows, C, G;
+  int64_t x_stride, z_stride; /* 0 = C */
+  float eps;
+  int32_t dtype, wdtype; /* gdr_dtype of the rows; of weight, bias and theirs */
+  int32_t center, shared_weight, act;
+} gdr_norm_shape;
+
+/* weight NULL: 1; bias NULL: 0; z NULL: no gate; stats: fp32 [rows][G][2],
+ * mu and 1/sqrt(..) for the backward (NULL: not written).  y may be x or z if
+ * that is dense (each group is read before it is written). */
+int gdr_norm_forward(const gdr_norm_shape* shape, const void* x, const void* weight,
+                     const void* bias, const void* z, void* y, float* stats, void* stream);
+
+int gdr_norm_backward_workspace_bytes(const gdr_norm_shape* shape, size_t* out);
+
+/* VJP of gdr_norm_forward from the same inputs and its stats: dx, dz
+ * [rows][C] (dz required with z), dweight, dbias in wdtype and the weight's
+ * shape (NULL: not formed; with both NULL no workspace is needed), summed in
+ * fp32 in a fixed order. */
+int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* weight,
+                      const void* bias, const void* z, const float* stats, const void* dy,
+                      void* dx, void* dweight, void* dbias, void* dz, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Static, human-readable text for a gdr_status value. */
 const char* gdr_strerror(int status);

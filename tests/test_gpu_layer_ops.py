@@ -1,0 +1,446 @@
+"""GPU parity of the short causal convolution, the selective state space scan
+and the group norm against their float64 oracle, element by element.
+
+Tolerance.  An output element is off by at most
+    half |ref| + n 2^-24 mag + 1e-30,
+half a rounding step of its type (2^-8 bf16, 0 for what stays in fp32 as the
+fp32 store is among the n), mag the sum of the absolute values of its terms
+(the oracle's mag=True), n the roundings in fp32 on the way to it:
+  * conv: K products and sums, the activation (an exponential whose argument
+    |s| <= 30 carries |s| units, a reciprocal and two products): n = 64; the
+    weight's gradients add one sum per row: n = 64 + rows.
+  * scan: delta carries at most 3 |raw| + 8 <= 64 units (|raw| <= 18); a
+    decay's argument error |delta A| (units of delta + 2) is weighted by the
+    decay itself, |x| e^-|x| < 0.37 over any path, so the decays of a path
+    carry at most 0.37 * 66 + 4 per step: n = 128 + 4 steps forward, twice
+    that backward (the adjoint runs over the states), plus one per row in the
+    sums over rows, and the 64 channels, 4 waves and tiles of a group.
+  * norm: sums of up to 16 terms a lane, then a tree; the statistics' errors
+    enter twice: n = 128, plus one per row in the sums over rows.
+"""
+import numpy as np
+import pytest
+
+import oracle.layer_oracle as L
+
+pytestmark = pytest.mark.gpu
+
+ULP = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": 0.0}
+
+
+def torch_type(dtype):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+
+
+def round_to(a, dtype):
+    import torch
+    if a is None:
+        return None
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch_type(dtype))
+    return t.double().numpy()
+
+
+def dev_of(a, dtype, dev):
+    import torch
+    if a is None:
+        return None
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(dev).to(torch_type(dtype))
+
+
+def wide(t, pad=8):
+    """The same rows as a slice of wider ones (a row stride), pad elements
+    before and 2 pad behind, filled with NaN."""
+    import torch
+    if t is None:
+        return None
+    lead = t.shape[:-1]
+    w = torch.full((*lead, t.shape[-1] + 3 * pad), float("nan"), dtype=t.dtype, device=t.device)
+    w[..., pad:pad + t.shape[-1]] = t
+    return w[..., pad:pad + t.shape[-1]]
+
+
+def check(name, got, ref, mag, dtype, n):
+    got = got.double().cpu().numpy().reshape(ref.shape)
+    assert np.isfinite(got).all(), f"{name}: not finite"
+    tol = HALF[dtype] * np.abs(ref) + (n + 1) * ULP * mag * (1 + HALF[dtype]) + 1e-30
+    off = np.abs(got - ref) / tol
+    worst = float(off.max(initial=0.0))
+    if worst > 1.0:
+        pytest.fail(f"{name}: {worst:.2f} of the tolerance at {np.unravel_index(off.argmax(), off.shape)}")
+
+
+def seqs_of(B, T, spans):
+    return spans if spans is not None else [(b * T, (b + 1) * T) for b in range(B)]
+
+
+def dev_spans(spans, dev):
+    import torch
+    return None if spans is None else torch.tensor(spans, dtype=torch.int32, device=dev).reshape(-1, 2)
+
+
+def outside(rows, seqs):
+    m = np.ones(rows, bool)
+    for i, j in seqs:
+        m[i:j] = False
+    return m
+
+
+# packed prompts: empty ones, one row, gaps, rows before the first and behind
+# the last
+PACKED = [(2, 2), (2, 3), (5, 40), (40, 40), (40, 75), (80, 81), (81, 146), (150, 150)]
+PACKED_ROWS = 153
+
+
+# ---- convolution ---------------------------------------------------------------
+
+def conv_case(dev, dtype, B, T, C, K, *, wdtype=None, act="silu", bias=True, state=True, spans=None,
+              rows=None, stride=False, seed=0):
+    from gated_delta_rule_recurrence_amd import ops
+    r = np.random.default_rng(seed)
+    wdtype = wdtype or dtype
+    rows = B * T if rows is None else rows
+    n = lambda *s: round_to(r.normal(size=s), dtype)
+    x, dy = n(rows, C), n(rows, C)
+    w, b = round_to(r.normal(size=(C, K)), wdtype), round_to(r.normal(size=C), wdtype) if bias else None
+    st = n(B, K - 1, C) if state else None
+    dso = n(B, K - 1, C)
+    seqs = seqs_of(B, T, spans)
+    longest = T if spans is None else max([j - i for i, j in seqs] + [0])
+    xd = dev_of(x, dtype, dev)
+    xd = wide(xd) if stride else xd
+    args = [xd, dev_of(w, wdtype, dev), dev_of(b, wdtype, dev), dev_of(st, dtype, dev)]
+    kw = dict(act=act, spans=dev_spans(spans, dev), T=longest)
+    y, so = ops.gdr_conv_forward(*args, **kw)
+    dx, dw, db, ds = ops.gdr_conv_backward(*args, dev_of(dy, dtype, dev), dev_of(dso, dtype, dev),
+                                           want_dstate=True, **kw)
+    a = act == "silu"
+    ref, mag = (L.conv_forward(x, w, b, st, a, seqs, mag=m) for m in (False, True))
+    check("y", y, ref[0], mag[0], dtype, 64)
+    np.testing.assert_array_equal(so.double().cpu().numpy(), ref[1])  # copies
+    ref, mag = (L.conv_backward(x, w, b, st, a, seqs, dy, dso, mag=m) for m in (False, True))
+    check("dx", dx, ref[0], mag[0], dtype, 64)
+    check("dweight", dw, ref[1], mag[1], wdtype, 64 + rows)
+    if bias:
+        check("dbias", db, ref[2], mag[2], wdtype, 64 + rows)
+    else:
+        assert db is None
+    check("dstate", ds, ref[3], mag[3], dtype, 64)
+    out = outside(rows, seqs)
+    assert not y.view(rows, C)[out].any() and not dx.view(rows, C)[out].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_conv_taps(cuda, dtype, K):
+    conv_case(cuda, dtype, 2, 37, 24, K, seed=K)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C", [(1, 1, 8), (3, 2, 520), (1, 3, 1), (2, 17, 77), (1, 130, 33),
+                                   (5, 1, 640), (1, 300, 2056), (2, 64, 512)])
+def test_conv_sizes(cuda, dtype, B, T, C):
+    conv_case(cuda, dtype, B, T, C, 4, seed=T)
+
+
+@pytest.mark.parametrize("dtype,C", [("bf16", 40), ("f32", 30)])
+def test_conv_packed(cuda, dtype, C):
+    conv_case(cuda, dtype, len(PACKED), 0, C, 4, spans=PACKED, rows=PACKED_ROWS)
+
+
+@pytest.mark.parametrize("kw", [dict(bias=False), dict(state=False), dict(act="none"), dict(stride=True),
+                                dict(wdtype="f32"), dict(stride=True, bias=False, state=False)])
+def test_conv_options(cuda, kw):
+    conv_case(cuda, "bf16", 2, 45, 48, 4, **kw)
+
+
+def test_conv_odd_stride(cuda):
+    """Rows that vector loads cannot take: an odd row stride of the same
+    values gives the same bits."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    g = torch.Generator(device=cuda).manual_seed(1)
+    x = torch.randn(2, 50, 32, device=cuda, generator=g).bfloat16()
+    w = torch.randn(32, 4, device=cuda, generator=g).bfloat16()
+    odd = torch.zeros(2, 50, 35, dtype=x.dtype, device=cuda)
+    odd[..., :32] = x
+    a, sa = ops.gdr_conv_forward(x, w)
+    b, sb = ops.gdr_conv_forward(odd[..., :32], w)
+    assert torch.equal(a, b) and torch.equal(sa, sb)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_conv_tokens_follow_the_prompt(cuda, dtype):
+    """Prompt, then tokens one by one with the window updated in place:
+    bitwise one call over all of it."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    g = torch.Generator(device=cuda).manual_seed(2)
+    x = torch.randn(3, 70, 40, device=cuda, generator=g).to(torch_type(dtype))
+    w, b = (torch.randn(*s, device=cuda, generator=g).to(x.dtype) for s in ((40, 4), (40,)))
+    whole, end = ops.gdr_conv_forward(x, w, b)
+    y, st = ops.gdr_conv_forward(x[:, :64].contiguous(), w, b)
+    parts = [y]
+    for t in range(64, 70):
+        y, _ = ops.gdr_conv_forward(x[:, t:t + 1].contiguous(), w, b, st, state_out=st)
+        parts.append(y)
+    assert torch.equal(torch.cat(parts, 1), whole) and torch.equal(st, end)
+
+
+# ---- scan -----------------------------------------------------------------------
+
+def scan_inputs(dtype, B, rows, C, N, G, seed, decay=1.0):
+    r = np.random.default_rng(seed)
+    n = lambda *s: r.normal(size=s)
+    rnd = lambda a: round_to(a, dtype)
+    f32 = lambda a: round_to(a, "f32")
+    step = np.exp(r.uniform(np.log(1e-3), np.log(1e-1), C))
+    return dict(u=rnd(n(rows, C)), dt=rnd(0.5 * n(rows, C)),
+                A=f32(-decay * np.arange(1, N + 1) * np.exp(0.1 * n(C, N))), Bm=rnd(n(rows, G, N)),
+                Cm=rnd(n(rows, G, N)), D=f32(1 + 0.1 * n(C)), z=rnd(n(rows, C)),
+                dt_bias=f32(step + np.log(-np.expm1(-step))), S0=f32(0.5 * n(B, C, N)),
+                dy=rnd(n(rows, C)), dS_T=f32(n(B, C, N)))
+
+
+ARGS = ("u", "dt", "A", "Bm", "Cm", "D", "z", "dt_bias", "S0")
+GRADS = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dS0")
+F32 = {"A", "D", "dt_bias", "S0", "dS_T", "S_T", "dA", "dD", "ddt_bias", "dS0"}
+
+
+def scan_case(dev, dtype, B, T, C, N, G=1, *, without=(), softplus=True, spans=None, rows=None, stride=False,
+              seed=0, decay=1.0):
+    from gated_delta_rule_recurrence_amd import ops
+    rows = B * T if rows is None else rows
+    p = scan_inputs(dtype, B, rows, C, N, G, seed, decay)
+    if not softplus:
+        p["dt"] = np.abs(p["dt"]) * 0.125
+        p["dt_bias"] = np.abs(p["dt_bias"]) * 0.0
+    for k in without:
+        p[k] = None
+    seqs = seqs_of(B, T, spans)
+    longest = T if spans is None else max([j - i for i, j in seqs] + [0])
+    d = {k: dev_of(v, "f32" if k in F32 else dtype, dev) for k, v in p.items()}
+    if stride:
+        for k in ("u", "dt", "z"):
+            d[k] = wide(d[k])
+        for k in ("Bm", "Cm"):
+            d[k] = wide(d[k].reshape(rows, G * N))
+            d[k] = d[k].unflatten(-1, (G, N))
+    y, S_T, saved = ops.gdr_scan_forward(*[d[k] for k in ARGS], softplus=softplus,
+                                         spans=dev_spans(spans, dev), T=longest)
+    y2, S2, none = ops.gdr_scan_forward(*[d[k] for k in ARGS], softplus=softplus,
+                                        spans=dev_spans(spans, dev), T=longest, save=False)
+    assert none is None and (y == y2).all() and (S_T == S2).all()
+    grads = ops.gdr_scan_backward(*[d[k] for k in ARGS[:8]], saved, d["dy"], d["dS_T"])
+    args = [p[k] for k in ARGS] + [softplus, seqs]
+    ref, mag = (L.scan_forward(*args, mag=m) for m in (False, True))
+    n = 128 + 4 * longest
+    check("y", y, ref[0], mag[0], dtype, n)
+    check("S_T", S_T, ref[1], mag[1], "f32", n)
+    ref, mag = (L.scan_backward(*args, p["dy"], p["dS_T"], mag=m) for m in (False, True))
+    given = dict(zip(GRADS, ARGS))
+    for k, g in zip(GRADS, grads):
+        if k != "dS0" and given[k] in without:
+            assert g is None
+            continue
+        check(k, g, ref[k], mag[k], "f32" if k in F32 else dtype,
+              2 * n + (rows if k in ("dA", "dD", "ddt_bias") else 128))
+    out = outside(rows, seqs)
+    for k, g in zip(("y",) + GRADS, (y,) + grads):
+        if g is not None and k in ("y", "du", "ddt", "dB", "dC", "dz"):
+            assert not g.reshape(rows, -1)[out].any(), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 3, 4, 7, 8, 12, 16, 24, 32, 45, 64])
+def test_scan_states(cuda, dtype, N):
+    scan_case(cuda, dtype, 2, 37, 20, N, seed=N)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,G", [(1, 1, 8, 1), (3, 2, 65, 1), (1, 15, 64, 2), (2, 16, 66, 3), (1, 17, 130, 1),
+                                     (4, 1, 200, 4), (1, 64, 1, 1), (1, 65, 96, 1), (2, 300, 70, 2)])
+def test_scan_sizes(cuda, dtype, B, T, C, G):
+    scan_case(cuda, dtype, B, T, C, 16, G, seed=T)
+
+
+@pytest.mark.parametrize("dtype,N", [("bf16", 16), ("f32", 10), ("f32", 40)])
+def test_scan_packed(cuda, dtype, N):
+    scan_case(cuda, dtype, len(PACKED), 0, 40, N, 2, spans=PACKED, rows=PACKED_ROWS)
+
+
+@pytest.mark.parametrize("kw", [dict(without=("D",)), dict(without=("z",)), dict(without=("dt_bias",)),
+                                dict(without=("S0", "dS_T")), dict(softplus=False), dict(stride=True),
+                                dict(without=("D", "z", "dt_bias", "S0", "dS_T"), softplus=False),
+                                dict(decay=40.0), dict(decay=1e-3)])
+def test_scan_options(cuda, kw):
+    scan_case(cuda, "f32", 2, 100, 48, 16, 2, **kw)
+    scan_case(cuda, "bf16", 1, 33, 48, 16, 1, **kw)
+
+
+def test_scan_tokens_follow_the_prompt(cuda):
+    """Prompt, then tokens one by one with the state updated in place, against
+    one call over all of it: the recurrence is the same, only the prompt's
+    split into chunks rounds differently."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    B, T, C, N = 2, 90, 72, 16
+    p = scan_inputs("f32", B, B * T, C, N, 1, 4)
+    d = {k: dev_of(v, "f32", cuda) for k, v in p.items()}
+    for k in ("u", "dt", "z", "Bm", "Cm"):
+        d[k] = d[k].reshape(B, T, *d[k].shape[1:])
+    call = lambda a, b, S0, **kw: ops.gdr_scan_forward(
+        *[d[k][:, a:b].contiguous() if k in ("u", "dt", "z", "Bm", "Cm") else d[k] for k in ARGS[:8]], S0,
+        save=False, **kw)
+    whole, end, _ = call(0, T, d["S0"])
+    y, S, _ = call(0, 80, d["S0"])
+    parts = [y]
+    for t in range(80, T):
+        y, _, _ = call(t, t + 1, S, S_T=S)
+        parts.append(y)
+    mag = L.scan_forward(*[p[k] for k in ARGS], True, seqs_of(B, T, None), mag=True)
+    check("y", torch.cat(parts, 1), whole.double().cpu().numpy(), mag[0].reshape(B, T, C), "f32", 2 * (128 + 4 * T))
+    check("S_T", S, end.double().cpu().numpy(), mag[1], "f32", 2 * (128 + 4 * T))
+
+
+# ---- norm -----------------------------------------------------------------------
+
+def norm_case(dev, dtype, rows, C, G, *, wdtype=None, center=False, act="silu", gate=True, weight=True, bias=True,
+              shared=False, stride=False, seed=0, shift=0.0):
+    from gated_delta_rule_recurrence_amd import ops
+    r = np.random.default_rng(seed)
+    wdtype = wdtype or dtype
+    n = lambda *s: round_to(r.normal(size=s), dtype)
+    x, dy, z = round_to(r.normal(size=(rows, C)) + shift, dtype), n(rows, C), n(rows, C) if gate else None
+    width = C // G if shared else C
+    w = round_to(r.normal(size=width), wdtype) if weight else None
+    b = round_to(r.normal(size=width), wdtype) if bias else None
+    eps = 1e-5
+    xd, zd = dev_of(x, dtype, dev), dev_of(z, dtype, dev)
+    if stride:
+        xd, zd = wide(xd), wide(zd, 16)
+    args = [xd, dev_of(w, wdtype, dev), dev_of(b, wdtype, dev), zd]
+    kw = dict(groups=G, center=center, act=act)
+    y, stats = ops.gdr_norm_forward(*args, eps=eps, **kw)
+    dx, dw, db, dz = ops.gdr_norm_backward(*args, stats, dev_of(dy, dtype, dev), **kw)
+    eps = float(np.float32(eps))
+    a = act == "silu"
+    ref, mag = (L.norm_forward(x, w, b, z, G, eps, center, a, mag=m) for m in (False, True))
+    check("y", y, ref, mag, dtype, 128)
+    ref, mag = (L.norm_backward(x, w, b, z, G, eps, center, a, dy, mag=m) for m in (False, True))
+    fold = (lambda g: g.reshape(G, -1).sum(0)) if shared else (lambda g: g)
+    check("dx", dx, ref[0], mag[0], dtype, 128)
+    for name, g, have, i in (("dweight", dw, weight, 1), ("dbias", db, bias, 2)):
+        if have:
+            check(name, g, fold(ref[i]), fold(mag[i]), wdtype, 128 + rows * (G if shared else 1))
+        else:
+            assert g is None
+    if gate:
+        check("dz", dz, ref[3], mag[3], dtype, 128)
+    else:
+        assert dz is None
+
+
+# every lane count and vector count of the kernels, whole and ragged
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 5, 8, 24, 64, 72, 128, 100, 200, 256, 333, 512, 520, 700, 1024, 1500, 2048,
+                               2052, 4096, 4500, 8192])
+def test_norm_widths(cuda, dtype, D):
+    norm_case(cuda, dtype, 3, 2 * D, 2, center=D % 2 == 0, seed=D)
+
+
+@pytest.mark.parametrize("rows,G", [(1, 1), (2, 3), (7, 5), (100, 12), (33, 64), (517, 6)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_norm_rows(cuda, rows, G, shared):
+    norm_case(cuda, "f32", rows, G * 40, G, shared=shared, seed=rows)
+    norm_case(cuda, "bf16", rows, G * 128, G, shared=shared, center=True, seed=rows)
+
+
+@pytest.mark.parametrize("kw", [dict(gate=False), dict(act="none"), dict(gate=False, act="none"), dict(weight=False),
+                                dict(bias=False), dict(weight=False, bias=False), dict(center=True, gate=False),
+                                dict(center=True, shift=3.0), dict(stride=True), dict(wdtype="f32"),
+                                dict(stride=True, shared=True, center=True)])
+def test_norm_options(cuda, kw):
+    norm_case(cuda, "bf16", 19, 192, 3, **kw)
+    norm_case(cuda, "f32", 19, 192, 3, **{**kw, "wdtype": "bf16" if "wdtype" in kw else None})
+
+
+# ---- the layer: together, through autograd ---------------------------------------
+
+def test_layer_together(cuda):
+    """q, k, v from the convolution, the recurrence, the gated norm, and the
+    scan on the result: one training step through autograd against the
+    composed oracles, and the same tokens served one by one."""
+    import torch
+
+    import oracle.gdr_oracle as O
+    from gated_delta_rule_recurrence_amd import ops
+    B, T, Hk, Hv, Dk, Dv = 2, 40, 2, 4, 16, 24
+    nq, nv = Hk * Dk, Hv * Dv
+    C = 2 * nq + nv
+    r = np.random.default_rng(11)
+    f = lambda a: round_to(a, "f32")
+    x, w, b = f(r.normal(size=(B, T, C)) * 0.5), f(r.normal(size=(C, 4)) * 0.5), f(r.normal(size=C) * 0.1)
+    g, beta = f(r.uniform(0.7, 1.0, (B, T, Hv))), f(r.uniform(0.2, 0.9, (B, T, Hv)))
+    z, nw = f(r.normal(size=(B, T, nv))), f(1 + 0.1 * r.normal(size=Dv))
+    s = scan_inputs("f32", B, B * T, nv, 8, 2, 12)
+    dy = f(r.normal(size=(B, T, nv)))
+    leaf = lambda a: dev_of(a, "f32", cuda).requires_grad_()
+    X, W, Bi, G_, BE, Z, NW = map(leaf, (x, w, b, g, beta, z, nw))
+    SC = {k: leaf(s[k]) for k in ("dt", "A", "Bm", "Cm", "D", "z", "dt_bias")}
+    rows = lambda t, i=0, j=T: t.reshape(B, T, *t.shape[1:])[:, i:j].contiguous()
+
+    h, st = ops.causal_conv(X, W, Bi)
+    q, k, v = (h[..., :nq].reshape(B, T, Hk, Dk), h[..., nq:2 * nq].reshape(B, T, Hk, Dk),
+               h[..., 2 * nq:].reshape(B, T, Hv, Dv))
+    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    y, S = ops.gated_delta_rule(q, k, v, G_, BE, chunk=16)
+    o = ops.group_norm(y.reshape(B, T, nv), NW, None, Z, groups=Hv)
+    out, S2 = ops.selective_scan(o, rows(SC["dt"]), SC["A"], rows(SC["Bm"]), rows(SC["Cm"]), SC["D"],
+                                 rows(SC["z"]), SC["dt_bias"])
+    out.backward(dev_of(dy, "f32", cuda))
+
+    # the oracles, composed
+    seqs = seqs_of(B, T, None)
+    flat = lambda a: a.reshape(B * T, -1)
+    hr, _ = L.conv_forward(flat(x), w, b, None, True, seqs)
+    qr, kr, vr = (hr[:, i:j].reshape(B, T, H, D) for i, j, H, D in
+                  ((0, nq, Hk, Dk), (nq, 2 * nq, Hk, Dk), (2 * nq, C, Hv, Dv)))
+    yr, _ = O.forward(qr, kr, vr, g, beta, None)
+    orr = L.norm_forward(flat(yr), nw, None, flat(z), Hv, 1e-6, False, True)
+    sargs = [s[k] for k in ("dt", "A", "Bm", "Cm", "D", "z", "dt_bias")]
+    outr, _ = L.scan_forward(orr, *sargs, None, True, seqs)
+    gs = L.scan_backward(orr, *sargs, None, True, seqs, flat(dy))
+    dyr, dwr, _, dzr = L.norm_backward(flat(yr), nw, None, flat(z), Hv, 1e-6, False, True, gs["du"])
+    dq, dk, dv, dg, db, _ = O.backward(qr, kr, vr, g, beta, dyr.reshape(B, T, Hv, Dv), None, None)
+    dh = np.concatenate([flat(dq), flat(dk), flat(dv)], 1)
+    dxr, dcw, dcb, _ = L.conv_backward(flat(x), w, b, None, True, seqs, dh)
+    # the recurrence's bar for fp32 inputs (relative L2 1e-5), which the
+    # stages before and behind it multiply by their condition, at most 10 each
+    for name, got, ref in (("out", out, outr), ("dx", X.grad, dxr), ("dw", W.grad, dcw), ("db", Bi.grad, dcb),
+                           ("dg", G_.grad, dg), ("dbeta", BE.grad, db), ("dz", Z.grad, dzr),
+                           ("dnw", NW.grad, dwr.reshape(Hv, Dv).sum(0)), ("dA", SC["A"].grad, gs["dA"]),
+                           ("ddt", SC["dt"].grad, gs["ddt"]), ("dB", SC["Bm"].grad, gs["dB"])):
+        err = O.rel_l2(got.detach().double().cpu().numpy().reshape(ref.shape), ref)
+        assert err <= 1e-4, (name, err)
+
+    # served: a prompt of 30 tokens, then one by one
+    with torch.no_grad():
+        window = state = scan = None
+        served = []
+        for i, j in [(0, 30)] + [(t, t + 1) for t in range(30, T)]:
+            h, window = ops.gdr_conv_forward(X[:, i:j].contiguous(), W, Bi, window)
+            n = j - i
+            q, k, v = (h[..., :nq].reshape(B, n, Hk, Dk), h[..., nq:2 * nq].reshape(B, n, Hk, Dk),
+                       h[..., 2 * nq:].reshape(B, n, Hv, Dv))
+            y, state, _ = ops.gdr_forward(q.contiguous(), k.contiguous(), v.contiguous(), G_[:, i:j].contiguous(),
+                                          BE[:, i:j].contiguous(), state, chunk=16, save=False)
+            o, _ = ops.gdr_norm_forward(y.reshape(B, n, nv), NW, None, Z[:, i:j].contiguous(), groups=Hv,
+                                        save=False)
+            p, scan, _ = ops.gdr_scan_forward(o, rows(SC["dt"], i, j), SC["A"], rows(SC["Bm"], i, j),
+                                              rows(SC["Cm"], i, j), SC["D"], rows(SC["z"], i, j), SC["dt_bias"],
+                                              scan, save=False)
+            served.append(p)
+    err = O.rel_l2(torch.cat(served, 1).double().cpu().numpy().reshape(outr.shape), outr)
+    assert err <= 1e-4, err
