@@ -539,7 +539,7 @@ const char* gdr_strerror(int status) {
       return "the launch-event count must be in [0, GDR_MAX_LAUNCH_EVENTS]";
     case GDR_ERR_BAD_DIM:
       return "a dimension of a convolution, scan or norm is outside its range";
-    case GDR_ERR_BAD_STRIDE: return "a row stride is below the row's width or above 2^31 - 1";
+    case GDR_ERR_BAD_STRIDE: return "a row stride is below the row's width or above its limit";
     case GDR_ERR_BAD_ACT: return "act must be GDR_ACT_NONE or GDR_ACT_SILU, softplus 0 or 1";
     case GDR_ERR_BAD_EPS: return "eps must be finite and >= 0";
   }

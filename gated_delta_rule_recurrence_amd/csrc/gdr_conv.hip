@@ -16,7 +16,7 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows loaded ahead of their use
+constexpr int kUnroll = 4;  // rows of one turn; the next turn's are loaded ahead
 
 // Input row t of the sequence: x for t >= 0 (t < len), else the window, else 0.
 template <typename T, int V>
@@ -27,6 +27,18 @@ __device__ __forceinline__ Pack<T, V> input_row(const ConvArgs& a, const Span& s
   if (a.state == nullptr) return zero_pack<T, V>();
   return load_pack<T, V>(static_cast<const T*>(a.state) +
                          ((int64_t)b * (a.K - 1) + (a.K - 1 + t)) * a.C + c);
+}
+
+template <int K, int V>
+__device__ __forceinline__ void load_weights(const ConvArgs& a, int c, float (&w)[V * K],
+                                             float (&bias)[V]) {
+  ld_weights<V * K, (V > 1)>(a.w, (int64_t)c * K, a.w_bf16, w);
+  if (a.bias != nullptr) {
+    ld_weights<V, (V > 1)>(a.bias, c, a.w_bf16, bias);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = 0.f;
+  }
 }
 
 template <typename T, int K, int V>
@@ -40,13 +52,8 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
   if (t0l > 0 && t0l >= sp.len) return;
   const int t0 = (int)t0l, t1 = sp.len - t0 < steps ? sp.len : t0 + steps;
 
-  float w[K][V], bias[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = a.bias != nullptr ? ld_weight(a.bias, c + v, a.w_bf16) : 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[j][v] = ld_weight(a.w, (int64_t)(c + v) * K + j, a.w_bf16);
-  }
+  float w[V * K], bias[V];  // weight[c + v][j] at v K + j
+  load_weights<K, V>(a, c, w, bias);
   Pack<T, V> hist[K > 1 ? K - 1 : 1];
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) hist[i] = input_row<T, V>(a, sp, b, t0 - (K - 1) + i, c);
@@ -65,16 +72,24 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
 
   const T* xp = static_cast<const T*>(a.x) + (sp.first + t0) * a.x_stride + c;
   T* yp = static_cast<T*>(a.y) + (sp.first + t0) * a.C + c;
+  // rows t .. t + kUnroll - 1, clamped to the tile's last one
+  auto fetch = [&](int t, Pack<T, V>(&in)[kUnroll]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < kUnroll; ++r) {
+      const int at = t + r < t1 ? t + r : t1 - 1;
+      in[r] = load_pack<T, V>(xp + (int64_t)(at - t0) * a.x_stride);
+    }
+  };
   float win[K][V];  // win[K - 1]: the current input
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) unpack(hist[i], win[i]);
+  Pack<T, V> next[kUnroll];
+  if (t0 < t1) fetch(t0, next);
   for (int t = t0; t < t1; t += kUnroll) {
     Pack<T, V> in[kUnroll];
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r) {
-      const int64_t off = t + r < t1 ? (int64_t)r * a.x_stride : 0;  // clamped to row t
-      in[r] = load_pack<T, V>(xp + off);
-    }
+    for (int r = 0; r < kUnroll; ++r) in[r] = next[r];
+    if (t + kUnroll < t1) fetch(t + kUnroll, next);
 #pragma unroll
     for (int r = 0; r < kUnroll; ++r) {
       unpack(in[r], win[K - 1]);
@@ -83,14 +98,13 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
       for (int v = 0; v < V; ++v) {
         s[v] = bias[v];
 #pragma unroll
-        for (int j = 0; j < K; ++j) s[v] = fmaf(w[j][v], win[j][v], s[v]);
+        for (int j = 0; j < K; ++j) s[v] = fmaf(w[v * K + j], win[j][v], s[v]);
         if (a.act) s[v] = silu(s[v]);
 #pragma unroll
         for (int j = 0; j + 1 < K; ++j) win[j][v] = win[j + 1][v];
       }
       if (t + r < t1) store_pack(yp + (int64_t)r * a.C, s);
     }
-    xp += (int64_t)kUnroll * a.x_stride;
     yp += (int64_t)kUnroll * a.C;
   }
 }
@@ -121,13 +135,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
   }
   if (any) {
     const int t0 = (int)t0l, t1 = sp.len - t0 < steps ? sp.len : t0 + steps;
-    float w[K][V], bias[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      bias[v] = a.bias != nullptr ? ld_weight(a.bias, cc + v, a.w_bf16) : 0.f;
-#pragma unroll
-      for (int j = 0; j < K; ++j) w[j][v] = ld_weight(a.w, (int64_t)(cc + v) * K + j, a.w_bf16);
-    }
+    float w[V * K], bias[V];
+    load_weights<K, V>(a, cc, w, bias);
     float win[K][V], ds[K][V];  // the inputs and ds of the last K steps
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) unpack(input_row<T, V>(a, sp, b, t0 - (K - 1) + i, cc), win[i]);
@@ -141,19 +150,24 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
     // step t forms ds_t and completes dx of step t - (K - 1); the last K - 1
     // steps only complete.  Rows from sp.len on count as ds = 0.
     const int tend = t1 + K - 1;
+    Pack<T, V> nx[kUnroll], nd[kUnroll];
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        const int tt = t + r < sp.len ? t + r : sp.len - 1;  // -1: an empty sequence
+        nx[r] = tt < 0 ? zero_pack<T, V>() : load_pack<T, V>(xb + (int64_t)tt * a.x_stride);
+        nd[r] = tt < 0 ? zero_pack<T, V>() : load_pack<T, V>(dyb + (int64_t)tt * a.C);
+      }
+    };
+    fetch(t0);
     for (int t = t0; t < tend; t += kUnroll) {
       Pack<T, V> in[kUnroll], dyv[kUnroll];
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
-        const int tt = t + r < sp.len ? t + r : sp.len - 1;
-        if (tt >= 0) {
-          in[r] = load_pack<T, V>(xb + (int64_t)tt * a.x_stride);
-          dyv[r] = load_pack<T, V>(dyb + (int64_t)tt * a.C);
-        } else {
-          in[r] = zero_pack<T, V>();
-          dyv[r] = zero_pack<T, V>();
-        }
+        in[r] = nx[r];
+        dyv[r] = nd[r];
       }
+      if (t + kUnroll < tend) fetch(t + kUnroll);
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
         const int tt = t + r;
@@ -168,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
           if (a.act) {
             float s = bias[v];
 #pragma unroll
-            for (int j = 0; j < K; ++j) s = fmaf(w[j][v], win[j][v], s);
+            for (int j = 0; j < K; ++j) s = fmaf(w[v * K + j], win[j][v], s);
             d *= dsilu(s, sigmoid(s));
           }
           if (tt >= sp.len) d = 0.f;
@@ -182,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
           }
           out[v] = 0.f;
 #pragma unroll
-          for (int j = 0; j < K; ++j) out[v] = fmaf(w[j][v], ds[K - 1 - j][v], out[v]);
+          for (int j = 0; j < K; ++j) out[v] = fmaf(w[v * K + j], ds[K - 1 - j][v], out[v]);
 #pragma unroll
           for (int j = 0; j + 1 < K; ++j) win[j][v] = win[j + 1][v];
         }
@@ -249,12 +263,13 @@ bool vectors(const ConvArgs& a) {
 template <typename T, int K, int V>
 hipError_t fwd(const ConvArgs& a, hipStream_t s) {
   const int cblocks = (a.C + kThreads * V - 1) / (kThreads * V);
-  // tiles short enough to give every compute unit eight waves, long enough
-  // that the halo stays a small part of the loads
+  // 16 to 32 steps a tile, by what gives 256 compute units eight waves each:
+  // shorter tiles read more of the halo, longer ones leave fewer loads in
+  // flight (7 packed prompts of 6000 rows, 14336 channels: 72 us at 16 steps,
+  // 78 at 48; one sequence of 2048: 27 us at 28 steps, 30 at 16, 32 at 48)
   const int64_t waves = (int64_t)cblocks * (kThreads / 64) * a.B;
-  const int64_t want = (int64_t)device_cu_count() * 8;
-  int64_t steps = waves * a.T / want;
-  steps = steps < 16 ? 16 : (steps > 64 ? 64 : steps);
+  int64_t steps = waves * a.T / 2048;
+  steps = steps < 16 ? 16 : (steps > 32 ? 32 : steps);
   int64_t tiles = (a.T + steps - 1) / steps;
   while (tiles * cblocks > INT32_MAX) {
     steps *= 2;
@@ -271,8 +286,8 @@ hipError_t fwd(const ConvArgs& a, hipStream_t s) {
 template <typename T, int K, int V>
 hipError_t bwd(const ConvArgs& a, hipStream_t s) {
   const int cblocks = (a.C + 64 * V - 1) / (64 * V);
-  const int steps = conv_bwd_steps(a.B, a.T, a.C, sizeof(T) == 2);
-  const int64_t parts = conv_bwd_parts(a.B, a.T, a.C, sizeof(T) == 2);
+  const int steps = conv_bwd_steps(a.B, a.T, a.C);
+  const int64_t parts = conv_bwd_parts(a.B, a.T, a.C);
   hipLaunchKernelGGL((conv_bwd_kernel<T, K, V>), dim3((unsigned)(parts / a.B * cblocks), a.B),
                      dim3(kThreads), 0, s, a, cblocks, steps);
   hipError_t e = hipGetLastError();
@@ -285,7 +300,10 @@ hipError_t bwd(const ConvArgs& a, hipStream_t s) {
 template <typename T, bool BWD, int K>
 hipError_t launch_v(const ConvArgs& a, hipStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  if (vectors<T>(a)) return BWD ? bwd<T, K, V>(a, s) : fwd<T, K, V>(a, s);
+  // the backward holds 4 K + 2 values per channel: four channels a thread
+  // in either type (bf16: 8 bytes a load, 47.8 us against 66.5 with 16 bytes,
+  // 236 registers and two waves a SIMD)
+  if (vectors<T>(a)) return BWD ? bwd<T, K, 4>(a, s) : fwd<T, K, V>(a, s);
   return BWD ? bwd<T, K, 1>(a, s) : fwd<T, K, 1>(a, s);
 }
 
@@ -306,23 +324,22 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tiles that give the device about eight waves per compute unit, at least 16
-// steps (the halo) and at most 256.  The count assumes 256 compute units and
-// vector loads: it sizes a workspace, which must not depend on the device
-// that is current or on strides.
-int conv_bwd_steps(int64_t B, int64_t T, int64_t C, bool bf16) {
-  const int64_t V = bf16 ? 8 : 4;
-  const int64_t waves = (C + 64 * V - 1) / (64 * V) * B;
-  int64_t steps = waves * T / 2048;
-  steps = steps < 16 ? 16 : (steps > 256 ? 256 : steps);
+// 16 steps a wave, 32 where that still leaves 4096 waves (the halo and the
+// partial sums halve): 2048 rows of 14336 bf16 channels take 44.6 us at 16,
+// 45.8 at 32, 50.7 at 48.  Sized for 256 compute units and vector loads: it
+// sizes a workspace too, which must not depend on the current device or on
+// strides.
+int conv_bwd_steps(int64_t B, int64_t T, int64_t C) {
+  const int64_t waves = (C + 255) / 256 * B;
+  int64_t steps = waves * T / 32 >= 4096 ? 32 : 16;
   // the grid's x dimension holds (tiles / 4) x (channel blocks, at most one
   // per 64 channels)
   while ((T + 4 * steps - 1) / (4 * steps) * ((C + 63) / 64) > INT32_MAX) steps *= 2;
   return (int)steps;
 }
 
-int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C, bool bf16) {
-  const int64_t steps = 4 * (int64_t)conv_bwd_steps(B, T, C, bf16);
+int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C) {
+  const int64_t steps = 4 * (int64_t)conv_bwd_steps(B, T, C);
   const int64_t groups = (T + steps - 1) / steps;
   return B * (groups < 1 ? 1 : groups);
 }

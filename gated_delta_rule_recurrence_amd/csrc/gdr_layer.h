@@ -32,8 +32,8 @@ struct ConvArgs {
   float* part;        // [parts][K+1][C]
 };
 // Steps a wave takes in the backward, and the partial sums that leaves.
-int conv_bwd_steps(int64_t B, int64_t T, int64_t C, bool bf16);
-int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C, bool bf16);
+int conv_bwd_steps(int64_t B, int64_t T, int64_t C);
+int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C);
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs& a, bool bf16, hipStream_t s);
 
@@ -85,7 +85,7 @@ struct ScanArgs {
   const float* S0;      // [B][C][N] or null
   void* y;
   float* S_T;           // or null
-  float* ckpt;          // tile states (scan_tile_slots) or null
+  float* ckpt;          // [slots][C][Np]: the state every few steps, or null
   // chunked form (chunks > 1): the state (or adjoint) before every chunk and
   // the summed steps of every chunk
   int chunk;            // steps, a multiple of the tile
@@ -108,12 +108,13 @@ struct ScanArgs {
   float* pD;            // [B * chunks][2][C] partial dD, ddt_bias
   float* pB;            // [2][channel tiles][rows][G][N] partial dB, dC
 };
-// Padded states per channel, steps of one tile and channels of one block.
+// Padded states per channel, steps between saved states, channels of one
+// workgroup.
 int scan_padded(int64_t N);
-int scan_tile(int64_t N);
+int scan_save_steps(int64_t N);
 int scan_channels();
-// Steps of one chunk (0: the whole sequence runs as one).
-int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, bool bwd);
+// Steps of one chunk, a multiple of 16; stride: the widest row in elements.
+int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int64_t stride);
 hipError_t launch_scan_fwd(const ScanArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs& a, bool bf16, hipStream_t s);
 
@@ -162,7 +163,7 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.f) + (d == 0.f ? t : l);
 }
 
-// Loads V consecutive elements as floats; V = 1, or a 16-byte vector.
+// V consecutive elements: one, or a vector of 8 or 16 bytes.
 template <typename T, int V>
 struct Pack {
   T v[V];
@@ -174,6 +175,10 @@ struct Pack<float, 4> {
 template <>
 struct Pack<bf16, 8> {
   uint4 v;
+};
+template <>
+struct Pack<bf16, 4> {
+  uint2 v;
 };
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
@@ -209,6 +214,12 @@ __device__ __forceinline__ void unpack(const Pack<bf16, 8>& p, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
+__device__ __forceinline__ void unpack(const Pack<bf16, 4>& p, float (&f)[4]) {
+  f[0] = __uint_as_float(p.v.x << 16);
+  f[1] = __uint_as_float(p.v.x & 0xffff0000u);
+  f[2] = __uint_as_float(p.v.y << 16);
+  f[3] = __uint_as_float(p.v.y & 0xffff0000u);
+}
 // Stores V floats, each rounded to nearest even.
 __device__ __forceinline__ void store_pack(float* p, const float (&f)[1]) { *p = f[0]; }
 __device__ __forceinline__ void store_pack(bf16* p, const float (&f)[1]) {
@@ -222,10 +233,51 @@ __device__ __forceinline__ void store_pack(bf16* p, const float (&f)[8]) {
                                        cvt_pk_bf16(f[4], f[5]), cvt_pk_bf16(f[6], f[7])};
 }
 
+__device__ __forceinline__ void store_pack(bf16* p, const float (&f)[4]) {
+  *reinterpret_cast<uint2*>(p) = uint2{cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3])};
+}
+
+// One row element, rounded to nearest even.
+__device__ __forceinline__ void st_row(float* p, float x) { *p = x; }
+__device__ __forceinline__ void st_row(bf16* p, float x) {
+  p->bits = static_cast<uint16_t>(cvt_pk_bf16(x, x));
+}
+
 // A weight element of either type (loaded once per thread, so the branch is
 // of no account).
 __device__ __forceinline__ float ld_weight(const void* p, int64_t i, int is_bf16) {
   return is_bf16 ? to_f32(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+// N consecutive weights from element i on; N elements of the row type's
+// vectors start on a 16-byte boundary when VEC (i a multiple of a vector).
+template <int N, bool VEC>
+__device__ __forceinline__ void ld_weights(const void* p, int64_t i, int is_bf16, float (&w)[N]) {
+  if constexpr (VEC && N % 8 == 0) {
+    if (is_bf16) {
+#pragma unroll
+      for (int k = 0; k < N / 8; ++k) {
+        float f[8];
+        unpack(load_pack<bf16, 8>(static_cast<const bf16*>(p) + i + 8 * k), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[8 * k + e] = f[e];
+      }
+      return;
+    }
+  }
+  if constexpr (VEC && N % 4 == 0) {
+    if (!is_bf16) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        float f[4];
+        unpack(load_pack<float, 4>(static_cast<const float*>(p) + i + 4 * k), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[4 * k + e] = f[e];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) w[k] = ld_weight(p, i + k, is_bf16);
 }
 __device__ __forceinline__ void st_weight(void* p, int64_t i, float x, int is_bf16) {
   if (is_bf16)

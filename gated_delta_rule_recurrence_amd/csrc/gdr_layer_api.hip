@@ -13,6 +13,7 @@ namespace {
 constexpr int64_t kMaxChannels = INT64_C(1) << 20;
 constexpr int64_t kMaxRows = INT32_MAX / 2;  // rows and steps; twice it still is an int
 constexpr int64_t kMaxStride = INT32_MAX;
+constexpr int64_t kMaxScanStride = INT64_C(1) << 25;  // 16 rows of 4 bytes in 32 bits
 constexpr int64_t kMaxBatch = 65535;         // sequences index grid y
 constexpr int64_t kMaxIndex = INT64_C(1) << 61;
 
@@ -41,9 +42,9 @@ int alignment_ok(const void* const (&ptrs)[N]) {
 }
 
 bool dtype_ok(int32_t d) { return d == GDR_F32 || d == GDR_BF16; }
-bool stride_ok(int64_t* s, int64_t width) {
+bool stride_ok(int64_t* s, int64_t width, int64_t most = kMaxStride) {
   if (*s == 0) *s = width;
-  return *s >= width && *s <= kMaxStride;
+  return *s >= width && *s <= most;
 }
 
 // B, T, rows of a shape with sequences
@@ -76,13 +77,14 @@ int check(const gdr_scan_shape* in, gdr_scan_shape* s) {
     return GDR_ERR_BAD_DIM;
   if (!dtype_ok(s->dtype)) return GDR_ERR_BAD_DTYPE;
   if (s->softplus != 0 && s->softplus != 1) return GDR_ERR_BAD_ACT;
-  if (!stride_ok(&s->u_stride, s->C) || !stride_ok(&s->dt_stride, s->C) ||
-      !stride_ok(&s->z_stride, s->C) || !stride_ok(&s->b_stride, s->G * s->N) ||
-      !stride_ok(&s->c_stride, s->G * s->N))
+  const int64_t most = kMaxScanStride;
+  if (!stride_ok(&s->u_stride, s->C, most) || !stride_ok(&s->dt_stride, s->C, most) ||
+      !stride_ok(&s->z_stride, s->C, most) || !stride_ok(&s->b_stride, s->G * s->N, most) ||
+      !stride_ok(&s->c_stride, s->G * s->N, most))
     return GDR_ERR_BAD_STRIDE;
   // the grids: channel tiles x chunks, and T x G x N threads
   const int64_t tiles = s->G * ((s->C / s->G + 63) / 64);
-  if (tiles * (s->T / 32 + 1) > INT32_MAX || s->T * (s->G * s->N) / 256 + 1 > INT32_MAX)
+  if (tiles * (s->T / 16 + 1) > INT32_MAX || s->T * (s->G * s->N) / 256 + 1 > INT32_MAX)
     return GDR_ERR_OVERFLOW;
   return GDR_OK;
 }
@@ -112,10 +114,12 @@ struct ScanSizes {
 };
 
 int scan_sizes(const gdr_scan_shape& s, bool bwd, ScanSizes* z) {
-  const int64_t np = gdr::scan_padded(s.N), tile = gdr::scan_tile(s.N);
-  z->chunk = gdr::scan_chunk(s.B, s.T, s.C, s.G, s.N, bwd);
-  z->chunks = z->chunk > 0 ? (s.T + z->chunk - 1) / z->chunk : 1;
-  if (z->chunk == 0) z->chunk = s.T > 16 ? (s.T + 15) / 16 * 16 : 16;
+  const int64_t np = gdr::scan_padded(s.N), tile = gdr::scan_save_steps(s.N);
+  int64_t stride = s.C > s.G * s.N ? s.C : s.G * s.N;
+  for (int64_t w : {s.u_stride, s.dt_stride, s.z_stride, s.b_stride, s.c_stride})
+    if (w > stride) stride = w;
+  z->chunk = gdr::scan_chunk(s.B, s.T, s.C, s.G, s.N, stride);
+  z->chunks = s.T > 0 ? (s.T + z->chunk - 1) / z->chunk : 1;
   int64_t state, x;
   if (!product_ok(s.C, np * 4, &state) || !product_ok(state, s.rows / tile + s.B + 1, &z->ckpt))
     return GDR_ERR_OVERFLOW;
@@ -224,7 +228,7 @@ int conv_forward(const gdr_conv_shape* shape, const void* x, const void* w, cons
 int conv_backward_sizes(const gdr_conv_shape* shape, gdr_conv_shape* s, int64_t* bytes) {
   const int st = check(shape, s);
   if (st != GDR_OK) return st;
-  const int64_t parts = gdr::conv_bwd_parts(s->B, s->T, s->C, s->dtype == GDR_BF16);
+  const int64_t parts = gdr::conv_bwd_parts(s->B, s->T, s->C);
   if (!product_ok(parts, (s->K + 1) * s->C * 4, bytes)) return GDR_ERR_OVERFLOW;
   return GDR_OK;
 }

@@ -284,28 +284,38 @@ struct NormSumStore {
   }
 };
 
-// Sums of part[parts][2][reps][W] to [2][W]: thread = column, 16 row lanes
-// over parts * reps.
-__global__ __launch_bounds__(256) void norm_sums(const float* __restrict__ part, int64_t parts,
-                                                 int64_t reps, NormSumStore store) {
-  __shared__ float red[16][kSumCols + 1];
+// Sums of part[parts][2][reps][W] to [2][W]: 16 columns and 64 row lanes over
+// parts x reps, the row lanes' sums then added in order.
+constexpr int kSumRows = 64;
+__global__ __launch_bounds__(kSumCols* kSumRows) void norm_sums(const float* __restrict__ part,
+                                                                int parts, int reps,
+                                                                NormSumStore store) {
+  __shared__ float red[kSumRows][kSumCols + 1];
   const int tc = threadIdx.x % kSumCols, tr = threadIdx.x / kSumCols;
   const int64_t c = (int64_t)blockIdx.x * kSumCols + tc;
-  float s = 0.f;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < 2 * store.W) {
-    const int64_t half = c / store.W, d = c % store.W;
-    const float* const p = part + half * reps * store.W + d;
-    for (int64_t r = tr; r < parts * reps; r += 16)
-      s += p[(r / reps * 2 * reps + r % reps) * store.W];
-  }
-  red[tr][tc] = s;
-  __syncthreads();
-  if (tr == 0 && c < 2 * store.W) {
-    float t = red[0][tc];
+    const int64_t half = c / store.W, d = c % store.W, block = 2 * reps * store.W;
+    for (int k = 0; k < reps; ++k) {
+      const float* const p = part + (half * reps + k) * store.W + d;
+      int r = tr;
+      for (; r + 3 * kSumRows < parts; r += 4 * kSumRows)
 #pragma unroll
-    for (int k = 1; k < 16; ++k) t += red[k][tc];
-    store(c, t);
+        for (int u = 0; u < 4; ++u) s[u] += p[(r + u * kSumRows) * block];
+      for (; r < parts; r += kSumRows) s[0] += p[r * block];
+    }
   }
+  red[tr][tc] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (tr < 4) {  // four partial chains, then their sum
+    float t = red[tr][tc];
+#pragma unroll
+    for (int k = 1; k < kSumRows / 4; ++k) t += red[tr + 4 * k][tc];
+    red[tr][tc] = t;
+  }
+  __syncthreads();
+  if (tr == 0 && c < 2 * store.W)
+    store(c, (red[0][tc] + red[1][tc]) + (red[2][tc] + red[3][tc]));
 }
 
 template <typename T, int LANES, int NV, int V>
@@ -329,8 +339,9 @@ hipError_t bwd(const NormArgs& a, const NormPlan& p, hipStream_t s) {
   if (e != hipSuccess || (a.dw == nullptr && a.dbias == nullptr)) return e;
   const int64_t W = a.shared ? a.D : a.C;
   const int64_t reps = a.shared ? 1 : p.period / a.G;
-  hipLaunchKernelGGL(norm_sums, dim3((unsigned)((2 * W + kSumCols - 1) / kSumCols)), dim3(256), 0,
-                     s, a.part, p.parts, reps, NormSumStore{a.dw, a.dbias, W, a.w_bf16});
+  hipLaunchKernelGGL(norm_sums, dim3((unsigned)((2 * W + kSumCols - 1) / kSumCols)),
+                     dim3(kSumCols * kSumRows), 0, s, a.part, (int)p.parts, (int)reps,
+                     NormSumStore{a.dw, a.dbias, W, a.w_bf16});
   e = hipGetLastError();
   note_launch(s);
   return e;

@@ -39,6 +39,13 @@ constexpr int tile_steps() {
   return NPL <= 4 ? 16 : 64 / NPL;
 }
 
+// Steps between saved states: what the backward keeps in registers at a time
+// (the states and decays of that many steps).
+template <int NPL>
+constexpr int save_steps() {
+  return NPL <= 4 ? 8 : 4;
+}
+
 template <int K>
 __device__ __forceinline__ float quad_bcast(float x) {
   return dpp<K * 0x55>(x);
@@ -98,6 +105,9 @@ __device__ __forceinline__ Place place_of(const ScanArgs& a, int ctiles) {
   Place p;
   p.b = blockIdx.y;
   p.sp = span_of(a.spans, p.b, a.T, a.rows);
+  // the same for the whole workgroup: kept in scalar registers
+  p.sp.first = __builtin_amdgcn_readfirstlane((int)p.sp.first);
+  p.sp.len = __builtin_amdgcn_readfirstlane(p.sp.len);
   const int ct = blockIdx.x % ctiles, tpg = ctiles / a.G;
   p.j = blockIdx.x / ctiles;
   p.g = ct / tpg;
@@ -120,6 +130,46 @@ __device__ __forceinline__ int64_t slot_of(const Span& sp, int b, int n, int j) 
   return sp.first / n + b + j;
 }
 
+// Rows and states go through buffer resources: a base that the whole
+// workgroup shares, 32 bits of offset per lane, and a bound past which loads
+// give zero and stores are dropped.  That is what steps past a sequence's end
+// and lanes without a channel (kNoLane) need, with no masks.  The base is the
+// chunk's first row, so the offsets of its rows, and of its saved states,
+// have to stay below 2^31 bytes (scan_chunk sees to that): kNoLane plus any
+// of them is then past every bound and does not wrap.
+constexpr uint32_t kNoLane = 0x80000000u;
+struct Buffer {
+  const char* p;
+  uint32_t bytes;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource() const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, (int)bytes, 0x00020000);
+  }
+};
+__device__ __forceinline__ Buffer buffer_of(const void* p, int64_t offset, int64_t bytes) {
+  return Buffer{static_cast<const char*>(p) + offset, (uint32_t)bytes};
+}
+template <typename T>
+__device__ __forceinline__ T get(Buffer b, uint32_t offset);
+template <>
+__device__ __forceinline__ bf16 get<bf16>(Buffer b, uint32_t offset) {
+  return bf16{(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b.resource(), (int)offset, 0, 0)};
+}
+template <>
+__device__ __forceinline__ float get<float>(Buffer b, uint32_t offset) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b.resource(), (int)offset, 0, 0));
+}
+template <typename T>
+__device__ __forceinline__ void put(Buffer b, uint32_t offset, float x);
+template <>
+__device__ __forceinline__ void put<bf16>(Buffer b, uint32_t offset, float x) {
+  __builtin_amdgcn_raw_buffer_store_b16((unsigned short)cvt_pk_bf16(x, x), b.resource(), (int)offset, 0, 0);
+}
+template <>
+__device__ __forceinline__ void put<float>(Buffer b, uint32_t offset, float x) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b.resource(), (int)offset, 0, 0);
+}
+
+// A lane's NPL states of its channel, in the user's [C][N] layout
 template <int NPL>
 __device__ __forceinline__ void load_states(const float* p, int N, int r, bool ok,
                                             float (&h)[NPL]) {
@@ -133,47 +183,111 @@ __device__ __forceinline__ void store_states(float* p, int N, int r, bool ok,
   for (int i = 0; i < NPL; ++i)
     if (ok && r * NPL + i < N) p[r * NPL + i] = h[i];
 }
-// The same for buffers with 4 NPL states per channel: whole vectors.
+// and in a padded slot [C][4 NPL] of a library buffer
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <int NPL>
-struct alignas(NPL >= 4 ? 16 : 4 * NPL) States {
-  float v[NPL];
-};
+__device__ __forceinline__ Buffer slot_buffer(const float* p, int64_t slot, int C) {
+  const int64_t bytes = (int64_t)C * 16 * NPL;  // C <= 2^20: at most 2^28
+  return buffer_of(p, slot * bytes, bytes);
+}
+template <int NPL>
+__device__ __forceinline__ void get_states(Buffer b, uint32_t o, float (&h)[NPL]) {
+  if constexpr (NPL == 1) {
+    h[0] = get<float>(b, o);
+  } else if constexpr (NPL == 2) {
+    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(b.resource(), (int)o, 0, 0);
+    h[0] = __uint_as_float(v[0]);
+    h[1] = __uint_as_float(v[1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NPL; k += 4) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(b.resource(), (int)(o + 4 * k), 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[k + e] = __uint_as_float(v[e]);
+    }
+  }
+}
+template <int NPL>
+__device__ __forceinline__ void put_states(Buffer b, uint32_t o, const float (&h)[NPL]) {
+  if constexpr (NPL == 1) {
+    put<float>(b, o, h[0]);
+  } else if constexpr (NPL == 2) {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(h[0]), __float_as_uint(h[1])},
+                                          b.resource(),
+                                          (int)o, 0, 0);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NPL; k += 4)
+      __builtin_amdgcn_raw_buffer_store_b128(
+          u32x4{__float_as_uint(h[k]), __float_as_uint(h[k + 1]), __float_as_uint(h[k + 2]),
+                __float_as_uint(h[k + 3])},
+          b.resource(), (int)(o + 4 * k), 0, 0);
+  }
+}
 
 // The raw loads of one tile: this lane's steps of its channel, and this
-// thread's element of B and C.  Steps past the end read the last one.
-template <typename T, int NPL, bool IN, bool OUT>
+// thread's element of B and C; zeros past the sequence's end.  The offsets
+// walk from tile to tile.
+template <typename T, int NPL, int TT, bool IN, bool OUT, bool DY>
 struct Tile {
-  static constexpr int TT = tile_steps<NPL>(), Q = TT / 4, NP = 4 * NPL;
+  static constexpr int Q = TT / 4, NP = 4 * NPL;
   T u[Q], dt[Q], z[Q], dy[Q];
   T bm, cm;
+  Buffer bu, bdt, bz, bdy, bb, bc;   // the chunk's rows
+  uint32_t su, sdt, sz, sd, sb, sc;  // bytes from row to row
+  uint32_t ou, odt, oz, od, ob, oc;  // this lane in the first four rows of the tile at hand
 
-  __device__ __forceinline__ void load(const ScanArgs& a, const Place& p, int t0, bool with_dy) {
+  // At the tile that starts t0 steps into the chunk.
+  __device__ __forceinline__ void init(const ScanArgs& a, const Place& p, int t0) {
+    const int64_t row = p.sp.first + p.begin;
+    auto rows = [&](const void* q, int64_t stride, uint32_t& step) {
+      step = (uint32_t)stride * (uint32_t)sizeof(T);
+      return buffer_of(q, row * (int64_t)step, q != nullptr ? (int64_t)(p.end - p.begin) * step : 0);
+    };
+    bu = rows(a.u, a.u_stride, su);
+    bdt = rows(a.dt, a.dt_stride, sdt);
+    bz = rows(a.z, a.z_stride, sz);
+    bdy = rows(a.dy, a.C, sd);
+    bb = rows(a.Bm, a.b_stride, sb);
+    bc = rows(a.Cm, a.c_stride, sc);
+    auto lane = [&](uint32_t step) {
+      return t0 * step + (p.cok ? p.r * step + p.c * (uint32_t)sizeof(T) : kNoLane);
+    };
+    ou = lane(su);
+    odt = lane(sdt);
+    oz = lane(sz);
+    od = lane(sd);
+    const uint32_t t = threadIdx.x / NP, n = threadIdx.x % NP;
+    const bool ok = t < TT && (int)n < a.N;
+    const uint32_t on = (p.g * a.N + n) * (uint32_t)sizeof(T);
+    ob = t0 * sb + (ok ? t * sb + on : kNoLane);
+    oc = t0 * sc + (ok ? t * sc + on : kNoLane);
+  }
+  __device__ __forceinline__ void load() {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      int t = t0 + 4 * q + p.r;
-      t = t < p.sp.len ? t : p.sp.len - 1;
-      const int64_t row = p.sp.first + t;
-      if (IN) u[q] = static_cast<const T*>(a.u)[row * a.u_stride + p.c];
-      dt[q] = static_cast<const T*>(a.dt)[row * a.dt_stride + p.c];
-      if (OUT && a.z != nullptr) z[q] = static_cast<const T*>(a.z)[row * a.z_stride + p.c];
-      if (OUT && with_dy) dy[q] = static_cast<const T*>(a.dy)[row * a.C + p.c];
+      if (IN) u[q] = get<T>(bu, ou + 4 * q * su);
+      dt[q] = get<T>(bdt, odt + 4 * q * sdt);
+      if (OUT) z[q] = get<T>(bz, oz + 4 * q * sz);
+      if (DY) dy[q] = get<T>(bdy, od + 4 * q * sd);
     }
-    const int i = threadIdx.x;
-    int t = t0 + i / NP;
-    t = t < p.sp.len ? t : p.sp.len - 1;
-    const int n = i % NP < a.N ? i % NP : 0;
-    const int64_t row = p.sp.first + t;
-    if (IN) bm = static_cast<const T*>(a.Bm)[row * a.b_stride + (int64_t)p.g * a.N + n];
-    if (OUT) cm = static_cast<const T*>(a.Cm)[row * a.c_stride + (int64_t)p.g * a.N + n];
+    if (IN) bm = get<T>(bb, ob);
+    if (OUT) cm = get<T>(bc, oc);
   }
-  // B and C to LDS, zeros in the padding and past the end
-  __device__ __forceinline__ void stage(const ScanArgs& a, const Place& p, int t0, float* bs,
-                                        float* cs) const {
-    const int i = threadIdx.x;
-    if (i >= TT * NP) return;
-    const bool ok = t0 + i / NP < p.sp.len && i % NP < a.N;
-    if (IN) bs[i] = ok ? to_f32(bm) : 0.f;
-    if (OUT) cs[i] = ok ? to_f32(cm) : 0.f;
+  // Moves the loads (not od, the dense rows) one tile on or back.
+  template <int WAY>
+  __device__ __forceinline__ void advance() {
+    if (IN) ou += WAY * TT * su;
+    odt += WAY * TT * sdt;
+    if (OUT) oz += WAY * TT * sz;
+    if (IN) ob += WAY * TT * sb;
+    if (OUT) oc += WAY * TT * sc;
+  }
+  __device__ __forceinline__ void stage(float* bs, float* cs) const {
+    if (TT * NP < kThreads && threadIdx.x >= TT * NP) return;
+    if (IN) bs[threadIdx.x] = to_f32(bm);
+    if (OUT) cs[threadIdx.x] = to_f32(cm);
   }
 };
 
@@ -196,8 +310,9 @@ __device__ __forceinline__ void load_rates(const ScanArgs& a, const Place& p, fl
 // start); else the pass that writes y.
 template <typename T, int NPL, bool EDGE>
 __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctiles) {
-  using L = Tile<T, NPL, true, !EDGE>;
-  constexpr int TT = L::TT, Q = L::Q, NP = L::NP;
+  constexpr int TT = tile_steps<NPL>(), HT = save_steps<NPL>();
+  using L = Tile<T, NPL, TT, true, !EDGE, false>;
+  constexpr int Q = L::Q, NP = L::NP;
   __shared__ __align__(16) float Bs[2][TT * NP], Cs[2][EDGE ? 4 : TT * NP];
   const Place p = place_of(a, ctiles);
   if (EDGE ? p.j >= p.last : p.j > p.last) return;
@@ -206,46 +321,59 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctil
   load_rates<NPL>(a, p, A);
   const float bias = a.dt_bias != nullptr ? a.dt_bias[p.c] : 0.f;
   const float D = a.D != nullptr ? a.D[p.c] : 0.f;
-  float* const edge = a.chunks > 1 ? a.edge + (slot_of(p.sp, p.b, a.chunk, p.j) * a.C + p.c) * NP
-                                   : nullptr;
+  // this lane's states in a slot
+  const uint32_t oh = p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane;
   if (EDGE) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = 0.f;
   } else if (a.chunks > 1) {
-    const States<NPL> s = *reinterpret_cast<const States<NPL>*>(edge + r * NPL);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) h[i] = s.v[i];
+    get_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, p.j), a.C), oh, h);
   } else {
     load_states<NPL>(a.S0 + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r, p.cok && a.S0 != nullptr, h);
   }
   float sum = 0.f;
   L in;
-  if (p.begin < p.end) in.load(a, p, p.begin, false);
+  in.init(a, p, 0);
+  if (p.begin < p.end) in.load();
+  const int64_t steps = p.end - p.begin;
+  const Buffer by = buffer_of(a.y, (p.sp.first + p.begin) * (int64_t)in.sd, steps * in.sd);
+  // the saved states from this chunk's first on, of which this lane's next
+  const int64_t slot_bytes = (int64_t)a.C * NP * 4;
+  const Buffer saved =
+      buffer_of(a.ckpt, slot_of(p.sp, p.b, HT, p.begin / HT) * slot_bytes,
+                !EDGE && a.ckpt != nullptr ? (steps + HT - 1) / HT * slot_bytes : 0);
+  uint32_t osaved = oh;
   int buf = 0;
   for (int t0 = p.begin; t0 < p.end; t0 += TT, buf ^= 1) {
-    in.stage(a, p, t0, Bs[buf], Cs[buf]);
-    __syncthreads();
-    const L cur = in;
-    if (t0 + TT < p.end) in.load(a, p, t0 + TT, false);
-    if (!EDGE && a.ckpt != nullptr && p.cok) {
-      States<NPL> s;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) s.v[i] = h[i];
-      *reinterpret_cast<States<NPL>*>(
-          a.ckpt + (slot_of(p.sp, p.b, TT, t0 / TT) * a.C + p.c) * NP + r * NPL) = s;
-    }
+    // this lane's steps: delta, delta u, D u and the gate
+    float dl[Q], du[Q], skip[Q], gate[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int t = t0 + 4 * q + r;
-      const bool ok = p.cok && t < p.end;
-      const float u = to_f32(cur.u[q]);
-      const float dl = delta_of(to_f32(cur.dt[q]) + bias, a.softplus, ok);
-      const float du = ok ? dl * u : 0.f;
-      sum += dl;
+      const float u = to_f32(in.u[q]);
+      dl[q] = delta_of(to_f32(in.dt[q]) + bias, a.softplus, t0 + 4 * q + r < p.end);
+      du[q] = dl[q] * u;
+      if (EDGE) {
+        sum += dl[q];
+      } else {
+        const float g = silu(to_f32(in.z[q]));
+        skip[q] = D * u;
+        gate[q] = a.z != nullptr ? g : 1.f;
+      }
+    }
+    in.stage(Bs[buf], Cs[buf]);
+    in.template advance<1>();
+    if (t0 + TT < p.end) in.load();
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (!EDGE && 4 * q % HT == 0) {
+        if (a.ckpt != nullptr) put_states<NPL>(saved, osaved, h);
+        osaved += (uint32_t)slot_bytes;
+      }
       float acc[4];
       auto step = [&](auto kk) __attribute__((always_inline)) {
         constexpr int k = decltype(kk)::value;
-        const float dk = quad_bcast<k>(dl), duk = quad_bcast<k>(du);
+        const float dk = quad_bcast<k>(dl[q]), duk = quad_bcast<k>(du[q]);
         const float* const bp = Bs[buf] + (4 * q + k) * NP + r * NPL;
         const float* const cp = Cs[buf] + (EDGE ? 0 : (4 * q + k) * NP + r * NPL);
         acc[k] = 0.f;
@@ -260,20 +388,16 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctil
       step(std::integral_constant<int, 2>{});
       step(std::integral_constant<int, 3>{});
       if (!EDGE) {
-        float y = fmaf(D, u, quad_scatter_sum(acc, r));
-        if (a.z != nullptr) y *= silu(to_f32(cur.z[q]));
-        if (ok) st(static_cast<T*>(a.y), (p.sp.first + t) * a.C + p.c, y);
+        const float y = (skip[q] + quad_scatter_sum(acc, r)) * gate[q];
+        put<T>(by, in.od + 4 * q * in.sd, y);
       }
     }
+    in.od += TT * in.sd;
   }
   if (EDGE) {
-    if (!p.cok) return;
-    States<NPL> s;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) s.v[i] = h[i];
-    *reinterpret_cast<States<NPL>*>(edge + r * NPL) = s;
+    put_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, p.j), a.C), oh, h);
     sum = quad_sum(sum);
-    if (r == 0) a.dsum[slot_of(p.sp, p.b, a.chunk, p.j) * a.C + p.c] = sum;
+    if (r == 0 && p.cok) a.dsum[slot_of(p.sp, p.b, a.chunk, p.j) * a.C + p.c] = sum;
   } else if (p.j == p.last && a.S_T != nullptr) {
     store_states<NPL>(a.S_T + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r, p.cok, h);
   }
@@ -283,8 +407,9 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctil
 // from a zero E behind it, for every chunk but the first.
 template <typename T, int NPL>
 __global__ __launch_bounds__(kThreads) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
-  using L = Tile<T, NPL, false, true>;
-  constexpr int TT = L::TT, Q = L::Q, NP = L::NP;
+  constexpr int TT = tile_steps<NPL>();
+  using L = Tile<T, NPL, TT, false, true, true>;
+  constexpr int Q = L::Q, NP = L::NP;
   __shared__ __align__(16) float Cs[2][TT * NP];
   const Place p = place_of(a, ctiles);
   if (p.j == 0 || p.j > p.last) return;
@@ -297,24 +422,28 @@ __global__ __launch_bounds__(kThreads) void scan_adjoint_kernel(ScanArgs a, int 
   float sum = 0.f;
   L in;
   int t0 = p.begin + (p.end - p.begin - 1) / TT * TT;
-  in.load(a, p, t0, true);
+  in.init(a, p, t0 - p.begin);
+  in.load();
   int buf = 0;
   for (; t0 >= p.begin; t0 -= TT, buf ^= 1) {
-    in.stage(a, p, t0, nullptr, Cs[buf]);
+    float dl[Q], o[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      dl[q] = delta_of(to_f32(in.dt[q]) + bias, a.softplus, t0 + 4 * q + r < p.end);
+      const float g = silu(to_f32(in.z[q]));
+      o[q] = to_f32(in.dy[q]) * (a.z != nullptr ? g : 1.f);
+      sum += dl[q];
+    }
+    in.stage(nullptr, Cs[buf]);
+    in.template advance<-1>();
+    in.od -= TT * in.sd;
+    if (t0 > p.begin) in.load();
     __syncthreads();
-    const L cur = in;
-    if (t0 > p.begin) in.load(a, p, t0 - TT, true);
 #pragma unroll
     for (int q = Q - 1; q >= 0; --q) {
-      const bool ok = p.cok && t0 + 4 * q + r < p.end;
-      const float dl = delta_of(to_f32(cur.dt[q]) + bias, a.softplus, ok);
-      float o = to_f32(cur.dy[q]);
-      if (a.z != nullptr) o *= silu(to_f32(cur.z[q]));
-      o = ok ? o : 0.f;
-      sum += dl;
       auto step = [&](auto kk) __attribute__((always_inline)) {
         constexpr int k = decltype(kk)::value;
-        const float dk = quad_bcast<k>(dl), ok_ = quad_bcast<k>(o);
+        const float dk = quad_bcast<k>(dl[q]), ok_ = quad_bcast<k>(o[q]);
         const float* const cp = Cs[buf] + (4 * q + k) * NP + r * NPL;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) E[i] = exp2_hw(dk * A[i]) * fmaf(ok_, cp[i], E[i]);
@@ -325,14 +454,11 @@ __global__ __launch_bounds__(kThreads) void scan_adjoint_kernel(ScanArgs a, int 
       step(std::integral_constant<int, 0>{});
     }
   }
-  if (!p.cok) return;
   const int64_t slot = slot_of(p.sp, p.b, a.chunk, p.j);
-  States<NPL> s;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) s.v[i] = E[i];
-  *reinterpret_cast<States<NPL>*>(a.edge + (slot * a.C + p.c) * NP + r * NPL) = s;
+  put_states<NPL>(slot_buffer<NPL>(a.edge, slot, a.C),
+                  p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane, E);
   sum = quad_sum(sum);
-  if (r == 0) a.dsum[slot * a.C + p.c] = sum;
+  if (r == 0 && p.cok) a.dsum[slot * a.C + p.c] = sum;
 }
 
 // Turns the chunks' local end states into the state before every chunk
@@ -371,17 +497,22 @@ __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int NP)
   }
 }
 
-// The backward's main pass: per tile the states are formed again from the
-// saved one, with the decays kept in registers, and the adjoint runs back
-// over them.
+// The backward's main pass: tile by tile (of save_steps) the states are formed
+// again from the saved one, with their decays, in registers, and the adjoint
+// runs back over them.  One barrier a tile: the tile's B and C and its
+// waves' parts of dB, dC sit in two buffers in turn, and a tile's parts are
+// summed behind the next tile's barrier.
 template <typename T, int NPL>
-__global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, int ctiles) {
-  using L = Tile<T, NPL, true, true>;
-  constexpr int TT = L::TT, Q = L::Q, NP = L::NP;
-  __shared__ __align__(16) float Bs[TT * NP], Cs[TT * NP];
-  __shared__ float red[kWaves][TT][2][NP];
+__global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : 2)) void scan_bwd_kernel(ScanArgs a,
+                                                                               int ctiles) {
+  constexpr int TT = save_steps<NPL>();
+  using L = Tile<T, NPL, TT, true, true, true>;
+  constexpr int NP = L::NP, Q = L::Q;
+  __shared__ __align__(16) float Bs[2][TT * NP], Cs[2][TT * NP];
+  __shared__ float red[2][kWaves][TT][2][NP];
   const Place p = place_of(a, ctiles);
   const int r = p.r, lane = threadIdx.x & 63;
+  const uint32_t oh = p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane;
   float dA[NPL], sD = 0.f, sbias = 0.f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) dA[i] = 0.f;
@@ -391,94 +522,136 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, int c
     const float bias = a.dt_bias != nullptr ? a.dt_bias[p.c] : 0.f;
     const float D = a.D != nullptr ? a.D[p.c] : 0.f;
     if (a.chunks > 1) {
-      const States<NPL> s = *reinterpret_cast<const States<NPL>*>(
-          a.edge + (slot_of(p.sp, p.b, a.chunk, p.j) * a.C + p.c) * NP + r * NPL);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) E[i] = p.cok ? s.v[i] : 0.f;
+      get_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, p.j), a.C), oh, E);
     } else {
       load_states<NPL>(a.dS_T + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r,
                        p.cok && a.dS_T != nullptr, E);
     }
-    L in;
     const int tiles = (p.end - p.begin + TT - 1) / TT;
-    int t0 = p.begin + (tiles - 1) * TT;
-    if (tiles > 0) in.load(a, p, t0, true);
+    int left = p.end - p.begin - (tiles - 1) * TT;  // steps of the tile at hand
+    const int t_last = (tiles - 1) * TT;
+    L in;
+    in.init(a, p, tiles > 0 ? t_last : 0);
+    // the saved states, this channel tile's part of dB and dC, and the dense
+    // gradients, with this lane's place in the tile at hand
+    const int64_t steps = p.end - p.begin, row = p.sp.first + p.begin;
+    const int64_t slot_bytes = (int64_t)a.C * NP * 4;
+    const Buffer saved = buffer_of(a.ckpt, slot_of(p.sp, p.b, TT, p.begin / TT) * slot_bytes,
+                                   tiles * slot_bytes);
+    uint32_t osaved = oh + (tiles > 0 ? (uint32_t)(tiles - 1) * (uint32_t)slot_bytes : 0);
+    const int64_t dense = row * (int64_t)in.sd, dense_bytes = steps * in.sd;
+    const Buffer bdz = buffer_of(a.dz, dense, dense_bytes), bdu = buffer_of(a.du, dense, dense_bytes),
+                 bddt = buffer_of(a.ddt, dense, dense_bytes);
     const int tpg = ctiles / a.G;
-    for (int tile = tiles - 1; tile >= 0; --tile, t0 -= TT) {
-      in.stage(a, p, t0, Bs, Cs);
-      __syncthreads();
-      const L cur = in;
-      if (tile > 0) in.load(a, p, t0 - TT, true);
-      float h0[NPL];
-      {
-        const States<NPL> s = *reinterpret_cast<const States<NPL>*>(
-            a.ckpt + (slot_of(p.sp, p.b, TT, t0 / TT) * a.C + p.c) * NP + r * NPL);
+    const uint32_t sbc = (uint32_t)(a.G * a.N) * 4u;
+    const Buffer bdB = buffer_of(a.pB, ((int64_t)p.tile_in_group * a.rows + row) * sbc, steps * sbc);
+    const Buffer bdC =
+        buffer_of(a.pB, ((int64_t)(tpg + p.tile_in_group) * a.rows + row) * sbc, steps * sbc);
+    const int bstep = threadIdx.x / NP, bn = threadIdx.x % NP;
+    // (of the tile behind the one at hand: its parts are summed first)
+    uint32_t obc = (uint32_t)(t_last + TT) * sbc +
+                   (bn < a.N && bstep < TT ? bstep * sbc + (p.g * a.N + bn) * 4u : kNoLane);
+    // dB, dC of the tile behind: the sum over the waves
+    auto sum_waves = [&](int buf) __attribute__((always_inline)) {
+      if (TT * NP < kThreads && bstep >= TT) return;
+      float x = red[buf][0][bstep][0][bn], y = red[buf][0][bstep][1][bn];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) h0[i] = p.cok ? s.v[i] : 0.f;
+      for (int w = 1; w < kWaves; ++w) {
+        x += red[buf][w][bstep][0][bn];
+        y += red[buf][w][bstep][1][bn];
       }
-      float dl[Q], u[Q], o[Q], h[TT][NPL], dec[TT][NPL];
+      put<float>(bdB, obc, x);
+      put<float>(bdC, obc, y);
+    };
+    float next[NPL];
+    if (tiles > 0) {
+      in.load();
+      get_states<NPL>(saved, osaved, next);
+    }
+    int buf = 0;
+    for (int tile = tiles - 1; tile >= 0; --tile, buf ^= 1) {
+      // this lane's steps: delta and its slope, u, the gate's output and dy
+      // times the gate's slope
+      float dl[Q], slope[Q], u[Q], o[Q], dgate[Q], h0[NPL];
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const int t = t0 + 4 * q + r;
-        const bool ok = p.cok && t < p.end;
-        u[q] = ok ? to_f32(cur.u[q]) : 0.f;
-        dl[q] = delta_of(to_f32(cur.dt[q]) + bias, a.softplus, ok);
+        const bool ok = 4 * q + r < left;
+        const float raw = to_f32(in.dt[q]) + bias, sr = sigmoid(raw);
+        u[q] = to_f32(in.u[q]);
+        dl[q] = delta_of(raw, a.softplus, ok);
+        slope[q] = ok ? (a.softplus ? sr : 1.f) : 0.f;
+        const float dy = to_f32(in.dy[q]), z = to_f32(in.z[q]), sg = sigmoid(z);
+        dgate[q] = dy * dsilu(z, sg);
+        o[q] = dy * (a.z != nullptr ? z * sg : 1.f);
+        sD = fmaf(o[q], u[q], sD);
+      }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) h0[i] = next[i];
+      in.stage(Bs[buf], Cs[buf]);
+      const uint32_t dense_at = in.od;
+      in.template advance<-1>();
+      in.od -= TT * in.sd;
+      osaved -= (uint32_t)slot_bytes;
+      if (tile > 0) {
+        in.load();
+        get_states<NPL>(saved, osaved, next);
+      }
+      __syncthreads();
+      if (tile < tiles - 1) sum_waves(buf ^ 1);
+      obc -= TT * sbc;
+      float h[TT][NPL], dec[TT][NPL];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
         const float du = dl[q] * u[q];
         float acc[4];
         auto step = [&](auto kk) __attribute__((always_inline)) {
-          constexpr int k = decltype(kk)::value;
-          const float dk = quad_bcast<k>(dl[q]), duk = quad_bcast<k>(du);
-          const float* const bp = Bs + (4 * q + k) * NP + r * NPL;
-          const float* const cp = Cs + (4 * q + k) * NP + r * NPL;
-          acc[k] = 0.f;
+          constexpr int e = decltype(kk)::value;
+          const int s = 4 * q + e;
+          const float dk = quad_bcast<e>(dl[q]), duk = quad_bcast<e>(du);
+          const float* const bp = Bs[buf] + s * NP + r * NPL;
+          const float* const cp = Cs[buf] + s * NP + r * NPL;
+          acc[e] = 0.f;
 #pragma unroll
           for (int i = 0; i < NPL; ++i) {
-            const float prev = 4 * q + k > 0 ? h[4 * q + k > 0 ? 4 * q + k - 1 : 0][i] : h0[i];
-            dec[4 * q + k][i] = exp2_hw(dk * A[i]);
-            h[4 * q + k][i] = fmaf(dec[4 * q + k][i], prev, duk * bp[i]);
-            acc[k] = fmaf(cp[i], h[4 * q + k][i], acc[k]);
+            const float prev = s > 0 ? h[s > 0 ? s - 1 : 0][i] : h0[i];
+            dec[s][i] = exp2_hw(dk * A[i]);
+            h[s][i] = fmaf(dec[s][i], prev, duk * bp[i]);
+            acc[e] = fmaf(cp[i], h[s][i], acc[e]);
           }
         };
         step(std::integral_constant<int, 0>{});
         step(std::integral_constant<int, 1>{});
         step(std::integral_constant<int, 2>{});
         step(std::integral_constant<int, 3>{});
-        o[q] = to_f32(cur.dy[q]);
         if (a.z != nullptr) {
-          const float z = to_f32(cur.z[q]), sg = sigmoid(z);
           const float read = fmaf(D, u[q], quad_scatter_sum(acc, r));
-          if (ok)
-            st(static_cast<T*>(a.dz), (p.sp.first + t) * a.C + p.c, o[q] * read * dsilu(z, sg));
-          o[q] *= z * sg;
+          put<T>(bdz, dense_at + 4 * q * in.sd, dgate[q] * read);
         }
-        o[q] = ok ? o[q] : 0.f;
-        sD = fmaf(o[q], u[q], sD);
       }
 #pragma unroll
       for (int q = Q - 1; q >= 0; --q) {
-        const int t = t0 + 4 * q + r;
-        const bool ok = p.cok && t < p.end;
         const float du = dl[q] * u[q];
         float sB[4], sA[4];
         auto step = [&](auto kk) __attribute__((always_inline)) {
-          constexpr int k = decltype(kk)::value;
+          constexpr int e = decltype(kk)::value;
           constexpr int NH = NPL > 1 ? NPL / 2 : 1;
-          const int s = 4 * q + k;
-          const float dk = quad_bcast<k>(dl[q]), duk = quad_bcast<k>(du), o_ = quad_bcast<k>(o[q]);
-          const float* const bp = Bs + s * NP + r * NPL;
-          const float* const cp = Cs + s * NP + r * NPL;
+          const int s = 4 * q + e;
+          const float dk = quad_bcast<e>(dl[q]), duk = quad_bcast<e>(du);
+          const float o_ = quad_bcast<e>(o[q]);
+          const float* const bp = Bs[buf] + s * NP + r * NPL;
+          const float* const cp = Cs[buf] + s * NP + r * NPL;
           float v[2 * NPL];
-          sB[k] = sA[k] = 0.f;
+          sB[e] = sA[e] = 0.f;
 #pragma unroll
           for (int i = 0; i < NPL; ++i) {
             const float prev = s > 0 ? h[s > 0 ? s - 1 : 0][i] : h0[i];
-            const float e = fmaf(o_, cp[i], E[i]);
-            v[i] = e * duk;
+            const float ad = fmaf(o_, cp[i], E[i]);
+            v[i] = ad * duk;
             v[NPL + i] = o_ * h[s][i];
-            sB[k] = fmaf(e, bp[i], sB[k]);
-            E[i] = e * dec[s][i];
+            sB[e] = fmaf(ad, bp[i], sB[e]);
+            E[i] = ad * dec[s][i];
             const float m = E[i] * prev;
-            sA[k] = fmaf(A[i], m, sA[k]);
+            sA[e] = fmaf(A[i], m, sA[e]);
             dA[i] = fmaf(dk, m, dA[i]);
           }
           float w[NH];
@@ -489,7 +662,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, int c
           if ((lane & 12) == 0)
 #pragma unroll
             for (int i = 0; i < NH; ++i)
-              red[p.wave][s][lane >> 5][r * NPL + odd * NH + i] = w[i];
+              red[buf][p.wave][s][lane >> 5][r * NPL + odd * NH + i] = w[i];
         };
         step(std::integral_constant<int, 3>{});
         step(std::integral_constant<int, 2>{});
@@ -497,41 +670,25 @@ __global__ __launch_bounds__(kThreads, 2) void scan_bwd_kernel(ScanArgs a, int c
         step(std::integral_constant<int, 0>{});
         const float gB = quad_scatter_sum(sB, r);
         const float gA = kLn2 * quad_scatter_sum(sA, r);  // A holds log2(e) A
-        float ddt = fmaf(u[q], gB, gA);
-        if (a.softplus) ddt *= sigmoid(to_f32(cur.dt[q]) + bias);
-        if (ok) {
-          const int64_t at = (p.sp.first + t) * a.C + p.c;
-          st(static_cast<T*>(a.du), at, fmaf(D, o[q], dl[q] * gB));
-          st(static_cast<T*>(a.ddt), at, ddt);
-          sbias += ddt;
-        }
+        const float ddt = fmaf(u[q], gB, gA) * slope[q];
+        const uint32_t to = dense_at + 4 * q * in.sd;
+        put<T>(bdu, to, fmaf(D, o[q], dl[q] * gB));
+        put<T>(bddt, to, ddt);
+        sbias += ddt;
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 2 * TT * NP; i += kThreads) {
-        const int which = i / (TT * NP), s = i / NP % TT, n = i % NP;
-        if (t0 + s < p.end && n < a.N) {
-          float x = red[0][s][which][n];
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) x += red[w][s][which][n];
-          a.pB[(((int64_t)which * tpg + p.tile_in_group) * a.rows + p.sp.first + t0 + s) * a.G *
-                   a.N +
-               (int64_t)p.g * a.N + n] = x;
-        }
-      }
+      left = TT;
     }
+    __syncthreads();
+    if (tiles > 0) sum_waves(buf ^ 1);
     if (p.j == 0 && a.dS0 != nullptr)
       store_states<NPL>(a.dS0 + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r, p.cok, E);
   }
-  if (!p.cok) return;
   // partial dA, dD and ddt_bias: zeros from a chunk without steps
   float* const part = a.pA + ((int64_t)p.b * a.chunks + p.j) * a.C * (NP + 2);
-  States<NPL> s;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) s.v[i] = dA[i];
-  *reinterpret_cast<States<NPL>*>(part + (int64_t)p.c * NP + r * NPL) = s;
+  put_states<NPL>(buffer_of(part, 0, (int64_t)a.C * NP * 4), oh, dA);
   sD = quad_sum(sD);
   sbias = quad_sum(sbias);
-  if (r == 0) {
+  if (r == 0 && p.cok) {
     part[(int64_t)a.C * NP + p.c] = sD;
     part[(int64_t)a.C * (NP + 1) + p.c] = sbias;
   }
@@ -638,17 +795,25 @@ hipError_t launch(const ScanArgs& a, hipStream_t s) {
 }  // namespace
 
 int scan_padded(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
-int scan_tile(int64_t N) { return N <= 16 ? 16 : (N <= 32 ? 8 : 4); }
+int scan_save_steps(int64_t N) { return N <= 16 ? 8 : 4; }
 int scan_channels() { return kChannels; }
 
-int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, bool bwd) {
+int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int64_t stride) {
+  // the most steps whose rows and saved states stay below 2^31 bytes
+  const int64_t row = 4 * stride, state = 4 * C * scan_padded(N) / scan_save_steps(N);
+  const int64_t most = (INT64_C(1) << 31) / (row > state ? row : state) / 16 * 16;
+  if (B == 0 || T == 0) return 16;
+  // Split until about eight waves a SIMD of 256 compute units run side by
+  // side: at B = 4, T = 4096, C = 4096, N = 16 (1024 waves unsplit) the forward
+  // takes 745 us unsplit, 603 in 4 chunks, 535 in 8 and 530 in 16, although
+  // the first pass then repeats most of the recurrence.  Chunks under 64 steps
+  // cost more in scan_join than they gain.
   const int64_t waves = B * channel_tiles(C, G) * kWaves;
-  if (B == 0 || waves >= 2048 || T <= 64) return 0;
-  int64_t parts = 4096 / waves;
-  int64_t L = (T + parts - 1) / parts;
+  int64_t L = waves < 8192 ? T * waves / 8192 : T;
+  if (L < 64) L = 64;
+  if (L > T) L = T;
   L = (L + 15) / 16 * 16;
-  if (L < 32) L = 32;
-  return L < T ? L : 0;
+  return L < most ? L : most;
 }
 
 hipError_t launch_scan_fwd(const ScanArgs& a, bool is_bf16, hipStream_t s) {

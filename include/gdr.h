@@ -66,7 +66,7 @@ typedef enum {
                                    gdr_scan_shape or gdr_norm_shape outside
                                    the range stated there                   */
   GDR_ERR_BAD_STRIDE = -15,     /* a row stride below the row's width or
-                                   above 2^31 - 1                           */
+                                   above 2^31 - 1 (2^25 for a scan)         */
   GDR_ERR_BAD_ACT = -16,        /* act is not a gdr_act, or softplus not 0, 1 */
   GDR_ERR_BAD_EPS = -17         /* eps negative, infinite or NaN             */
 } gdr_status;
@@ -289,7 +289,7 @@ int gdr_conv_backward(const gdr_conv_shape* shape, const void* x, const void* we
  *     h_t[c][n] = exp(delta_t A[c][n]) h_{t-1}[c][n] + delta_t u_t[c] B_t[g][n]
  *     y_t[c] = (sum_n C_t[g][n] h_t[c][n] + D[c] u_t[c]) * silu(z_t[c])
  * 1 <= N <= GDR_SCAN_MAX_STATES, C a multiple of G, C <= 2^20, B <= 65535,
- * T and rows at most 2^30 - 1. */
+ * T and rows at most 2^30 - 1, strides (and G N) at most 2^25. */
 #define GDR_SCAN_MAX_STATES 64
 typedef struct {
   int64_t B, T, rows, C, N, G;
@@ -299,8 +299,8 @@ typedef struct {
   int32_t softplus; /* 0 or 1 */
 } gdr_scan_shape;
 
-/* Bytes of the save buffer (the states every 16 steps: 8 for N > 16, 4 for
- * N > 32), and of the scratch buffers (0 where the sequences run unsplit). */
+/* Bytes of the save buffer (the states every 8 steps, every 4 for N > 16),
+ * and of the scratch buffers (0 where the sequences run unsplit). */
 int gdr_scan_checkpoint_bytes(const gdr_scan_shape* shape, size_t* out);
 int gdr_scan_forward_workspace_bytes(const gdr_scan_shape* shape, size_t* out);
 int gdr_scan_backward_workspace_bytes(const gdr_scan_shape* shape, size_t* out);

@@ -85,13 +85,13 @@ def test_structures_match_the_header(lib):
 
 @pytest.mark.parametrize("B,T,C,N", [(1, 2048, 4096, 16), (4, 4096, 4096, 16), (2, 100, 40, 40), (3, 1, 64, 5)])
 def test_scan_save_buffer(lib, B, T, C, N):
-    """A state per tile of 16 (8 for N > 16, 4 for N > 32) steps, states
+    """A state every 8 steps (4 for N > 16), states
     padded to a power of two, a slot per sequence and one more to spare."""
     s = _lib.GdrScanShape(B, T, B * T, C, N, 1, 0, 0, 0, 0, 0, 1, 1)
     pad = 4
     while pad < N:
         pad *= 2
-    tile = 16 if N <= 16 else 8 if N <= 32 else 4
+    tile = 8 if N <= 16 else 4
     assert _lib.size_of("gdr_scan_checkpoint_bytes", s) == C * pad * 4 * (B * T // tile + B + 1)
 
 
