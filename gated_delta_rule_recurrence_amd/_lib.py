@@ -218,6 +218,7 @@ def size_of(query: str, shape) -> int:
 def layer_raw(name: str, shape, pointers, stream, workspace_bytes=None) -> int:
     """A convolution, scan or norm call by its name, with integer device
     addresses (0 = NULL; the workspace last); returns the status."""
-    tail = () if workspace_bytes is None else (workspace_bytes,)
-    return getattr(load(), name)(ctypes.byref(shape), *[p or None for p in pointers], *tail,
-                                 stream or None)
+    call = getattr(_lib or load(), name)
+    if workspace_bytes is None:
+        return call(shape, *pointers, stream)
+    return call(shape, *pointers, workspace_bytes, stream)

@@ -113,8 +113,9 @@ struct ScanArgs {
 int scan_padded(int64_t N);
 int scan_save_steps(int64_t N);
 int scan_channels();
-// Steps of one chunk, a multiple of 16; stride: the widest row in elements.
-int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int64_t stride);
+// Steps of one chunk, a multiple of 16, from a's B, T, C, N, G and rows;
+// stride: the widest row in elements.
+int64_t scan_chunk(const ScanArgs& a, int64_t stride, bool bwd);
 hipError_t launch_scan_fwd(const ScanArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs& a, bool bf16, hipStream_t s);
 
@@ -286,15 +287,14 @@ __device__ __forceinline__ void st_weight(void* p, int64_t i, float x, int is_bf
     static_cast<float*>(p)[i] = x;
 }
 
-// Sums over the rows of part[rows][width], 16 columns and 16 row lanes per
-// workgroup, in a fixed order: column c goes to store(c, sum).
+// Sums over the rows of part[rows][width] by a workgroup of 256: 16 columns,
+// of which c is this thread's, and 16 row lanes, in a fixed order.  The sum
+// comes out in the first 16 threads.
 constexpr int kSumCols = 16;
-template <typename Store>
-__global__ __launch_bounds__(256) void column_sums(const float* __restrict__ part, int64_t rows,
-                                                   int64_t width, Store store) {
+__device__ __forceinline__ float column_sum(const float* __restrict__ part, int64_t rows,
+                                            int64_t width, int64_t c) {
   __shared__ float red[16][kSumCols + 1];
   const int tc = threadIdx.x % kSumCols, tr = threadIdx.x / kSumCols;
-  const int64_t c = (int64_t)blockIdx.x * kSumCols + tc;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < width) {
     int64_t r = tr;
@@ -305,12 +305,18 @@ __global__ __launch_bounds__(256) void column_sums(const float* __restrict__ par
   }
   red[tr][tc] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  if (tr == 0 && c < width) {
-    float t = red[0][tc];
+  float t = red[0][tc];
+  if (tr == 0)
 #pragma unroll
     for (int k = 1; k < 16; ++k) t += red[k][tc];
-    store(c, t);
-  }
+  return t;
+}
+template <typename Store>
+__global__ __launch_bounds__(256) void column_sums(const float* __restrict__ part, int64_t rows,
+                                                   int64_t width, Store store) {
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + threadIdx.x % kSumCols;
+  const float t = column_sum(part, rows, width, c);
+  if (threadIdx.x < kSumCols && c < width) store(c, t);
 }
 template <typename Store>
 hipError_t launch_column_sums(const float* part, int64_t rows, int64_t width, Store store,

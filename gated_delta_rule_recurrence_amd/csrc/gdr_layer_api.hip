@@ -14,7 +14,7 @@ constexpr int64_t kMaxChannels = INT64_C(1) << 20;
 constexpr int64_t kMaxRows = INT32_MAX / 2;  // rows and steps; twice it still is an int
 constexpr int64_t kMaxStride = INT32_MAX;
 constexpr int64_t kMaxScanStride = INT64_C(1) << 25;  // 16 rows of 4 bytes in 32 bits
-constexpr int64_t kMaxBatch = 65535;         // sequences index grid y
+constexpr int64_t kMaxBatch = 65535;         // sequences index grid y, groups z
 constexpr int64_t kMaxIndex = INT64_C(1) << 61;
 
 int64_t round_up256(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -73,7 +73,7 @@ int check(const gdr_scan_shape* in, gdr_scan_shape* s) {
   const int st = sequences_ok(s->B, s->T, s->rows);
   if (st != GDR_OK) return st;
   if (s->C < 1 || s->C > kMaxChannels || s->N < 1 || s->N > GDR_SCAN_MAX_STATES || s->G < 1 ||
-      s->G > s->C || s->C % s->G != 0)
+      s->G > s->C || s->G > kMaxBatch || s->C % s->G != 0)
     return GDR_ERR_BAD_DIM;
   if (!dtype_ok(s->dtype)) return GDR_ERR_BAD_DTYPE;
   if (s->softplus != 0 && s->softplus != 1) return GDR_ERR_BAD_ACT;
@@ -118,7 +118,14 @@ int scan_sizes(const gdr_scan_shape& s, bool bwd, ScanSizes* z) {
   int64_t stride = s.C > s.G * s.N ? s.C : s.G * s.N;
   for (int64_t w : {s.u_stride, s.dt_stride, s.z_stride, s.b_stride, s.c_stride})
     if (w > stride) stride = w;
-  z->chunk = gdr::scan_chunk(s.B, s.T, s.C, s.G, s.N, stride);
+  gdr::ScanArgs a{};
+  a.B = (int)s.B;
+  a.T = (int)s.T;
+  a.C = (int)s.C;
+  a.N = (int)s.N;
+  a.G = (int)s.G;
+  a.rows = s.rows;
+  z->chunk = gdr::scan_chunk(a, stride, bwd);
   z->chunks = s.T > 0 ? (s.T + z->chunk - 1) / z->chunk : 1;
   int64_t state, x;
   if (!product_ok(s.C, np * 4, &state) || !product_ok(state, s.rows / tile + s.B + 1, &z->ckpt))

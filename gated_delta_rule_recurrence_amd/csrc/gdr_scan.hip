@@ -21,10 +21,9 @@
 //
 // Long sequences with few channels are split into chunks of L steps that run
 // side by side: a first pass leaves every chunk's end state from a zero
-// start (edge) and its sum of delta (dsum), scan_join turns those into the
-// state before every chunk, h_in(j + 1) = exp(A dsum_j) h_in(j) + edge_j, and
-// the main pass starts from them.  The backward joins the adjoint the same
-// way.
+// start (edge) and its sum of delta (dsum); the main pass joins those of the
+// chunks before its own, h_in(j + 1) = exp(A dsum_j) h_in(j) + edge_j, and
+// starts from there.  The backward joins the adjoint the same way.
 #include "gdr_layer.h"
 
 namespace gdr {
@@ -33,6 +32,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChannels = 64;  // of one workgroup
+constexpr int kMaxChunks = 64;
+constexpr int kMaxStep = 4;    // steps that scan_step_kernel takes
 
 template <int NPL>
 constexpr int tile_steps() {
@@ -101,6 +102,8 @@ struct Place {
   int begin, end;  // steps of the chunk
   int j, last;     // chunk, last chunk that has steps (0 for an empty sequence)
 };
+// (The divisions cost a short call more than its loads: skipped where there
+// is one chunk, one group.)
 __device__ __forceinline__ Place place_of(const ScanArgs& a, int ctiles) {
   Place p;
   p.b = blockIdx.y;
@@ -108,17 +111,27 @@ __device__ __forceinline__ Place place_of(const ScanArgs& a, int ctiles) {
   // the same for the whole workgroup: kept in scalar registers
   p.sp.first = __builtin_amdgcn_readfirstlane((int)p.sp.first);
   p.sp.len = __builtin_amdgcn_readfirstlane(p.sp.len);
-  const int ct = blockIdx.x % ctiles, tpg = ctiles / a.G;
-  p.j = blockIdx.x / ctiles;
-  p.g = ct / tpg;
-  p.tile_in_group = ct % tpg;
+  int ct = blockIdx.x;
+  p.j = p.last = 0;
+  if (a.chunks > 1) {
+    p.j = ct / ctiles;
+    ct -= p.j * ctiles;
+    p.last = p.sp.len > 0 ? (p.sp.len - 1) / a.chunk : 0;
+  }
+  int Cg = a.C;
+  p.g = 0;
+  p.tile_in_group = ct;
+  if (a.G > 1) {
+    const int tpg = ctiles / a.G;
+    p.g = ct / tpg;
+    p.tile_in_group = ct - p.g * tpg;
+    Cg = a.C / a.G;
+  }
   p.wave = threadIdx.x >> 6;
   p.r = threadIdx.x & 3;
-  const int Cg = a.C / a.G;
   const int in = p.tile_in_group * kChannels + (threadIdx.x >> 2);
   p.cok = in < Cg;
   p.c = p.g * Cg + (p.cok ? in : 0);
-  p.last = p.sp.len > 0 ? (p.sp.len - 1) / a.chunk : 0;
   const int64_t b0 = (int64_t)p.j * a.chunk, b1 = b0 + a.chunk;
   p.begin = (int)(b0 < p.sp.len ? b0 : p.sp.len);
   p.end = (int)(b1 < p.sp.len ? b1 : p.sp.len);
@@ -173,12 +186,32 @@ __device__ __forceinline__ void put<float>(Buffer b, uint32_t offset, float x) {
 template <int NPL>
 __device__ __forceinline__ void load_states(const float* p, int N, int r, bool ok,
                                             float (&h)[NPL]) {
+  if (NPL % 4 == 0 && N == 4 * NPL) {  // whole vectors
+#pragma unroll
+    for (int k = 0; k < NPL; k += 4) {
+      const f4 v = ok ? *reinterpret_cast<const f4*>(p + r * NPL + k) : f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[k + e < NPL ? k + e : 0] = v[e];
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NPL; ++i) h[i] = ok && r * NPL + i < N ? p[r * NPL + i] : 0.f;
 }
 template <int NPL>
 __device__ __forceinline__ void store_states(float* p, int N, int r, bool ok,
                                              const float (&h)[NPL]) {
+  if (NPL % 4 == 0 && N == 4 * NPL) {
+    if (!ok) return;
+#pragma unroll
+    for (int k = 0; k < NPL; k += 4) {
+      f4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = h[k + e < NPL ? k + e : 0];
+      *reinterpret_cast<f4*>(p + r * NPL + k) = v;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
     if (ok && r * NPL + i < N) p[r * NPL + i] = h[i];
@@ -299,10 +332,40 @@ __device__ __forceinline__ float delta_of(float raw, int plus, bool ok) {
 
 template <int NPL>
 __device__ __forceinline__ void load_rates(const ScanArgs& a, const Place& p, float (&A)[NPL]) {
+  load_states<NPL>(a.A + (int64_t)p.c * a.N, a.N, p.r, p.cok, A);
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int n = p.r * NPL + i;
-    A[i] = p.cok && n < a.N ? kLog2e * a.A[(int64_t)p.c * a.N + n] : 0.f;
+  for (int i = 0; i < NPL; ++i) A[i] *= kLog2e;
+}
+
+// The state before chunk j (FWD), or the adjoint behind it: the chunks' local
+// ones joined in the order of the recurrence, h <- exp(A dsum) h + edge, eight
+// chunks' loads in flight (four with more than 4 states a lane).  Every
+// workgroup joins for itself: kMaxChunks keeps that shorter than a kernel
+// between the passes would take (5 to 8 us).
+template <bool FWD, int NPL>
+__device__ __forceinline__ void join_chunks(const ScanArgs& a, const Place& p, uint32_t oh,
+                                            const float (&A)[NPL], float (&h)[NPL]) {
+  const int64_t slot_bytes = (int64_t)a.C * NPL * 16;
+  const int64_t s0 = slot_of(p.sp, p.b, a.chunk, 0);
+  const char* const edge = reinterpret_cast<const char*>(a.edge) + s0 * slot_bytes;
+  const float* const dsum = a.dsum + s0 * a.C + p.c;
+  const int n = FWD ? p.j : p.last - p.j;
+  constexpr int U = NPL <= 4 ? 8 : 4;
+  for (int k0 = 0; k0 < n; k0 += U) {
+    float e[U][NPL], d[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int at = k0 + k < n ? k0 + k : n - 1;
+      const int64_t i = FWD ? at : p.last - at;
+      get_states<NPL>(buffer_of(edge, i * slot_bytes, slot_bytes), oh, e[k]);
+      d[k] = dsum[i * a.C];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (k0 + k >= n) break;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(A[i] * d[k]), h[i], e[k][i]);
+    }
   }
 }
 
@@ -326,10 +389,9 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctil
   if (EDGE) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = 0.f;
-  } else if (a.chunks > 1) {
-    get_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, p.j), a.C), oh, h);
   } else {
     load_states<NPL>(a.S0 + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r, p.cok && a.S0 != nullptr, h);
+    join_chunks<true, NPL>(a, p, oh, A, h);
   }
   float sum = 0.f;
   L in;
@@ -403,6 +465,75 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctil
   }
 }
 
+// NPL consecutive elements of a row of B or C as floats (zeros past N).
+template <typename T, int NPL>
+__device__ __forceinline__ void load_bc(const T* row, int r, int N, bool whole, float (&x)[NPL]) {
+  if (NPL % 4 == 0 && whole) {
+#pragma unroll
+    for (int k = 0; k < NPL; k += 4) {
+      float f[4];
+      unpack(load_pack<T, 4>(row + r * NPL + k), f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[k + e < NPL ? k + e : 0] = f[e];
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const float v = ld(row, r * NPL + i < N ? r * NPL + i : 0);
+    x[i] = r * NPL + i < N ? v : 0.f;
+  }
+}
+
+// Sequences of at most kMaxStep steps (single tokens): the states stream once
+// in and once out, so HBM bytes bound it.  The same quads, but no tiles, LDS
+// or barriers: every lane prepares its channel's step and reads its states'
+// B and C by itself (48 tokens, 5120 channels, N = 16: 11.2 us, 24 us in the
+// tiled kernel; two or four sequences a workgroup, with one load of A, 12.2).
+template <typename T, int NPL>
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
+  const int r = threadIdx.x & 3, g = blockIdx.z, Cg = a.G > 1 ? a.C / a.G : a.C;
+  const int in = blockIdx.x * kChannels + (threadIdx.x >> 2);
+  if (in >= Cg) return;
+  const int c = g * Cg + in, b = blockIdx.y;
+  // whole vectors of B and C
+  const bool whole = a.N == 4 * NPL && a.b_stride % 4 == 0 && a.c_stride % 4 == 0;
+  float h[NPL], A[NPL];
+  load_states<NPL>(a.S0 + ((int64_t)b * a.C + c) * a.N, a.N, r, a.S0 != nullptr, h);
+  load_states<NPL>(a.A + (int64_t)c * a.N, a.N, r, true, A);
+  const float bias = a.dt_bias != nullptr ? a.dt_bias[c] : 0.f;
+  const float D = a.D != nullptr ? a.D[c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) A[i] *= kLog2e;
+  const Span sp = span_of(a.spans, b, a.T, a.rows);
+  if (a.ckpt != nullptr && sp.len > 0)
+    put_states<NPL>(slot_buffer<NPL>(a.ckpt, slot_of(sp, b, save_steps<NPL>(), 0), a.C),
+                    (uint32_t)(c * 4 * NPL + r * NPL) * 4u, h);
+  for (int t = 0; t < sp.len; ++t) {
+    const int64_t row = sp.first + t;
+    const float u = ld(static_cast<const T*>(a.u), row * a.u_stride + c);
+    const float raw = ld(static_cast<const T*>(a.dt), row * a.dt_stride + c) + bias;
+    const float z = a.z != nullptr ? ld(static_cast<const T*>(a.z), row * a.z_stride + c) : 0.f;
+    float B[NPL], C[NPL];
+    load_bc<T, NPL>(static_cast<const T*>(a.Bm) + row * a.b_stride + (int64_t)g * a.N, r, a.N,
+                    whole, B);
+    load_bc<T, NPL>(static_cast<const T*>(a.Cm) + row * a.c_stride + (int64_t)g * a.N, r, a.N,
+                    whole, C);
+    const float dl = delta_of(raw, a.softplus, true), du = dl * u;
+    float acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      h[i] = fmaf(exp2_hw(dl * A[i]), h[i], du * B[i]);
+      acc = fmaf(C[i], h[i], acc);
+    }
+    float y = fmaf(D, u, quad_sum(acc));
+    if (a.z != nullptr) y *= silu(z);
+    if (r == 0) st_row(static_cast<T*>(a.y) + row * a.C + c, y);
+  }
+  if (a.S_T != nullptr)
+    store_states<NPL>(a.S_T + ((int64_t)b * a.C + c) * a.N, a.N, r, true, h);
+}
+
 // The adjoint's first pass: E before the chunk (a_1 E_1 of its first step)
 // from a zero E behind it, for every chunk but the first.
 template <typename T, int NPL>
@@ -461,42 +592,6 @@ __global__ __launch_bounds__(kThreads) void scan_adjoint_kernel(ScanArgs a, int 
   if (r == 0 && p.cok) a.dsum[slot * a.C + p.c] = sum;
 }
 
-// Turns the chunks' local end states into the state before every chunk
-// (FWD), or the local adjoints into the adjoint behind every chunk.  One
-// thread per channel and padded state; four chunks' loads in flight.
-template <bool FWD>
-__global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanArgs a, int NP) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= (int64_t)a.C * NP) return;
-  const int b = blockIdx.y;
-  const Span sp = span_of(a.spans, b, a.T, a.rows);
-  const int last = sp.len > 0 ? (sp.len - 1) / a.chunk : 0;
-  const int c = (int)(i / NP), n = (int)(i % NP);
-  const bool ok = n < a.N;
-  const float A = ok ? kLog2e * a.A[(int64_t)c * a.N + n] : 0.f;
-  const float* const start = FWD ? a.S0 : a.dS_T;
-  float h = ok && start != nullptr ? start[((int64_t)b * a.C + c) * a.N + n] : 0.f;
-  const int64_t s0 = slot_of(sp, b, a.chunk, 0), stride = (int64_t)a.C * NP;
-  constexpr int U = 4;
-  for (int k0 = 0; k0 <= last; k0 += U) {
-    float e[U], d[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      // chunks in the order of the recurrence; the one at its end has no edge
-      const bool has = k0 + k < last;
-      const int64_t s = s0 + (has ? (FWD ? k0 + k : last - k0 - k) : (FWD ? 0 : last));
-      e[k] = a.edge[s * stride + i];
-      d[k] = a.dsum[s * a.C + c];
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (k0 + k > last) break;
-      a.edge[(s0 + (FWD ? k0 + k : last - k0 - k)) * stride + i] = h;
-      if (k0 + k < last) h = fmaf(exp2_hw(A * d[k]), h, e[k]);
-    }
-  }
-}
-
 // The backward's main pass: tile by tile (of save_steps) the states are formed
 // again from the saved one, with their decays, in registers, and the adjoint
 // runs back over them.  One barrier a tile: the tile's B and C and its
@@ -521,12 +616,9 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : 2)) void scan_bwd_kernel(
     load_rates<NPL>(a, p, A);
     const float bias = a.dt_bias != nullptr ? a.dt_bias[p.c] : 0.f;
     const float D = a.D != nullptr ? a.D[p.c] : 0.f;
-    if (a.chunks > 1) {
-      get_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, p.j), a.C), oh, E);
-    } else {
-      load_states<NPL>(a.dS_T + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r,
-                       p.cok && a.dS_T != nullptr, E);
-    }
+    load_states<NPL>(a.dS_T + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r,
+                     p.cok && a.dS_T != nullptr, E);
+    join_chunks<false, NPL>(a, p, oh, A, E);
     const int tiles = (p.end - p.begin + TT - 1) / TT;
     int left = p.end - p.begin - (tiles - 1) * TT;  // steps of the tile at hand
     const int t_last = (tiles - 1) * TT;
@@ -694,40 +786,44 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : 2)) void scan_bwd_kernel(
   }
 }
 
-// dB, dC of every row of a sequence: the sums over the channel tiles.
+// The backward's sums, in one launch: workgroups [0, ca) of sequence 0 sum
+// the chunks' partial dA, dD, ddt_bias, 16 columns and 16 chunk lanes each;
+// the others sum dB, dC of their sequence's rows over the channel tiles.
+struct SumGrid {
+  int ca, tpg, parts, NP;
+};
 template <typename T>
-__global__ __launch_bounds__(kThreads) void scan_sum_bc(ScanArgs a, int tpg) {
+__global__ __launch_bounds__(kThreads) void scan_sums(ScanArgs a, SumGrid g) {
+  if ((int)blockIdx.x < g.ca) {
+    if (blockIdx.y > 0) return;
+    const int64_t width = (int64_t)a.C * (g.NP + 2);
+    const int64_t i = (int64_t)blockIdx.x * kSumCols + threadIdx.x % kSumCols;
+    const float x = column_sum(a.pA, g.parts, width, i);
+    if (threadIdx.x >= kSumCols || i >= width) return;
+    if (i < (int64_t)a.C * g.NP) {
+      const int64_t c = i / g.NP, n = i % g.NP;
+      if (n < a.N) a.dA[c * a.N + n] = x;
+    } else if (i < (int64_t)a.C * (g.NP + 1)) {
+      if (a.dD != nullptr) a.dD[i - (int64_t)a.C * g.NP] = x;
+    } else if (a.ddt_bias != nullptr) {
+      a.ddt_bias[i - (int64_t)a.C * (g.NP + 1)] = x;
+    }
+    return;
+  }
   const Span sp = span_of(a.spans, blockIdx.y, a.T, a.rows);
   const int64_t w = (int64_t)a.G * a.N;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = (int64_t)(blockIdx.x - g.ca) * kThreads + threadIdx.x;
   if (i >= w * sp.len) return;
   const int64_t at = sp.first * w + i, all = a.rows * w;
   float sb = 0.f, sc = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < tpg; ++k) {
+  for (int k = 0; k < g.tpg; ++k) {
     sb += a.pB[k * all + at];
-    sc += a.pB[(tpg + k) * all + at];
+    sc += a.pB[(g.tpg + k) * all + at];
   }
   st(static_cast<T*>(a.dB), at, sb);
   st(static_cast<T*>(a.dC), at, sc);
 }
-
-struct ScanSumStore {
-  float* dA;
-  float* dD;
-  float* ddt_bias;
-  int C, N, NP;
-  __device__ void operator()(int64_t i, float x) const {
-    if (i < (int64_t)C * NP) {
-      const int64_t c = i / NP, n = i % NP;
-      if (n < N) dA[c * N + n] = x;
-    } else if (i < (int64_t)C * (NP + 1)) {
-      if (dD != nullptr) dD[i - (int64_t)C * NP] = x;
-    } else if (ddt_bias != nullptr) {
-      ddt_bias[i - (int64_t)C * (NP + 1)] = x;
-    }
-  }
-};
 
 hipError_t noted(hipStream_t s) {
   const hipError_t e = hipGetLastError();
@@ -741,15 +837,17 @@ int channel_tiles(int64_t C, int64_t G) {
 
 template <typename T, int NPL>
 hipError_t fwd(const ScanArgs& a, hipStream_t s) {
-  const int ct = channel_tiles(a.C, a.G), np = 4 * NPL;
+  const int ct = channel_tiles(a.C, a.G);
+  if (a.T <= kMaxStep) {
+    hipLaunchKernelGGL((scan_step_kernel<T, NPL>),
+                       dim3((unsigned)(ct / a.G), a.B, a.G),
+                       dim3(kThreads), 0, s, a);
+    return noted(s);
+  }
   const dim3 grid((unsigned)(ct * a.chunks), a.B);
   hipError_t e;
   if (a.chunks > 1) {
     hipLaunchKernelGGL((scan_fwd_kernel<T, NPL, true>), grid, dim3(kThreads), 0, s, a, ct);
-    if ((e = noted(s)) != hipSuccess) return e;
-    hipLaunchKernelGGL((scan_join_kernel<true>),
-                       dim3((unsigned)(((int64_t)a.C * np + kThreads - 1) / kThreads), a.B),
-                       dim3(kThreads), 0, s, a, np);
     if ((e = noted(s)) != hipSuccess) return e;
   }
   hipLaunchKernelGGL((scan_fwd_kernel<T, NPL, false>), grid, dim3(kThreads), 0, s, a, ct);
@@ -764,19 +862,13 @@ hipError_t bwd(const ScanArgs& a, hipStream_t s) {
   if (a.chunks > 1) {
     hipLaunchKernelGGL((scan_adjoint_kernel<T, NPL>), grid, dim3(kThreads), 0, s, a, ct);
     if ((e = noted(s)) != hipSuccess) return e;
-    hipLaunchKernelGGL((scan_join_kernel<false>),
-                       dim3((unsigned)(((int64_t)a.C * np + kThreads - 1) / kThreads), a.B),
-                       dim3(kThreads), 0, s, a, np);
-    if ((e = noted(s)) != hipSuccess) return e;
   }
   hipLaunchKernelGGL((scan_bwd_kernel<T, NPL>), grid, dim3(kThreads), 0, s, a, ct);
   if ((e = noted(s)) != hipSuccess) return e;
-  e = launch_column_sums(a.pA, (int64_t)a.B * a.chunks, (int64_t)a.C * (np + 2),
-                         ScanSumStore{a.dA, a.dD, a.ddt_bias, a.C, a.N, np}, s);
-  if (e != hipSuccess || a.T == 0) return e;
-  const int64_t per = (int64_t)a.T * a.G * a.N;
-  hipLaunchKernelGGL((scan_sum_bc<T>), dim3((unsigned)((per + kThreads - 1) / kThreads), a.B),
-                     dim3(kThreads), 0, s, a, ct / a.G);
+  const int64_t columns = (int64_t)a.C * (np + 2), values = (int64_t)a.T * a.G * a.N;
+  const SumGrid g{(int)((columns + kSumCols - 1) / kSumCols), ct / a.G, a.B * a.chunks, np};
+  const int64_t blocks = g.ca + (values + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL((scan_sums<T>), dim3((unsigned)blocks, a.B), dim3(kThreads), 0, s, a, g);
   return noted(s);
 }
 
@@ -798,21 +890,32 @@ int scan_padded(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <
 int scan_save_steps(int64_t N) { return N <= 16 ? 8 : 4; }
 int scan_channels() { return kChannels; }
 
-int64_t scan_chunk(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int64_t stride) {
-  // the most steps whose rows and saved states stay below 2^31 bytes
-  const int64_t row = 4 * stride, state = 4 * C * scan_padded(N) / scan_save_steps(N);
-  const int64_t most = (INT64_C(1) << 31) / (row > state ? row : state) / 16 * 16;
-  if (B == 0 || T == 0) return 16;
-  // Split until about eight waves a SIMD of 256 compute units run side by
-  // side: at B = 4, T = 4096, C = 4096, N = 16 (1024 waves unsplit) the forward
-  // takes 745 us unsplit, 603 in 4 chunks, 535 in 8 and 530 in 16, although
-  // the first pass then repeats most of the recurrence.  Chunks under 64 steps
-  // cost more in scan_join than they gain.
-  const int64_t waves = B * channel_tiles(C, G) * kWaves;
-  int64_t L = waves < 8192 ? T * waves / 8192 : T;
-  if (L < 64) L = 64;
-  if (L > T) L = T;
+int64_t scan_chunk(const ScanArgs& a, int64_t stride, bool bwd) {
+  const int64_t T = a.T;
+  if (a.B == 0 || T == 0) return 16;
+  // Waves of the unsplit grid; packed sequences count for their rows.
+  // Measured at C = 4096, N = 16, bf16, forward / backward in us, by chunks:
+  //    256 waves (T = 2048)   1: 236 / 588   8: 91 / 164   16: 85 / 154   32: 88 / 155
+  //    512                    1: 238 / 598   8: 161 / 304  16: 161 / 309
+  //   1024 (T = 4096)         1: 469 / 1181  8: 538 / 1022 16: 546 / 1031
+  //   2048 (T = 2048)         1: 390 / 891   2: 552 / 1043 8: 531 / 1022
+  // A chunk more than one repeats most of the recurrence in the first pass,
+  // which pays while the device has waves missing: below one wave a SIMD
+  // forward, two backward (its main pass waits more).  Then about 6144 waves,
+  // and chunks of at least 32 steps; joining bounds their number.
+  const int64_t waves = a.rows * channel_tiles(a.C, a.G) * kWaves / T;
+  int64_t S = 1;
+  if (waves < (bwd ? 2048 : 1024)) {
+    S = 6144 / (waves > 0 ? waves : 1);
+    S = S < 8 ? 8 : (S > kMaxChunks ? kMaxChunks : S);
+  }
+  int64_t L = (T + S - 1) / S;
+  if (L < 32) L = 32 < T ? 32 : T;
   L = (L + 15) / 16 * 16;
+  // the most steps whose rows and saved states stay below 2^31 bytes
+  const int64_t row = 4 * stride;
+  const int64_t state = 4 * (int64_t)a.C * scan_padded(a.N) / scan_save_steps(a.N);
+  const int64_t most = (INT64_C(1) << 31) / (row > state ? row : state) / 16 * 16;
   return L < most ? L : most;
 }
 

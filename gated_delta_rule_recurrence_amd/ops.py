@@ -7,6 +7,7 @@ torch.float32.
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -221,6 +222,14 @@ def _act(act) -> int:
     return _ACTS[act]
 
 
+def _dense(name, t, shape, dtype, device):
+    """_check_tensor, for the calls whose host time counts: one condition
+    where all is well."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype
+            and t.device == device and t.is_contiguous()):
+        _check_tensor(name, t, shape, dtype, device)
+
+
 def _row_stride(name, t, tail, dtype, device, rows=None):
     """Checks a tensor of rows whose last dimensions are `tail` and dense;
     returns (rows, elements from one row to the next)."""
@@ -231,19 +240,33 @@ def _row_stride(name, t, tail, dtype, device, rows=None):
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     k = len(tail)
-    shape, strides = t.shape, t.stride()
-    if len(shape) <= k or tuple(shape[-k:]) != tuple(tail):
+    shape = t.shape
+    if len(shape) <= k or shape[-k:] != tail:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected rows of {tuple(tail)}")
     width = 1
-    for size, stride in zip(reversed(shape[-k:]), reversed(strides[-k:])):
-        if size != 1 and stride != width:
-            raise ValueError(f"{name}: a row's {tuple(tail)} elements must be contiguous")
+    for size in tail:
         width *= size
-    n, step = 1, 0
+    if t.is_contiguous():
+        n, step = (t.numel() // width if width else 0), width
+    else:
+        n, step = _collapse(name, shape, t.stride(), k, width)
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} has {n} rows, expected {rows}")
+    return n, step
+
+
+def _collapse(name, shape, strides, k, width):
+    """(rows, row stride) of a tensor that is not dense as a whole."""
+    inner = 1
+    for size, stride in zip(reversed(shape[-k:]), reversed(strides[-k:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name}: the elements of a row must be contiguous (got strides "
+                             f"{strides})")
+        inner *= size
+    n, step = 1, width
     for size, stride in zip(reversed(shape[:-k]), reversed(strides[:-k])):
         if size == 0:
-            n = 0
-            break
+            return 0, width
         if size == 1:
             continue
         if n == 1:
@@ -253,9 +276,7 @@ def _row_stride(name, t, tail, dtype, device, rows=None):
         n *= size
     if n > 1 and step < width:
         raise ValueError(f"{name}: the rows overlap (got strides {strides})")
-    if rows is not None and n != rows:
-        raise ValueError(f"{name} has {n} rows, expected {rows}")
-    return n, (step if n > 1 else width)
+    return n, step
 
 
 def _gpu(x):
@@ -273,7 +294,7 @@ def _sequences(x, rows, tail, spans, T, device):
     if spans is not None:
         if spans.dim() != 2:
             raise ValueError(f"spans has shape {tuple(spans.shape)}, expected (B, 2)")
-        _check_tensor("spans", spans, (spans.shape[0], 2), torch.int32, device)
+        _dense("spans", spans, (spans.shape[0], 2), torch.int32, device)
         return spans.shape[0], rows if T is None else int(T)
     if T is None:
         if x.dim() != len(tail) + 2:
@@ -295,44 +316,79 @@ def _out(given, name, shape, dtype, device, spans):
     if given is None:
         make = torch.empty if spans is None else torch.zeros
         return make(shape, dtype=dtype, device=device)
-    _check_tensor(name, given, shape, dtype, device)
+    _dense(name, given, shape, dtype, device)
     return given
 
 
 def _scratch(workspace, nbytes, device):
+    if nbytes == 0:
+        return None
     if workspace is None:
-        return torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=device)
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError("workspace too small")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace
 
 
-def _launch(name, shape, tensors, device, workspace=None):
+def _raw_stream(device) -> int:
+    """The current stream's handle without a Stream object around it (2 us
+    of a call), where this PyTorch has that."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _stream(device) if get is None else get(device.index)
+
+
+def _launch(name, shape, tensors, device, workspace=None, nbytes=None):
     ptrs = [0 if t is None else t.data_ptr() for t in tensors]
-    nbytes = None
-    if workspace is not None:
-        ptrs.append(workspace.data_ptr())
-        nbytes = workspace.numel() * workspace.element_size()
+    if nbytes is not None:
+        ptrs.append(0 if workspace is None else workspace.data_ptr())
     if torch.cuda.current_device() == device.index:
-        status = _lib.layer_raw(name, shape, ptrs, _stream(device), nbytes)
+        status = _lib.layer_raw(name, shape, ptrs, _raw_stream(device), nbytes)
     else:  # a stream's kernels are launched with its device current
         with torch.cuda.device(device):
-            status = _lib.layer_raw(name, shape, ptrs, _stream(device), nbytes)
-    _lib.check(status, name)
+            status = _lib.layer_raw(name, shape, ptrs, _raw_stream(device), nbytes)
+    if status != 0:
+        _lib.check(status, name)
 
 
-def _conv_shape(x, weight, bias, state, spans, T, act):
+# The C structure of a call's sizes and the bytes of its buffers: they follow
+# from the sizes alone, so that calls of the same sizes share them.
+
+@functools.lru_cache(maxsize=1024)
+def _conv_plan(*sizes):
+    shape = _lib.GdrConvShape(*sizes, 0)
+    return shape, _lib.size_of("gdr_conv_backward_workspace_bytes", shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_plan(*sizes):
+    shape = _lib.GdrScanShape(*sizes)
+    return (shape, _lib.size_of("gdr_scan_checkpoint_bytes", shape),
+            _lib.size_of("gdr_scan_forward_workspace_bytes", shape),
+            _lib.size_of("gdr_scan_backward_workspace_bytes", shape))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_plan(*sizes):
+    shape = _lib.GdrNormShape(*sizes)
+    return shape, _lib.size_of("gdr_norm_backward_workspace_bytes", shape)
+
+
+def _conv_sizes(x, weight, bias, state, spans, T, act):
     dev, dt = _gpu(x)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [C, K]")
     C, K = weight.shape
     wdt = _weight_dtype("weight", weight)
-    _check_tensor("weight", weight, (C, K), wdt, dev)
+    _dense("weight", weight, (C, K), wdt, dev)
     rows, xs = _row_stride("x", x, (C,), dt, dev)
     B, T = _sequences(x, rows, (C,), spans, T, dev)
     if bias is not None:
-        _check_tensor("bias", bias, (C,), wdt, dev)
+        _dense("bias", bias, (C,), wdt, dev)
     if state is not None:
-        _check_tensor("state", state, (B, K - 1, C), dt, dev)
-    return _lib.GdrConvShape(B, T, rows, C, K, xs, _DTYPES[dt], _DTYPES[wdt], _act(act), 0)
+        _dense("state", state, (B, K - 1, C), dt, dev)
+    return _conv_plan(B, T, rows, C, K, xs, _DTYPES[dt], _DTYPES[wdt], _act(act))
 
 
 def gdr_conv_forward(x, weight, bias=None, state=None, *, act="silu", spans=None, T=None,
@@ -342,7 +398,7 @@ def gdr_conv_forward(x, weight, bias=None, state=None, *, act="silu", spans=None
     x [B,T,C] (or rows, see above), weight [C,K], bias [C] or None, state
     [B,K-1,C] (the inputs before each sequence) or None.  state_out may be
     state (in place)."""
-    shape = _conv_shape(x, weight, bias, state, spans, T, act)
+    shape, _ = _conv_sizes(x, weight, bias, state, spans, T, act)
     dev, dt = x.device, x.dtype
     y = _out(y, "y", x.shape, dt, dev, spans)
     if not out_state:
@@ -356,20 +412,20 @@ def gdr_conv_forward(x, weight, bias=None, state=None, *, act="silu", spans=None
 def gdr_conv_backward(x, weight, bias, state, dy, dstate_out=None, *, act="silu", spans=None,
                       T=None, want_dstate=False, workspace=None):
     """Returns (dx, dweight, dbias or None, dstate or None)."""
-    shape = _conv_shape(x, weight, bias, state, spans, T, act)
+    shape, nbytes = _conv_sizes(x, weight, bias, state, spans, T, act)
     dev, dt = x.device, x.dtype
-    _check_tensor("dy", dy, x.shape, dt, dev)
+    _dense("dy", dy, x.shape, dt, dev)
     window = (shape.B, shape.K - 1, shape.C)
     if dstate_out is not None:
-        _check_tensor("dstate_out", dstate_out, window, dt, dev)
+        _dense("dstate_out", dstate_out, window, dt, dev)
     dx = _out(None, "dx", x.shape, dt, dev, spans)
     make = torch.empty_like if shape.B > 0 else torch.zeros_like
     dweight = make(weight)
     dbias = None if bias is None else make(bias)
     dstate = torch.empty(window, dtype=dt, device=dev) if want_dstate else None
-    workspace = _scratch(workspace, _lib.size_of("gdr_conv_backward_workspace_bytes", shape), dev)
+    workspace = _scratch(workspace, nbytes, dev)
     _launch("gdr_conv_backward", shape, (x, weight, bias, state, spans, dy, dstate_out, dx,
-                                         dweight, dbias, dstate), dev, workspace)
+                                         dweight, dbias, dstate), dev, workspace, nbytes)
     return dx, dweight, dbias, dstate
 
 
@@ -384,11 +440,13 @@ class ScanSaved:
     softplus: bool
 
 
-def _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus):
+def _scan_sizes(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus):
     dev, ty = _gpu(u)
     f32 = torch.float32
-    if A.dim() != 2 or Bm.dim() < 3:
-        raise ValueError("A must be [C, N] and Bm, Cm [.., G, N]")
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a tensor [C, N]")
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() < 3:
+        raise ValueError("Bm must be a tensor [.., G, N]")
     C, N = A.shape
     G = Bm.shape[-2]
     rows, us = _row_stride("u", u, (C,), ty, dev)
@@ -396,14 +454,13 @@ def _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus):
     _, bs = _row_stride("Bm", Bm, (G, N), ty, dev, rows)
     _, cs = _row_stride("Cm", Cm, (G, N), ty, dev, rows)
     zs = C if z is None else _row_stride("z", z, (C,), ty, dev, rows)[1]
-    _check_tensor("A", A, (C, N), f32, dev)
+    _dense("A", A, (C, N), f32, dev)
     if D is not None:
-        _check_tensor("D", D, (C,), f32, dev)
+        _dense("D", D, (C,), f32, dev)
     if dt_bias is not None:
-        _check_tensor("dt_bias", dt_bias, (C,), f32, dev)
+        _dense("dt_bias", dt_bias, (C,), f32, dev)
     B, T = _sequences(u, rows, (C,), spans, T, dev)
-    return _lib.GdrScanShape(B, T, rows, C, N, G, us, dts, zs, bs, cs, _DTYPES[ty],
-                             1 if softplus else 0)
+    return _scan_plan(B, T, rows, C, N, G, us, dts, zs, bs, cs, _DTYPES[ty], 1 if softplus else 0)
 
 
 def gdr_scan_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, softplus=True,
@@ -413,24 +470,23 @@ def gdr_scan_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *,
 
     u, dt, z [B,T,C] (or rows, see above); A [C,N], D, dt_bias [C] fp32; Bm,
     Cm [B,T,G,N]; S0 [B,C,N] fp32 or None.  S_T may be S0 (in place)."""
-    shape = _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus)
+    shape, save_bytes, nbytes, _ = _scan_sizes(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus)
     dev = u.device
     states = (shape.B, shape.C, shape.N)
     if S0 is not None:
-        _check_tensor("S0", S0, states, torch.float32, dev)
+        _dense("S0", S0, states, torch.float32, dev)
     y = _out(y, "y", u.shape, u.dtype, dev, spans)
     S_T = _out(S_T, "S_T", states, torch.float32, dev, None) if out_state else None
     saved = None
     if save:
-        nbytes = _lib.size_of("gdr_scan_checkpoint_bytes", shape)
         if ckpt is None:
-            ckpt = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=dev)
-        if ckpt.numel() * ckpt.element_size() < nbytes:
+            ckpt = torch.empty((max(save_bytes, 1),), dtype=torch.uint8, device=dev)
+        if ckpt.numel() * ckpt.element_size() < save_bytes:
             raise ValueError("ckpt buffer too small")
         saved = ScanSaved(ckpt, spans, shape.T, bool(softplus))
-    workspace = _scratch(workspace, _lib.size_of("gdr_scan_forward_workspace_bytes", shape), dev)
+    workspace = _scratch(workspace, nbytes, dev)
     _launch("gdr_scan_forward", shape, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, spans, y, S_T,
-                                        ckpt if save else None), dev, workspace)
+                                        ckpt if save else None), dev, workspace, nbytes)
     return y, S_T, saved
 
 
@@ -439,46 +495,47 @@ def gdr_scan_backward(u, dt, A, Bm, Cm, D, z, dt_bias, saved: ScanSaved, dy, dS_
     """Returns (du, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dS0); None where the
     forward had no such input, and dS0 only where wanted."""
     spans = saved.spans
-    shape = _scan_shape(u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.T, saved.softplus)
+    shape, _, _, nbytes = _scan_sizes(u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.T,
+                                      saved.softplus)
     dev, ty = u.device, u.dtype
     states = (shape.B, shape.C, shape.N)
-    _check_tensor("dy", dy, u.shape, ty, dev)
+    _dense("dy", dy, u.shape, ty, dev)
     if dS_T is not None:
-        _check_tensor("dS_T", dS_T, states, torch.float32, dev)
+        _dense("dS_T", dS_T, states, torch.float32, dev)
     du, ddt, dB, dC = (_out(None, "", t.shape, ty, dev, spans) for t in (u, dt, Bm, Cm))
     dz = None if z is None else _out(None, "", z.shape, ty, dev, spans)
     make = torch.empty_like if shape.B > 0 else torch.zeros_like
     dA = make(A)
     dD, dbias = (None if t is None else make(t) for t in (D, dt_bias))
     dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
-    workspace = _scratch(workspace, _lib.size_of("gdr_scan_backward_workspace_bytes", shape), dev)
+    workspace = _scratch(workspace, nbytes, dev)
     _launch("gdr_scan_backward", shape, (u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.ckpt, dy,
                                          dS_T, du, ddt, dA, dB, dC, dD, dz, dbias, dS0), dev,
-            workspace)
+            workspace, nbytes)
     return du, ddt, dA, dB, dC, dD, dz, dbias, dS0
 
 
-def _norm_shape(x, weight, bias, z, groups, eps, center, act):
+def _norm_sizes(x, weight, bias, z, groups, eps, center, act):
     dev, dt = _gpu(x)
     C = x.shape[-1]
     if groups < 1 or C % groups:
         raise ValueError(f"{C} channels are not {groups} groups")
-    wdt, shared = dt, False
-    for name, w in (("weight", weight), ("bias", bias)):
-        if w is None:
-            continue
-        wdt = _weight_dtype(name, w if weight is None else weight)
-        shared = w.numel() != C
-        width = C // groups if (w if weight is None else weight).numel() != C else C
-        _check_tensor(name, w, (width,), wdt, dev)
+    wdt, width = dt, C
+    like = weight if weight is not None else bias
+    if like is not None:  # weight and bias have one type and one shape
+        wdt = _weight_dtype("weight" if weight is not None else "bias", like)
+        width = C if like.numel() == C else C // groups
+        for name, w in (("weight", weight), ("bias", bias)):
+            if w is not None:
+                _dense(name, w, (width,), wdt, dev)
     rows, xs = _row_stride("x", x, (C,), dt, dev)
     zs = C
     if z is not None:
         if z.shape != x.shape:
             raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(x.shape)}")
         zs = _row_stride("z", z, (C,), dt, dev, rows)[1]
-    return _lib.GdrNormShape(rows, C, groups, xs, zs, eps, _DTYPES[dt], _DTYPES[wdt],
-                             1 if center else 0, 1 if shared else 0, _act(act))
+    return _norm_plan(rows, C, groups, xs, zs, eps, _DTYPES[dt], _DTYPES[wdt], 1 if center else 0,
+                      1 if width != C else 0, _act(act))
 
 
 def gdr_norm_forward(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, center=False,
@@ -487,7 +544,7 @@ def gdr_norm_forward(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, cen
     stats or None).  x, z [..., C]; weight, bias [C], or [C // groups] used by
     every group.  The activation takes z where there is one, else the normed
     rows."""
-    shape = _norm_shape(x, weight, bias, z, groups, eps, center, act)
+    shape, _ = _norm_sizes(x, weight, bias, z, groups, eps, center, act)
     dev = x.device
     y = _out(y, "y", x.shape, x.dtype, dev, None)
     if save:
@@ -502,20 +559,18 @@ def gdr_norm_backward(x, weight, bias, z, stats, dy, *, groups, center=False, ac
                       workspace=None):
     """Returns (dx, dweight, dbias, dz); None where the forward had no such
     input."""
-    shape = _norm_shape(x, weight, bias, z, groups, 0.0, center, act)
+    shape, nbytes = _norm_sizes(x, weight, bias, z, groups, 0.0, center, act)
     dev = x.device
-    _check_tensor("dy", dy, x.shape, x.dtype, dev)
-    _check_tensor("stats", stats, (shape.rows, shape.G, 2), torch.float32, dev)
+    _dense("dy", dy, x.shape, x.dtype, dev)
+    _dense("stats", stats, (shape.rows, shape.G, 2), torch.float32, dev)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dz = None if z is None else torch.empty(z.shape, dtype=x.dtype, device=dev)
     dweight, dbias = (None if w is None else torch.empty_like(w) for w in (weight, bias))
     if weight is None and bias is None:
         nbytes = 0
-    else:
-        nbytes = _lib.size_of("gdr_norm_backward_workspace_bytes", shape)
     workspace = _scratch(workspace, nbytes, dev)
     _launch("gdr_norm_backward", shape, (x, weight, bias, z, stats, dy, dx, dweight, dbias, dz),
-            dev, workspace)
+            dev, workspace, nbytes)
     return dx, dweight, dbias, dz
 
 

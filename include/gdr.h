@@ -288,8 +288,8 @@ int gdr_conv_backward(const gdr_conv_shape* shape, const void* x, const void* we
  *     delta_t = softplus(dt_t[c] + dt_bias[c])   (softplus = 0: the sum itself)
  *     h_t[c][n] = exp(delta_t A[c][n]) h_{t-1}[c][n] + delta_t u_t[c] B_t[g][n]
  *     y_t[c] = (sum_n C_t[g][n] h_t[c][n] + D[c] u_t[c]) * silu(z_t[c])
- * 1 <= N <= GDR_SCAN_MAX_STATES, C a multiple of G, C <= 2^20, B <= 65535,
- * T and rows at most 2^30 - 1, strides (and G N) at most 2^25. */
+ * 1 <= N <= GDR_SCAN_MAX_STATES, C a multiple of G, C <= 2^20, B and G at
+ * most 65535, T and rows at most 2^30 - 1, strides (and G N) at most 2^25. */
 #define GDR_SCAN_MAX_STATES 64
 typedef struct {
   int64_t B, T, rows, C, N, G;
