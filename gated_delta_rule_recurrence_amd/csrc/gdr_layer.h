@@ -60,12 +60,11 @@ struct NormArgs {
 struct NormPlan {
   int lanes, nv;      // lanes and vectors per lane of one group
   bool vec;
-  int64_t period;     // groups after which the weight repeats for every lane
+  int64_t period;     // groups after which a lane meets the same channels again
   int64_t slabs;      // waves (blocks, for lanes > 64) that cover one period
-  int64_t parts;      // blocks per slab in the backward
+  int64_t parts;      // workgroups per slab
 };
-bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool shared, bool bf16,
-               NormPlan* p);
+bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool bf16, NormPlan* p);
 hipError_t launch_norm_fwd(const NormArgs& a, const NormPlan& p, bool bf16, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, const NormPlan& p, bool bf16, hipStream_t s);
 
@@ -162,6 +161,21 @@ __device__ __forceinline__ float softplus(float x) {
   const float w = 1.f + t, d = w - 1.f;
   const float l = kLn2 * __builtin_amdgcn_logf(w) * t * __builtin_amdgcn_rcpf(d);
   return fmaxf(x, 0.f) + (d == 0.f ? t : l);
+}
+
+// a + b with their upper halves (32 lanes) or odd rows (16 lanes) swapped for
+// the other's lower or even ones: lanes of the lower half (even rows) get the
+// sum of a's two halves (rows), the others that of b's.  With a = b: every
+// lane the sum over both.
+__device__ __forceinline__ float swap32_sum(float a, float b) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                  false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+__device__ __forceinline__ float swap16_sum(float a, float b) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                  false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
 // V consecutive elements: one, or a vector of 8 or 16 bytes.

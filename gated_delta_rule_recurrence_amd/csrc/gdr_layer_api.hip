@@ -100,8 +100,7 @@ int check(const gdr_norm_shape* in, gdr_norm_shape* s, gdr::NormPlan* p) {
   if (!(s->eps >= 0.f) || isinf(s->eps)) return GDR_ERR_BAD_EPS;
   if (!stride_ok(&s->x_stride, s->C) || !stride_ok(&s->z_stride, s->C)) return GDR_ERR_BAD_STRIDE;
   if (s->rows * s->G > INT32_MAX) return GDR_ERR_OVERFLOW;
-  if (!gdr::norm_plan(s->rows, s->C, s->G, s->x_stride, s->z_stride, s->shared_weight != 0,
-                      s->dtype == GDR_BF16, p))
+  if (!gdr::norm_plan(s->rows, s->C, s->G, s->x_stride, s->z_stride, s->dtype == GDR_BF16, p))
     return GDR_ERR_BAD_DIM;
   return GDR_OK;
 }
@@ -387,8 +386,8 @@ int norm_forward(const gdr_norm_shape* shape, const void* x, const void* w, cons
 
 int64_t norm_workspace(const gdr_norm_shape& s, const gdr::NormPlan& p) {
   const int64_t D = s.C / s.G;
-  // part[parts][2][period][D], or part[parts][2][D] for a shared weight
-  return p.parts * 2 * (s.shared_weight != 0 ? D : p.period * D) * 4;
+  // part[parts][2][period][D], or part[parts x slabs][2][D] for a shared weight
+  return p.parts * 2 * (s.shared_weight != 0 ? p.slabs * D : p.period * D) * 4;
 }
 
 int norm_backward(const gdr_norm_shape* shape, const void* x, const void* w, const void* bias,

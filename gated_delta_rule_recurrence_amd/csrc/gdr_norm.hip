@@ -12,11 +12,10 @@
 // registers between the statistics and the output.  Groups of up to 64
 // vectors share a wave (LANES = 8 .. 64), wider ones take a whole workgroup.
 // A "slab" is what one wave (one workgroup, for LANES > 64) takes at a time:
-// consecutive groups of the flattened [rows * G] list.  In the backward a
-// slab position walks the list in steps of `period` groups, a multiple of G
-// (of anything, for a weight that every group shares), so that a lane meets
-// the same weights, and keeps them and the sums dw, db in registers, all the
-// way.
+// consecutive groups of the flattened [rows * G] list.  A wave walks the list
+// in steps of a multiple of `period` groups, itself a multiple of G, so that
+// a lane meets the same channels all the way: it holds their weights, and the
+// backward its sums dw and db, in registers.
 #include "gdr_layer.h"
 
 namespace gdr {
@@ -27,22 +26,21 @@ constexpr int kThreads = 256;
 // Sum over the LANES lanes of a group, the same bits in every lane.
 template <int LANES>
 __device__ __forceinline__ float group_sum(float x, float* red) {
-  if constexpr (LANES <= 64) {
-#pragma unroll
-    for (int m = 1; m < LANES; m <<= 1) x += __shfl_xor(x, m, 64);
-    return x;
-  } else {
-    constexpr int W = LANES / 64;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+  x += dpp<kDppQuadSwap1>(x);
+  x += dpp<kDppQuadSwap2>(x);
+  x += dpp<kDppHalfMirror>(x);
+  if constexpr (LANES >= 16) x += dpp<kDppMirror>(x);
+  if constexpr (LANES >= 32) x = swap16_sum(x, x);
+  if constexpr (LANES >= 64) x = swap32_sum(x, x);
+  if constexpr (LANES > 64) {
     __syncthreads();  // the last sum has been read
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
     __syncthreads();
-    float t = red[0];
+    x = red[0];
 #pragma unroll
-    for (int i = 1; i < W; ++i) t += red[i];
-    return t;
+    for (int i = 1; i < LANES / 64; ++i) x += red[i];
   }
+  return x;
 }
 
 template <typename T, int LANES, int NV, int V>
@@ -58,14 +56,17 @@ struct Norm {
                                                  float (&w)[NV][V], float (&b)[NV][V]) {
     const int64_t base = a.shared ? 0 : (int64_t)g * a.D;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const int d = at(lane, i);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int d = at(lane, i) + v;
-        const bool ok = d < a.D;
-        w[i][v] = ok ? (a.w != nullptr ? ld_weight(a.w, base + d, a.w_bf16) : 1.f) : 0.f;
-        b[i][v] = ok && a.bias != nullptr ? ld_weight(a.bias, base + d, a.w_bf16) : 0.f;
+        w[i][v] = d < a.D ? 1.f : 0.f;
+        b[i][v] = 0.f;
       }
+      if (d >= a.D) continue;  // (a group is whole vectors)
+      if (a.w != nullptr) ld_weights<V, (V > 1)>(a.w, base + d, a.w_bf16, w[i]);
+      if (a.bias != nullptr) ld_weights<V, (V > 1)>(a.bias, base + d, a.w_bf16, b[i]);
+    }
   }
   // A group's channels of one tensor (zeros past the group's end).
   static __device__ __forceinline__ void load(const void* p, int64_t off, int lane, int D, bool ok,
@@ -77,102 +78,116 @@ struct Norm {
   }
 };
 
+// Where a lane walks: its channels' group g, its first row and the rows from
+// one turn to the next (rows G fits in 31 bits).
+struct Walk {
+  int g;
+  int64_t row, step;
+};
+template <typename P>
+__device__ __forceinline__ Walk walk_of(const NormArgs& a, int period, int slabs, int part,
+                                        int parts, int wave, int sub) {
+  const int slab = (int)blockIdx.x % slabs;
+  const int place = slab * P::kUnits + sub;
+  const int turns = period / a.G;  // rows of a period
+  return Walk{place % a.G, (int64_t)(part * P::kSlabs + wave) * turns + place / a.G,
+              (int64_t)parts * P::kSlabs * turns};
+}
+
 template <typename T, int LANES, int NV, int V>
 __global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_fwd_kernel(NormArgs a,
-                                                                                   int64_t units) {
+                                                                                   int period,
+                                                                                   int slabs) {
   using P = Norm<T, LANES, NV, V>;
   __shared__ float red[LANES > 64 ? LANES / 64 : 1];
   const int lane = LANES > 64 ? threadIdx.x : threadIdx.x & (LANES - 1);
-  const int64_t unit = (int64_t)blockIdx.x * (P::kBlock / LANES) + threadIdx.x / LANES;
-  const bool ok = unit < units;
-  const uint32_t u32 = (uint32_t)(ok ? unit : 0);  // rows G fits in 31 bits
-  const int64_t row = u32 / (uint32_t)a.G;
-  const int g = (int)(u32 - (uint32_t)row * (uint32_t)a.G);
-  const int64_t xo = row * a.x_stride + (int64_t)g * a.D;
-  Pack<T, V> xr[NV], zr[NV];
-  P::load(a.x, xo, lane, a.D, ok, xr);
-  if (a.z != nullptr) P::load(a.z, row * a.z_stride + (int64_t)g * a.D, lane, a.D, ok, zr);
+  const int wave = LANES > 64 ? 0 : threadIdx.x >> 6;
+  const int sub = LANES > 64 ? 0 : (threadIdx.x & 63) / LANES;
+  const Walk k = walk_of<P>(a, period, slabs, blockIdx.x / slabs, gridDim.x / slabs, wave, sub);
+  const int64_t go = (int64_t)k.g * a.D;
+  Pack<T, V> xn[NV], zn[NV];  // the next turn's rows
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    P::load(a.x, row * a.x_stride + go, lane, a.D, row < a.rows, xn);
+    if (a.z != nullptr) P::load(a.z, row * a.z_stride + go, lane, a.D, row < a.rows, zn);
+  };
+  fetch(k.row);
   float w[NV][V], bias[NV][V];
-  P::weights(a, lane, g, w, bias);
-
-  float x[NV][V], mu = 0.f, s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) unpack(xr[i], x[i]);
+  P::weights(a, lane, k.g, w, bias);
   const float inv = 1.f / (float)a.D;
-  if (a.center) {
+  for (int64_t row = k.row; row < a.rows; row += k.step) {
+    Pack<T, V> xr[NV], zr[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) s += x[i][v];
-    mu = group_sum<LANES>(s, red) * inv;
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[i][v] = P::at(lane, i) + v < a.D ? x[i][v] - mu : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) s = fmaf(x[i][v], x[i][v], s);
-  const float r = 1.f / sqrtf(fmaf(group_sum<LANES>(s, red), inv, a.eps));
-  if (!ok) return;
-  if (a.stats != nullptr && lane == 0) {
-    a.stats[2 * unit] = mu;
-    a.stats[2 * unit + 1] = r;
-  }
-  T* const y = static_cast<T*>(a.y) + row * a.C + (int64_t)g * a.D;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float o[V], z[V];
-    if (a.z != nullptr) unpack(zr[i], z);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float n = fmaf(x[i][v] * r, w[i][v], bias[i][v]);
-      const float in = a.z != nullptr ? z[v] : n;
-      o[v] = a.act ? silu(in) : in;
-      if (a.z != nullptr) o[v] *= n;
+    for (int i = 0; i < NV; ++i) {
+      xr[i] = xn[i];
+      zr[i] = zn[i];
     }
-    if (P::at(lane, i) < a.D) store_pack(y + P::at(lane, i), o);
+    fetch(row + k.step);
+    float x[NV][V], mu = 0.f, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) unpack(xr[i], x[i]);
+    if (a.center) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s += x[i][v];
+      mu = group_sum<LANES>(s, red) * inv;
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i][v] = P::at(lane, i) + v < a.D ? x[i][v] - mu : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s = fmaf(x[i][v], x[i][v], s);
+    const float r = 1.f / sqrtf(fmaf(group_sum<LANES>(s, red), inv, a.eps));
+    if (a.stats != nullptr && lane == 0) {
+      a.stats[2 * (row * a.G + k.g)] = mu;
+      a.stats[2 * (row * a.G + k.g) + 1] = r;
+    }
+    T* const y = static_cast<T*>(a.y) + row * a.C + go;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[V], z[V];
+      if (a.z != nullptr) unpack(zr[i], z);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float n = fmaf(x[i][v] * r, w[i][v], bias[i][v]);
+        const float in = a.z != nullptr ? z[v] : n;
+        o[v] = a.act ? silu(in) : in;
+        if (a.z != nullptr) o[v] *= n;
+      }
+      if (P::at(lane, i) < a.D) store_pack(y + P::at(lane, i), o);
+    }
   }
 }
 
 template <typename T, int LANES, int NV, int V>
 __global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_bwd_kernel(
-    NormArgs a, int64_t units, int64_t period, int slabs) {
+    NormArgs a, int period, int slabs) {
   using P = Norm<T, LANES, NV, V>;
   __shared__ float red[LANES > 64 ? LANES / 64 : 1];
   const int lane = LANES > 64 ? threadIdx.x : threadIdx.x & (LANES - 1);
-  const int slab = blockIdx.x % slabs;
-  const int64_t part = blockIdx.x / slabs, parts = gridDim.x / slabs;  // shared: one slab
-  // this lane's place in the period, and its phase among the walkers of it
+  const int wave = LANES > 64 ? 0 : threadIdx.x >> 6;
   const int sub = LANES > 64 ? 0 : (threadIdx.x & 63) / LANES;
-  const int64_t place = (int64_t)slab * P::kUnits + sub;
-  const int64_t phase = part * P::kSlabs + (LANES > 64 ? 0 : threadIdx.x >> 6);
-  const int64_t step = period * parts * P::kSlabs;
-  const int g = (int)(place % a.G);
+  const int part = blockIdx.x / slabs;
+  const Walk k = walk_of<P>(a, period, slabs, part, gridDim.x / slabs, wave, sub);
+  const int64_t go = (int64_t)k.g * a.D;
   float w[NV][V], bias[NV][V], dw[NV][V], db[NV][V];
-  P::weights(a, lane, g, w, bias);
+  P::weights(a, lane, k.g, w, bias);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[i][v] = db[i][v] = 0.f;
   const float inv = 1.f / (float)a.D;
 
-  // every lane of a wave (workgroup, LANES > 64) makes the same number of
-  // turns: the first unit of the slab decides
-  for (int64_t base = period * phase + (int64_t)slab * P::kUnits; base < units; base += step) {
-    const int64_t unit = base + sub;
-    const bool ok = unit < units;
-    // rows G fits in 31 bits; a shared weight's period is no multiple of G
-    const uint32_t ur = (uint32_t)(ok ? unit : 0) / (uint32_t)a.G;
-    const int64_t row = ur;
-    const int64_t go = (int64_t)((uint32_t)(ok ? unit : 0) - ur * (uint32_t)a.G) * a.D;
+  for (int64_t row = k.row; row < a.rows; row += k.step) {
     Pack<T, V> xr[NV], zr[NV], dyr[NV];
-    P::load(a.x, row * a.x_stride + go, lane, a.D, ok, xr);
-    P::load(a.dy, row * a.C + go, lane, a.D, ok, dyr);
-    if (a.z != nullptr) P::load(a.z, row * a.z_stride + go, lane, a.D, ok, zr);
-    const float mu = ok ? a.stats[2 * unit] : 0.f, r = ok ? a.stats[2 * unit + 1] : 0.f;
+    P::load(a.x, row * a.x_stride + go, lane, a.D, true, xr);
+    P::load(a.dy, row * a.C + go, lane, a.D, true, dyr);
+    if (a.z != nullptr) P::load(a.z, row * a.z_stride + go, lane, a.D, true, zr);
+    const float mu = a.stats[2 * (row * a.G + k.g)], r = a.stats[2 * (row * a.G + k.g) + 1];
     float xh[NV][V], e[NV][V], se = 0.f, sx = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -182,7 +197,7 @@ __global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_bwd_kern
       if (a.z != nullptr) unpack(zr[i], z);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool in = ok && P::at(lane, i) + v < a.D;
+        const bool in = P::at(lane, i) + v < a.D;
         xh[i][v] = in ? (xh[i][v] - mu) * r : 0.f;
         const float n = fmaf(xh[i][v], w[i][v], bias[i][v]);
         float dn = dy[v];
@@ -200,7 +215,7 @@ __global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_bwd_kern
         se += e[i][v];
         sx = fmaf(e[i][v], xh[i][v], sx);
       }
-      if (a.z != nullptr && ok && P::at(lane, i) < a.D)
+      if (a.z != nullptr && P::at(lane, i) < a.D)
         store_pack(static_cast<T*>(a.dz) + row * a.C + go + P::at(lane, i), dz);
     }
     sx = group_sum<LANES>(sx, red) * inv;
@@ -210,24 +225,26 @@ __global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_bwd_kern
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) o[v] = r * (e[i][v] - se - xh[i][v] * sx);
-      if (ok && P::at(lane, i) < a.D)
+      if (P::at(lane, i) < a.D)
         store_pack(static_cast<T*>(a.dx) + row * a.C + go + P::at(lane, i), o);
     }
   }
   if (a.dw == nullptr && a.dbias == nullptr) return;
   // Sums over the workgroup's waves (and, for a shared weight, over a wave's
-  // groups), then part[part][2][period][D], or part[part][2][D] shared.
-  if constexpr (LANES <= 64) {
-    __shared__ float sum[P::kSlabs - 1][2][64];
-    const int q = threadIdx.x >> 6, wl = threadIdx.x & 63;
-    const int64_t width = a.shared ? a.D : period * a.D;
-    const int64_t base = a.shared ? 0 : place * a.D;
-    float* const p = a.part + part * 2 * width + base;
+  // groups), then part[part][2][period][D], or part[workgroup][2][D] shared.
+  const int64_t width = a.shared ? a.D : (int64_t)period * a.D;
+  const int64_t place = (int64_t)((int)blockIdx.x % slabs) * P::kUnits + sub;
+  float* const p = a.part + (a.shared ? (int64_t)blockIdx.x * 2 * width
+                                      : part * 2 * width + place * a.D);
+  __shared__ float sum[LANES > 64 ? 1 : P::kSlabs - 1][2][64];
+  const int wl = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float s0 = dw[i][v], s1 = db[i][v];
+    for (int v = 0; v < V; ++v) {
+      float s0 = dw[i][v], s1 = db[i][v];
+      const int d = P::at(lane, i) + v;
+      if constexpr (LANES <= 64) {
         if (a.shared)
 #pragma unroll
           for (int m = LANES; m < 64; m <<= 1) {
@@ -235,37 +252,23 @@ __global__ __launch_bounds__((Norm<T, LANES, NV, V>::kBlock)) void norm_bwd_kern
             s1 += __shfl_xor(s1, m, 64);
           }
         __syncthreads();
-        if (q > 0) {
-          sum[q - 1][0][wl] = s0;
-          sum[q - 1][1][wl] = s1;
+        if (wave > 0) {
+          sum[wave - 1][0][wl] = s0;
+          sum[wave - 1][1][wl] = s1;
         }
         __syncthreads();
-        const int d = P::at(lane, i) + v;
-        if (q == 0 && d < a.D && (!a.shared || wl < LANES)) {
+        if (wave == 0)
 #pragma unroll
-          for (int k = 0; k < P::kSlabs - 1; ++k) {
-            s0 += sum[k][0][wl];
-            s1 += sum[k][1][wl];
+          for (int q = 0; q < P::kSlabs - 1; ++q) {
+            s0 += sum[q][0][wl];
+            s1 += sum[q][1][wl];
           }
-          p[d] = s0;
-          p[width + d] = s1;
-        }
       }
-  } else {
-    const int64_t width = a.shared ? a.D : period * a.D;
-    const int64_t base = a.shared ? 0 : place * a.D;
-    float* const p = a.part + part * 2 * width + base;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int d = P::at(lane, i) + v;
-        if (d < a.D) {
-          p[d] = dw[i][v];
-          p[width + d] = db[i][v];
-        }
+      if (wave == 0 && d < a.D && (!a.shared || sub == 0)) {
+        p[d] = s0;
+        p[width + d] = s1;
       }
-  }
+    }
 }
 
 // Column c of a partial row [2][reps][W]: the repeats of W (a period that
@@ -319,11 +322,10 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void norm_sums(const float* __r
 }
 
 template <typename T, int LANES, int NV, int V>
-hipError_t fwd(const NormArgs& a, const NormPlan&, hipStream_t s) {
+hipError_t fwd(const NormArgs& a, const NormPlan& p, hipStream_t s) {
   using P = Norm<T, LANES, NV, V>;
-  const int64_t units = a.rows * a.G, per = P::kBlock / LANES;
-  hipLaunchKernelGGL((norm_fwd_kernel<T, LANES, NV, V>), dim3((unsigned)((units + per - 1) / per)),
-                     dim3(P::kBlock), 0, s, a, units);
+  hipLaunchKernelGGL((norm_fwd_kernel<T, LANES, NV, V>), dim3((unsigned)(p.slabs * p.parts)),
+                     dim3(P::kBlock), 0, s, a, (int)p.period, (int)p.slabs);
   const hipError_t e = hipGetLastError();
   note_launch(s);
   return e;
@@ -333,14 +335,15 @@ template <typename T, int LANES, int NV, int V>
 hipError_t bwd(const NormArgs& a, const NormPlan& p, hipStream_t s) {
   using P = Norm<T, LANES, NV, V>;
   hipLaunchKernelGGL((norm_bwd_kernel<T, LANES, NV, V>), dim3((unsigned)(p.slabs * p.parts)),
-                     dim3(P::kBlock), 0, s, a, a.rows * a.G, p.period, (int)p.slabs);
+                     dim3(P::kBlock), 0, s, a, (int)p.period, (int)p.slabs);
   hipError_t e = hipGetLastError();
   note_launch(s);
   if (e != hipSuccess || (a.dw == nullptr && a.dbias == nullptr)) return e;
   const int64_t W = a.shared ? a.D : a.C;
+  const int64_t parts = a.shared ? p.parts * p.slabs : p.parts;
   const int64_t reps = a.shared ? 1 : p.period / a.G;
   hipLaunchKernelGGL(norm_sums, dim3((unsigned)((2 * W + kSumCols - 1) / kSumCols)),
-                     dim3(kSumCols * kSumRows), 0, s, a.part, (int)p.parts, (int)reps,
+                     dim3(kSumCols * kSumRows), 0, s, a.part, (int)parts, (int)reps,
                      NormSumStore{a.dw, a.dbias, W, a.w_bf16});
   e = hipGetLastError();
   note_launch(s);
@@ -394,8 +397,7 @@ int64_t gcd64(int64_t a, int64_t b) { return b == 0 ? a : gcd64(b, a % b); }
 // Lanes and vectors of a group: at most 16 channels per lane (the backward
 // holds six values per channel), so groups of up to 1024 channels take (part
 // of) a wave and up to 8192 a workgroup.
-bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool shared, bool bf16,
-               NormPlan* p) {
+bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool bf16, NormPlan* p) {
   const int64_t D = C / G, V = bf16 ? 8 : 4;
   p->vec = D % V == 0 && xs % V == 0 && zs % V == 0;
   const int64_t v = p->vec ? V : 1, n = (D + v - 1) / v;  // vectors of a group
@@ -414,7 +416,7 @@ bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool 
   while (p->lanes * p->nv < n) p->nv *= 2;
   if (p->nv == 8 || (p->nv < most_nv && p->lanes > 256)) p->nv = most_nv;
   const int64_t per = p->lanes > 64 ? 1 : 64 / p->lanes;
-  p->period = shared ? per : G / gcd64(G, per) * per;
+  p->period = G / gcd64(G, per) * per;
   p->slabs = p->period / per;
   // about 2048 workgroups (of four waves; 512 of sixteen) in all, a part
   // per workgroup of a slab, and no more parts than there are units for

@@ -69,16 +69,6 @@ __device__ __forceinline__ float quad_sum(float x) {
 
 // Sum of a[i] over the 16 quads of a wave (lanes of equal r).  CNT values go
 // in; values CNT / 4 * (l / 16) .. of lane l come out (CNT = 2: value l / 32).
-__device__ __forceinline__ float swap32_sum(float a, float b) {
-  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                  false);
-  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
-}
-__device__ __forceinline__ float swap16_sum(float a, float b) {
-  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                  false);
-  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
-}
 template <int CNT>
 __device__ __forceinline__ void quads_scatter_sum(const float (&a)[CNT],
                                                   float (&o)[CNT > 2 ? CNT / 4 : 1]) {
@@ -175,7 +165,8 @@ template <typename T>
 __device__ __forceinline__ void put(Buffer b, uint32_t offset, float x);
 template <>
 __device__ __forceinline__ void put<bf16>(Buffer b, uint32_t offset, float x) {
-  __builtin_amdgcn_raw_buffer_store_b16((unsigned short)cvt_pk_bf16(x, x), b.resource(), (int)offset, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b16((unsigned short)cvt_pk_bf16(x, x), b.resource(),
+                                        (int)offset, 0, 0);
 }
 template <>
 __device__ __forceinline__ void put<float>(Buffer b, uint32_t offset, float x) {
@@ -276,7 +267,8 @@ struct Tile {
     const int64_t row = p.sp.first + p.begin;
     auto rows = [&](const void* q, int64_t stride, uint32_t& step) {
       step = (uint32_t)stride * (uint32_t)sizeof(T);
-      return buffer_of(q, row * (int64_t)step, q != nullptr ? (int64_t)(p.end - p.begin) * step : 0);
+      return buffer_of(q, row * (int64_t)step,
+                       q != nullptr ? (int64_t)(p.end - p.begin) * step : 0);
     };
     bu = rows(a.u, a.u_stride, su);
     bdt = rows(a.dt, a.dt_stride, sdt);
@@ -632,8 +624,9 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : 2)) void scan_bwd_kernel(
                                    tiles * slot_bytes);
     uint32_t osaved = oh + (tiles > 0 ? (uint32_t)(tiles - 1) * (uint32_t)slot_bytes : 0);
     const int64_t dense = row * (int64_t)in.sd, dense_bytes = steps * in.sd;
-    const Buffer bdz = buffer_of(a.dz, dense, dense_bytes), bdu = buffer_of(a.du, dense, dense_bytes),
-                 bddt = buffer_of(a.ddt, dense, dense_bytes);
+    const Buffer bdz = buffer_of(a.dz, dense, dense_bytes);
+    const Buffer bdu = buffer_of(a.du, dense, dense_bytes);
+    const Buffer bddt = buffer_of(a.ddt, dense, dense_bytes);
     const int tpg = ctiles / a.G;
     const uint32_t sbc = (uint32_t)(a.G * a.N) * 4u;
     const Buffer bdB = buffer_of(a.pB, ((int64_t)p.tile_in_group * a.rows + row) * sbc, steps * sbc);
