@@ -590,7 +590,7 @@ __global__ __launch_bounds__(kThreads) void scan_adjoint_kernel(ScanArgs a, int 
 // waves' parts of dB, dC sit in two buffers in turn, and a tile's parts are
 // summed behind the next tile's barrier.
 template <typename T, int NPL>
-__global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : 2)) void scan_bwd_kernel(ScanArgs a,
+__global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void scan_bwd_kernel(ScanArgs a,
                                                                                int ctiles) {
   constexpr int TT = save_steps<NPL>();
   using L = Tile<T, NPL, TT, true, true, true>;
@@ -629,7 +629,8 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : 2)) void scan_bwd_kernel(
     const Buffer bddt = buffer_of(a.ddt, dense, dense_bytes);
     const int tpg = ctiles / a.G;
     const uint32_t sbc = (uint32_t)(a.G * a.N) * 4u;
-    const Buffer bdB = buffer_of(a.pB, ((int64_t)p.tile_in_group * a.rows + row) * sbc, steps * sbc);
+    const Buffer bdB =
+        buffer_of(a.pB, ((int64_t)p.tile_in_group * a.rows + row) * sbc, steps * sbc);
     const Buffer bdC =
         buffer_of(a.pB, ((int64_t)(tpg + p.tile_in_group) * a.rows + row) * sbc, steps * sbc);
     const int bstep = threadIdx.x / NP, bn = threadIdx.x % NP;
