@@ -296,11 +296,14 @@ def _sequences(x, rows, tail, spans, T, device):
             raise ValueError(f"spans has shape {tuple(spans.shape)}, expected (B, 2)")
         _dense("spans", spans, (spans.shape[0], 2), torch.int32, device)
         return spans.shape[0], rows if T is None else int(T)
+    batch = x.dim() == len(tail) + 2  # [B, T, ...]
     if T is None:
-        if x.dim() != len(tail) + 2:
+        if not batch:
             raise ValueError("T is needed where the rows are not [B, T, ...]")
         return x.shape[0], x.shape[1]
     T = int(T)
+    if batch and x.shape[1] == T:
+        return x.shape[0], T
     if T < 0 or (rows % T if T else rows):
         raise ValueError(f"{rows} rows are not sequences of {T}")
     return (rows // T if T else 0), T

@@ -80,6 +80,13 @@ def dev_spans(spans, dev):
     return None if spans is None else torch.tensor(spans, dtype=torch.int32, device=dev).reshape(-1, 2)
 
 
+def spoil(a, seqs):
+    """NaN in the rows of no sequence: nothing may read them."""
+    if a is not None:
+        a[outside(len(a), seqs)] = float("nan")
+    return a
+
+
 def outside(rows, seqs):
     m = np.ones(rows, bool)
     for i, j in seqs:
@@ -108,12 +115,12 @@ def conv_case(dev, dtype, B, T, C, K, *, wdtype=None, act="silu", bias=True, sta
     dso = n(B, K - 1, C)
     seqs = seqs_of(B, T, spans)
     longest = T if spans is None else max([j - i for i, j in seqs] + [0])
-    xd = dev_of(x, dtype, dev)
+    xd = spoil(dev_of(x, dtype, dev), seqs)
     xd = wide(xd) if stride else xd
     args = [xd, dev_of(w, wdtype, dev), dev_of(b, wdtype, dev), dev_of(st, dtype, dev)]
     kw = dict(act=act, spans=dev_spans(spans, dev), T=longest)
     y, so = ops.gdr_conv_forward(*args, **kw)
-    dx, dw, db, ds = ops.gdr_conv_backward(*args, dev_of(dy, dtype, dev), dev_of(dso, dtype, dev),
+    dx, dw, db, ds = ops.gdr_conv_backward(*args, spoil(dev_of(dy, dtype, dev), seqs), dev_of(dso, dtype, dev),
                                            want_dstate=True, **kw)
     a = act == "silu"
     ref, mag = (L.conv_forward(x, w, b, st, a, seqs, mag=m) for m in (False, True))
@@ -221,6 +228,8 @@ def scan_case(dev, dtype, B, T, C, N, G=1, *, without=(), softplus=True, spans=N
     seqs = seqs_of(B, T, spans)
     longest = T if spans is None else max([j - i for i, j in seqs] + [0])
     d = {k: dev_of(v, "f32" if k in F32 else dtype, dev) for k, v in p.items()}
+    for k in ("u", "dt", "z", "Bm", "Cm", "dy"):
+        spoil(d[k], seqs)
     if stride:
         for k in ("u", "dt", "z"):
             d[k] = wide(d[k])
@@ -263,6 +272,29 @@ def test_scan_states(cuda, dtype, N):
                                      (4, 1, 200, 4), (1, 64, 1, 1), (1, 65, 96, 1), (2, 300, 70, 2)])
 def test_scan_sizes(cuda, dtype, B, T, C, G):
     scan_case(cuda, dtype, B, T, C, 16, G, seed=T)
+
+
+# up to 4 steps (a kernel of its own), and across its border
+@pytest.mark.parametrize("dtype,N", [("bf16", 16), ("f32", 7), ("bf16", 33)])
+@pytest.mark.parametrize("T", [2, 3, 4, 5])
+def test_scan_few_steps(cuda, dtype, N, T):
+    scan_case(cuda, dtype, 3, T, 70, N, 2, seed=T)
+    scan_case(cuda, dtype, 4, 0, 35, N, spans=[(0, 1), (1, 1), (1, 1 + T), (2 + T, 3 + T)], rows=4 + T)
+
+
+def test_scan_unsplit(cuda):
+    """Enough waves that forward and backward run every sequence as one chunk
+    of several tiles (17 x 33 channel tiles x 4 waves), in groups that end
+    inside a channel tile."""
+    scan_case(cuda, "f32", 17, 35, 2112, 4, 1)
+    scan_case(cuda, "bf16", 19, 21, 2100, 3, 4)
+
+
+@pytest.mark.parametrize("T,C,N", [(1000, 24, 16), (2100, 8, 5), (700, 16, 40)])
+def test_scan_many_chunks(cuda, T, C, N):
+    """Sequences split into up to 64 chunks; a batch of unequal ones too."""
+    scan_case(cuda, "f32", 1, T, C, N, seed=T)
+    scan_case(cuda, "f32", 3, 0, C, N, spans=[(0, T // 3), (T // 3, T // 3 + 1), (T // 2, T)], rows=T + 5)
 
 
 @pytest.mark.parametrize("dtype,N", [("bf16", 16), ("f32", 10), ("f32", 40)])
@@ -364,6 +396,323 @@ def test_norm_rows(cuda, rows, G, shared):
 def test_norm_options(cuda, kw):
     norm_case(cuda, "bf16", 19, 192, 3, **kw)
     norm_case(cuda, "f32", 19, 192, 3, **{**kw, "wdtype": "bf16" if "wdtype" in kw else None})
+
+
+# ---- all three: streams, graphs, repeats, spans, large offsets ----------------------
+
+def small_state(dev, dtype="bf16", seed=0):
+    """Inputs of one small call of each operator."""
+    import torch
+    g = torch.Generator(device=dev).manual_seed(seed)
+    n = lambda *s: torch.randn(*s, device=dev, generator=g)
+    t = torch_type(dtype)
+    B, T, C, N = 2, 150, 96, 16
+    r = lambda *s: n(*s).to(t)
+    return dict(conv=(r(B, T, C), r(C, 4), r(C), r(B, 3, C)), dy=r(B, T, C),
+                scan=(r(B, T, C), r(B, T, C), -torch.exp(n(C, N)), r(B, T, 2, N), r(B, T, 2, N), n(C), r(B, T, C),
+                      n(C), n(B, C, N)),
+                norm=(r(B, T, C), r(C), r(C), r(B, T, C)))
+
+
+def run_all(s):
+    """Forward and backward of the three; every output, in order."""
+    from gated_delta_rule_recurrence_amd import ops
+    out = [*ops.gdr_conv_forward(*s["conv"])]
+    out += ops.gdr_conv_backward(*s["conv"], s["dy"], want_dstate=True)
+    y, S_T, saved = ops.gdr_scan_forward(*s["scan"])
+    out += [y, S_T, *ops.gdr_scan_backward(*s["scan"][:8], saved, s["dy"])]
+    y, stats = ops.gdr_norm_forward(*s["norm"], groups=4, center=True)
+    out += [y, *ops.gdr_norm_backward(*s["norm"], stats, s["dy"], groups=4, center=True)]
+    return out
+
+
+def same(a, b):
+    import torch
+    return len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_repeats_are_bitwise_equal(cuda, dtype):
+    s = small_state(cuda, dtype)
+    first = run_all(s)
+    for _ in range(3):
+        assert same(run_all(s), first)
+
+
+def test_another_stream(cuda):
+    import torch
+    s = small_state(cuda)
+    first = run_all(s)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = run_all(s)
+    torch.cuda.current_stream().wait_stream(side)
+    assert same(out, first)
+
+
+def test_two_streams_at_once(cuda):
+    """Two calls in flight share no library state."""
+    import torch
+    states = [small_state(cuda, seed=k) for k in range(2)]
+    want = [run_all(s) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = []
+    for _ in range(5):
+        got = []
+        for st, s in zip(streams, states):
+            with torch.cuda.stream(st):
+                got.append(run_all(s))
+    torch.cuda.synchronize()
+    assert same(got[0], want[0]) and same(got[1], want[1])
+
+
+def test_captured_and_replayed(cuda):
+    """A graph of all forward and backward calls, replayed on new inputs with
+    eager calls and synchronizations between."""
+    import torch
+    s = small_state(cuda)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run_all(s)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run_all(s)
+    flat = lambda d: [t for k in ("conv", "scan", "norm") for t in d[k]] + [d["dy"]]
+    for seed in (1, 2, 3):
+        new = small_state(cuda, seed=seed)
+        for a, b in zip(flat(s), flat(new)):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, run_all(new)), seed
+        graph.replay()
+        assert same(out, run_all(s)), seed
+
+
+def test_states_in_place(cuda):
+    """state_out = state and S_T = S0, over prompts of several tiles and
+    chunks: the values of the call with buffers apart."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    s = small_state(cuda)
+    x, w, b, st = s["conv"]
+    y0, so = ops.gdr_conv_forward(x, w, b, st)
+    mine = st.clone()
+    y1, _ = ops.gdr_conv_forward(x, w, b, mine, state_out=mine)
+    assert torch.equal(y0, y1) and torch.equal(so, mine)
+    y0, S_T, _ = ops.gdr_scan_forward(*s["scan"], save=False)
+    mine = s["scan"][8].clone()
+    y1, _, _ = ops.gdr_scan_forward(*s["scan"][:8], mine, save=False, S_T=mine)
+    assert torch.equal(y0, y1) and torch.equal(S_T, mine)
+    x, w, b, z = s["norm"]
+    y0, _ = ops.gdr_norm_forward(x, w, b, z, groups=4)
+    mine = x.clone()
+    ops.gdr_norm_forward(mine, w, b, z, groups=4, y=mine)
+    assert torch.equal(y0, mine)
+
+
+def test_spans_are_cut_to_the_rows(cuda):
+    """Spans outside 0 .. rows, and longer than T."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    s = small_state(cuda)
+    rows = lambda t: t.reshape(300, *t.shape[2:])
+    wild = torch.tensor([[-7, 100], [100, 90], [120, 150], [200, 1 << 30]], dtype=torch.int32, device=cuda)
+    tame = torch.tensor([[0, 80], [100, 100], [120, 150], [200, 280]], dtype=torch.int32, device=cuda)
+    got = []
+    for spans in (wild, tame):
+        x, w, b, st = s["conv"]
+        st = torch.cat([st, st])
+        out = [*ops.gdr_conv_forward(rows(x), w, b, st, spans=spans, T=80)]
+        out += ops.gdr_conv_backward(rows(x), w, b, st, rows(s["dy"]), spans=spans, T=80, want_dstate=True)
+        u, dt, A, Bm, Cm, D, z, bias, S0 = s["scan"]
+        args = [rows(u), rows(dt), A, rows(Bm), rows(Cm), D, rows(z), bias]
+        y, S_T, saved = ops.gdr_scan_forward(*args, torch.cat([S0, S0]), spans=spans, T=80)
+        out += [y, S_T, *ops.gdr_scan_backward(*args, saved, rows(s["dy"]))]
+        got.append(out)
+    assert same(*got)
+
+
+def test_no_rows_and_no_sequences(cuda):
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    s = small_state(cuda)
+    x, w, b, st = s["conv"]
+    y, so = ops.gdr_conv_forward(x[:, :0], w, b, st)
+    assert y.shape == (2, 0, 96) and torch.equal(so, st)
+    dx, dw, db, ds = ops.gdr_conv_backward(x[:, :0], w, b, st, x[:, :0].contiguous(), st, want_dstate=True)
+    assert not dw.any() and not db.any() and torch.equal(ds, st)
+    u, dt, A, Bm, Cm, D, z, bias, S0 = s["scan"]
+    none = [u[:, :0], dt[:, :0], A, Bm[:, :0], Cm[:, :0], D, z[:, :0], bias]
+    y, S_T, saved = ops.gdr_scan_forward(*none, S0)
+    assert y.shape == (2, 0, 96) and torch.equal(S_T, S0)
+    g = ops.gdr_scan_backward(*none, saved, u[:, :0].contiguous(), S0)
+    assert not g[2].any() and not g[5].any() and not g[7].any() and torch.equal(g[8], S0)
+    none = [t[:0] if t.dim() > 2 else t for t in s["scan"]]
+    y, S_T, saved = ops.gdr_scan_forward(*none)
+    g = ops.gdr_scan_backward(*none[:8], saved, u[:0])
+    assert y.shape == (0, 150, 96) and S_T.shape == (0, 96, 16) and not g[2].any()
+    dx, dw, db, ds = ops.gdr_conv_backward(x[:0], w, b, st[:0], x[:0], want_dstate=True)
+    assert not dw.any() and not db.any()
+    x, w, b, z = s["norm"]
+    y, stats = ops.gdr_norm_forward(x[:0], w, b, z[:0], groups=4)
+    dx, dw, db, dz = ops.gdr_norm_backward(x[:0], w, b, z[:0], stats, x[:0], groups=4)
+    assert y.shape == (0, 150, 96) and not dw.any() and not db.any()
+
+
+def test_offsets_beyond_32_bits(cuda):
+    """Rows whose elements lie past 2^32 (and states, of the norm's row count,
+    past 2^31): the last sequence of a long packed buffer, against the same
+    rows in a buffer of their own."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    C, R, n, N = 16384, 1 << 18, 90, 4
+    g = torch.Generator(device=cuda).manual_seed(3)
+    big = torch.empty(R + n, C, dtype=torch.bfloat16, device=cuda)
+    tail = torch.randn(n, C, device=cuda, generator=g).bfloat16()
+    big[R:] = tail
+    spans = torch.tensor([[5, 40], [R, R + n]], dtype=torch.int32, device=cuda)
+    big[5:40] = tail[:35]
+    own = torch.tensor([[0, 35], [35, 35 + n]], dtype=torch.int32, device=cuda)
+    both = torch.cat([tail[:35], tail])
+    w = torch.randn(C, 4, device=cuda, generator=g).bfloat16()
+    out = torch.empty_like(big)
+    ops.gdr_conv_forward(big, w, spans=spans, T=n, y=out)
+    y, _ = ops.gdr_conv_forward(both, w, spans=own, T=n)
+    assert torch.equal(out[R:], y[35:]) and torch.equal(out[5:40], y[:35])
+    A = -torch.exp(torch.randn(C, N, device=cuda, generator=g))
+    bm = torch.zeros(R + n, 1, N, dtype=torch.bfloat16, device=cuda)
+    mine = torch.randn(35 + n, 1, N, device=cuda, generator=g).bfloat16()
+    bm[5:40], bm[R:] = mine[:35], mine[35:]
+    _, S_T, _ = ops.gdr_scan_forward(big, big, A, bm, bm, spans=spans, T=n, save=False, y=out)
+    y, S, _ = ops.gdr_scan_forward(both, both, A, mine, mine, spans=own, T=n, save=False)
+    # (split into other chunks, so rounded otherwise)
+    assert torch.allclose(S_T, S, rtol=1e-4, atol=1e-4)
+    assert torch.allclose(out[R:].float(), y[35:].float(), rtol=2e-2, atol=2e-2)
+    assert torch.allclose(out[5:40].float(), y[:35].float(), rtol=2e-2, atol=2e-2)
+    ops.gdr_norm_forward(big, groups=128, save=False, y=out, act=None)
+    y, _ = ops.gdr_norm_forward(tail, groups=128, save=False, act=None)
+    assert torch.equal(out[R:], y)
+
+
+def test_gradients_against_differences(cuda):
+    """Central differences of the fp32 forward along a random direction v
+    against the gradient.  (f(x + h v) - f(x - h v)) / 2h is the mean of
+    g(e) = <grad f(x + e v), v> over [-h, h]; Simpson's rule gives that mean as
+    (g(-h) + 4 g(0) + g(h)) / 6 up to h^4 / 180 of f's fifth derivative, where
+    g(0) alone would leave h^2 / 6 of the third (seen in A, whose decays
+    compound over 150 steps).  At h = 1e-2 that leaves the rounding of the
+    difference, 2^-24 |<dy, y>|_1 / h: below 2e-3 of sum |grad v|."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    s = small_state(cuda, "f32", seed=9)
+    gen = torch.Generator(device=cuda).manual_seed(10)
+    fs = dict(conv=lambda *a: ops.causal_conv(*a)[0], scan=lambda *a: ops.selective_scan(*a)[0],
+              norm=lambda *a: ops.group_norm(*a, groups=4, center=True))
+    dy, h = s["dy"], 1e-2
+    for name, f in fs.items():
+        args = [(t * 0.5 if name == "scan" and i != 2 else t).clone() for i, t in enumerate(s[name])]
+        for i, t in enumerate(args):
+            v = torch.randn(t.shape, device=cuda, generator=gen)
+            value, slope, scale = {}, {}, 0.0
+            for e in (-h, 0.0, h):
+                x = (t + e * v).requires_grad_()
+                y = f(*[x if k == i else a for k, a in enumerate(args)])
+                value[e] = (y.detach().double() * dy.double()).sum()
+                y.backward(dy)
+                slope[e] = (x.grad.double() * v.double()).sum()
+                scale = max(scale, float((x.grad.double() * v.double()).abs().sum()))
+            got = (value[h] - value[-h]) / (2 * h)
+            want = (slope[-h] + 4 * slope[0.0] + slope[h]) / 6
+            assert abs(got - want) <= 2e-3 * scale, (name, i, float(got), float(want), scale)
+
+
+def test_autograd_of_shared_and_broadcast_inputs(cuda):
+    """One tensor as several inputs (its gradients add up), an expanded bias
+    and a strided slice as x."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    s = small_state(cuda, "f32")
+    u, dt, A, Bm, Cm, D, z, bias, S0 = s["scan"]
+    one = Bm.clone().requires_grad_()
+    y, _ = ops.selective_scan(u, dt, A, one, one, D, z, bias)
+    y.backward(s["dy"])
+    b, c = Bm.clone().requires_grad_(), Bm.clone().requires_grad_()
+    y, _ = ops.selective_scan(u, dt, A, b, c, D, z, bias)
+    y.backward(s["dy"])
+    torch.testing.assert_close(one.grad, b.grad + c.grad, rtol=1e-6, atol=1e-6)
+    x = torch.randn(2, 150, 300, device=cuda).requires_grad_()
+    w = s["conv"][1]
+    y, _ = ops.causal_conv(x[..., 104:200], w)
+    y.backward(s["dy"])
+    x2 = x.detach()[..., 104:200].contiguous().requires_grad_()
+    y, _ = ops.causal_conv(x2, w)
+    y.backward(s["dy"])
+    assert torch.equal(x.grad[..., 104:200], x2.grad) and not x.grad[..., :104].any()
+
+
+def test_refusals(cuda):
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib, ops
+    s = small_state(cuda)
+    x, w, b, st = s["conv"]
+    u, dt, A, Bm, Cm, D, z, bias, S0 = s["scan"]
+    with pytest.raises(_lib.GdrError, match="aligned"):
+        ops.gdr_conv_forward(x[..., 1:95], w[1:95].contiguous())
+    with pytest.raises(_lib.GdrError, match="dimension"):
+        ops.gdr_conv_forward(x, torch.zeros(96, 9, device=cuda, dtype=x.dtype))
+    for bad in (lambda: ops.gdr_conv_forward(x, w.float(), b), lambda: ops.gdr_conv_forward(x, w, b, st[:1]),
+                lambda: ops.gdr_conv_forward(x.half(), w), lambda: ops.gdr_conv_forward(x, w, act="tanh"),
+                lambda: ops.gdr_conv_forward(x, w[:90]), lambda: ops.gdr_conv_forward(x.transpose(0, 1), w),
+                lambda: ops.gdr_conv_forward(x, w, spans=torch.zeros(2, 2, device=cuda)),
+                lambda: ops.gdr_conv_forward(x, w, y=torch.empty(2, 150, 95, device=cuda, dtype=x.dtype)),
+                lambda: ops.gdr_scan_forward(u, dt[:, :149], A, Bm, Cm),
+                lambda: ops.gdr_scan_forward(u, dt, A, Bm, Cm[:, :, :1]),
+                lambda: ops.gdr_scan_forward(u, dt, A.bfloat16(), Bm, Cm),
+                lambda: ops.gdr_scan_forward(u, dt.float(), A, Bm, Cm),
+                lambda: ops.gdr_scan_forward(u, dt, A, Bm, Cm, S0=S0[:1]),
+                lambda: ops.gdr_scan_forward(u, dt, A, Bm, Cm, z=z.cpu()),
+                lambda: ops.gdr_norm_forward(x, groups=7), lambda: ops.gdr_norm_forward(x, w, groups=4),
+                lambda: ops.gdr_norm_forward(x, x[0, 0, :10].contiguous(), groups=4),
+                lambda: ops.gdr_norm_forward(x, z=x[:1], groups=4)):
+        with pytest.raises((ValueError, TypeError)):
+            bad()
+    with pytest.raises(_lib.GdrError, match="dimension"):
+        ops.gdr_scan_forward(u, dt, torch.zeros(96, 65, device=cuda), torch.zeros(2, 150, 2, 65, device=cuda).bfloat16(),
+                             torch.zeros(2, 150, 2, 65, device=cuda).bfloat16())
+    with pytest.raises(_lib.GdrError, match="dimension"):  # groups of 3 of 96 channels: 32 a group
+        ops.gdr_scan_forward(u, dt, A, Bm[:, :, :1].expand(2, 150, 5, 16).contiguous(),
+                             Cm[:, :, :1].expand(2, 150, 5, 16).contiguous())
+    with pytest.raises(_lib.GdrError, match="eps"):
+        ops.gdr_norm_forward(x, groups=4, eps=-1.0)
+    with pytest.raises(_lib.GdrError, match="dimension"):
+        ops.gdr_norm_forward(torch.zeros(1, 8200, device=cuda), groups=1)
+
+
+def test_launch_events_cover_the_new_calls(cuda):
+    """The measurement hook: each event recorded once per call."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib
+    s = small_state(cuda)
+    want = run_all(s)
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
+    for e in events:
+        e.record()
+    torch.cuda.synchronize()
+    assert _lib.set_launch_events([e.cuda_event for e in events]) == 0
+    try:
+        got = run_all(s)
+        torch.cuda.synchronize()
+        spans = [a.elapsed_time(b) for a, b in zip(events, events[1:])]
+    finally:
+        assert _lib.set_launch_events([]) == 0
+    assert same(got, want) and all(t >= 0 for t in spans)
 
 
 # ---- the layer: together, through autograd ---------------------------------------

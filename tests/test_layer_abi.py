@@ -130,7 +130,8 @@ def test_sequences():
     x = torch.zeros(2, 5, 12)
     assert ops._sequences(x, 10, (12,), None, None, cpu) == (2, 5)
     assert ops._sequences(x, 10, (12,), None, 2, cpu) == (5, 2)
-    assert ops._sequences(x[:, :0], 0, (12,), None, 0, cpu) == (0, 0)
+    assert ops._sequences(x[:, :0], 0, (12,), None, 0, cpu) == (2, 0)
+    assert ops._sequences(torch.zeros(0, 12), 0, (12,), None, 0, cpu) == (0, 0)
     for rows, T in ((10, 3), (10, 0), (10, -1)):
         with pytest.raises(ValueError):
             ops._sequences(x, rows, (12,), None, T, cpu)
