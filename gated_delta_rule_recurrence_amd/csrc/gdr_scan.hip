@@ -29,6 +29,11 @@
 namespace gdr {
 namespace {
 
+// Registers for n waves a SIMD and no fewer: for the eight that fit, the
+// compiler orders the recurrence's loads and exponentials so tightly that the
+// adjoint pass takes 227 us instead of 206 (4 x 4096 x 4096).
+#define SCAN_WAVES(n) __attribute__((amdgpu_waves_per_eu(n, n)))
+
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChannels = 64;  // of one workgroup
@@ -318,7 +323,8 @@ struct Tile {
 
 // delta of a raw step; 0, an identity step, outside the sequence.
 __device__ __forceinline__ float delta_of(float raw, int plus, bool ok) {
-  const float d = plus ? softplus(raw) : raw;
+  const float sp = softplus(raw);  // (not under the condition: a branch per step)
+  const float d = plus ? sp : raw;
   return ok ? d : 0.f;
 }
 
@@ -344,6 +350,8 @@ __device__ __forceinline__ void join_chunks(const ScanArgs& a, const Place& p, u
   const int n = FWD ? p.j : p.last - p.j;
   constexpr int U = NPL <= 4 ? 8 : 4;
   for (int k0 = 0; k0 < n; k0 += U) {
+    // (all loads first, with none under a condition, which would put a wait
+    // between them; a chunk past the last counts as no steps)
     float e[U][NPL], d[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -354,9 +362,12 @@ __device__ __forceinline__ void join_chunks(const ScanArgs& a, const Place& p, u
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (k0 + k >= n) break;
+      const bool in = k0 + k < n;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) h[i] = fmaf(exp2_hw(A[i] * d[k]), h[i], e[k][i]);
+      for (int i = 0; i < NPL; ++i) {
+        const float next = fmaf(exp2_hw(A[i] * d[k]), h[i], e[k][i]);
+        h[i] = in ? next : h[i];
+      }
     }
   }
 }
@@ -364,7 +375,7 @@ __device__ __forceinline__ void join_chunks(const ScanArgs& a, const Place& p, u
 // EDGE: the first pass (end state of every chunk but the last from a zero
 // start); else the pass that writes y.
 template <typename T, int NPL, bool EDGE>
-__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, int ctiles) {
+__global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
   constexpr int TT = tile_steps<NPL>(), HT = save_steps<NPL>();
   using L = Tile<T, NPL, TT, true, !EDGE, false>;
   constexpr int Q = L::Q, NP = L::NP;
@@ -495,8 +506,6 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
   load_states<NPL>(a.A + (int64_t)c * a.N, a.N, r, true, A);
   const float bias = a.dt_bias != nullptr ? a.dt_bias[c] : 0.f;
   const float D = a.D != nullptr ? a.D[c] : 0.f;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) A[i] *= kLog2e;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
   if (a.ckpt != nullptr && sp.len > 0)
     put_states<NPL>(slot_buffer<NPL>(a.ckpt, slot_of(sp, b, save_steps<NPL>(), 0), a.C),
@@ -511,11 +520,13 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
                     whole, B);
     load_bc<T, NPL>(static_cast<const T*>(a.Cm) + row * a.c_stride + (int64_t)g * a.N, r, a.N,
                     whole, C);
-    const float dl = delta_of(raw, a.softplus, true), du = dl * u;
+    // (log2 e goes to delta: to scale A first would wait for it before the
+    // step's loads go out)
+    const float dl = delta_of(raw, a.softplus, true), du = dl * u, dl2 = kLog2e * dl;
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      h[i] = fmaf(exp2_hw(dl * A[i]), h[i], du * B[i]);
+      h[i] = fmaf(exp2_hw(dl2 * A[i]), h[i], du * B[i]);
       acc = fmaf(C[i], h[i], acc);
     }
     float y = fmaf(D, u, quad_sum(acc));
@@ -529,7 +540,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
 // The adjoint's first pass: E before the chunk (a_1 E_1 of its first step)
 // from a zero E behind it, for every chunk but the first.
 template <typename T, int NPL>
-__global__ __launch_bounds__(kThreads) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
+__global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
   constexpr int TT = tile_steps<NPL>();
   using L = Tile<T, NPL, TT, false, true, true>;
   constexpr int Q = L::Q, NP = L::NP;
@@ -895,12 +906,12 @@ int64_t scan_chunk(const ScanArgs& a, int64_t stride, bool bwd) {
   //   2048 (T = 2048)         1: 390 / 891   2: 552 / 1043 8: 531 / 1022
   // A chunk more than one repeats most of the recurrence in the first pass,
   // which pays while the device has waves missing: below one wave a SIMD
-  // forward, two backward (its main pass waits more).  Then about 6144 waves,
+  // forward, two backward (its main pass waits more).  Then 4096 waves or more,
   // and chunks of at least 32 steps; joining bounds their number.
   const int64_t waves = a.rows * channel_tiles(a.C, a.G) * kWaves / T;
   int64_t S = 1;
   if (waves < (bwd ? 2048 : 1024)) {
-    S = 6144 / (waves > 0 ? waves : 1);
+    S = 4096 / (waves > 0 ? waves : 1);
     S = S < 8 ? 8 : (S > kMaxChunks ? kMaxChunks : S);
   }
   int64_t L = (T + S - 1) / S;
