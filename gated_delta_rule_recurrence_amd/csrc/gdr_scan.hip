@@ -468,70 +468,94 @@ __global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_
   }
 }
 
-// NPL consecutive elements of a row of B or C as floats (zeros past N).
-template <typename T, int NPL>
-__device__ __forceinline__ void load_bc(const T* row, int r, int N, bool whole, float (&x)[NPL]) {
-  if (NPL % 4 == 0 && whole) {
+// A lane's NPL elements of a dense row of N (A, S0, B or C) as floats, zeros
+// past N.  WHOLE: N = 4 NPL and the row starts on a multiple of four
+// elements, so they are whole vectors.
+template <typename T, int NPL, bool WHOLE>
+__device__ __forceinline__ void get_row(Buffer b, uint32_t o, int r, int N, float (&x)[NPL]) {
+  constexpr int kBytes = NPL * sizeof(T);
+  const uint32_t at = o + r * kBytes;
+  if constexpr (!WHOLE || kBytes < 4) {
 #pragma unroll
-    for (int k = 0; k < NPL; k += 4) {
-      float f[4];
-      unpack(load_pack<T, 4>(row + r * NPL + k), f);
+    for (int i = 0; i < NPL; ++i)
+      x[i] = to_f32(get<T>(b, r * NPL + i < N ? at + i * (uint32_t)sizeof(T) : kNoLane));
+  } else if constexpr (sizeof(T) == 4) {
+    get_states<NPL>(b, at, x);
+  } else {
+    uint32_t w[NPL / 2];
+    if constexpr (kBytes == 4) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(b.resource(), (int)at, 0, 0);
+    } else if constexpr (kBytes == 8) {
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(b.resource(), (int)at, 0, 0);
+      w[0] = v[0];
+      w[1] = v[1];
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[k + e < NPL ? k + e : 0] = f[e];
+      for (int k = 0; k < NPL / 2; k += 4) {
+        const u32x4 v =
+            __builtin_amdgcn_raw_buffer_load_b128(b.resource(), (int)(at + 4 * k), 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[k + e] = v[e];
+      }
     }
-    return;
-  }
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const float v = ld(row, r * NPL + i < N ? r * NPL + i : 0);
-    x[i] = r * NPL + i < N ? v : 0.f;
+    for (int i = 0; i < NPL / 2; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
 }
 
 // Sequences of at most kMaxStep steps (single tokens): the states stream once
 // in and once out, so HBM bytes bound it.  The same quads, but no tiles, LDS
 // or barriers: every lane prepares its channel's step and reads its states'
-// B and C by itself (48 tokens, 5120 channels, N = 16: 11.2 us, 24 us in the
-// tiled kernel; two or four sequences a workgroup, with one load of A, 12.2).
-template <typename T, int NPL>
+// B and C by itself.  Everything is loaded without a branch (absent tensors
+// are empty buffers), so that one latency covers the lot.
+// HBMNOTE
+template <typename T, int NPL, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
   const int r = threadIdx.x & 3, g = blockIdx.z, Cg = a.G > 1 ? a.C / a.G : a.C;
   const int in = blockIdx.x * kChannels + (threadIdx.x >> 2);
   if (in >= Cg) return;
   const int c = g * Cg + in, b = blockIdx.y;
-  // whole vectors of B and C
-  const bool whole = a.N == 4 * NPL && a.b_stride % 4 == 0 && a.c_stride % 4 == 0;
+  Span sp = span_of(a.spans, b, a.T, a.rows);
+  sp.first = __builtin_amdgcn_readfirstlane((int)sp.first);
+  sp.len = __builtin_amdgcn_readfirstlane(sp.len);
+  auto all = [](const void* p, int64_t offset, int64_t bytes) {
+    return buffer_of(p, offset, p != nullptr ? bytes : 0);
+  };
+  const int64_t states = (int64_t)a.C * a.N * 4;  // at most 2^28
+  const uint32_t oc = (uint32_t)c * a.N * 4u;
   float h[NPL], A[NPL];
-  load_states<NPL>(a.S0 + ((int64_t)b * a.C + c) * a.N, a.N, r, a.S0 != nullptr, h);
-  load_states<NPL>(a.A + (int64_t)c * a.N, a.N, r, true, A);
-  const float bias = a.dt_bias != nullptr ? a.dt_bias[c] : 0.f;
-  const float D = a.D != nullptr ? a.D[c] : 0.f;
-  const Span sp = span_of(a.spans, b, a.T, a.rows);
-  if (a.ckpt != nullptr && sp.len > 0)
-    put_states<NPL>(slot_buffer<NPL>(a.ckpt, slot_of(sp, b, save_steps<NPL>(), 0), a.C),
-                    (uint32_t)(c * 4 * NPL + r * NPL) * 4u, h);
+  get_row<float, NPL, WHOLE>(all(a.S0, b * states, states), oc, r, a.N, h);
+  get_row<float, NPL, WHOLE>(all(a.A, 0, states), oc, r, a.N, A);
+  const float bias = get<float>(all(a.dt_bias, 0, a.C * 4), c * 4u);
+  const float D = get<float>(all(a.D, 0, a.C * 4), c * 4u);
   for (int t = 0; t < sp.len; ++t) {
-    const int64_t row = sp.first + t;
-    const float u = ld(static_cast<const T*>(a.u), row * a.u_stride + c);
-    const float raw = ld(static_cast<const T*>(a.dt), row * a.dt_stride + c) + bias;
-    const float z = a.z != nullptr ? ld(static_cast<const T*>(a.z), row * a.z_stride + c) : 0.f;
+    const int64_t row = (sp.first + t) * (int64_t)sizeof(T);
+    const uint32_t ot = c * (uint32_t)sizeof(T), on = g * a.N * (uint32_t)sizeof(T);
+    const int64_t width = a.C * (int64_t)sizeof(T), bc = (int64_t)a.G * a.N * sizeof(T);
     float B[NPL], C[NPL];
-    load_bc<T, NPL>(static_cast<const T*>(a.Bm) + row * a.b_stride + (int64_t)g * a.N, r, a.N,
-                    whole, B);
-    load_bc<T, NPL>(static_cast<const T*>(a.Cm) + row * a.c_stride + (int64_t)g * a.N, r, a.N,
-                    whole, C);
+    const float u = to_f32(get<T>(all(a.u, row * a.u_stride, width), ot));
+    const float dt = to_f32(get<T>(all(a.dt, row * a.dt_stride, width), ot));
+    const float z = to_f32(get<T>(all(a.z, row * a.z_stride, width), ot));
+    get_row<T, NPL, WHOLE>(all(a.Bm, row * a.b_stride, bc), on, r, a.N, B);
+    get_row<T, NPL, WHOLE>(all(a.Cm, row * a.c_stride, bc), on, r, a.N, C);
+    if (t == 0 && a.ckpt != nullptr)
+      put_states<NPL>(slot_buffer<NPL>(a.ckpt, slot_of(sp, b, save_steps<NPL>(), 0), a.C),
+                      (uint32_t)(c * 4 * NPL + r * NPL) * 4u, h);
     // (log2 e goes to delta: to scale A first would wait for it before the
     // step's loads go out)
-    const float dl = delta_of(raw, a.softplus, true), du = dl * u, dl2 = kLog2e * dl;
+    const float dl = delta_of(dt + bias, a.softplus, true), du = dl * u, dl2 = kLog2e * dl;
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       h[i] = fmaf(exp2_hw(dl2 * A[i]), h[i], du * B[i]);
       acc = fmaf(C[i], h[i], acc);
     }
-    float y = fmaf(D, u, quad_sum(acc));
-    if (a.z != nullptr) y *= silu(z);
-    if (r == 0) st_row(static_cast<T*>(a.y) + row * a.C + c, y);
+    const float gate = silu(z);
+    const float y = fmaf(D, u, quad_sum(acc)) * (a.z != nullptr ? gate : 1.f);
+    put<T>(all(a.y, row * a.C, width), r == 0 ? ot : kNoLane, y);
   }
   if (a.S_T != nullptr)
     store_states<NPL>(a.S_T + ((int64_t)b * a.C + c) * a.N, a.N, r, true, h);
@@ -844,9 +868,11 @@ template <typename T, int NPL>
 hipError_t fwd(const ScanArgs& a, hipStream_t s) {
   const int ct = channel_tiles(a.C, a.G);
   if (a.T <= kMaxStep) {
-    hipLaunchKernelGGL((scan_step_kernel<T, NPL>),
-                       dim3((unsigned)(ct / a.G), a.B, a.G),
-                       dim3(kThreads), 0, s, a);
+    const dim3 grid((unsigned)(ct / a.G), a.B, a.G);
+    if (a.N == 4 * NPL && a.b_stride % 4 == 0 && a.c_stride % 4 == 0)
+      hipLaunchKernelGGL((scan_step_kernel<T, NPL, true>), grid, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((scan_step_kernel<T, NPL, false>), grid, dim3(kThreads), 0, s, a);
     return noted(s);
   }
   const dim3 grid((unsigned)(ct * a.chunks), a.B);
