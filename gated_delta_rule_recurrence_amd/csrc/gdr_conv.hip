@@ -18,78 +18,108 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows of one turn; the next turn's are loaded ahead
 
-// Input row t of the sequence: x for t >= 0 (t < len), else the window, else 0.
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> input_row(const ConvArgs& a, const Span& sp, int b, int t,
-                                                int c) {
-  if (t >= 0)
-    return load_pack<T, V>(static_cast<const T*>(a.x) + (sp.first + t) * a.x_stride + c);
-  if (a.state == nullptr) return zero_pack<T, V>();
-  return load_pack<T, V>(static_cast<const T*>(a.state) +
-                         ((int64_t)b * (a.K - 1) + (a.K - 1 + t)) * a.C + c);
+// Input row t of the sequence: x for 0 <= t < end, the window for t < 0, else
+// a row of no bytes, read as zeros.  t is the same for the whole wave; the
+// choices are between integers, which the compiler keeps in scalar registers
+// (a choice between conditions goes through vector registers, and every load
+// then becomes a loop over its lanes).
+template <typename T>
+__device__ __forceinline__ Buffer input_row(const ConvArgs& a, const Span& sp, int b, int t,
+                                            int end) {
+  constexpr int64_t kSize = sizeof(T);
+  const int row = a.C * (int)kSize;
+  const int inside = (t - end) >> 31 & row, carried = a.state != nullptr ? row : 0;
+  const char* const x = static_cast<const char*>(a.x) + (sp.first + t) * a.x_stride * kSize;
+  const char* const s =
+      static_cast<const char*>(a.state) + ((int64_t)b * (a.K - 1) + (a.K - 1 + t)) * row;
+  return buffer_of(t >= 0 ? x : s, 0, t >= 0 ? inside : carried);
 }
-
-template <int K, int V>
-__device__ __forceinline__ void load_weights(const ConvArgs& a, int c, float (&w)[V * K],
-                                             float (&bias)[V]) {
-  ld_weights<V * K, (V > 1)>(a.w, (int64_t)c * K, a.w_bf16, w);
-  if (a.bias != nullptr) {
-    ld_weights<V, (V > 1)>(a.bias, c, a.w_bf16, bias);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) bias[v] = 0.f;
-  }
+// Row t of a dense tensor of the sequence's rows, 0 <= t; no bytes from end on.
+template <typename T>
+__device__ __forceinline__ Buffer dense_row(const ConvArgs& a, const void* p, const Span& sp, int t,
+                                            int end) {
+  const int row = a.C * (int)sizeof(T);
+  return buffer_of(p, (sp.first + t) * row, (t - end) >> 31 & row);
+}
+template <typename T, int V>
+__device__ __forceinline__ void put_pack(Buffer b, uint32_t offset, const Pack<T, V>& x) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  constexpr int kBytes = V * sizeof(T);
+  if constexpr (kBytes == 2)
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, x), b.resource(),
+                                          (int)offset, 0, 0);
+  else if constexpr (kBytes == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), b.resource(),
+                                          (int)offset, 0, 0);
+  else if constexpr (kBytes == 8)
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), b.resource(), (int)offset,
+                                          0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b.resource(), (int)offset,
+                                           0, 0);
+}
+// The sequence's rows, in scalar registers.
+__device__ __forceinline__ Span uniform_span(const ConvArgs& a, int b) {
+  Span sp = span_of(a.spans, b, a.T, a.rows);
+  sp.first = __builtin_amdgcn_readfirstlane((int)sp.first);
+  sp.len = __builtin_amdgcn_readfirstlane(sp.len);
+  return sp;
 }
 
 template <typename T, int K, int V>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblocks, int steps) {
-  const int c = ((blockIdx.x % cblocks) * kThreads + threadIdx.x) * V;
-  const int tile = blockIdx.x / cblocks;
+  const int tile = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / cblocks));
+  const int c = ((int)(blockIdx.x - (uint32_t)tile * cblocks) * kThreads + (int)threadIdx.x) * V;
   const int b = blockIdx.y;
   if (c >= a.C) return;
-  const Span sp = span_of(a.spans, b, a.T, a.rows);
+  const Span sp = uniform_span(a, b);
   const int64_t t0l = (int64_t)tile * steps;
   if (t0l > 0 && t0l >= sp.len) return;
   const int t0 = (int)t0l, t1 = sp.len - t0 < steps ? sp.len : t0 + steps;
+  const uint32_t oc = (uint32_t)c * (uint32_t)sizeof(T);
 
-  float w[V * K], bias[V];  // weight[c + v][j] at v K + j
-  load_weights<K, V>(a, c, w, bias);
-  Pack<T, V> hist[K > 1 ? K - 1 : 1];
+  // all the first loads before any use: the rows before the tile, its first
+  // rows, the weights, and (the first tile) the window left behind
+  Pack<T, V> hist[K > 1 ? K - 1 : 1], next[kUnroll], left[K > 1 ? K - 1 : 1];
 #pragma unroll
-  for (int i = 0; i < K - 1; ++i) hist[i] = input_row<T, V>(a, sp, b, t0 - (K - 1) + i, c);
-
-  // the window left behind: the last K - 1 of (window, x).  The thread that
-  // read the window's channels writes them, after all its reads of it.
-  if (tile == 0 && a.state_out != nullptr) {
-    Pack<T, V> out[K > 1 ? K - 1 : 1];
+  for (int i = 0; i < K - 1; ++i)
+    hist[i] = get_pack<T, V>(input_row<T>(a, sp, b, t0 - (K - 1) + i, sp.len), oc);
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) out[i] = input_row<T, V>(a, sp, b, sp.len - (K - 1) + i, c);
-    T* const o = static_cast<T*>(a.state_out) + (int64_t)b * (K - 1) * a.C + c;
+  for (int r = 0; r < kUnroll; ++r)
+    next[r] = get_pack<T, V>(input_row<T>(a, sp, b, t0 + r, t1), oc);
+  Weights<V * K, (V > 1)> wr;
+  Weights<V, (V > 1)> br;
+  wr.load(a.w, (int64_t)c * K, (int64_t)a.C * K, a.w_bf16);
+  br.load(a.bias, c, a.C, a.w_bf16);
+  const bool leave = tile == 0 && a.state_out != nullptr;
+  if (leave)
 #pragma unroll
     for (int i = 0; i < K - 1; ++i)
-      *reinterpret_cast<Pack<T, V>*>(o + (int64_t)i * a.C) = out[i];
+      left[i] = get_pack<T, V>(input_row<T>(a, sp, b, sp.len - (K - 1) + i, sp.len), oc);
+  float w[V * K], bias[V];  // weight[c + v][j] at v K + j
+  wr.get(a.w_bf16, w);
+  br.get(a.w_bf16, bias);
+  // the last K - 1 of (window, x).  The thread that read the window's
+  // channels writes them, after all its reads of it: state_out may be state.
+  if (leave) {
+    const int64_t size = a.C * (int64_t)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i)
+      put_pack(buffer_of(a.state_out, ((int64_t)b * (K - 1) + i) * size, size), oc, left[i]);
   }
 
-  const T* xp = static_cast<const T*>(a.x) + (sp.first + t0) * a.x_stride + c;
-  T* yp = static_cast<T*>(a.y) + (sp.first + t0) * a.C + c;
-  // rows t .. t + kUnroll - 1, clamped to the tile's last one
-  auto fetch = [&](int t, Pack<T, V>(&in)[kUnroll]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int r = 0; r < kUnroll; ++r) {
-      const int at = t + r < t1 ? t + r : t1 - 1;
-      in[r] = load_pack<T, V>(xp + (int64_t)(at - t0) * a.x_stride);
-    }
-  };
   float win[K][V];  // win[K - 1]: the current input
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) unpack(hist[i], win[i]);
-  Pack<T, V> next[kUnroll];
-  if (t0 < t1) fetch(t0, next);
   for (int t = t0; t < t1; t += kUnroll) {
     Pack<T, V> in[kUnroll];
 #pragma unroll
     for (int r = 0; r < kUnroll; ++r) in[r] = next[r];
-    if (t + kUnroll < t1) fetch(t + kUnroll, next);
+    if (t + kUnroll < t1)
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r)
+        next[r] = get_pack<T, V>(input_row<T>(a, sp, b, t + kUnroll + r, t1), oc);
 #pragma unroll
     for (int r = 0; r < kUnroll; ++r) {
       unpack(in[r], win[K - 1]);
@@ -99,13 +129,16 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
         s[v] = bias[v];
 #pragma unroll
         for (int j = 0; j < K; ++j) s[v] = fmaf(w[v * K + j], win[j][v], s[v]);
-        if (a.act) s[v] = silu(s[v]);
 #pragma unroll
         for (int j = 0; j + 1 < K; ++j) win[j][v] = win[j + 1][v];
       }
-      if (t + r < t1) store_pack(yp + (int64_t)r * a.C, s);
+      if (a.act)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = silu(s[v]);
+      Pack<T, V> out;
+      pack(s, out);
+      put_pack(dense_row<T>(a, a.y, sp, t + r, t1), oc, out);
     }
-    yp += (int64_t)kUnroll * a.C;
   }
 }
 
@@ -115,13 +148,13 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
 template <typename T, int K, int V>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblocks, int steps) {
   __shared__ float red[3][K + 1][V][64];
-  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int c = ((blockIdx.x % cblocks) * 64 + lane) * V;
-  const int group = blockIdx.x / cblocks;
+  const int lane = threadIdx.x & 63, q = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / cblocks));
+  const int c = ((int)(blockIdx.x - (uint32_t)group * cblocks) * 64 + lane) * V;
   const int b = blockIdx.y;
   const bool cok = c < a.C;
   const int cc = cok ? c : 0;
-  const Span sp = span_of(a.spans, b, a.T, a.rows);
+  const Span sp = uniform_span(a, b);
   const int64_t t0l = ((int64_t)group * 4 + q) * steps;
   const bool first = t0l == 0;
   const bool any = cok && (first || t0l < sp.len);
@@ -135,31 +168,36 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
   }
   if (any) {
     const int t0 = (int)t0l, t1 = sp.len - t0 < steps ? sp.len : t0 + steps;
+    const uint32_t oc = (uint32_t)cc * (uint32_t)sizeof(T);
+    Pack<T, V> hist[K > 1 ? K - 1 : 1], nx[kUnroll], nd[kUnroll];
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i)
+      hist[i] = get_pack<T, V>(input_row<T>(a, sp, b, t0 - (K - 1) + i, sp.len), oc);
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        nx[r] = get_pack<T, V>(input_row<T>(a, sp, b, t + r, sp.len), oc);
+        nd[r] = get_pack<T, V>(dense_row<T>(a, a.dy, sp, t + r, sp.len), oc);
+      }
+    };
+    fetch(t0);
+    Weights<V * K, (V > 1)> wr;
+    Weights<V, (V > 1)> br;
+    wr.load(a.w, (int64_t)cc * K, (int64_t)a.C * K, a.w_bf16);
+    br.load(a.bias, cc, a.C, a.w_bf16);
     float w[V * K], bias[V];
-    load_weights<K, V>(a, cc, w, bias);
+    wr.get(a.w_bf16, w);
+    br.get(a.w_bf16, bias);
     float win[K][V], ds[K][V];  // the inputs and ds of the last K steps
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) unpack(input_row<T, V>(a, sp, b, t0 - (K - 1) + i, cc), win[i]);
+    for (int i = 0; i < K - 1; ++i) unpack(hist[i], win[i]);
 #pragma unroll
     for (int i = 0; i < K; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) ds[i][v] = 0.f;
-    const T* const xb = static_cast<const T*>(a.x) + sp.first * a.x_stride + cc;
-    const T* const dyb = static_cast<const T*>(a.dy) + sp.first * a.C + cc;
-    T* const dxb = static_cast<T*>(a.dx) + sp.first * a.C + cc;
     // step t forms ds_t and completes dx of step t - (K - 1); the last K - 1
     // steps only complete.  Rows from sp.len on count as ds = 0.
     const int tend = t1 + K - 1;
-    Pack<T, V> nx[kUnroll], nd[kUnroll];
-    auto fetch = [&](int t) __attribute__((always_inline)) {
-#pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        const int tt = t + r < sp.len ? t + r : sp.len - 1;  // -1: an empty sequence
-        nx[r] = tt < 0 ? zero_pack<T, V>() : load_pack<T, V>(xb + (int64_t)tt * a.x_stride);
-        nd[r] = tt < 0 ? zero_pack<T, V>() : load_pack<T, V>(dyb + (int64_t)tt * a.C);
-      }
-    };
-    fetch(t0);
     for (int t = t0; t < tend; t += kUnroll) {
       Pack<T, V> in[kUnroll], dyv[kUnroll];
 #pragma unroll
@@ -176,16 +214,17 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
         unpack(in[r], win[K - 1]);
         unpack(dyv[r], dyf);
         const bool mine = tt < t1;
+        if (a.act)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float d = dyf[v];
-          if (a.act) {
+          for (int v = 0; v < V; ++v) {
             float s = bias[v];
 #pragma unroll
             for (int j = 0; j < K; ++j) s = fmaf(w[v * K + j], win[j][v], s);
-            d *= dsilu(s, sigmoid(s));
+            dyf[v] *= dsilu(s, sigmoid(s));
           }
-          if (tt >= sp.len) d = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float d = tt < sp.len ? dyf[v] : 0.f;
 #pragma unroll
           for (int j = 0; j + 1 < K; ++j) ds[j][v] = ds[j + 1][v];
           ds[K - 1][v] = d;
@@ -202,19 +241,20 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
         }
         const int to = tt - (K - 1);  // the input whose gradient is complete
         if (to < t0 && !first) continue;
+        const int64_t size = a.C * (int64_t)sizeof(T);
         if (a.dstate_out != nullptr && to >= sp.len - (K - 1)) {
           float e[V];
-          unpack(load_pack<T, V>(static_cast<const T*>(a.dstate_out) +
-                                 ((int64_t)b * (K - 1) + (to - (sp.len - (K - 1)))) * a.C + cc),
-                 e);
+          const int64_t i = (int64_t)b * (K - 1) + (to - (sp.len - (K - 1)));
+          unpack(get_pack<T, V>(buffer_of(a.dstate_out, i * size, size), oc), e);
 #pragma unroll
           for (int v = 0; v < V; ++v) out[v] += e[v];
         }
+        Pack<T, V> o;
+        pack(out, o);
         if (to >= 0)
-          store_pack(dxb + (int64_t)to * a.C, out);
+          put_pack(dense_row<T>(a, a.dx, sp, to, sp.len), oc, o);
         else if (a.dstate != nullptr)
-          store_pack(static_cast<T*>(a.dstate) + ((int64_t)b * (K - 1) + (K - 1 + to)) * a.C + cc,
-                     out);
+          put_pack(buffer_of(a.dstate, ((int64_t)b * (K - 1) + (K - 1 + to)) * size, size), oc, o);
       }
     }
   }

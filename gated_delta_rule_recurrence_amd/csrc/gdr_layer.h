@@ -235,65 +235,104 @@ __device__ __forceinline__ void unpack(const Pack<bf16, 4>& p, float (&f)[4]) {
   f[2] = __uint_as_float(p.v.y << 16);
   f[3] = __uint_as_float(p.v.y & 0xffff0000u);
 }
-// Stores V floats, each rounded to nearest even.
-__device__ __forceinline__ void store_pack(float* p, const float (&f)[1]) { *p = f[0]; }
-__device__ __forceinline__ void store_pack(bf16* p, const float (&f)[1]) {
-  *p = from_f32<bf16>(f[0]);
+// V floats, each rounded to nearest even.
+__device__ __forceinline__ void pack(const float (&f)[1], Pack<float, 1>& p) { p.v[0] = f[0]; }
+__device__ __forceinline__ void pack(const float (&f)[1], Pack<bf16, 1>& p) {
+  p.v[0].bits = static_cast<uint16_t>(cvt_pk_bf16(f[0], f[0]));
 }
-__device__ __forceinline__ void store_pack(float* p, const float (&f)[4]) {
-  *reinterpret_cast<float4*>(p) = float4{f[0], f[1], f[2], f[3]};
+__device__ __forceinline__ void pack(const float (&f)[4], Pack<float, 4>& p) {
+  p.v = float4{f[0], f[1], f[2], f[3]};
 }
-__device__ __forceinline__ void store_pack(bf16* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) = uint4{cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3]),
-                                       cvt_pk_bf16(f[4], f[5]), cvt_pk_bf16(f[6], f[7])};
+__device__ __forceinline__ void pack(const float (&f)[4], Pack<bf16, 4>& p) {
+  p.v = uint2{cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3])};
+}
+__device__ __forceinline__ void pack(const float (&f)[8], Pack<bf16, 8>& p) {
+  p.v = uint4{cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3]), cvt_pk_bf16(f[4], f[5]),
+              cvt_pk_bf16(f[6], f[7])};
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* p, const float (&f)[V]) {
+  Pack<T, V> x;
+  pack(f, x);
+  *reinterpret_cast<Pack<T, V>*>(p) = x;
 }
 
-__device__ __forceinline__ void store_pack(bf16* p, const float (&f)[4]) {
-  *reinterpret_cast<uint2*>(p) = uint2{cvt_pk_bf16(f[0], f[1]), cvt_pk_bf16(f[2], f[3])};
+// A buffer resource: a base that the whole wave shares, 32 bits of offset per
+// lane, and a bound past which loads give zero and stores are dropped.  An
+// absent tensor is a buffer of no bytes, read without a branch.
+struct Buffer {
+  const char* p;
+  uint32_t bytes;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource() const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, (int)bytes, 0x00020000);
+  }
+};
+__device__ __forceinline__ Buffer buffer_of(const void* p, int64_t offset, int64_t bytes) {
+  return Buffer{static_cast<const char*>(p) + offset, (uint32_t)bytes};
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> get_pack(Buffer b, uint32_t offset) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  constexpr int kBytes = V * sizeof(T);
+  if constexpr (kBytes == 2)
+    return __builtin_bit_cast(
+        Pack<T, V>, __builtin_amdgcn_raw_buffer_load_b16(b.resource(), (int)offset, 0, 0));
+  else if constexpr (kBytes == 4)
+    return __builtin_bit_cast(
+        Pack<T, V>, __builtin_amdgcn_raw_buffer_load_b32(b.resource(), (int)offset, 0, 0));
+  else if constexpr (kBytes == 8)
+    return __builtin_bit_cast(
+        Pack<T, V>,
+        (u32x2)__builtin_amdgcn_raw_buffer_load_b64(b.resource(), (int)offset, 0, 0));
+  else
+    return __builtin_bit_cast(
+        Pack<T, V>,
+        (u32x4)__builtin_amdgcn_raw_buffer_load_b128(b.resource(), (int)offset, 0, 0));
 }
 
-// One row element, rounded to nearest even.
-__device__ __forceinline__ void st_row(float* p, float x) { *p = x; }
-__device__ __forceinline__ void st_row(bf16* p, float x) {
-  p->bits = static_cast<uint16_t>(cvt_pk_bf16(x, x));
-}
-
-// A weight element of either type (loaded once per thread, so the branch is
-// of no account).
-__device__ __forceinline__ float ld_weight(const void* p, int64_t i, int is_bf16) {
-  return is_bf16 ? to_f32(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-// N consecutive weights from element i on; N elements of the row type's
-// vectors start on a 16-byte boundary when VEC (i a multiple of a vector).
+// N consecutive weights of either type from element `first` of a tensor of
+// `count`, loaded raw without a branch (what the type does not ask for lies
+// past the end and costs no memory; a null tensor gives zeros) and converted
+// at use.  VEC: `first` and N are multiples of four.
 template <int N, bool VEC>
-__device__ __forceinline__ void ld_weights(const void* p, int64_t i, int is_bf16, float (&w)[N]) {
-  if constexpr (VEC && N % 8 == 0) {
-    if (is_bf16) {
+struct Weights {
+  static constexpr uint32_t kPastEnd = 0xf0000000u;  // weights end below 2^26
+  static constexpr int kUnit = VEC ? (N % 8 == 0 ? 8 : 4) : 1;
+  static constexpr int kUnits = N / kUnit;
+  Pack<bf16, kUnit> lo[kUnits];             // bf16; for units of eight also the
+  Pack<float, VEC ? 4 : 1> hi[kUnits];      // first half of the floats in hi
+
+  __device__ __forceinline__ void load(const void* p, int64_t first, int64_t count, int is_bf16) {
+    const uint32_t size = is_bf16 ? 2 : 4;
+    const Buffer b = buffer_of(p, 0, p != nullptr ? count * size : 0);
+    const uint32_t at = (uint32_t)first * size;
 #pragma unroll
-      for (int k = 0; k < N / 8; ++k) {
-        float f[8];
-        unpack(load_pack<bf16, 8>(static_cast<const bf16*>(p) + i + 8 * k), f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[8 * k + e] = f[e];
-      }
-      return;
+    for (int k = 0; k < kUnits; ++k) {
+      const uint32_t o = at + size * kUnit * k;
+      lo[k] = get_pack<bf16, kUnit>(b, kUnit == 8 || is_bf16 ? o : kPastEnd);
+      hi[k] = get_pack<float, VEC ? 4 : 1>(b, is_bf16 ? kPastEnd : o + (kUnit == 8 ? 16 : 0));
     }
   }
-  if constexpr (VEC && N % 4 == 0) {
-    if (!is_bf16) {
+  __device__ __forceinline__ void get(int is_bf16, float (&w)[N]) const {
 #pragma unroll
-      for (int k = 0; k < N / 4; ++k) {
-        float f[4];
-        unpack(load_pack<float, 4>(static_cast<const float*>(p) + i + 4 * k), f);
+    for (int k = 0; k < kUnits; ++k) {
+      float f[kUnit], g[VEC ? 4 : 1];
+      unpack(lo[k], f);
+      unpack(hi[k], g);
+      if constexpr (kUnit == 8) {
+        const float4 first = __builtin_bit_cast(float4, lo[k]);
+        const float half[4] = {first.x, first.y, first.z, first.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * k + e] = f[e];
+        for (int e = 0; e < 8; ++e)
+          w[8 * k + e] = is_bf16 ? f[e] : (e < 4 ? half[e & 3] : g[e & 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) w[kUnit * k + e] = is_bf16 ? f[e] : g[e];
       }
-      return;
     }
   }
-#pragma unroll
-  for (int k = 0; k < N; ++k) w[k] = ld_weight(p, i + k, is_bf16);
-}
+};
 __device__ __forceinline__ void st_weight(void* p, int64_t i, float x, int is_bf16) {
   if (is_bf16)
     static_cast<bf16*>(p)[i] = from_f32<bf16>(x);

@@ -54,18 +54,25 @@ struct Norm {
 
   static __device__ __forceinline__ void weights(const NormArgs& a, int lane, int g,
                                                  float (&w)[NV][V], float (&b)[NV][V]) {
-    const int64_t base = a.shared ? 0 : (int64_t)g * a.D;
+    const int64_t base = a.shared ? 0 : (int64_t)g * a.D, count = a.shared ? a.D : a.C;
+    Weights<V, (V > 1)> wr[NV], br[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int d = at(lane, i);
+      // (a group is whole vectors)
+      const int64_t first = at(lane, i) < a.D ? base + at(lane, i) : count;
+      wr[i].load(a.w, first, count, a.w_bf16);
+      br[i].load(a.bias, first, count, a.w_bf16);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      wr[i].get(a.w_bf16, w[i]);
+      br[i].get(a.w_bf16, b[i]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        w[i][v] = d < a.D ? 1.f : 0.f;
-        b[i][v] = 0.f;
+        const bool in = at(lane, i) + v < a.D;
+        w[i][v] = in ? (a.w != nullptr ? w[i][v] : 1.f) : 0.f;
+        b[i][v] = in ? b[i][v] : 0.f;
       }
-      if (d >= a.D) continue;  // (a group is whole vectors)
-      if (a.w != nullptr) ld_weights<V, (V > 1)>(a.w, base + d, a.w_bf16, w[i]);
-      if (a.bias != nullptr) ld_weights<V, (V > 1)>(a.bias, base + d, a.w_bf16, b[i]);
     }
   }
   // A group's channels of one tensor (zeros past the group's end).
