@@ -325,6 +325,29 @@ __device__ __forceinline__ void load_rates(const ScanArgs& a, const Place& p, fl
   for (int i = 0; i < NPL; ++i) A[i] *= kLog2e;
 }
 
+// A sequence of several chunks keeps a copy of the state it starts from (the
+// backward: of the adjoint it starts from) in the slot that no chunk's end
+// uses, the last (the first), written by the first pass: the main pass then
+// reads neither S0 nor dS_T while other workgroups of it write S_T or dS0,
+// which may be the same memory.
+template <int NPL>
+__device__ __forceinline__ void start_states(const ScanArgs& a, const Place& p, const float* given,
+                                             int slot, uint32_t oh, float (&h)[NPL]) {
+  if (p.last > 0 && given != nullptr)
+    get_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, slot), a.C), oh, h);
+  else
+    load_states<NPL>(given + ((int64_t)p.b * a.C + p.c) * a.N, a.N, p.r,
+                     p.cok && given != nullptr, h);
+}
+template <int NPL>
+__device__ __forceinline__ void copy_start(const ScanArgs& a, const Place& p, const float* given,
+                                           int slot, uint32_t oh) {
+  if (given == nullptr) return;
+  float h[NPL];
+  load_states<NPL>(given + ((int64_t)p.b * a.C + p.c) * a.N, a.N, p.r, p.cok, h);
+  put_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, slot), a.C), oh, h);
+}
+
 // The state before chunk j (FWD), or the adjoint behind it: the chunks' local
 // ones joined in the order of the recurrence, h <- exp(A dsum) h + edge, eight
 // chunks' loads in flight (four with more than 4 states a lane).  Every
@@ -365,25 +388,30 @@ __device__ __forceinline__ void join_chunks(const ScanArgs& a, const Place& p, u
 // EDGE: the first pass (end state of every chunk but the last from a zero
 // start); else the pass that writes y.
 template <typename T, int NPL, bool EDGE>
-__global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
+__global__ __launch_bounds__(kThreads)
+SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
   constexpr int TT = tile_steps<NPL>(), HT = save_steps<NPL>();
   using L = Tile<T, NPL, TT, true, !EDGE, false>;
   constexpr int Q = L::Q, NP = L::NP;
   __shared__ __align__(16) float Bs[2][TT * NP], Cs[2][EDGE ? 4 : TT * NP];
   const Place p = place_of(a, ctiles);
-  if (EDGE ? p.j >= p.last : p.j > p.last) return;
+  if (p.j > p.last) return;
   const int r = p.r;
+  // this lane's states in a slot
+  const uint32_t oh = p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane;
+  if (EDGE && p.j == p.last) {
+    if (p.last > 0) copy_start<NPL>(a, p, a.S0, p.last, oh);
+    return;
+  }
   float A[NPL], h[NPL];
   load_rates<NPL>(a, p, A);
   const float bias = a.dt_bias != nullptr ? a.dt_bias[p.c] : 0.f;
   const float D = a.D != nullptr ? a.D[p.c] : 0.f;
-  // this lane's states in a slot
-  const uint32_t oh = p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane;
   if (EDGE) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = 0.f;
   } else {
-    load_states<NPL>(a.S0 + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r, p.cok && a.S0 != nullptr, h);
+    start_states<NPL>(a, p, a.S0, p.last, oh, h);
     join_chunks<true, NPL>(a, p, oh, A, h);
   }
   float sum = 0.f;
@@ -555,14 +583,20 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
 // The adjoint's first pass: E before the chunk (a_1 E_1 of its first step)
 // from a zero E behind it, for every chunk but the first.
 template <typename T, int NPL>
-__global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
+__global__ __launch_bounds__(kThreads)
+SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
   constexpr int TT = tile_steps<NPL>();
   using L = Tile<T, NPL, TT, false, true, true>;
   constexpr int Q = L::Q, NP = L::NP;
   __shared__ __align__(16) float Cs[2][TT * NP];
   const Place p = place_of(a, ctiles);
-  if (p.j == 0 || p.j > p.last) return;
+  if (p.j > p.last) return;
   const int r = p.r;
+  const uint32_t oh = p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane;
+  if (p.j == 0) {
+    if (p.last > 0) copy_start<NPL>(a, p, a.dS_T, 0, oh);
+    return;
+  }
   float A[NPL], E[NPL];
   load_rates<NPL>(a, p, A);
 #pragma unroll
@@ -604,8 +638,7 @@ __global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_
     }
   }
   const int64_t slot = slot_of(p.sp, p.b, a.chunk, p.j);
-  put_states<NPL>(slot_buffer<NPL>(a.edge, slot, a.C),
-                  p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane, E);
+  put_states<NPL>(slot_buffer<NPL>(a.edge, slot, a.C), oh, E);
   sum = quad_sum(sum);
   if (r == 0 && p.cok) a.dsum[slot * a.C + p.c] = sum;
 }
@@ -616,8 +649,8 @@ __global__ __launch_bounds__(kThreads) SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_
 // waves' parts of dB, dC sit in two buffers in turn, and a tile's parts are
 // summed behind the next tile's barrier.
 template <typename T, int NPL>
-__global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void scan_bwd_kernel(ScanArgs a,
-                                                                               int ctiles) {
+__global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void scan_bwd_kernel(
+    ScanArgs a, int ctiles) {
   constexpr int TT = save_steps<NPL>();
   using L = Tile<T, NPL, TT, true, true, true>;
   constexpr int NP = L::NP, Q = L::Q;
@@ -634,8 +667,7 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
     load_rates<NPL>(a, p, A);
     const float bias = a.dt_bias != nullptr ? a.dt_bias[p.c] : 0.f;
     const float D = a.D != nullptr ? a.D[p.c] : 0.f;
-    load_states<NPL>(a.dS_T + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r,
-                     p.cok && a.dS_T != nullptr, E);
+    start_states<NPL>(a, p, a.dS_T, 0, oh, E);
     join_chunks<false, NPL>(a, p, oh, A, E);
     const int tiles = (p.end - p.begin + TT - 1) / TT;
     int left = p.end - p.begin - (tiles - 1) * TT;  // steps of the tile at hand

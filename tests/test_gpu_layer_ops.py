@@ -517,6 +517,30 @@ def test_states_in_place(cuda):
     assert torch.equal(y0, mine)
 
 
+def test_split_scan_in_place(cuda):
+    """S_T = S0 where many workgroups share a sequence's chunks, more than the
+    device holds at once: packed sequences of many chunks, one and none."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    g = torch.Generator(device=cuda).manual_seed(5)
+    C, N, rows = 4096, 16, 6144
+    spans = torch.tensor([[0, 4000], [4000, 4000], [4000, 4020], [4020, rows]], dtype=torch.int32,
+                         device=cuda)
+
+    def rand(*shape):
+        return torch.randn(*shape, device=cuda, generator=g)
+
+    u, dt = rand(rows, C).bfloat16(), rand(rows, C).bfloat16()
+    A, S0 = -torch.exp(rand(C, N)), rand(4, C, N)
+    Bm, Cm = rand(rows, 1, N).bfloat16(), rand(rows, 1, N).bfloat16()
+    y0, S_T, _ = ops.gdr_scan_forward(u, dt, A, Bm, Cm, S0=S0, spans=spans, T=4000, save=False)
+    for _ in range(4):
+        mine = S0.clone()
+        y1, _, _ = ops.gdr_scan_forward(u, dt, A, Bm, Cm, S0=mine, spans=spans, T=4000, save=False,
+                                        S_T=mine)
+        assert torch.equal(y0, y1) and torch.equal(S_T, mine)
+
+
 def test_spans_are_cut_to_the_rows(cuda):
     """Spans outside 0 .. rows, and longer than T."""
     import torch
