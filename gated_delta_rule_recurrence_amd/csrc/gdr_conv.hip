@@ -311,7 +311,7 @@ hipError_t fwd(const ConvArgs& a, hipStream_t s) {
   int64_t steps = waves * a.T / 2048;
   steps = steps < 16 ? 16 : (steps > 32 ? 32 : steps);
   int64_t tiles = (a.T + steps - 1) / steps;
-  while (tiles * cblocks > INT32_MAX) {
+  while (tiles * cblocks > kMaxGrid) {
     steps *= 2;
     tiles = (a.T + steps - 1) / steps;
   }
@@ -374,7 +374,7 @@ int conv_bwd_steps(int64_t B, int64_t T, int64_t C) {
   int64_t steps = waves * T / 32 >= 4096 ? 32 : 16;
   // the grid's x dimension holds (tiles / 4) x (channel blocks, at most one
   // per 64 channels)
-  while ((T + 4 * steps - 1) / (4 * steps) * ((C + 63) / 64) > INT32_MAX) steps *= 2;
+  while ((T + 4 * steps - 1) / (4 * steps) * ((C + 63) / 64) > kMaxGrid) steps *= 2;
   return (int)steps;
 }
 

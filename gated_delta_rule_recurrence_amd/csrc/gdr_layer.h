@@ -103,8 +103,7 @@ struct ScanArgs {
   void* dz;
   float* ddt_bias;
   float* dS0;           // or null
-  float* pA;            // [B * chunks][C][Np] partial dA
-  float* pD;            // [B * chunks][2][C] partial dD, ddt_bias
+  float* pA;            // [B * chunks]: partial dA [C][Np], dD [C], ddt_bias [C]
   float* pB;            // [2][channel tiles][rows][G][N] partial dB, dC
 };
 // Padded states per channel, steps between saved states, channels of one
@@ -117,6 +116,10 @@ int scan_channels();
 int64_t scan_chunk(const ScanArgs& a, int64_t stride, bool bwd);
 hipError_t launch_scan_fwd(const ScanArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs& a, bool bf16, hipStream_t s);
+
+// Workgroups of 256 along a grid's x dimension, whose threads have to stay
+// below 2^32.
+constexpr int64_t kMaxGrid = (INT64_C(1) << 24) - 1;
 
 // ---- device helpers ---------------------------------------------------------
 

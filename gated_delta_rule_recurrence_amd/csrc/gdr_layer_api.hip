@@ -14,7 +14,7 @@ constexpr int64_t kMaxChannels = INT64_C(1) << 20;
 constexpr int64_t kMaxRows = INT32_MAX / 2;  // rows and steps; twice it still is an int
 constexpr int64_t kMaxStride = INT32_MAX;
 constexpr int64_t kMaxScanStride = INT64_C(1) << 25;  // 16 rows of 4 bytes in 32 bits
-constexpr int64_t kMaxBatch = 65535;         // sequences index grid y, groups z
+constexpr int64_t kMaxBatch = 65535;  // sequences index grid y, groups z
 constexpr int64_t kMaxIndex = INT64_C(1) << 61;
 
 int64_t round_up256(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -82,10 +82,6 @@ int check(const gdr_scan_shape* in, gdr_scan_shape* s) {
       !stride_ok(&s->z_stride, s->C, most) || !stride_ok(&s->b_stride, s->G * s->N, most) ||
       !stride_ok(&s->c_stride, s->G * s->N, most))
     return GDR_ERR_BAD_STRIDE;
-  // the grids: channel tiles x chunks, and T x G x N threads
-  const int64_t tiles = s->G * ((s->C / s->G + 63) / 64);
-  if (tiles * (s->T / 16 + 1) > INT32_MAX || s->T * (s->G * s->N) / 256 + 1 > INT32_MAX)
-    return GDR_ERR_OVERFLOW;
   return GDR_OK;
 }
 
@@ -126,6 +122,8 @@ int scan_sizes(const gdr_scan_shape& s, bool bwd, ScanSizes* z) {
   a.rows = s.rows;
   z->chunk = gdr::scan_chunk(a, stride, bwd);
   z->chunks = s.T > 0 ? (s.T + z->chunk - 1) / z->chunk : 1;
+  const int64_t tiles = (s.C / s.G + gdr::scan_channels() - 1) / gdr::scan_channels();
+  if (s.G * tiles * z->chunks > gdr::kMaxGrid) return GDR_ERR_OVERFLOW;
   int64_t state, x;
   if (!product_ok(s.C, np * 4, &state) || !product_ok(state, s.rows / tile + s.B + 1, &z->ckpt))
     return GDR_ERR_OVERFLOW;
@@ -143,7 +141,6 @@ int scan_sizes(const gdr_scan_shape& s, bool bwd, ScanSizes* z) {
     if (!product_ok(s.C * (np + 2) * 4, s.B * z->chunks, &x)) return GDR_ERR_OVERFLOW;
     z->bytes += round_up256(x);
     z->bc = z->bytes;
-    const int64_t tiles = (s.C / s.G + gdr::scan_channels() - 1) / gdr::scan_channels();
     if (!product_ok(s.rows * 8, s.G * s.N * tiles, &x)) return GDR_ERR_OVERFLOW;
     z->bytes += round_up256(x);
   }

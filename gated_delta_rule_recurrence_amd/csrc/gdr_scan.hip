@@ -322,7 +322,12 @@ template <int NPL>
 __device__ __forceinline__ void load_rates(const ScanArgs& a, const Place& p, float (&A)[NPL]) {
   load_states<NPL>(a.A + (int64_t)p.c * a.N, a.N, p.r, p.cok, A);
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) A[i] *= kLog2e;
+  for (int i = 0; i < NPL; ++i) {
+    A[i] *= kLog2e;
+    // an infinite rate becomes the largest one: a step past the sequence's
+    // end has delta = 0, and its decay has to be 1
+    A[i] = __builtin_isinf(A[i]) ? __builtin_copysignf(3.402823466e38f, A[i]) : A[i];
+  }
 }
 
 // A sequence of several chunks keeps a copy of the state it starts from (the
@@ -863,18 +868,20 @@ __global__ __launch_bounds__(kThreads) void scan_sums(ScanArgs a, SumGrid g) {
     return;
   }
   const Span sp = span_of(a.spans, blockIdx.y, a.T, a.rows);
-  const int64_t w = (int64_t)a.G * a.N;
-  const int64_t i = (int64_t)(blockIdx.x - g.ca) * kThreads + threadIdx.x;
-  if (i >= w * sp.len) return;
-  const int64_t at = sp.first * w + i, all = a.rows * w;
-  float sb = 0.f, sc = 0.f;
+  const int64_t w = (int64_t)a.G * a.N, all = a.rows * w;
+  const int64_t turn = (int64_t)(gridDim.x - g.ca) * kThreads;
+  for (int64_t i = (int64_t)(blockIdx.x - g.ca) * kThreads + threadIdx.x; i < w * sp.len;
+       i += turn) {
+    const int64_t at = sp.first * w + i;
+    float sb = 0.f, sc = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < g.tpg; ++k) {
-    sb += a.pB[k * all + at];
-    sc += a.pB[(g.tpg + k) * all + at];
+    for (int k = 0; k < g.tpg; ++k) {
+      sb += a.pB[k * all + at];
+      sc += a.pB[(g.tpg + k) * all + at];
+    }
+    st(static_cast<T*>(a.dB), at, sb);
+    st(static_cast<T*>(a.dC), at, sc);
   }
-  st(static_cast<T*>(a.dB), at, sb);
-  st(static_cast<T*>(a.dC), at, sc);
 }
 
 hipError_t noted(hipStream_t s) {
@@ -921,7 +928,8 @@ hipError_t bwd(const ScanArgs& a, hipStream_t s) {
   if ((e = noted(s)) != hipSuccess) return e;
   const int64_t columns = (int64_t)a.C * (np + 2), values = (int64_t)a.T * a.G * a.N;
   const SumGrid g{(int)((columns + kSumCols - 1) / kSumCols), ct / a.G, a.B * a.chunks, np};
-  const int64_t blocks = g.ca + (values + kThreads - 1) / kThreads;
+  int64_t blocks = g.ca + (values + kThreads - 1) / kThreads;
+  if (blocks > kMaxGrid) blocks = kMaxGrid;  // (ca is at most 2^20 66 / 16)
   hipLaunchKernelGGL((scan_sums<T>), dim3((unsigned)blocks, a.B), dim3(kThreads), 0, s, a, g);
   return noted(s);
 }

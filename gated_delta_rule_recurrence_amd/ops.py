@@ -355,6 +355,13 @@ def _launch(name, shape, tensors, device, workspace=None, nbytes=None):
         _lib.check(status, name)
 
 
+def _gradient(t):
+    """An incoming gradient as the library takes it: dense and on a 16-byte
+    boundary (a dense view into the middle of another gradient may not be)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 # The C structure of a call's sizes and the bytes of its buffers: they follow
 # from the sizes alone, so that calls of the same sizes share them.
 
@@ -577,6 +584,11 @@ def gdr_norm_backward(x, weight, bias, z, stats, dy, *, groups, center=False, ac
     return dx, dweight, dbias, dz
 
 
+def _wanted(args):
+    """Whether a gradient of any of them will be asked for."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args)
+
+
 class CausalConv(torch.autograd.Function):
     """y, state_out = causal_conv(x, weight, bias, state) with the library VJP."""
 
@@ -593,8 +605,8 @@ class CausalConv(torch.autograd.Function):
         x, weight, bias, state, spans = ctx.saved_tensors
         act, T = ctx.settings
         dx, dw, db, ds = gdr_conv_backward(
-            x, weight, bias, state, dy.contiguous(), dstate_out.contiguous(), act=act, spans=spans,
-            T=T, want_dstate=state is not None)
+            x, weight, bias, state, _gradient(dy), _gradient(dstate_out), act=act, spans=spans, T=T,
+            want_dstate=state is not None)
         return dx, dw, db, ds, None, None, None
 
 
@@ -611,14 +623,15 @@ class SelectiveScan(torch.autograd.Function):
         y, S_T, ctx.saved = gdr_scan_forward(u, dt, A, Bm, Cm, D, z, dt_bias, S0,
                                              softplus=softplus, spans=spans, T=T, save=save)
         ctx.has_S0 = S0 is not None
-        ctx.save_for_backward(u, dt, A, Bm, Cm, D, z, dt_bias)
+        # (spans too, so that a change of theirs in between is noticed)
+        ctx.save_for_backward(u, dt, A, Bm, Cm, D, z, dt_bias, spans)
         return y, S_T
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dS_T):
-        grads = gdr_scan_backward(*ctx.saved_tensors, ctx.saved, dy.contiguous(),
-                                  dS_T.contiguous(), want_dS0=ctx.has_S0)
+        grads = gdr_scan_backward(*ctx.saved_tensors[:8], ctx.saved, _gradient(dy),
+                                  _gradient(dS_T), want_dS0=ctx.has_S0)
         return (*grads, None, None, None, None)
 
 
@@ -627,17 +640,16 @@ def selective_scan(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *, s
     """Autograd-enabled selective state space scan: returns (y, S_T).  The
     states for the backward are saved only where a gradient is wanted."""
     args = (u, dt, A, Bm, Cm, D, z, dt_bias, S0)
-    save = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args)
-    return SelectiveScan.apply(*args, softplus, spans, T, save)
+    return SelectiveScan.apply(*args, softplus, spans, T, _wanted(args))
 
 
 class GroupNorm(torch.autograd.Function):
     """y = group_norm(x, weight, bias, z) with the library VJP."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, z, groups, eps, center, act):
+    def forward(ctx, x, weight, bias, z, groups, eps, center, act, save):
         y, stats = gdr_norm_forward(x, weight, bias, z, groups=groups, eps=eps, center=center,
-                                    act=act)
+                                    act=act, save=save)
         ctx.settings = dict(groups=groups, center=center, act=act)
         ctx.save_for_backward(x, weight, bias, z, stats)
         return y
@@ -645,11 +657,12 @@ class GroupNorm(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        dx, dw, db, dz = gdr_norm_backward(*ctx.saved_tensors, dy.contiguous(), **ctx.settings)
-        return dx, dw, db, dz, None, None, None, None
+        dx, dw, db, dz = gdr_norm_backward(*ctx.saved_tensors, _gradient(dy), **ctx.settings)
+        return dx, dw, db, dz, None, None, None, None, None
 
 
 def group_norm(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, center=False, act="silu"):
     """Autograd-enabled group norm of the last dimension (see
     gdr_norm_forward): returns y."""
-    return GroupNorm.apply(x, weight, bias, z, groups, eps, center, act)
+    return GroupNorm.apply(x, weight, bias, z, groups, eps, center, act,
+                           _wanted((x, weight, bias, z)))

@@ -563,6 +563,100 @@ def test_spans_are_cut_to_the_rows(cuda):
     assert same(*got)
 
 
+def test_a_longest_length_far_above_the_rows(cuda):
+    """T is a bound: grids that follow it are cut to what a launch takes."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    s = small_state(cuda)
+    spans = torch.tensor([[0, 80], [100, 290]], dtype=torch.int32, device=cuda)
+
+    def rows(t):
+        return t.reshape(300, *t.shape[2:])[..., :8].contiguous()
+
+    x, w, b, st = s["conv"]
+    x, dy, w, b, st = rows(x), rows(s["dy"]), w[:8].contiguous(), b[:8].contiguous(), st[..., :8].contiguous()
+    u, dt, A, Bm, Cm, D, z, bias, S0 = s["scan"]
+    u, dt, z, A, D, bias, S0 = (rows(u), rows(dt), rows(z), A[:8].contiguous(), D[:8].contiguous(),
+                                bias[:8].contiguous(), S0[:, :8].contiguous())
+    Bm, Cm = Bm.reshape(300, *Bm.shape[2:])[:, :1].contiguous(), Cm.reshape(300, *Cm.shape[2:])[:, :1].contiguous()
+    args = u, dt, A, Bm, Cm, D, z, bias
+    got = []
+    for T in (190, 2 ** 30 - 1):
+        out = [*ops.gdr_conv_forward(x, w, b, st, spans=spans, T=T)]
+        out += ops.gdr_conv_backward(x, w, b, st, dy, spans=spans, T=T, want_dstate=True)
+        y, S_T, saved = ops.gdr_scan_forward(*args, S0, spans=spans, T=T)
+        out += [y, S_T, *ops.gdr_scan_backward(*args, saved, dy)]
+        got.append(out)
+    # Other tiles and chunks, so other orders of the same sums: each side within
+    # 128 + 4 * 190 + 300 < 1200 roundings of 2^-24 of the sum of magnitudes, taken as
+    # at most 7 times the largest value of the tensor (1e-3 = 2400 * 7 * 2^-24), and a
+    # rounded bf16 within a whole step, 2^-7.
+    for a, b in zip(*got):
+        a, b = a.float(), b.float()
+        assert ((a - b).abs() <= 2.0 ** -7 * a.abs() + 1e-3 * a.abs().max()).all()
+
+
+def test_infinite_rates(cuda):
+    """A = -inf forgets at every step, and is no matter behind a sequence's
+    last step, whatever the tiles and chunks."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    for T in (1, 3, 21, 150):
+        u, dt, A, Bm, Cm, D, z, bias, S0 = small_state(cuda)["scan"]
+        rows = [t[:, :T].contiguous() for t in (u, dt, Bm, Cm, z)]
+        got = []
+        for rate in (-float("inf"), -1e30):
+            A = A.clone()
+            A[::3] = rate
+            y, S_T, _ = ops.gdr_scan_forward(rows[0], rows[1], A, rows[2], rows[3], D, rows[4], bias, S0)
+            assert torch.isfinite(y).all() and torch.isfinite(S_T).all()
+            got.append((y, S_T))
+        assert same(*got), T
+
+
+def test_gradients_that_arrive_as_views(cuda):
+    """Dense views that start off a 16-byte boundary, and sums' broadcasts."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    g = torch.Generator(device=cuda).manual_seed(11)
+
+    def rand(*shape):
+        return torch.randn(*shape, device=cuda, generator=g)
+
+    x, w, A = rand(1, 7, 5), rand(5, 4), -torch.exp(rand(5, 3))
+    Bm = rand(1, 7, 1, 3)
+    dy = rand(1, 1 + 7 * 5)
+    view = dy[:, 1:].view(1, 7, 5)
+    assert view.is_contiguous() and view.data_ptr() % 16
+    for f in (lambda t: ops.causal_conv(t, w)[0], lambda t: ops.selective_scan(t, t, A, Bm, Bm)[0],
+              lambda t: ops.group_norm(t, groups=5, center=False)):
+        got = []
+        for d in (view, view.clone()):
+            t = x.clone().requires_grad_()
+            f(t).backward(d)
+            got.append((t.grad,))
+        assert same(*got)
+        t, r = x.clone().requires_grad_(), x.clone().requires_grad_()
+        f(t).sum().backward()
+        f(r).backward(torch.ones_like(x))
+        assert torch.equal(t.grad, r.grad)
+
+
+def test_spans_changed_before_the_backward(cuda):
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    x = torch.randn(12, 8, device=cuda, requires_grad=True)
+    A, Bm = -torch.ones(8, 4, device=cuda), torch.randn(12, 1, 4, device=cuda)
+    spans = torch.tensor([[0, 12]], dtype=torch.int32, device=cuda)
+    for f in (lambda: ops.causal_conv(x, torch.ones(8, 4, device=cuda), spans=spans)[0],
+              lambda: ops.selective_scan(x, x, A, Bm, Bm, spans=spans)[0]):
+        y = f()
+        spans[0, 1] = 9
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+        spans[0, 1] = 12
+
+
 def test_no_rows_and_no_sequences(cuda):
     import torch
     from gated_delta_rule_recurrence_amd import ops
