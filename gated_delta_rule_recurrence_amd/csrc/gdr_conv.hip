@@ -34,12 +34,22 @@ __device__ __forceinline__ Buffer input_row(const ConvArgs& a, const Span& sp, i
       static_cast<const char*>(a.state) + ((int64_t)b * (a.K - 1) + (a.K - 1 + t)) * row;
   return buffer_of(t >= 0 ? x : s, 0, t >= 0 ? inside : carried);
 }
-// Row t of a dense tensor of the sequence's rows, 0 <= t; no bytes from end on.
+// A walk over rows: row r from here on, of no bytes unless r < left.
+struct Rows {
+  const char* p;
+  int64_t step;  // bytes from row to row
+  int row;       // bytes of one
+  __device__ __forceinline__ Buffer at(int r, int left) const {
+    return buffer_of(p, r * step, (r - left) >> 31 & row);
+  }
+  __device__ __forceinline__ void advance(int rows) { p += rows * step; }
+};
+// From row t of the sequence, in x or in a dense tensor
 template <typename T>
-__device__ __forceinline__ Buffer dense_row(const ConvArgs& a, const void* p, const Span& sp, int t,
-                                            int end) {
-  const int row = a.C * (int)sizeof(T);
-  return buffer_of(p, (sp.first + t) * row, (t - end) >> 31 & row);
+__device__ __forceinline__ Rows rows_of(const ConvArgs& a, const void* p, int64_t stride,
+                                        const Span& sp, int t) {
+  const int64_t step = stride * (int64_t)sizeof(T);
+  return Rows{static_cast<const char*>(p) + (sp.first + t) * step, step, a.C * (int)sizeof(T)};
 }
 template <typename T, int V>
 __device__ __forceinline__ void put_pack(Buffer b, uint32_t offset, const Pack<T, V>& x) {
@@ -85,9 +95,9 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
 #pragma unroll
   for (int i = 0; i < K - 1; ++i)
     hist[i] = get_pack<T, V>(input_row<T>(a, sp, b, t0 - (K - 1) + i, sp.len), oc);
+  Rows xs = rows_of<T>(a, a.x, a.x_stride, sp, t0), ys = rows_of<T>(a, a.y, a.C, sp, t0);
 #pragma unroll
-  for (int r = 0; r < kUnroll; ++r)
-    next[r] = get_pack<T, V>(input_row<T>(a, sp, b, t0 + r, t1), oc);
+  for (int r = 0; r < kUnroll; ++r) next[r] = get_pack<T, V>(xs.at(r, t1 - t0), oc);
   Weights<V * K, (V > 1)> wr;
   Weights<V, (V > 1)> br;
   wr.load(a.w, (int64_t)c * K, (int64_t)a.C * K, a.w_bf16);
@@ -116,10 +126,11 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
     Pack<T, V> in[kUnroll];
 #pragma unroll
     for (int r = 0; r < kUnroll; ++r) in[r] = next[r];
-    if (t + kUnroll < t1)
+    const int left = t1 - t;
+    xs.advance(kUnroll);
+    if (left > kUnroll)
 #pragma unroll
-      for (int r = 0; r < kUnroll; ++r)
-        next[r] = get_pack<T, V>(input_row<T>(a, sp, b, t + kUnroll + r, t1), oc);
+      for (int r = 0; r < kUnroll; ++r) next[r] = get_pack<T, V>(xs.at(r, left - kUnroll), oc);
 #pragma unroll
     for (int r = 0; r < kUnroll; ++r) {
       unpack(in[r], win[K - 1]);
@@ -137,8 +148,9 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
         for (int v = 0; v < V; ++v) s[v] = silu(s[v]);
       Pack<T, V> out;
       pack(s, out);
-      put_pack(dense_row<T>(a, a.y, sp, t + r, t1), oc, out);
+      put_pack(ys.at(r, left), oc, out);
     }
+    ys.advance(kUnroll);
   }
 }
 
@@ -173,14 +185,18 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
 #pragma unroll
     for (int i = 0; i < K - 1; ++i)
       hist[i] = get_pack<T, V>(input_row<T>(a, sp, b, t0 - (K - 1) + i, sp.len), oc);
-    auto fetch = [&](int t) __attribute__((always_inline)) {
+    Rows xs = rows_of<T>(a, a.x, a.x_stride, sp, t0), dys = rows_of<T>(a, a.dy, a.C, sp, t0);
+    Rows dxs = rows_of<T>(a, a.dx, a.C, sp, t0);
+    auto fetch = [&](int left) __attribute__((always_inline)) {
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
-        nx[r] = get_pack<T, V>(input_row<T>(a, sp, b, t + r, sp.len), oc);
-        nd[r] = get_pack<T, V>(dense_row<T>(a, a.dy, sp, t + r, sp.len), oc);
+        nx[r] = get_pack<T, V>(xs.at(r, left), oc);
+        nd[r] = get_pack<T, V>(dys.at(r, left), oc);
       }
+      xs.advance(kUnroll);
+      dys.advance(kUnroll);
     };
-    fetch(t0);
+    fetch(sp.len - t0);
     Weights<V * K, (V > 1)> wr;
     Weights<V, (V > 1)> br;
     wr.load(a.w, (int64_t)cc * K, (int64_t)a.C * K, a.w_bf16);
@@ -205,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
         in[r] = nx[r];
         dyv[r] = nd[r];
       }
-      if (t + kUnroll < tend) fetch(t + kUnroll);
+      if (t + kUnroll < tend) fetch(sp.len - (t + kUnroll));
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
         const int tt = t + r;
@@ -252,10 +268,11 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
         Pack<T, V> o;
         pack(out, o);
         if (to >= 0)
-          put_pack(dense_row<T>(a, a.dx, sp, to, sp.len), oc, o);
+          put_pack(dxs.at(r - (K - 1), sp.len - t), oc, o);
         else if (a.dstate != nullptr)
           put_pack(buffer_of(a.dstate, ((int64_t)b * (K - 1) + (K - 1 + to)) * size, size), oc, o);
       }
+      dxs.advance(kUnroll);
     }
   }
   if (q > 0) {
