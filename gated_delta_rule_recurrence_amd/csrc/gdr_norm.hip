@@ -425,10 +425,16 @@ bool norm_plan(int64_t rows, int64_t C, int64_t G, int64_t xs, int64_t zs, bool 
   const int64_t per = p->lanes > 64 ? 1 : 64 / p->lanes;
   p->period = G / gcd64(G, per) * per;
   p->slabs = p->period / per;
-  // about 2048 workgroups (of four waves; 512 of sixteen) in all, a part
-  // per workgroup of a slab, and no more parts than there are units for
+  // Workgroups in all: three per compute unit of 256 (at 512, 768, 1024, 2048
+  // the training step of 131072 x 2048 in groups of 128 takes 81 + 144 + 5,
+  // 76 + 125 + 5, 79 + 130 + 5, 82 + 131 + 8 us; 1237 rows of six groups of 185
+  // in fp32 7 + 9 + 3, 7 + 9 + 4, 8 + 10 + 4, 9 + 11 + 4: more leave a wave
+  // too few rows for its weights).  Where a workgroup walks as one, 131072
+  // threads (4096 x 8192, 512 lanes: 48 + 85 + 8 at 256, 46 + 102 + 12 at 512;
+  // 16384 x 4096, 256 lanes: 86 + 181 + 5 at 256, 75 + 131 + 7 at 512, 70 + 151
+  // + 11 at 1024).  And no more than there are units for.
   const int64_t walkers = p->lanes > 64 ? 1 : kThreads / 64;
-  const int64_t want = p->lanes > 64 ? 512 : 2048;
+  const int64_t want = p->lanes > 64 ? 131072 / p->lanes : 768;
   const int64_t turns = (rows * G + p->period - 1) / p->period;
   int64_t parts = (want + p->slabs - 1) / p->slabs;
   const int64_t most = (turns + walkers - 1) / walkers;
