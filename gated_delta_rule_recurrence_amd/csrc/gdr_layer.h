@@ -154,16 +154,15 @@ __device__ __forceinline__ float sigmoid(float x) {
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 __device__ __forceinline__ float dsilu(float x, float sg) { return sg * (1.f + x * (1.f - sg)); }
 
-// log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  log1p(t) for t in (0, 1] is
-// log(w) t / (w - 1) with w = 1 + t as rounded: the rounding of w enters
-// numerator and denominator alike and cancels, so that small steps (t down
-// to the smallest float) keep their relative accuracy.  Also gives the
-// derivative, sigmoid(x).
+// log(1 + e^x) = max(x, 0) + log1p(t), t = e^-|x| in (0, 1].  With w = 1 + t
+// as rounded, log1p(t) = log(w + c) for c = t - (w - 1), formed exactly, of
+// which log(w) + c leaves c t / w: below 1.5 2^-24 of log1p(t) for any t, so
+// that small steps (t down to the smallest float, where w = 1) keep their
+// relative accuracy.
 __device__ __forceinline__ float softplus(float x) {
   const float t = exp2_hw(-kLog2e * fabsf(x));
-  const float w = 1.f + t, d = w - 1.f;
-  const float l = kLn2 * __builtin_amdgcn_logf(w) * t * __builtin_amdgcn_rcpf(d);
-  return fmaxf(x, 0.f) + (d == 0.f ? t : l);
+  const float w = 1.f + t;
+  return fmaxf(x, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), t - (w - 1.f));
 }
 
 // a + b with their upper halves (32 lanes) or odd rows (16 lanes) swapped for

@@ -255,6 +255,15 @@ def _row_stride(name, t, tail, dtype, device, rows=None):
     return n, step
 
 
+def _row_stride_as(name, t, like, step, tail, dtype, device, rows):
+    """_row_stride(..)[1] of rows laid out as `like`'s, checked before, as a
+    rule: one condition then."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
+            and t.shape == like.shape and t.stride() == like.stride()):
+        return step
+    return _row_stride(name, t, tail, dtype, device, rows)[1]
+
+
 def _collapse(name, shape, strides, k, width):
     """(rows, row stride) of a tensor that is not dense as a whole."""
     inner = 1
@@ -335,11 +344,13 @@ def _scratch(workspace, nbytes, device):
     return workspace
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device) -> int:
     """The current stream's handle without a Stream object around it (2 us
     of a call), where this PyTorch has that."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return _stream(device) if get is None else get(device.index)
+    return _stream(device) if _current_raw_stream is None else _current_raw_stream(device.index)
 
 
 def _launch(name, shape, tensors, device, workspace=None, nbytes=None):
@@ -460,10 +471,10 @@ def _scan_sizes(u, dt, A, Bm, Cm, D, z, dt_bias, spans, T, softplus):
     C, N = A.shape
     G = Bm.shape[-2]
     rows, us = _row_stride("u", u, (C,), ty, dev)
-    _, dts = _row_stride("dt", dt, (C,), ty, dev, rows)
+    dts = _row_stride_as("dt", dt, u, us, (C,), ty, dev, rows)
     _, bs = _row_stride("Bm", Bm, (G, N), ty, dev, rows)
-    _, cs = _row_stride("Cm", Cm, (G, N), ty, dev, rows)
-    zs = C if z is None else _row_stride("z", z, (C,), ty, dev, rows)[1]
+    cs = _row_stride_as("Cm", Cm, Bm, bs, (G, N), ty, dev, rows)
+    zs = C if z is None else _row_stride_as("z", z, u, us, (C,), ty, dev, rows)
     _dense("A", A, (C, N), f32, dev)
     if D is not None:
         _dense("D", D, (C,), f32, dev)
@@ -543,7 +554,7 @@ def _norm_sizes(x, weight, bias, z, groups, eps, center, act):
     if z is not None:
         if z.shape != x.shape:
             raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(x.shape)}")
-        zs = _row_stride("z", z, (C,), dt, dev, rows)[1]
+        zs = _row_stride_as("z", z, x, xs, (C,), dt, dev, rows)
     return _norm_plan(rows, C, groups, xs, zs, eps, _DTYPES[dt], _DTYPES[wdt], 1 if center else 0,
                       1 if width != C else 0, _act(act))
 
