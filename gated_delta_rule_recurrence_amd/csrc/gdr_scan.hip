@@ -31,7 +31,9 @@ namespace {
 
 // Registers for n waves a SIMD and no fewer: for the eight that fit, the
 // compiler orders the recurrence's loads and exponentials so tightly that the
-// adjoint pass takes 227 us instead of 206 (4 x 4096 x 4096).
+// adjoint pass takes 227 us instead of 201 (4 x 4096 x 4096; at four, as at
+// six).  Packed prompts (five in 4100 rows of 4096): 149 us at four, 159 at
+// six, 152 at five or three.
 #define SCAN_WAVES(n) __attribute__((amdgpu_waves_per_eu(n, n)))
 
 constexpr int kThreads = 256;
@@ -245,14 +247,16 @@ __device__ __forceinline__ void put_states(Buffer b, uint32_t o, const float (&h
   }
 }
 
-// The raw loads of one tile: this lane's steps of its channel, and this
-// thread's element of B and C; zeros past the sequence's end.  The offsets
-// walk from tile to tile.
+// The loads of a tile: this lane's steps of its channel, and this thread's
+// element of B and C; zeros past the sequence's end.  The offsets walk from
+// tile to tile.
 template <typename T, int NPL, int TT, bool IN, bool OUT, bool DY>
 struct Tile {
   static constexpr int Q = TT / 4, NP = 4 * NPL;
-  T u[Q], dt[Q], z[Q], dy[Q];
-  T bm, cm;
+  struct Raw {
+    T u[Q], dt[Q], z[Q], dy[Q];
+    T bm, cm;
+  };
   Buffer bu, bdt, bz, bdy, bb, bc;   // the chunk's rows
   uint32_t su, sdt, sz, sd, sb, sc;  // bytes from row to row
   uint32_t ou, odt, oz, od, ob, oc;  // this lane in the first four rows of the tile at hand
@@ -284,30 +288,31 @@ struct Tile {
     ob = t0 * sb + (ok ? t * sb + on : kNoLane);
     oc = t0 * sc + (ok ? t * sc + on : kNoLane);
   }
-  __device__ __forceinline__ void load() {
+  __device__ __forceinline__ void load(Raw& w) const {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      if (IN) u[q] = get<T>(bu, ou + 4 * q * su);
-      dt[q] = get<T>(bdt, odt + 4 * q * sdt);
-      if (OUT) z[q] = get<T>(bz, oz + 4 * q * sz);
-      if (DY) dy[q] = get<T>(bdy, od + 4 * q * sd);
+      if (IN) w.u[q] = get<T>(bu, ou + 4 * q * su);
+      w.dt[q] = get<T>(bdt, odt + 4 * q * sdt);
+      if (OUT) w.z[q] = get<T>(bz, oz + 4 * q * sz);
+      if (DY) w.dy[q] = get<T>(bdy, od + 4 * q * sd);
     }
-    if (IN) bm = get<T>(bb, ob);
-    if (OUT) cm = get<T>(bc, oc);
+    if (IN) w.bm = get<T>(bb, ob);
+    if (OUT) w.cm = get<T>(bc, oc);
   }
-  // Moves the loads (not od, the dense rows) one tile on or back.
+  // Moves the loads one tile on or back.
   template <int WAY>
   __device__ __forceinline__ void advance() {
     if (IN) ou += WAY * TT * su;
     odt += WAY * TT * sdt;
     if (OUT) oz += WAY * TT * sz;
+    if (DY) od += WAY * TT * sd;
     if (IN) ob += WAY * TT * sb;
     if (OUT) oc += WAY * TT * sc;
   }
-  __device__ __forceinline__ void stage(float* bs, float* cs) const {
+  static __device__ __forceinline__ void stage(const Raw& w, float* bs, float* cs) {
     if (TT * NP < kThreads && threadIdx.x >= TT * NP) return;
-    if (IN) bs[threadIdx.x] = to_f32(bm);
-    if (OUT) cs[threadIdx.x] = to_f32(cm);
+    if (IN) bs[threadIdx.x] = to_f32(w.bm);
+    if (OUT) cs[threadIdx.x] = to_f32(w.cm);
   }
 };
 
@@ -394,7 +399,7 @@ __device__ __forceinline__ void join_chunks(const ScanArgs& a, const Place& p, u
 // start); else the pass that writes y.
 template <typename T, int NPL, bool EDGE>
 __global__ __launch_bounds__(kThreads)
-SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
+SCAN_WAVES((NPL <= 8 ? 4 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
   constexpr int TT = tile_steps<NPL>(), HT = save_steps<NPL>();
   using L = Tile<T, NPL, TT, true, !EDGE, false>;
   constexpr int Q = L::Q, NP = L::NP;
@@ -420,37 +425,47 @@ SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
     join_chunks<true, NPL>(a, p, oh, A, h);
   }
   float sum = 0.f;
+  // Loads of two tiles in flight: at one wave a SIMD a tile's arithmetic is
+  // shorter than the way to memory (4 x 4096 x 4096, unsplit: 444 us, 456 with
+  // one; 4 x 2048 x 4096 with 4 states: 196, 228).  The first passes have the
+  // waves to hide it and lose 5 to 10% to the second set of registers.
+  constexpr int kAhead = EDGE ? 1 : 2;
   L in;
   in.init(a, p, 0);
-  if (p.begin < p.end) in.load();
-  const int64_t steps = p.end - p.begin;
-  const Buffer by = buffer_of(a.y, (p.sp.first + p.begin) * (int64_t)in.sd, steps * in.sd);
+  uint32_t oy = in.od;
+  typename L::Raw raw[kAhead];
+  const int steps = p.end - p.begin;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    if (k * TT < steps) in.load(raw[k]);
+    in.template advance<1>();
+  }
+  const Buffer by = buffer_of(a.y, (p.sp.first + p.begin) * (int64_t)in.sd, (int64_t)steps * in.sd);
   // the saved states from this chunk's first on, of which this lane's next
   const int64_t slot_bytes = (int64_t)a.C * NP * 4;
   const Buffer saved =
       buffer_of(a.ckpt, slot_of(p.sp, p.b, HT, p.begin / HT) * slot_bytes,
-                !EDGE && a.ckpt != nullptr ? (steps + HT - 1) / HT * slot_bytes : 0);
+                !EDGE && a.ckpt != nullptr ? (int64_t)((steps + HT - 1) / HT) * slot_bytes : 0);
   uint32_t osaved = oh;
-  int buf = 0;
-  for (int t0 = p.begin; t0 < p.end; t0 += TT, buf ^= 1) {
+  auto tile = [&](typename L::Raw& w, int t0, int buf) __attribute__((always_inline)) {
     // this lane's steps: delta, delta u, D u and the gate
     float dl[Q], du[Q], skip[Q], gate[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const float u = to_f32(in.u[q]);
-      dl[q] = delta_of(to_f32(in.dt[q]) + bias, a.softplus, t0 + 4 * q + r < p.end);
+      const float u = to_f32(w.u[q]);
+      dl[q] = delta_of(to_f32(w.dt[q]) + bias, a.softplus, t0 + 4 * q + r < p.end);
       du[q] = dl[q] * u;
       if (EDGE) {
         sum += dl[q];
       } else {
-        const float g = silu(to_f32(in.z[q]));
+        const float g = silu(to_f32(w.z[q]));
         skip[q] = D * u;
         gate[q] = a.z != nullptr ? g : 1.f;
       }
     }
-    in.stage(Bs[buf], Cs[buf]);
+    L::stage(w, Bs[buf], Cs[buf]);
+    if (t0 + kAhead * TT < p.end) in.load(w);
     in.template advance<1>();
-    if (t0 + TT < p.end) in.load();
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -477,10 +492,15 @@ SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_fwd_kernel(ScanArgs a, int ctiles) {
       step(std::integral_constant<int, 3>{});
       if (!EDGE) {
         const float y = (skip[q] + quad_scatter_sum(acc, r)) * gate[q];
-        put<T>(by, in.od + 4 * q * in.sd, y);
+        put<T>(by, oy + 4 * q * in.sd, y);
       }
     }
-    in.od += TT * in.sd;
+    oy += TT * in.sd;
+  };
+  int buf = 0;
+  for (int t0 = p.begin; t0 < p.end; t0 += kAhead * TT, buf ^= 1) {
+    tile(raw[0], t0, kAhead > 1 ? 0 : buf);
+    if (kAhead > 1 && t0 + TT < p.end) tile(raw[kAhead - 1], t0 + TT, 1);
   }
   if (EDGE) {
     put_states<NPL>(slot_buffer<NPL>(a.edge, slot_of(p.sp, p.b, a.chunk, p.j), a.C), oh, h);
@@ -589,7 +609,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
 // from a zero E behind it, for every chunk but the first.
 template <typename T, int NPL>
 __global__ __launch_bounds__(kThreads)
-SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
+SCAN_WAVES((NPL <= 8 ? 4 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) {
   constexpr int TT = tile_steps<NPL>();
   using L = Tile<T, NPL, TT, false, true, true>;
   constexpr int Q = L::Q, NP = L::NP;
@@ -611,21 +631,21 @@ SCAN_WAVES((NPL <= 8 ? 6 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) 
   L in;
   int t0 = p.begin + (p.end - p.begin - 1) / TT * TT;
   in.init(a, p, t0 - p.begin);
-  in.load();
+  typename L::Raw w;
+  in.load(w);
   int buf = 0;
   for (; t0 >= p.begin; t0 -= TT, buf ^= 1) {
     float dl[Q], o[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      dl[q] = delta_of(to_f32(in.dt[q]) + bias, a.softplus, t0 + 4 * q + r < p.end);
-      const float g = silu(to_f32(in.z[q]));
-      o[q] = to_f32(in.dy[q]) * (a.z != nullptr ? g : 1.f);
+      dl[q] = delta_of(to_f32(w.dt[q]) + bias, a.softplus, t0 + 4 * q + r < p.end);
+      const float g = silu(to_f32(w.z[q]));
+      o[q] = to_f32(w.dy[q]) * (a.z != nullptr ? g : 1.f);
       sum += dl[q];
     }
-    in.stage(nullptr, Cs[buf]);
+    L::stage(w, nullptr, Cs[buf]);
     in.template advance<-1>();
-    in.od -= TT * in.sd;
-    if (t0 > p.begin) in.load();
+    if (t0 > p.begin) in.load(w);
     __syncthreads();
 #pragma unroll
     for (int q = Q - 1; q >= 0; --q) {
@@ -679,6 +699,7 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
     const int t_last = (tiles - 1) * TT;
     L in;
     in.init(a, p, tiles > 0 ? t_last : 0);
+    typename L::Raw w;
     // the saved states, this channel tile's part of dB and dC, and the dense
     // gradients, with this lane's place in the tile at hand
     const int64_t steps = p.end - p.begin, row = p.sp.first + p.begin;
@@ -714,7 +735,7 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
     };
     float next[NPL];
     if (tiles > 0) {
-      in.load();
+      in.load(w);
       get_states<NPL>(saved, osaved, next);
     }
     int buf = 0;
@@ -725,24 +746,23 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const bool ok = 4 * q + r < left;
-        const float raw = to_f32(in.dt[q]) + bias, sr = sigmoid(raw);
-        u[q] = to_f32(in.u[q]);
+        const float raw = to_f32(w.dt[q]) + bias, sr = sigmoid(raw);
+        u[q] = to_f32(w.u[q]);
         dl[q] = delta_of(raw, a.softplus, ok);
         slope[q] = ok ? (a.softplus ? sr : 1.f) : 0.f;
-        const float dy = to_f32(in.dy[q]), z = to_f32(in.z[q]), sg = sigmoid(z);
+        const float dy = to_f32(w.dy[q]), z = to_f32(w.z[q]), sg = sigmoid(z);
         dgate[q] = dy * dsilu(z, sg);
         o[q] = dy * (a.z != nullptr ? z * sg : 1.f);
         sD = fmaf(o[q], u[q], sD);
       }
 #pragma unroll
       for (int i = 0; i < NPL; ++i) h0[i] = next[i];
-      in.stage(Bs[buf], Cs[buf]);
+      L::stage(w, Bs[buf], Cs[buf]);
       const uint32_t dense_at = in.od;
       in.template advance<-1>();
-      in.od -= TT * in.sd;
       osaved -= (uint32_t)slot_bytes;
       if (tile > 0) {
-        in.load();
+        in.load(w);
         get_states<NPL>(saved, osaved, next);
       }
       __syncthreads();
