@@ -8,9 +8,13 @@
 //   dB_t = sum_c E_t delta u,  du = D o + delta sum_n E_t B_t,
 //   ddelta = sum_n E_t (u B_t + A a h_{t-1}),  dA = sum_t E_t delta a h_{t-1},
 //   ddt = ddelta sigmoid(dt + dt_bias),  dS0 = a_1 E_1.
-// Every state and step takes one exponential (a quarter-rate instruction)
+// Every state and step takes one exponential (two of a vector unit's turns)
 // and 4 (forward) or 12 (backward) products and sums: bound by the vector
-// units, not by HBM.
+// units, not by HBM.  Measured (bf16, N = 16, at 39 T lane-operations/s): 4 x
+// 4096 x 4096, forward unsplit 444 us, 16 operations' time a state and step
+// (57% busy, one wave a SIMD), backward 201 + 795 us, 7 and 29 (92 and 99%
+// busy).  Of the backward's 29 the formula takes 14, the sums of dB and dC
+// over channels 4, preparing the steps 4, sums over states and broadcasts 3.
 //
 // Mapping: the four lanes of a DPP quad share a channel, NPL states each; a
 // wave has 16 channels, a workgroup 64.  Time runs in tiles of TT steps: lane
@@ -235,8 +239,7 @@ __device__ __forceinline__ void put_states(Buffer b, uint32_t o, const float (&h
     put<float>(b, o, h[0]);
   } else if constexpr (NPL == 2) {
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(h[0]), __float_as_uint(h[1])},
-                                          b.resource(),
-                                          (int)o, 0, 0);
+                                          b.resource(), (int)o, 0, 0);
   } else {
 #pragma unroll
     for (int k = 0; k < NPL; k += 4)
@@ -977,10 +980,10 @@ int64_t scan_chunk(const ScanArgs& a, int64_t stride, bool bwd) {
   if (a.B == 0 || T == 0) return 16;
   // Waves of the unsplit grid; packed sequences count for their rows.
   // Measured at C = 4096, N = 16, bf16, forward / backward in us, by chunks:
-  //    256 waves (T = 2048)   1: 236 / 588   8: 91 / 164   16: 85 / 154   32: 88 / 155
-  //    512                    1: 238 / 598   8: 161 / 304  16: 161 / 309
-  //   1024 (T = 4096)         1: 469 / 1181  8: 538 / 1022 16: 546 / 1031
-  //   2048 (T = 2048)         1: 390 / 891   2: 552 / 1043 8: 531 / 1022
+  //    256 waves (T = 2048)  1: 236 / 588   8: 91 / 168   16: 83 / 153   32: 88 / 157
+  //    512                   1: 238 / 598   8: 161 / 304  16: 161 / 309
+  //   1024 (T = 4096)        1: 449 / 1181  3: 537 / 1043  8: 535 / 1006  16: 547 / 1031
+  //   2048 (T = 2048)        1: 390 / 891   2: 552 / 1043  8: 531 / 1022
   // A chunk more than one repeats most of the recurrence in the first pass,
   // which pays while the device has waves missing: below one wave a SIMD
   // forward, two backward (its main pass waits more).  Then 4096 waves or more,
