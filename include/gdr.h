@@ -242,8 +242,8 @@ int gdr_set_launch_events(void* const* events, int n);
  * (packed prompts, batches padded on either side); T is then the longest
  * sequence's length, and steps past T are not taken.  Rows of no sequence
  * are neither read nor written.  A sequence of no rows keeps its state.
- * Spans outside 0 .. rows are cut to that range; ones that overlap give
- * unspecified values.
+ * Spans outside 0 .. rows are cut to that range; ones that overlap, or in
+ * another order, give unspecified values.
  * ------------------------------------------------------------------------- */
 typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_act; /* x, x / (1 + e^-x) */
 

@@ -495,6 +495,48 @@ def test_captured_and_replayed(cuda):
         assert same(out, run_all(s)), seed
 
 
+def run_packed(s, spans, T, window=None, states=None):
+    """Forward and backward of the convolution and the scan over packed rows;
+    states in place where they are given."""
+    from gated_delta_rule_recurrence_amd import ops
+    flat = lambda t: None if t is None else t.reshape(-1, *t.shape[2:])
+    x, w, b, _ = s["conv"]
+    kw = dict(spans=spans, T=T)
+    y, win = ops.gdr_conv_forward(flat(x), w, b, window, state_out=window, **kw)
+    out = [y, win, *ops.gdr_conv_backward(flat(x), w, b, None, flat(s["dy"]), **kw)[:3]]
+    u, dt, A, Bm, Cm, D, z, bias, _ = s["scan"]
+    args = flat(u), flat(dt), A, flat(Bm), flat(Cm), D, flat(z), bias
+    y, S_T, saved = ops.gdr_scan_forward(*args, states, S_T=states, **kw)
+    return out + [y, S_T, *ops.gdr_scan_backward(*args, saved, flat(s["dy"]), want_dS0=False)[:8]]
+
+
+def test_a_graph_whose_spans_change(cuda):
+    """A graph over packed rows, replayed on other cuts of the rows (empty
+    sequences, gaps, one long one), its states carried from replay to replay."""
+    import torch
+    s = small_state(cuda, seed=4)
+    cuts = [[(0, 100), (100, 100), (110, 290)], [(0, 0), (3, 4), (4, 300)], [(290, 300), (300, 300), (300, 300)],
+            [(0, 20), (40, 60), (80, 297)]]
+    spans = torch.tensor(cuts[0], dtype=torch.int32, device=cuda)
+    window, S = torch.zeros(3, 3, 96, dtype=torch.bfloat16, device=cuda), torch.zeros(3, 96, 16, device=cuda)
+    mine, mine_S = window.clone(), S.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run_packed(s, spans, 300, window, S)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run_packed(s, spans, 300, window, S)
+    window.zero_(), S.zero_()
+    for cut in cuts:
+        spans.copy_(torch.tensor(cut, dtype=torch.int32, device=cuda))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, run_packed(s, spans, 300, mine, mine_S)), cut
+        assert torch.equal(window, mine) and torch.equal(S, mine_S)
+
+
 def test_states_in_place(cuda):
     """state_out = state and S_T = S0, over prompts of several tiles and
     chunks: the values of the call with buffers apart."""
