@@ -398,6 +398,39 @@ def test_norm_options(cuda, kw):
     norm_case(cuda, "f32", 19, 192, 3, **{**kw, "wdtype": "bf16" if "wdtype" in kw else None})
 
 
+@pytest.mark.parametrize("dtype,rows,C,G,shared", [("f32", 60000, 8, 1, False), ("bf16", 30000, 24, 2, True),
+                                                   ("f32", 1300, 1500, 1, False), ("bf16", 1300, 6000, 2, True)])
+def test_norm_many_rows(cuda, dtype, rows, C, G, shared):
+    """More rows than the walkers of the grid take in one turn."""
+    norm_case(cuda, dtype, rows, C, G, shared=shared, center=shared, seed=rows)
+
+
+def some_spans(r, B):
+    """B ascending spans with gaps, some empty, and rows behind the last."""
+    at = np.sort(r.integers(0, 160, size=2 * B))
+    return [(int(at[2 * b]), int(at[2 * b + 1])) for b in range(B)], int(at[-1]) + int(r.integers(0, 5))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(cuda, seed):
+    r = np.random.default_rng(1000 + seed)
+    pick = lambda *v: v[int(r.integers(len(v)))]
+    flip = lambda: bool(r.integers(2))
+    dtype, B, T = pick("bf16", "f32"), int(r.integers(1, 6)), int(r.integers(1, 120))
+    spans, rows = some_spans(r, B) if flip() else (None, None)
+    G = int(r.integers(1, 4))
+    C, N, K = G * int(r.integers(1, 90)), int(r.integers(1, 65)), int(r.integers(1, 9))
+    case = dict(dtype=dtype, B=B, T=T, spans=spans, rows=rows, C=C, G=G, N=N, K=K)
+    print(case, flush=True)
+    conv_case(cuda, dtype, B, T, C, K, wdtype=pick(None, "f32", "bf16"), act=pick("silu", "none"), bias=flip(),
+              state=flip(), spans=spans, rows=rows, stride=flip(), seed=seed)
+    without = [k for k in ("D", "z", "dt_bias", "S0", "dS_T") if flip()]
+    scan_case(cuda, dtype, B, T, C, N, G, without=without, spans=spans, rows=rows, stride=flip(), seed=seed)
+    norm_case(cuda, dtype, int(r.integers(1, 400)), C, G, wdtype=pick(None, "f32", "bf16"), center=flip(),
+              act=pick("silu", "none"), gate=flip(), weight=flip(), bias=flip(), shared=flip(), stride=flip(),
+              seed=seed)
+
+
 # ---- all three: streams, graphs, repeats, spans, large offsets ----------------------
 
 def small_state(dev, dtype="bf16", seed=0):
