@@ -324,23 +324,37 @@ def _weight_dtype(name, w):
     return w.dtype
 
 
-def _out(given, name, shape, dtype, device, spans):
+def _out(given, name, shape, dtype, device):
     if given is None:
-        make = torch.empty if spans is None else torch.zeros
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     _dense(name, given, shape, dtype, device)
     return given
 
 
-def _scratch(workspace, nbytes, device):
+def _dense_like(t, spans=None):
+    """A dense tensor of t's shape (an empty_like costs half of an empty)."""
+    make = torch.empty_like if spans is None else torch.zeros_like
+    return make(t, memory_format=torch.contiguous_format)
+
+
+def _rows_out(given, name, like, spans=None):
+    """The output rows of a call on rows `like`."""
+    if given is None:
+        return _dense_like(like, spans)
+    _dense(name, given, like.shape, like.dtype, like.device)
+    return given
+
+
+def _scratch(workspace, nbytes, like, name="workspace"):
     if nbytes == 0:
         return None
+    device = like.device
     if workspace is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+        return like.new_empty(nbytes, dtype=torch.uint8)
     if workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError("workspace too small")
+        raise ValueError(f"{name} too small")
     if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
+        raise ValueError(f"{name} must be contiguous and on {device}")
     return workspace
 
 
@@ -421,11 +435,11 @@ def gdr_conv_forward(x, weight, bias=None, state=None, *, act="silu", spans=None
     state (in place)."""
     shape, _ = _conv_sizes(x, weight, bias, state, spans, T, act)
     dev, dt = x.device, x.dtype
-    y = _out(y, "y", x.shape, dt, dev, spans)
+    y = _rows_out(y, "y", x, spans)
     if not out_state:
         state_out = None
     else:
-        state_out = _out(state_out, "state_out", (shape.B, shape.K - 1, shape.C), dt, dev, None)
+        state_out = _out(state_out, "state_out", (shape.B, shape.K - 1, shape.C), dt, dev)
     _launch("gdr_conv_forward", shape, (x, weight, bias, state, spans, y, state_out), dev)
     return y, state_out
 
@@ -439,12 +453,12 @@ def gdr_conv_backward(x, weight, bias, state, dy, dstate_out=None, *, act="silu"
     window = (shape.B, shape.K - 1, shape.C)
     if dstate_out is not None:
         _dense("dstate_out", dstate_out, window, dt, dev)
-    dx = _out(None, "dx", x.shape, dt, dev, spans)
+    dx = _dense_like(x, spans)
     make = torch.empty_like if shape.B > 0 else torch.zeros_like
     dweight = make(weight)
     dbias = None if bias is None else make(bias)
     dstate = torch.empty(window, dtype=dt, device=dev) if want_dstate else None
-    workspace = _scratch(workspace, nbytes, dev)
+    workspace = _scratch(workspace, nbytes, x)
     _launch("gdr_conv_backward", shape, (x, weight, bias, state, spans, dy, dstate_out, dx,
                                          dweight, dbias, dstate), dev, workspace, nbytes)
     return dx, dweight, dbias, dstate
@@ -496,16 +510,13 @@ def gdr_scan_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, S0=None, *,
     states = (shape.B, shape.C, shape.N)
     if S0 is not None:
         _dense("S0", S0, states, torch.float32, dev)
-    y = _out(y, "y", u.shape, u.dtype, dev, spans)
-    S_T = _out(S_T, "S_T", states, torch.float32, dev, None) if out_state else None
+    y = _rows_out(y, "y", u, spans)
+    S_T = _out(S_T, "S_T", states, torch.float32, dev) if out_state else None
     saved = None
     if save:
-        if ckpt is None:
-            ckpt = torch.empty((max(save_bytes, 1),), dtype=torch.uint8, device=dev)
-        if ckpt.numel() * ckpt.element_size() < save_bytes:
-            raise ValueError("ckpt buffer too small")
+        ckpt = _scratch(ckpt, max(save_bytes, 1), u, "ckpt")
         saved = ScanSaved(ckpt, spans, shape.T, bool(softplus))
-    workspace = _scratch(workspace, nbytes, dev)
+    workspace = _scratch(workspace, nbytes, u)
     _launch("gdr_scan_forward", shape, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, spans, y, S_T,
                                         ckpt if save else None), dev, workspace, nbytes)
     return y, S_T, saved
@@ -523,13 +534,14 @@ def gdr_scan_backward(u, dt, A, Bm, Cm, D, z, dt_bias, saved: ScanSaved, dy, dS_
     _dense("dy", dy, u.shape, ty, dev)
     if dS_T is not None:
         _dense("dS_T", dS_T, states, torch.float32, dev)
-    du, ddt, dB, dC = (_out(None, "", t.shape, ty, dev, spans) for t in (u, dt, Bm, Cm))
-    dz = None if z is None else _out(None, "", z.shape, ty, dev, spans)
+    du, ddt, dB, dC = [_dense_like(t, spans) for t in (u, dt, Bm, Cm)]
+    dz = None if z is None else _dense_like(z, spans)
     make = torch.empty_like if shape.B > 0 else torch.zeros_like
     dA = make(A)
-    dD, dbias = (None if t is None else make(t) for t in (D, dt_bias))
+    dD = None if D is None else make(D)
+    dbias = None if dt_bias is None else make(dt_bias)
     dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
-    workspace = _scratch(workspace, nbytes, dev)
+    workspace = _scratch(workspace, nbytes, u)
     _launch("gdr_scan_backward", shape, (u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.ckpt, dy,
                                          dS_T, du, ddt, dA, dB, dC, dD, dz, dbias, dS0), dev,
             workspace, nbytes)
@@ -567,9 +579,9 @@ def gdr_norm_forward(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, cen
     rows."""
     shape, _ = _norm_sizes(x, weight, bias, z, groups, eps, center, act)
     dev = x.device
-    y = _out(y, "y", x.shape, x.dtype, dev, None)
+    y = _rows_out(y, "y", x)
     if save:
-        stats = _out(stats, "stats", (shape.rows, shape.G, 2), torch.float32, dev, None)
+        stats = _out(stats, "stats", (shape.rows, shape.G, 2), torch.float32, dev)
     else:
         stats = None
     _launch("gdr_norm_forward", shape, (x, weight, bias, z, y, stats), dev)
@@ -584,12 +596,13 @@ def gdr_norm_backward(x, weight, bias, z, stats, dy, *, groups, center=False, ac
     dev = x.device
     _dense("dy", dy, x.shape, x.dtype, dev)
     _dense("stats", stats, (shape.rows, shape.G, 2), torch.float32, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dz = None if z is None else torch.empty(z.shape, dtype=x.dtype, device=dev)
-    dweight, dbias = (None if w is None else torch.empty_like(w) for w in (weight, bias))
+    dx = _dense_like(x)
+    dz = None if z is None else _dense_like(z)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
     if weight is None and bias is None:
         nbytes = 0
-    workspace = _scratch(workspace, nbytes, dev)
+    workspace = _scratch(workspace, nbytes, x)
     _launch("gdr_norm_backward", shape, (x, weight, bias, z, stats, dy, dx, dweight, dbias, dz),
             dev, workspace, nbytes)
     return dx, dweight, dbias, dz
