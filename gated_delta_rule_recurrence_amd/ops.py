@@ -3,11 +3,13 @@
 PyTorch supplies device memory and the current HIP stream; the arithmetic all
 happens in libgdr.so.  Tensors must be contiguous, on one GPU, and q, k, v,
 g, beta, dy share one dtype (torch.float32 or torch.bfloat16); states are
-torch.float32.
+torch.float32.  The operators around the recurrence (further down) take rows
+with a stride too.
 """
 from __future__ import annotations
 
 import functools
+import math
 from dataclasses import dataclass
 from typing import Optional
 
@@ -241,11 +243,9 @@ def _row_stride(name, t, tail, dtype, device, rows=None):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     k = len(tail)
     shape = t.shape
-    if len(shape) <= k or shape[-k:] != tail:
+    if len(shape) <= k or (shape[-1] != tail[0] if k == 1 else shape[-k:] != tail):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected rows of {tuple(tail)}")
-    width = 1
-    for size in tail:
-        width *= size
+    width = tail[0] if k == 1 else math.prod(tail)
     if t.is_contiguous():
         n, step = (t.numel() // width if width else 0), width
     else:
@@ -558,9 +558,10 @@ def _norm_sizes(x, weight, bias, z, groups, eps, center, act):
     if like is not None:  # weight and bias have one type and one shape
         wdt = _weight_dtype("weight" if weight is not None else "bias", like)
         width = C if like.numel() == C else C // groups
-        for name, w in (("weight", weight), ("bias", bias)):
-            if w is not None:
-                _dense(name, w, (width,), wdt, dev)
+        if weight is not None:
+            _dense("weight", weight, (width,), wdt, dev)
+        if bias is not None:
+            _dense("bias", bias, (width,), wdt, dev)
     rows, xs = _row_stride("x", x, (C,), dt, dev)
     zs = C
     if z is not None:
