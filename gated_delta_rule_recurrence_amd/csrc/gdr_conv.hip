@@ -388,7 +388,7 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// 16 steps a wave, 32 where that still leaves three waves a SIMD, 3072 (the
+// 16 steps a wave, 32 where that still leaves 3200 waves, three a SIMD (the
 // halo and the partial sums halve): 2048 rows of 14336 bf16 channels take
 // 41.2 us at 16, 42.3 at 24, 39.5 at 32; 3 x 777 rows of 1001 in fp32, too few
 // for that, 11.2 at 16, 12 at 24, 13 at 32.  Sized for vector loads: it
@@ -396,7 +396,7 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 // strides.
 int conv_bwd_steps(int64_t B, int64_t T, int64_t C) {
   const int64_t waves = (C + 255) / 256 * B;
-  int64_t steps = waves * T / 32 >= 3072 ? 32 : 16;
+  int64_t steps = waves * T / 32 >= 3200 ? 32 : 16;
   // the grid's x dimension holds (tiles / 4) x (channel blocks, at most one
   // per 64 channels)
   while ((T + 4 * steps - 1) / (4 * steps) * ((C + 63) / 64) > kMaxGrid) steps *= 2;
