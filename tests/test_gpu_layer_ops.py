@@ -671,6 +671,26 @@ def test_a_longest_length_far_above_the_rows(cuda):
         assert ((a - b).abs() <= 2.0 ** -7 * a.abs() + 1e-3 * a.abs().max()).all()
 
 
+@pytest.mark.parametrize("T", [1, 20])
+def test_steps_keep_their_relative_accuracy(cuda, T):
+    """y = delta where u, B and C are 1 and nothing is carried (A so low that
+    every decay is 0): softplus over its range, tiny steps included.  The
+    exponential's argument is rounded twice, |raw| units each, and the constant
+    in it once more; then come fewer than 8 roundings, with the logarithm's."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    C = 4096
+    raw = np.linspace(-86.0, 90.0, T * C).astype(np.float32)
+    dt = torch.from_numpy(raw).to(cuda).view(1, T, C)
+    one = torch.ones(1, T, 1, 1, device=cuda)
+    A = torch.full((C, 1), -float("inf"), device=cuda)
+    y, _, _ = ops.gdr_scan_forward(torch.ones_like(dt), dt, A, one, one, save=False)
+    x = raw.astype(np.float64)
+    ref = np.maximum(x, 0) + np.log1p(np.exp(-np.abs(x)))
+    off = np.abs(y.double().cpu().numpy().ravel() - ref) / ref
+    assert (off <= (3 * np.abs(np.minimum(x, 0)) + 8) * ULP).all()
+
+
 def test_infinite_rates(cuda):
     """A = -inf forgets at every step, and is no matter behind a sequence's
     last step, whatever the tiles and chunks."""
