@@ -15,7 +15,7 @@
 // per tile plus a halo of K - 1 rows.  A row is a buffer whose bound is its
 // end, or nothing where there is no such row: no load and no store has a
 // branch around it, and the first loads go out together (one token for 64
-// requests: 6.8 us, of which two trips to memory, spans and then the rest,
+// requests: 5.6 us, of which two trips to memory, spans and then the rest,
 // and the launch are most; 14.7 with a wait between each kind).
 #include "gdr_layer.h"
 
@@ -23,7 +23,7 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows of one turn; the next turn's are loaded ahead
+constexpr int kUnroll = 4;  // rows of one turn
 
 // Input row t of the sequence: x for 0 <= t < end, the window for t < 0, else
 // a row of no bytes, read as zeros.  t is the same for the whole wave; the
@@ -84,7 +84,8 @@ __device__ __forceinline__ Span uniform_span(const ConvArgs& a, int b) {
   return sp;
 }
 
-template <typename T, int K, int V>
+// U rows of one turn (the next turn's are loaded ahead).
+template <typename T, int K, int V, int U>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblocks, int steps) {
   const int tile = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / cblocks));
   const int c = ((int)(blockIdx.x - (uint32_t)tile * cblocks) * kThreads + (int)threadIdx.x) * V;
@@ -98,22 +99,22 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
 
   // all the first loads before any use: the rows before the tile, its first
   // rows, the weights, and (the first tile) the window left behind
-  Pack<T, V> hist[K > 1 ? K - 1 : 1], next[kUnroll], left[K > 1 ? K - 1 : 1];
+  Pack<T, V> hist[K > 1 ? K - 1 : 1], next[U], last[K > 1 ? K - 1 : 1];
 #pragma unroll
   for (int i = 0; i < K - 1; ++i)
     hist[i] = get_pack<T, V>(input_row<T>(a, sp, b, t0 - (K - 1) + i, sp.len), oc);
   Rows xs = rows_of<T>(a, a.x, a.x_stride, sp, t0), ys = rows_of<T>(a, a.y, a.C, sp, t0);
 #pragma unroll
-  for (int r = 0; r < kUnroll; ++r) next[r] = get_pack<T, V>(xs.at(r, t1 - t0), oc);
+  for (int r = 0; r < U; ++r) next[r] = get_pack<T, V>(xs.at(r, t1 - t0), oc);
   Weights<V * K, (V > 1)> wr;
   Weights<V, (V > 1)> br;
   wr.load(a.w, (int64_t)c * K, (int64_t)a.C * K, a.w_bf16);
   br.load(a.bias, c, a.C, a.w_bf16);
   const bool leave = tile == 0 && a.state_out != nullptr;
-  if (leave)
+  if (leave && U > 1)  // (of a single token they are those rows, one on)
 #pragma unroll
     for (int i = 0; i < K - 1; ++i)
-      left[i] = get_pack<T, V>(input_row<T>(a, sp, b, sp.len - (K - 1) + i, sp.len), oc);
+      last[i] = get_pack<T, V>(input_row<T>(a, sp, b, sp.len - (K - 1) + i, sp.len), oc);
   float w[V * K], bias[V];  // weight[c + v][j] at v K + j
   wr.get(a.w_bf16, w);
   br.get(a.w_bf16, bias);
@@ -122,24 +123,29 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
   if (leave) {
     const int64_t size = a.C * (int64_t)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i)
-      put_pack(buffer_of(a.state_out, ((int64_t)b * (K - 1) + i) * size, size), oc, left[i]);
+    for (int i = 0; i < K - 1; ++i) {
+      if (U == 1) {
+        const Pack<T, V> on = i + 2 < K ? hist[i + 2 < K ? i + 1 : 0] : next[0];
+        last[i] = sp.len > 0 ? on : hist[i];
+      }
+      put_pack(buffer_of(a.state_out, ((int64_t)b * (K - 1) + i) * size, size), oc, last[i]);
+    }
   }
 
   float win[K][V];  // win[K - 1]: the current input
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) unpack(hist[i], win[i]);
-  for (int t = t0; t < t1; t += kUnroll) {
-    Pack<T, V> in[kUnroll];
+  for (int t = t0; t < t1; t += U) {
+    Pack<T, V> in[U];
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r) in[r] = next[r];
+    for (int r = 0; r < U; ++r) in[r] = next[r];
     const int left = t1 - t;
-    xs.advance(kUnroll);
-    if (left > kUnroll)
+    xs.advance(U);
+    if (left > U)
 #pragma unroll
-      for (int r = 0; r < kUnroll; ++r) next[r] = get_pack<T, V>(xs.at(r, left - kUnroll), oc);
+      for (int r = 0; r < U; ++r) next[r] = get_pack<T, V>(xs.at(r, left - U), oc);
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r) {
+    for (int r = 0; r < U; ++r) {
       unpack(in[r], win[K - 1]);
       float s[V];
 #pragma unroll
@@ -157,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int cblo
       pack(s, out);
       put_pack(ys.at(r, left), oc, out);
     }
-    ys.advance(kUnroll);
+    ys.advance(U);
   }
 }
 
@@ -340,8 +346,15 @@ hipError_t fwd(const ConvArgs& a, hipStream_t s) {
     tiles = (a.T + steps - 1) / steps;
   }
   if (tiles < 1) tiles = 1;
-  hipLaunchKernelGGL((conv_fwd_kernel<T, K, V>), dim3((unsigned)(tiles * cblocks), a.B),
-                     dim3(kThreads), 0, s, a, cblocks, (int)steps);
+  // single tokens: a turn of one row (64 requests: 5.6 us, 6.8 with the
+  // arithmetic of four; a test for the end within the turn costs prompts 2.5%)
+  const dim3 grid((unsigned)(tiles * cblocks), a.B);
+  if (a.T == 1)
+    hipLaunchKernelGGL((conv_fwd_kernel<T, K, V, 1>), grid, dim3(kThreads), 0, s, a, cblocks,
+                       (int)steps);
+  else
+    hipLaunchKernelGGL((conv_fwd_kernel<T, K, V, kUnroll>), grid, dim3(kThreads), 0, s, a, cblocks,
+                       (int)steps);
   const hipError_t e = hipGetLastError();
   note_launch(s);
   return e;

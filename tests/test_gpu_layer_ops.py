@@ -156,6 +156,15 @@ def test_conv_packed(cuda, dtype, C):
     conv_case(cuda, dtype, len(PACKED), 0, C, 4, spans=PACKED, rows=PACKED_ROWS)
 
 
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 8])
+def test_conv_single_tokens(cuda, K):
+    """One token for some of the sequences, none for the others."""
+    spans = [(0, 1), (1, 1), (1, 2), (3, 4), (4, 4)]
+    for dtype, C in (("bf16", 2056), ("f32", 33)):
+        conv_case(cuda, dtype, 5, 0, C, K, spans=spans, rows=6, seed=K)
+        conv_case(cuda, dtype, 5, 0, C, K, spans=[(2, 2)] * 5, rows=6, state=K != 3, seed=K)
+
+
 @pytest.mark.parametrize("kw", [dict(bias=False), dict(state=False), dict(act="none"), dict(stride=True),
                                 dict(wdtype="f32"), dict(stride=True, bias=False, state=False)])
 def test_conv_options(cuda, kw):
