@@ -302,8 +302,8 @@ struct Weights {
   static constexpr uint32_t kPastEnd = 0xf0000000u;  // weights end below 2^26
   static constexpr int kUnit = VEC ? (N % 8 == 0 ? 8 : 4) : 1;
   static constexpr int kUnits = N / kUnit;
-  Pack<bf16, kUnit> lo[kUnits];             // bf16; for units of eight also the
-  Pack<float, VEC ? 4 : 1> hi[kUnits];      // first half of the floats in hi
+  Pack<bf16, kUnit> lo[kUnits];         // the bf16 ones, or the first four floats of eight
+  Pack<float, VEC ? 4 : 1> hi[kUnits];  // the floats, or the last four of eight
 
   __device__ __forceinline__ void load(const void* p, int64_t first, int64_t count, int is_bf16) {
     const uint32_t size = is_bf16 ? 2 : 4;
