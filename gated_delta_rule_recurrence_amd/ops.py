@@ -527,10 +527,14 @@ def gdr_scan_backward(u, dt, A, Bm, Cm, D, z, dt_bias, saved: ScanSaved, dy, dS_
     """Returns (du, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dS0); None where the
     forward had no such input, and dS0 only where wanted."""
     spans = saved.spans
-    shape, _, _, nbytes = _scan_sizes(u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.T,
-                                      saved.softplus)
+    shape, save_bytes, _, nbytes = _scan_sizes(u, dt, A, Bm, Cm, D, z, dt_bias, spans, saved.T,
+                                               saved.softplus)
     dev, ty = u.device, u.dtype
     states = (shape.B, shape.C, shape.N)
+    # (the kernel reads the states of as many rows as the inputs have)
+    if not isinstance(saved.ckpt, torch.Tensor):
+        raise TypeError("saved.ckpt must be a torch.Tensor")
+    _scratch(saved.ckpt, save_bytes, u, "saved.ckpt")
     _dense("dy", dy, u.shape, ty, dev)
     if dS_T is not None:
         _dense("dS_T", dS_T, states, torch.float32, dev)
