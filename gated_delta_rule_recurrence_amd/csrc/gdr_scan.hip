@@ -814,6 +814,13 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
           const float* const cp = Cs[buf] + s * NP + r * NPL;
           float v[2 * NPL];
           sB[e] = sA[e] = 0.f;
+          // A step past the end passes E on and adds nothing.  It is skipped:
+          // its delta and slope of 0 times an infinite rate, state or product
+          // would be NaN in dA and ddt_bias.  (A branch the whole wave takes:
+          // 4 x 4096 x 4096 985 -> 1005 us a backward pass, N = 64 at 2048 x
+          // 4096 630 -> 602; masks, or a form of their own for last tiles,
+          // push the kernel past its registers: 1480.)
+          if (s > 0 && s >= left) return;
 #pragma unroll
           for (int i = 0; i < NPL; ++i) {
             const float prev = s > 0 ? h[s > 0 ? s - 1 : 0][i] : h0[i];

@@ -1,0 +1,67 @@
+"""GPU tests of the convolution, the scan and the norm at their edges:
+infinities beside the steps that pad a tile, steps that change nothing,
+outputs over inputs, partial sums of packed rows, the measurement hook."""
+import numpy as np
+import pytest
+
+import oracle.layer_oracle as L
+from test_gpu_layer_ops import ARGS, F32, GRADS, check, dev_of, same, scan_inputs, small_state
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- scan: the steps that pad a sequence's last tile ------------------------------
+
+@pytest.mark.parametrize("T", [1, 3, 21, 150])
+def test_infinite_rates_backward(cuda, T):
+    """A = -inf is what the lowest finite rates are, in every gradient: the
+    adjoint of the last state passes the padding steps, whose decay is 1."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    u, dt, A, Bm, Cm, D, z, bias, S0 = small_state(cuda)["scan"]
+    u, dt, Bm, Cm, z = [t[:, :T].contiguous() for t in (u, dt, Bm, Cm, z)]
+    dy = small_state(cuda)["dy"][:, :T].contiguous()
+    dS_T = 3 * torch.randn(S0.shape, device=cuda, generator=torch.Generator(device=cuda).manual_seed(1))
+    got = []
+    for rate in (-float("inf"), -1e30):
+        A = A.clone()
+        A[::3] = rate
+        args = u, dt, A, Bm, Cm, D, z, bias
+        y, S_T, saved = ops.gdr_scan_forward(*args, S0)
+        grads = ops.gdr_scan_backward(*args, saved, dy, dS_T)
+        for name, g in zip(GRADS, grads):
+            assert torch.isfinite(g).all(), name
+        got.append([y, S_T, *grads])
+    assert same(*got)
+
+
+@pytest.mark.parametrize("N", [1, 7, 16, 40])
+@pytest.mark.parametrize("T", [1, 3, 21, 150])
+def test_an_infinite_last_input(cuda, N, T):
+    """u = inf in the last step makes the last state infinite.  dA, dS0, du
+    and the earlier ddt do not depend on that state and are those of the
+    formula; ddt of the last step and its sum are infinite, not NaN."""
+    from gated_delta_rule_recurrence_amd import ops
+    C, B = 40, 2
+    p = scan_inputs("f32", B, B * T, C, N, 1, T)
+    for b in range(B):
+        p["u"][(b + 1) * T - 1, 3::5] = np.inf
+    d = {k: dev_of(v, "f32", cuda) for k, v in p.items()}
+    d = {k: v.view(B, T, *v.shape[1:]) if k not in F32 else v for k, v in d.items()}
+    _, _, saved = ops.gdr_scan_forward(*[d[k] for k in ARGS])
+    got = dict(zip(GRADS, ops.gdr_scan_backward(*[d[k] for k in ARGS[:8]], saved, d["dy"], d["dS_T"])))
+    args = [p[k] for k in ARGS] + [True, [(b * T, (b + 1) * T) for b in range(B)]]
+    with np.errstate(invalid="ignore"):
+        ref, mag = (L.scan_backward(*args, p["dy"], p["dS_T"], mag=m) for m in (False, True))
+    n = 2 * (128 + 4 * T)
+    check("dA", got["dA"], ref["dA"], mag["dA"], "f32", n + B * T)
+    check("dS0", got["dS0"], ref["dS0"], mag["dS0"], "f32", n)
+    check("du", got["du"], ref["du"], mag["du"], "f32", n + 128)
+    ddt = got["ddt"].double().cpu().numpy().reshape(B * T, C)
+    finite = np.isfinite(ref["ddt"])
+    assert finite.sum() == B * (T * C - 8) and (ddt[~finite] == ref["ddt"][~finite]).all()
+    off = np.abs(ddt - ref["ddt"])[finite]
+    assert (off <= (n + 129) * 2.0 ** -24 * mag["ddt"][finite]).all()
+    total, want = got["ddt_bias"].double().cpu().numpy(), ref["ddt_bias"]
+    assert (np.isinf(total) | np.isnan(want))[3::5].all() and np.isfinite(np.delete(total, np.s_[3::5])).all()
+    assert (total[np.isinf(want)] == want[np.isinf(want)]).all()
