@@ -597,7 +597,11 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs a) {
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      h[i] = fmaf(exp2_hw(dl2 * A[i]), h[i], du * B[i]);
+      // a step of delta = 0 changes nothing, at an infinite rate too (as
+      // load_rates has it; here that would wait for A before the step's loads:
+      // 48 tokens 8.24 us without, 8.32 so, 8.39 with it)
+      const float e = dl2 == 0.f ? 0.f : dl2 * A[i];
+      h[i] = fmaf(exp2_hw(e), h[i], du * B[i]);
       acc = fmaf(C[i], h[i], acc);
     }
     const float gate = silu(z);

@@ -65,3 +65,28 @@ def test_an_infinite_last_input(cuda, N, T):
     total, want = got["ddt_bias"].double().cpu().numpy(), ref["ddt_bias"]
     assert (np.isinf(total) | np.isnan(want))[3::5].all() and np.isfinite(np.delete(total, np.s_[3::5])).all()
     assert (total[np.isinf(want)] == want[np.isinf(want)]).all()
+
+
+# ---- scan: a step of delta = 0 -----------------------------------------------------
+
+@pytest.mark.parametrize("T", [1, 4, 5, 40])
+@pytest.mark.parametrize("N", [3, 16, 33])
+@pytest.mark.parametrize("softplus", [False, True])
+def test_no_step_keeps_the_state(cuda, T, N, softplus):
+    """delta = 0 is an identity step whatever the rate, A = -inf too, in the
+    kernel of few steps as in the tiled one: S_T is S0 and y reads it."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    C, B = 70, 2
+    g = torch.Generator(device=cuda).manual_seed(T)
+    S0 = torch.randn(B, C, N, device=cuda, generator=g)
+    A = -torch.exp(torch.randn(C, N, device=cuda, generator=g))
+    A[::3] = -float("inf")
+    u, Cm = torch.randn(B, T, C, device=cuda, generator=g), torch.randn(B, T, 1, N, device=cuda, generator=g)
+    # (e^-200 is 0 in 32 bits)
+    dt = torch.full((B, T, C), -200.0 if softplus else 0.0, device=cuda)
+    y, S_T, _ = ops.gdr_scan_forward(u, dt, A, Cm, Cm, S0=S0, softplus=softplus)
+    assert torch.equal(S_T, S0)
+    ref = torch.einsum("btn,bcn->btc", Cm[:, :, 0].double().cpu(), S0.double().cpu())
+    mag = torch.einsum("btn,bcn->btc", Cm[:, :, 0].double().cpu().abs(), S0.double().cpu().abs())
+    assert ((y.double().cpu() - ref).abs() <= (N + 4) * 2.0 ** -24 * mag).all()
