@@ -19,6 +19,7 @@ GDR_DECAY_LOG = 1
 GDR_ACT_NONE = 0
 GDR_ACT_SILU = 1
 CONV_MAX_TAPS = 8  # GDR_CONV_MAX_TAPS
+CONV_IN_PLACE_STEPS = 16  # GDR_CONV_IN_PLACE_STEPS
 SCAN_MAX_STATES = 64  # GDR_SCAN_MAX_STATES
 
 # entry points declared in include/gdr.h, with their ctypes signatures
@@ -185,6 +186,7 @@ def forward_noalloc_raw(shape, q, k, v, g, beta, S0, y, S_T, ckpt, stream, mask=
 NOALLOC_SCRATCH_BYTES = 128 << 20  # GDR_NOALLOC_SCRATCH_BYTES
 GDR_ERR_SCRATCH_LIMIT = -12
 GDR_ERR_BAD_COUNT = -13
+GDR_ERR_OVERLAP = -18
 MAX_LAUNCH_EVENTS = 8  # GDR_MAX_LAUNCH_EVENTS
 
 

@@ -542,6 +542,9 @@ const char* gdr_strerror(int status) {
     case GDR_ERR_BAD_STRIDE: return "a row stride is below the row's width or above its limit";
     case GDR_ERR_BAD_ACT: return "act must be GDR_ACT_NONE or GDR_ACT_SILU, softplus 0 or 1";
     case GDR_ERR_BAD_EPS: return "eps must be finite and >= 0";
+    case GDR_ERR_OVERLAP:
+      return "a convolution's output rows overlap its input rows (allowed in place, dense, for at "
+             "most GDR_CONV_IN_PLACE_STEPS steps)";
   }
   return "unknown gdr status";
 }

@@ -339,7 +339,7 @@ hipError_t fwd(const ConvArgs& a, hipStream_t s) {
   // 78 at 48; one sequence of 2048: 27 us at 28 steps, 30 at 16, 32 at 48)
   const int64_t waves = (int64_t)cblocks * (kThreads / 64) * a.B;
   int64_t steps = waves * a.T / 2048;
-  steps = steps < 16 ? 16 : (steps > 32 ? 32 : steps);
+  steps = steps < kConvTile ? kConvTile : (steps > 32 ? 32 : steps);
   int64_t tiles = (a.T + steps - 1) / steps;
   while (tiles * cblocks > kMaxGrid) {
     steps *= 2;
@@ -409,7 +409,7 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 // strides.
 int conv_bwd_steps(int64_t B, int64_t T, int64_t C) {
   const int64_t waves = (C + 255) / 256 * B;
-  int64_t steps = waves * T / 32 >= 3200 ? 32 : 16;
+  int64_t steps = waves * T / 32 >= 3200 ? 32 : kConvTile;
   // the grid's x dimension holds (tiles / 4) x (channel blocks, at most one
   // per 64 channels)
   while ((T + 4 * steps - 1) / (4 * steps) * ((C + 63) / 64) > kMaxGrid) steps *= 2;

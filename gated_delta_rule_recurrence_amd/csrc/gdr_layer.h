@@ -31,6 +31,10 @@ struct ConvArgs {
   void* dstate;       // or null
   float* part;        // [parts][K+1][C]
 };
+// Fewest steps of a tile, in either direction: a sequence of no more is
+// marched through by one thread per channel, which reads a row before it
+// writes the output over it.
+constexpr int kConvTile = 16;
 // Steps a wave takes in the backward, and the partial sums that leaves.
 int conv_bwd_steps(int64_t B, int64_t T, int64_t C);
 int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C);

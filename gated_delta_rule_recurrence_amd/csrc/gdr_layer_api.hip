@@ -209,6 +209,20 @@ int rows_ok(int64_t B, int64_t T, int64_t rows, const int32_t* spans) {
   return spans == nullptr && rows != B * T ? GDR_ERR_BAD_DIM : GDR_OK;
 }
 
+// The rows [rows][C] of q, `stride` elements apart, against the dense output
+// rows at p: apart, or the same ones of sequences that are one tile each.
+static_assert(gdr::kConvTile == GDR_CONV_IN_PLACE_STEPS, "what the header promises");
+int over_rows_ok(const gdr_conv_shape& s, const void* q, int64_t stride, const void* p) {
+  const uintptr_t size = s.dtype == GDR_BF16 ? 2 : 4, width = s.C * size, step = stride * size;
+  const uintptr_t in = reinterpret_cast<uintptr_t>(q), out = reinterpret_cast<uintptr_t>(p);
+  const uintptr_t bytes = s.rows * width;
+  if (out + bytes <= in || out >= in + (s.rows - 1) * step + width) return GDR_OK;
+  if (out == in && stride == s.C && s.T <= GDR_CONV_IN_PLACE_STEPS) return GDR_OK;
+  // (between two rows of q)
+  if (out > in && (out - in) % step >= width && (out - in) % step + bytes <= step) return GDR_OK;
+  return GDR_ERR_OVERLAP;
+}
+
 int conv_forward(const gdr_conv_shape* shape, const void* x, const void* w, const void* bias,
                  const void* state, const int32_t* spans, void* y, void* state_out,
                  void* stream) {
@@ -218,6 +232,7 @@ int conv_forward(const gdr_conv_shape* shape, const void* x, const void* w, cons
   const bool has_rows = s.B > 0 && s.T > 0 && s.rows > 0;
   if (st == GDR_OK) st = pointers_ok({x, w, static_cast<const void*>(y)}, has_rows);
   if (st == GDR_OK) st = alignment_ok({x, w, bias, state, spans, y, state_out});
+  if (st == GDR_OK && has_rows) st = over_rows_ok(s, x, s.x_stride, y);
   if (st != GDR_OK) return st;
   if (s.B == 0 || (!has_rows && (state_out == nullptr || s.K == 1))) return GDR_OK;
   if (w == nullptr) return GDR_ERR_NULL_ARG;
@@ -252,6 +267,8 @@ int conv_backward(const gdr_conv_shape* shape, const void* x, const void* w, con
   if (st == GDR_OK)
     st = alignment_ok({x, w, bias, state, spans, dy, dstate_out, dx, dw, dbias, dstate,
                        static_cast<const void*>(workspace)});
+  if (st == GDR_OK && has_rows) st = over_rows_ok(s, x, s.x_stride, dx);
+  if (st == GDR_OK && has_rows) st = over_rows_ok(s, dy, s.C, dx);
   if (st != GDR_OK) return st;
   if (s.B == 0) return GDR_OK;
   if (workspace_bytes < (size_t)need) return GDR_ERR_WORKSPACE;

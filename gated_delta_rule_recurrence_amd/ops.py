@@ -432,7 +432,7 @@ def gdr_conv_forward(x, weight, bias=None, state=None, *, act="silu", spans=None
 
     x [B,T,C] (or rows, see above), weight [C,K], bias [C] or None, state
     [B,K-1,C] (the inputs before each sequence) or None.  state_out may be
-    state (in place)."""
+    state (in place), and y may be x for at most 16 steps a sequence."""
     shape, _ = _conv_sizes(x, weight, bias, state, spans, T, act)
     dev, dt = x.device, x.dtype
     y = _rows_out(y, "y", x, spans)

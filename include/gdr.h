@@ -68,7 +68,9 @@ typedef enum {
   GDR_ERR_BAD_STRIDE = -15,     /* a row stride below the row's width or
                                    above 2^31 - 1 (2^25 for a scan)         */
   GDR_ERR_BAD_ACT = -16,        /* act is not a gdr_act, or softplus not 0, 1 */
-  GDR_ERR_BAD_EPS = -17         /* eps negative, infinite or NaN             */
+  GDR_ERR_BAD_EPS = -17,        /* eps negative, infinite or NaN             */
+  GDR_ERR_OVERLAP = -18         /* a convolution's output rows overlap its
+                                   input rows in a way not allowed there    */
 } gdr_status;
 
 /* Size of the device-side scratch array behind gdr_forward_noalloc (128 MiB;
@@ -230,7 +232,8 @@ int gdr_set_launch_events(void* const* events, int n);
  * convolution that makes its q, k, v, the selective state space scan (the
  * sibling recurrence, with a diagonal state per channel) and the group norm
  * with a gate behind it.  Ownership, streams, errors and determinism as
- * above; every data pointer is 16-byte aligned.
+ * above; every data pointer is 16-byte aligned.  Outputs and workspaces overlap
+ * no input and no other output except where it says so.
  *
  * Rows.  Activations are rows [rows][width] of one element type; x, u, dt, z,
  * B and C may be slices of wider rows (a *_stride field: elements from one
@@ -253,6 +256,7 @@ typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_act; /* x, x / (1 + e^-x
  * 1 <= K <= GDR_CONV_MAX_TAPS, 1 <= C <= 2^20, B <= 65535, T and rows at most
  * 2^30 - 1. */
 #define GDR_CONV_MAX_TAPS 8
+#define GDR_CONV_IN_PLACE_STEPS 16
 typedef struct {
   int64_t B, T, rows, C, K;
   int64_t x_stride;      /* 0 = C */
@@ -265,7 +269,9 @@ typedef struct {
  *        (dtype; NULL: 0), spans (NULL: dense)
  *   out: y [rows][C]; state_out [B][K-1][C]: the last K - 1 inputs of each
  *        sequence, its state included (NULL: not written).  state_out may be
- *        state (in place).
+ *        state (in place).  y may be x where T <= GDR_CONV_IN_PLACE_STEPS and
+ *        x is dense; longer sequences are cut into tiles that read each
+ *        other's rows, so a y that overlaps x is refused.
  * Single tokens are calls with T = 1 that pass the state along. */
 int gdr_conv_forward(const gdr_conv_shape* shape, const void* x, const void* weight,
                      const void* bias, const void* state, const int32_t* spans, void* y,
@@ -276,7 +282,8 @@ int gdr_conv_backward_workspace_bytes(const gdr_conv_shape* shape, size_t* out);
 /* VJP of gdr_conv_forward for <dy, y> + <dstate_out, state_out> (dstate_out
  * NULL: 0).  dx [rows][C]; dweight [C][K], dbias [C] (NULL: not written), in
  * wdtype, summed in fp32 in a fixed order; dstate [B][K-1][C] (NULL: not
- * written; not the dstate_out buffer).  Nothing is saved by the forward:
+ * written; not the dstate_out buffer).  dx overlaps dy or x only as y may x
+ * in the forward.  Nothing is saved by the forward:
  * s_t is formed again from x. */
 int gdr_conv_backward(const gdr_conv_shape* shape, const void* x, const void* weight,
                       const void* bias, const void* state, const int32_t* spans, const void* dy,

@@ -90,3 +90,41 @@ def test_no_step_keeps_the_state(cuda, T, N, softplus):
     ref = torch.einsum("btn,bcn->btc", Cm[:, :, 0].double().cpu(), S0.double().cpu())
     mag = torch.einsum("btn,bcn->btc", Cm[:, :, 0].double().cpu().abs(), S0.double().cpu().abs())
     assert ((y.double().cpu() - ref).abs() <= (N + 4) * 2.0 ** -24 * mag).all()
+
+
+# ---- convolution: y over x ---------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,C", [("bf16", 2056), ("bf16", 33), ("f32", 1500)])
+@pytest.mark.parametrize("T", [1, 7, 16])
+def test_conv_over_its_input(cuda, dtype, C, T):
+    """Up to 16 steps y may be x; more are refused, and so is a part of x."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib, ops
+    g = torch.Generator(device=cuda).manual_seed(T)
+    n = lambda *s: torch.randn(*s, device=cuda, generator=g).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    x, w, b, st = n(5, T, C), n(C, 4), n(C), n(5, 3, C)
+    y, so = ops.gdr_conv_forward(x, w, b, st)
+    mine = x.clone()
+    y1, so1 = ops.gdr_conv_forward(mine, w, b, st, y=mine)
+    assert y1 is mine and torch.equal(y, y1) and torch.equal(so, so1)
+    spans = torch.tensor([[0, T], [T, T], [2 * T, 3 * T]], dtype=torch.int32, device=cuda)
+    rows = x.view(5 * T, C)
+    y, so = ops.gdr_conv_forward(rows, w, b, st[:3], spans=spans, T=T, y=rows.clone())
+    mine = rows.clone()
+    y1, so1 = ops.gdr_conv_forward(mine, w, b, st[:3], spans=spans, T=T, y=mine)
+    assert torch.equal(y, y1) and torch.equal(so, so1)
+    mine = n(17, C)
+    with pytest.raises(_lib.GdrError, match="overlap"):
+        ops.gdr_conv_forward(mine, w, b, T=17, y=mine)
+
+
+def test_conv_between_its_rows(cuda):
+    """A y in the gap between x's rows overlaps none of them."""
+    import torch
+    from gated_delta_rule_recurrence_amd import ops
+    w = torch.randn(32, 4, device=cuda)
+    wide = torch.randn(2, 2048, device=cuda)
+    want, _ = ops.gdr_conv_forward(wide[:, :32].contiguous(), w, T=2)
+    y = wide[0, 64:128].view(2, 32)
+    got, _ = ops.gdr_conv_forward(wide[:, :32], w, T=2, y=y)
+    assert got is y and torch.equal(got, want)

@@ -55,3 +55,35 @@ def test_scan_backward_checks_the_saved_buffer(on_cpu):
     with pytest.raises(TypeError, match="saved.ckpt"):
         ops.gdr_scan_backward(*many, saved, many[0])
     assert on_cpu[2:] == ["gdr_scan_forward"]
+
+
+# ---- rows over rows (never launched: refused calls only, at made-up addresses) -----
+
+X, FAR = 1 << 20, 1 << 40
+
+
+def conv_shape(B, T, C, stride=0, bf16=False, K=4):
+    dt = _lib.GDR_BF16 if bf16 else _lib.GDR_F32
+    return _lib.GdrConvShape(B, T, B * T, C, K, stride, dt, dt, _lib.GDR_ACT_SILU, 0)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("B,T,C,stride,x,y", [
+    (2, 17, 32, 0, X, X),              # in place, more than one tile
+    (1, 16, 32, 40, X, X),             # one tile, but not the same rows
+    (1, 16, 32, 0, X, X + 16),         # one tile, shifted
+    (1, 40, 32, 0, X + 16, X),
+    (1, 40, 32, 0, X, X + 40 * 64 - 16),   # the last bytes of either type
+    (1, 40, 32, 0, X + 40 * 64 - 16, X),
+    (2, 40, 32, 512, X, X + 512),      # dense rows that run into x's next ones
+])
+def test_conv_refuses_rows_over_rows(lib, B, T, C, stride, x, y, bf16):
+    s = conv_shape(B, T, C, stride, bf16)
+    far = [FAR + (k << 30) for k in range(8)]
+    assert _lib.layer_raw("gdr_conv_forward", s, (x, far[0], far[1], 0, 0, y, 0), 0) == _lib.GDR_ERR_OVERLAP
+    assert "overlap" in _lib.strerror(_lib.GDR_ERR_OVERLAP)
+    n = _lib.size_of("gdr_conv_backward_workspace_bytes", s)
+    ptrs = lambda x, dy, dx: (x, far[0], far[1], 0, 0, dy, 0, dx, far[2], far[3], 0, far[4])
+    assert _lib.layer_raw("gdr_conv_backward", s, ptrs(x, far[5], y), 0, n) == _lib.GDR_ERR_OVERLAP
+    if stride == 0:
+        assert _lib.layer_raw("gdr_conv_backward", s, ptrs(far[5], x, y), 0, n) == _lib.GDR_ERR_OVERLAP
