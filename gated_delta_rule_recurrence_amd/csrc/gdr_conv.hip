@@ -182,6 +182,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
   const Span sp = uniform_span(a, b);
   const int64_t t0l = ((int64_t)group * 4 + q) * steps;
   const bool first = t0l == 0;
+  // (numbered through the pieces: a workgroup past the sequence has no sums)
+  if (a.packed && group > 0 && (int64_t)group * 4 * steps >= sp.len) return;
   const bool any = cok && (first || t0l < sp.len);
 
   float dw[K][V], db[V];
@@ -297,8 +299,13 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
     }
   }
   __syncthreads();
-  if (q == 0 && cok) {
-    const int64_t part = (int64_t)b * (gridDim.x / cblocks) + group;
+  if (q > 0) return;
+  int64_t part = (int64_t)b * (gridDim.x / cblocks) + group;
+  if (a.packed) {
+    part = pieces_before(a.spans, b, a.T, a.rows, 4 * steps) + group;
+    if (sp.len == 0 || part >= a.parts) return;  // (parts: of sequences that overlap)
+  }
+  if (cok) {
     float* const p = a.part + part * (K + 1) * a.C + cc;
 #pragma unroll
     for (int j = 0; j <= K; ++j)
@@ -311,18 +318,23 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int cblo
   }
 }
 
-struct ConvSumStore {
-  void* dw;
-  void* dbias;
-  int C, K, w_bf16;
-  __device__ void operator()(int64_t i, float x) const {
-    const int j = (int)(i / C), c = (int)(i % C);
-    if (j < K)
-      st_weight(dw, (int64_t)c * K + j, x, w_bf16);
-    else if (dbias != nullptr)
-      st_weight(dbias, c, x, w_bf16);
+// dw and dbias from the partial sums.
+__global__ __launch_bounds__(kThreads) void conv_sums(ConvArgs a) {
+  int64_t parts = a.parts;
+  if (a.packed) {
+    const int64_t used = pieces_before(a.spans, a.B, a.T, a.rows, 4 * a.steps);
+    parts = used < parts ? used : parts;
   }
-};
+  const int64_t i = (int64_t)blockIdx.x * kSumCols + threadIdx.x % kSumCols;
+  const int64_t width = (int64_t)(a.K + 1) * a.C;
+  const float x = column_sum(a.part, parts, width, i);
+  if (threadIdx.x >= kSumCols || i >= width) return;
+  const int j = (int)(i / a.C), c = (int)(i % a.C);
+  if (j < a.K)
+    st_weight(a.dw, (int64_t)c * a.K + j, x, a.w_bf16);
+  else if (a.dbias != nullptr)
+    st_weight(a.dbias, c, x, a.w_bf16);
+}
 
 template <typename T>
 bool vectors(const ConvArgs& a) {
@@ -360,18 +372,26 @@ hipError_t fwd(const ConvArgs& a, hipStream_t s) {
   return e;
 }
 
+// Workgroups along a sequence, at least one: four waves of `steps` each.
+int64_t conv_groups(int64_t T, int64_t steps) {
+  const int64_t groups = (T + 4 * steps - 1) / (4 * steps);
+  return groups < 1 ? 1 : groups;
+}
+
 template <typename T, int K, int V>
 hipError_t bwd(const ConvArgs& a, hipStream_t s) {
   const int cblocks = (a.C + 64 * V - 1) / (64 * V);
-  const int steps = conv_bwd_steps(a.B, a.T, a.C);
-  const int64_t parts = conv_bwd_parts(a.B, a.T, a.C);
-  hipLaunchKernelGGL((conv_bwd_kernel<T, K, V>), dim3((unsigned)(parts / a.B * cblocks), a.B),
-                     dim3(kThreads), 0, s, a, cblocks, steps);
+  hipLaunchKernelGGL((conv_bwd_kernel<T, K, V>),
+                     dim3((unsigned)(conv_groups(a.T, a.steps) * cblocks), a.B), dim3(kThreads), 0,
+                     s, a, cblocks, a.steps);
   hipError_t e = hipGetLastError();
   note_launch(s);
   if (e != hipSuccess) return e;
-  return launch_column_sums(a.part, parts, (int64_t)(K + 1) * a.C,
-                            ConvSumStore{a.dw, a.dbias, a.C, K, a.w_bf16}, s);
+  const int64_t blocks = ((int64_t)(K + 1) * a.C + kSumCols - 1) / kSumCols;
+  hipLaunchKernelGGL(conv_sums, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+  e = hipGetLastError();
+  note_launch(s);
+  return e;
 }
 
 template <typename T, bool BWD, int K>
@@ -407,19 +427,24 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 // for that, 11.2 at 16, 12 at 24, 13 at 32.  Sized for vector loads: it
 // sizes a workspace too, which must not depend on the current device or on
 // strides.
-int conv_bwd_steps(int64_t B, int64_t T, int64_t C) {
-  const int64_t waves = (C + 255) / 256 * B;
-  int64_t steps = waves * T / 32 >= 3200 ? 32 : kConvTile;
+//
+// Packed sequences count for the rows they can have.  Their workgroups' sums
+// are numbered through the pieces that the sequences are cut into where that
+// bounds them lower than B times the longest sequence (14336 channels: 64
+// sequences in 65536 rows, T not stated, 165 MB of sums instead of 9.4 GB;
+// seven prompts in 6000 rows, 156 us instead of 161, T not stated 196).
+void conv_bwd_plan(int64_t B, int64_t T, int64_t rows, int64_t C, ConvArgs* a) {
+  const int64_t all = B * T < rows ? B * T : rows;
+  int64_t steps = (C + 255) / 256 * all / 32 >= 3200 ? 32 : kConvTile;
   // the grid's x dimension holds (tiles / 4) x (channel blocks, at most one
   // per 64 channels)
-  while ((T + 4 * steps - 1) / (4 * steps) * ((C + 63) / 64) > kMaxGrid) steps *= 2;
-  return (int)steps;
-}
-
-int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C) {
-  const int64_t steps = 4 * (int64_t)conv_bwd_steps(B, T, C);
-  const int64_t groups = (T + steps - 1) / steps;
-  return B * (groups < 1 ? 1 : groups);
+  while (conv_groups(T, steps) * ((C + 63) / 64) > kMaxGrid) steps *= 2;
+  a->steps = (int)steps;
+  int64_t pieces = rows / (4 * steps) + B;
+  if (pieces > rows) pieces = rows < 1 ? 1 : rows;
+  a->parts = B * conv_groups(T, steps);
+  a->packed = pieces < a->parts;
+  if (a->packed) a->parts = pieces;
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, bool is_bf16, hipStream_t s) {

@@ -29,15 +29,17 @@ struct ConvArgs {
   void* dw;
   void* dbias;        // or null
   void* dstate;       // or null
+  int steps;          // of one wave
+  int64_t parts;      // partial sums
+  int packed;         // numbered through the sequences' pieces (pieces_before)
   float* part;        // [parts][K+1][C]
 };
 // Fewest steps of a tile, in either direction: a sequence of no more is
 // marched through by one thread per channel, which reads a row before it
 // writes the output over it.
 constexpr int kConvTile = 16;
-// Steps a wave takes in the backward, and the partial sums that leaves.
-int conv_bwd_steps(int64_t B, int64_t T, int64_t C);
-int64_t conv_bwd_parts(int64_t B, int64_t T, int64_t C);
+// The backward's steps, parts and packed for a's B, T, rows and C.
+void conv_bwd_plan(int64_t B, int64_t T, int64_t rows, int64_t C, ConvArgs* a);
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs& a, bool bf16, hipStream_t s);
 
@@ -141,6 +143,19 @@ __device__ __forceinline__ Span span_of(const int32_t* spans, int b, int T, int6
   int64_t n = e - s;
   n = n < 0 ? 0 : (n > T ? T : n);
   return Span{s, (int)n};
+}
+
+// Pieces of n steps that the sequences before b are cut into, summed by the
+// 64 lanes of a wave.  Disjoint sequences have at most rows / n + B pieces,
+// and at most one a row.
+__device__ __forceinline__ int64_t pieces_before(const int32_t* spans, int b, int T, int64_t rows,
+                                                 int n) {
+  int64_t s = 0;
+  for (int i = threadIdx.x & 63; i < b; i += 64)
+    s += ((int64_t)span_of(spans, i, T, rows).len + n - 1) / n;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) s += __shfl_xor((long long)s, m, 64);
+  return s;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -370,22 +385,4 @@ __device__ __forceinline__ float column_sum(const float* __restrict__ part, int6
     for (int k = 1; k < 16; ++k) t += red[k][tc];
   return t;
 }
-template <typename Store>
-__global__ __launch_bounds__(256) void column_sums(const float* __restrict__ part, int64_t rows,
-                                                   int64_t width, Store store) {
-  const int64_t c = (int64_t)blockIdx.x * kSumCols + threadIdx.x % kSumCols;
-  const float t = column_sum(part, rows, width, c);
-  if (threadIdx.x < kSumCols && c < width) store(c, t);
-}
-template <typename Store>
-hipError_t launch_column_sums(const float* part, int64_t rows, int64_t width, Store store,
-                              hipStream_t s) {
-  const int64_t blocks = (width + kSumCols - 1) / kSumCols;
-  hipLaunchKernelGGL((column_sums<Store>), dim3((unsigned)blocks), dim3(256), 0, s, part, rows,
-                     width, store);
-  const hipError_t e = hipGetLastError();
-  note_launch(s);
-  return e;
-}
-
 }  // namespace gdr

@@ -243,11 +243,12 @@ int conv_forward(const gdr_conv_shape* shape, const void* x, const void* w, cons
   return hip_status(gdr::launch_conv_fwd(a, s.dtype == GDR_BF16, static_cast<hipStream_t>(stream)));
 }
 
-int conv_backward_sizes(const gdr_conv_shape* shape, gdr_conv_shape* s, int64_t* bytes) {
+int conv_backward_sizes(const gdr_conv_shape* shape, gdr_conv_shape* s, gdr::ConvArgs* plan,
+                        int64_t* bytes) {
   const int st = check(shape, s);
   if (st != GDR_OK) return st;
-  const int64_t parts = gdr::conv_bwd_parts(s->B, s->T, s->C);
-  if (!product_ok(parts, (s->K + 1) * s->C * 4, bytes)) return GDR_ERR_OVERFLOW;
+  gdr::conv_bwd_plan(s->B, s->T, s->rows, s->C, plan);
+  if (!product_ok(plan->parts, (s->K + 1) * s->C * 4, bytes)) return GDR_ERR_OVERFLOW;
   return GDR_OK;
 }
 
@@ -256,8 +257,9 @@ int conv_backward(const gdr_conv_shape* shape, const void* x, const void* w, con
                   void* dx, void* dw, void* dbias, void* dstate, void* workspace,
                   size_t workspace_bytes, void* stream) {
   gdr_conv_shape s;
+  gdr::ConvArgs plan{};
   int64_t need = 0;
-  int st = conv_backward_sizes(shape, &s, &need);
+  int st = conv_backward_sizes(shape, &s, &plan, &need);
   if (st == GDR_OK) st = rows_ok(s.B, s.T, s.rows, spans);
   const bool has_rows = s.B > 0 && s.T > 0 && s.rows > 0;
   if (st == GDR_OK)
@@ -274,6 +276,9 @@ int conv_backward(const gdr_conv_shape* shape, const void* x, const void* w, con
   if (workspace_bytes < (size_t)need) return GDR_ERR_WORKSPACE;
   gdr::ConvArgs a = conv_args(s, x, w, bias, state, spans);
   if (!has_rows) a.rows = 0;
+  a.steps = plan.steps;
+  a.parts = plan.parts;
+  a.packed = plan.packed;
   a.dy = dy;
   a.dstate_out = s.K > 1 ? dstate_out : nullptr;
   a.dx = dx;
@@ -456,8 +461,9 @@ int gdr_conv_forward(const gdr_conv_shape* shape, const void* x, const void* wei
 
 int gdr_conv_backward_workspace_bytes(const gdr_conv_shape* shape, size_t* out) {
   gdr_conv_shape s;
+  gdr::ConvArgs plan{};
   int64_t bytes = 0;
-  const int st = conv_backward_sizes(shape, &s, &bytes);
+  const int st = conv_backward_sizes(shape, &s, &plan, &bytes);
   return store_size(st, bytes, out);
 }
 

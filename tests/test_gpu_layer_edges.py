@@ -128,3 +128,66 @@ def test_conv_between_its_rows(cuda):
     y = wide[0, 64:128].view(2, 32)
     got, _ = ops.gdr_conv_forward(wide[:, :32], w, T=2, y=y)
     assert got is y and torch.equal(got, want)
+
+
+# ---- partial sums of packed rows ---------------------------------------------------
+
+def many_spans(r, B, longest):
+    """B sequences with gaps, every third of few rows, some empty ones wherever
+    (0, 0) puts them, and rows behind the last."""
+    at, out = int(r.integers(0, 5)), []
+    for b in range(B):
+        n = int(r.integers(0, 4 if b % 3 else longest))
+        out.append((at, at + n) if n else (0, 0))
+        at += n + int(r.integers(0, 3)) * int(r.integers(0, 40))
+    return out, at + 3
+
+
+def outside(rows, seqs):
+    m = np.ones(rows, bool)
+    for i, j in seqs:
+        m[i:j] = False
+    return m
+
+
+def spoiled(d, seqs):
+    """NaN in the rows of no sequence."""
+    d[outside(len(d), seqs)] = float("nan")
+    return d
+
+
+def scratch(size, name, shape, device):
+    """A workspace of the size that the call asks for, full of NaN."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib
+    n = _lib.size_of(name, shape)
+    assert n <= size
+    return torch.full((n // 4,), float("nan"), device=device)
+
+
+@pytest.mark.parametrize("dtype,C", [("bf16", 40), ("f32", 36), ("f32", 33)])
+@pytest.mark.parametrize("B,longest", [(3, 700), (150, 100), (70, 300)])
+def test_conv_sums_of_packed_rows(cuda, dtype, C, B, longest):
+    """T not stated, so as long as all rows: dweight and dbias from the pieces
+    that there are, whatever the workspace held."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib, ops
+    K, r = 4, np.random.default_rng(B)
+    seqs, rows = many_spans(r, B, longest)
+    rnd = lambda *s: torch.from_numpy(r.normal(size=s)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    x, dy, w, b, st = rnd(rows, C), rnd(rows, C), rnd(C, K), rnd(C), rnd(B, K - 1, C)
+    spans = torch.tensor(seqs, dtype=torch.int32, device=cuda)
+    args = [spoiled(x.to(cuda), seqs), w.to(cuda), b.to(cuda), st.to(cuda), spoiled(dy.to(cuda), seqs)]
+    dt = _lib.GDR_BF16 if dtype == "bf16" else _lib.GDR_F32
+    shape = _lib.GdrConvShape(B, rows, rows, C, K, 0, dt, dt, _lib.GDR_ACT_SILU, 0)
+    ws = scratch((rows // 64 + B) * (K + 1) * C * 4, "gdr_conv_backward_workspace_bytes", shape, cuda)
+    got = ops.gdr_conv_backward(*args, spans=spans, want_dstate=True, workspace=ws)
+    again = ops.gdr_conv_backward(*args, spans=spans, want_dstate=True, workspace=ws)
+    assert same(got, again)
+    f = lambda t: t.double().numpy()
+    ref, mag = (L.conv_backward(f(x), f(w), f(b), f(st), True, seqs, f(dy), mag=m) for m in (False, True))
+    check("dx", got[0], ref[0], mag[0], dtype, 64)
+    check("dweight", got[1], ref[1], mag[1], dtype, 64 + rows)
+    check("dbias", got[2], ref[2], mag[2], dtype, 64 + rows)
+    check("dstate", got[3], ref[3], mag[3], dtype, 64)
+    assert not got[0][outside(rows, seqs)].any()

@@ -87,3 +87,21 @@ def test_conv_refuses_rows_over_rows(lib, B, T, C, stride, x, y, bf16):
     assert _lib.layer_raw("gdr_conv_backward", s, ptrs(x, far[5], y), 0, n) == _lib.GDR_ERR_OVERLAP
     if stride == 0:
         assert _lib.layer_raw("gdr_conv_backward", s, ptrs(far[5], x, y), 0, n) == _lib.GDR_ERR_OVERLAP
+
+
+# ---- partial sums of packed rows ---------------------------------------------------
+
+PACKS = [(64, 65536, 65536), (1000, 65536, 65536), (7, 6000, 6000), (64, 65536, 4096), (3, 300, 2 ** 30 - 1),
+         (5, 0, 300), (5, 300, 0), (1, 1, 300), (4, 2048, 512)]
+
+
+@pytest.mark.parametrize("B,rows,T", PACKS)
+def test_conv_partial_sums_follow_the_rows(lib, B, rows, T):
+    """B sequences of packed rows, T at most the longest (all rows, where
+    nobody says): one partial sum of dweight and dbias for every started piece
+    of at least 64 steps, of which disjoint sequences have rows / 64 + B at
+    most, whatever T is."""
+    C, K = 14336, 4
+    s = _lib.GdrConvShape(B, T, rows, C, K, 0, _lib.GDR_BF16, _lib.GDR_BF16, _lib.GDR_ACT_SILU, 0)
+    n = _lib.size_of("gdr_conv_backward_workspace_bytes", s)
+    assert 0 < n <= (rows // 64 + B) * (K + 1) * C * 4
