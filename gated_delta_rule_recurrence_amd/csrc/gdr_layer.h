@@ -109,7 +109,9 @@ struct ScanArgs {
   void* dz;
   float* ddt_bias;
   float* dS0;           // or null
-  float* pA;            // [B * chunks]: partial dA [C][Np], dD [C], ddt_bias [C]
+  int64_t parts;        // partial sums
+  int packed;           // numbered through the sequences' chunks (pieces_before)
+  float* pA;            // [parts]: partial dA [C][Np], dD [C], ddt_bias [C]
   float* pB;            // [2][channel tiles][rows][G][N] partial dB, dC
 };
 // Padded states per channel, steps between saved states, channels of one

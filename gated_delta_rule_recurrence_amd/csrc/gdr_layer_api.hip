@@ -104,6 +104,8 @@ int check(const gdr_norm_shape* in, gdr_norm_shape* s, gdr::NormPlan* p) {
 // ---- scan: chunks and buffers ------------------------------------------------
 struct ScanSizes {
   int64_t chunk, chunks;     // of the longest sequence
+  int64_t parts;             // partial sums of the backward
+  bool packed;
   int64_t edge, dsum, part, bc, bytes;  // byte offsets of the workspace, its size
   int64_t ckpt;              // bytes of the save buffer
 };
@@ -137,8 +139,16 @@ int scan_sizes(const gdr_scan_shape& s, bool bwd, ScanSizes* z) {
     z->bytes = z->dsum + round_up256(slots * s.C * 4);
   }
   if (bwd) {
+    // one for every chunk that the rows can have, where those are fewer than
+    // B times the longest sequence's (4096 channels of 16 states: 1000
+    // sequences in 65536 rows, T not stated, 300 MB instead of 4.7 GB)
+    int64_t pieces = s.rows / z->chunk + s.B;
+    if (pieces > s.rows) pieces = s.rows < 1 ? 1 : s.rows;
+    z->parts = s.B * z->chunks;
+    z->packed = pieces < z->parts;
+    if (z->packed) z->parts = pieces;
     z->part = z->bytes;
-    if (!product_ok(s.C * (np + 2) * 4, s.B * z->chunks, &x)) return GDR_ERR_OVERFLOW;
+    if (!product_ok(s.C * (np + 2) * 4, z->parts, &x)) return GDR_ERR_OVERFLOW;
     z->bytes += round_up256(x);
     z->bc = z->bytes;
     if (!product_ok(s.rows * 8, s.G * s.N * tiles, &x)) return GDR_ERR_OVERFLOW;
@@ -361,6 +371,8 @@ int scan_backward(const gdr_scan_shape* shape, const void* u, const void* dt, co
   a.dz = dz;
   a.ddt_bias = ddt_bias;
   a.dS0 = dS0;
+  a.parts = sz.parts;
+  a.packed = sz.packed;
   char* const w = static_cast<char*>(workspace);
   a.pA = reinterpret_cast<float*>(w + sz.part);
   a.pB = reinterpret_cast<float*>(w + sz.bc);

@@ -691,6 +691,16 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
   const Place p = place_of(a, ctiles);
   const int r = p.r, lane = threadIdx.x & 63;
   const uint32_t oh = p.cok ? (uint32_t)(p.c * NP + r * NPL) * 4u : kNoLane;
+  // the place of its partial sums (formed here: in the end it would keep the
+  // spans and sizes alive beside the tiles, 2% of the kernel), below 2^31
+  // as it is at most one a row
+  int place = (int)((int64_t)p.b * a.chunks + p.j);
+  if (a.packed) {
+    const int64_t at = pieces_before(a.spans, p.b, a.T, a.rows, a.chunk) + p.j;
+    // (past the last: of sequences that overlap)
+    place = p.j > p.last || p.sp.len == 0 || at >= a.parts ? -1 : (int)at;
+    place = __builtin_amdgcn_readfirstlane(place);
+  }
   float dA[NPL], sD = 0.f, sbias = 0.f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) dA[i] = 0.f;
@@ -866,8 +876,10 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
     if (p.j == 0 && a.dS0 != nullptr)
       store_states<NPL>(a.dS0 + ((int64_t)p.b * a.C + p.c) * a.N, a.N, r, p.cok, E);
   }
-  // partial dA, dD and ddt_bias: zeros from a chunk without steps
-  float* const part = a.pA + ((int64_t)p.b * a.chunks + p.j) * a.C * (NP + 2);
+  // partial dA, dD and ddt_bias: zeros from a chunk without steps, or none
+  // where they are numbered through the chunks that have some
+  if (place < 0) return;
+  float* const part = a.pA + (int64_t)place * a.C * (NP + 2);
   put_states<NPL>(buffer_of(part, 0, (int64_t)a.C * NP * 4), oh, dA);
   sD = quad_sum(sD);
   sbias = quad_sum(sbias);
@@ -881,7 +893,7 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
 // the chunks' partial dA, dD, ddt_bias, 16 columns and 16 chunk lanes each;
 // the others sum dB, dC of their sequence's rows over the channel tiles.
 struct SumGrid {
-  int ca, tpg, parts, NP;
+  int ca, tpg, NP;
 };
 template <typename T>
 __global__ __launch_bounds__(kThreads) void scan_sums(ScanArgs a, SumGrid g) {
@@ -889,7 +901,12 @@ __global__ __launch_bounds__(kThreads) void scan_sums(ScanArgs a, SumGrid g) {
     if (blockIdx.y > 0) return;
     const int64_t width = (int64_t)a.C * (g.NP + 2);
     const int64_t i = (int64_t)blockIdx.x * kSumCols + threadIdx.x % kSumCols;
-    const float x = column_sum(a.pA, g.parts, width, i);
+    int64_t parts = a.parts;
+    if (a.packed) {
+      const int64_t used = pieces_before(a.spans, a.B, a.T, a.rows, a.chunk);
+      parts = used < parts ? used : parts;
+    }
+    const float x = column_sum(a.pA, parts, width, i);
     if (threadIdx.x >= kSumCols || i >= width) return;
     if (i < (int64_t)a.C * g.NP) {
       const int64_t c = i / g.NP, n = i % g.NP;
@@ -961,7 +978,7 @@ hipError_t bwd(const ScanArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((scan_bwd_kernel<T, NPL>), grid, dim3(kThreads), 0, s, a, ct);
   if ((e = noted(s)) != hipSuccess) return e;
   const int64_t columns = (int64_t)a.C * (np + 2), values = (int64_t)a.T * a.G * a.N;
-  const SumGrid g{(int)((columns + kSumCols - 1) / kSumCols), ct / a.G, a.B * a.chunks, np};
+  const SumGrid g{(int)((columns + kSumCols - 1) / kSumCols), ct / a.G, np};
   int64_t blocks = g.ca + (values + kThreads - 1) / kThreads;
   if (blocks > kMaxGrid) blocks = kMaxGrid;  // (ca is at most 2^20 66 / 16)
   hipLaunchKernelGGL((scan_sums<T>), dim3((unsigned)blocks, a.B), dim3(kThreads), 0, s, a, g);

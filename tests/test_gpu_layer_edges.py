@@ -191,3 +191,34 @@ def test_conv_sums_of_packed_rows(cuda, dtype, C, B, longest):
     check("dbias", got[2], ref[2], mag[2], dtype, 64 + rows)
     check("dstate", got[3], ref[3], mag[3], dtype, 64)
     assert not got[0][outside(rows, seqs)].any()
+
+
+@pytest.mark.parametrize("dtype,C,N,G", [("bf16", 40, 16, 1), ("f32", 70, 7, 2), ("f32", 24, 40, 1)])
+@pytest.mark.parametrize("B,longest", [(3, 700), (150, 60)])
+def test_scan_sums_of_packed_rows(cuda, dtype, C, N, G, B, longest):
+    """The same for the scan, whose saved states and chunks ask for ascending
+    sequences (an empty one may lie anywhere)."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib, ops
+    seqs, rows = many_spans(np.random.default_rng(B + N), B, longest)
+    p = scan_inputs(dtype, B, rows, C, N, G, B)
+    d = {k: dev_of(v, "f32" if k in F32 else dtype, cuda) for k, v in p.items()}
+    for k in ("u", "dt", "z", "Bm", "Cm", "dy"):
+        spoiled(d[k], seqs)
+    spans = torch.tensor(seqs, dtype=torch.int32, device=cuda)
+    y, S_T, saved = ops.gdr_scan_forward(*[d[k] for k in ARGS], spans=spans)
+    dt = _lib.GDR_BF16 if dtype == "bf16" else _lib.GDR_F32
+    shape = _lib.GdrScanShape(B, rows, rows, C, N, G, 0, 0, 0, 0, 0, dt, 1)
+    ws = scratch(1 << 30, "gdr_scan_backward_workspace_bytes", shape, cuda)
+    got = [ops.gdr_scan_backward(*[d[k] for k in ARGS[:8]], saved, d["dy"], d["dS_T"], workspace=ws)
+           for _ in range(2)]
+    assert same(*got)
+    args = [p[k] for k in ARGS] + [True, seqs]
+    n = 128 + 4 * longest
+    ref, mag = (L.scan_forward(*args, mag=m) for m in (False, True))
+    check("y", y, ref[0], mag[0], dtype, n)
+    check("S_T", S_T, ref[1], mag[1], "f32", n)
+    ref, mag = (L.scan_backward(*args, p["dy"], p["dS_T"], mag=m) for m in (False, True))
+    for k, g in zip(GRADS, got[0]):
+        check(k, g, ref[k], mag[k], "f32" if k in F32 else dtype,
+              2 * n + (rows if k in ("dA", "dD", "ddt_bias") else 128))

@@ -105,3 +105,16 @@ def test_conv_partial_sums_follow_the_rows(lib, B, rows, T):
     s = _lib.GdrConvShape(B, T, rows, C, K, 0, _lib.GDR_BF16, _lib.GDR_BF16, _lib.GDR_ACT_SILU, 0)
     n = _lib.size_of("gdr_conv_backward_workspace_bytes", s)
     assert 0 < n <= (rows // 64 + B) * (K + 1) * C * 4
+
+
+@pytest.mark.parametrize("B,rows,T", PACKS)
+@pytest.mark.parametrize("C,N,G", [(4096, 16, 1), (2048, 64, 2), (100, 5, 4)])
+def test_scan_partial_sums_follow_the_rows(lib, B, rows, T, C, N, G):
+    """The same for the scan's dA, dD and ddt_bias: a partial sum for every
+    started chunk (16 steps at least), as the states between chunks have it."""
+    s = _lib.GdrScanShape(B, T, rows, C, N, G, 0, 0, 0, 0, 0, _lib.GDR_BF16, 1)
+    pad = next(p for p in (4, 8, 16, 32, 64) if p >= N)
+    pieces = rows // 16 + B + 1
+    tiles = -(-C // G // 64)  # dB, dC: one of each a tile of 64 channels
+    most = pieces * C * (pad + 2) * 4 + pieces * C * (pad + 1) * 4 + rows * 8 * G * N * tiles + 4 * 256
+    assert _lib.size_of("gdr_scan_backward_workspace_bytes", s) <= most
