@@ -222,3 +222,45 @@ def test_scan_sums_of_packed_rows(cuda, dtype, C, N, G, B, longest):
     for k, g in zip(GRADS, got[0]):
         check(k, g, ref[k], mag[k], "f32" if k in F32 else dtype,
               2 * n + (rows if k in ("dA", "dD", "ddt_bias") else 128))
+
+
+# ---- the measurement hook ----------------------------------------------------------
+
+def test_every_call_records_every_event(cuda):
+    """One call at a time, over events recorded before it: the hook's events
+    all move behind a mark set just before the call, in order, and a kernel's
+    time lies between those of two launches."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib, ops
+    s = small_state(cuda)
+    _, _, saved = ops.gdr_scan_forward(*s["scan"])
+    _, stats = ops.gdr_norm_forward(*s["norm"], groups=4)
+    calls = [  # with their kernels: 2 x 150 steps of the scan run in chunks
+        (1, lambda: ops.gdr_conv_forward(*s["conv"])),
+        (2, lambda: ops.gdr_conv_backward(*s["conv"], s["dy"])),
+        (2, lambda: ops.gdr_scan_forward(*s["scan"])),
+        (3, lambda: ops.gdr_scan_backward(*s["scan"][:8], saved, s["dy"])),
+        (1, lambda: ops.gdr_norm_forward(*s["norm"], groups=4)),
+        (2, lambda: ops.gdr_norm_backward(*s["norm"], stats, s["dy"], groups=4))]
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
+    first, mark = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    busy = torch.zeros(1 << 24, device=cuda)
+    for kernels, call in calls:
+        call()
+        torch.cuda.synchronize()
+        first.record()
+        for e in events:
+            e.record()
+        busy.add_(1)  # (tens of microseconds between the first records and the mark)
+        mark.record()
+        assert _lib.set_launch_events([e.cuda_event for e in events]) == 0
+        try:
+            call()
+        finally:
+            assert _lib.set_launch_events([]) == 0
+        torch.cuda.synchronize()
+        start = first.elapsed_time(mark)
+        times = [first.elapsed_time(e) for e in events]
+        assert start > 0 and times[0] > start, (kernels, start, times)
+        assert all(b > a for a, b in zip(times[:kernels], times[1:kernels])), (kernels, times)
+        assert all(b >= a for a, b in zip(times, times[1:])), (kernels, times)
