@@ -421,12 +421,14 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// 16 steps a wave, 32 where that still leaves 3200 waves, three a SIMD (the
-// halo and the partial sums halve): 2048 rows of 14336 bf16 channels take
-// 41.2 us at 16, 42.3 at 24, 39.5 at 32; 3 x 777 rows of 1001 in fp32, too few
-// for that, 11.2 at 16, 12 at 24, 13 at 32.  Sized for vector loads: it
-// sizes a workspace too, which must not depend on the current device or on
-// strides.
+// 16 steps a wave, 32 where that still leaves two waves a SIMD (the halo and
+// the partial sums halve).  A backward pass in us at 16 / 32 steps, by the
+// waves that 32 leave (bf16, 14336 or 4096 channels): 1792 26.7 / 27.3, 2048
+// 26.6 / 26.6, 2576 35.3 / 32.0, 3024 37.5 / 37.2, 3584 42.2 / 40.0, 4096 46.8 /
+// 42.2; fp32, 8192 channels: 2560 63.2 / 56.8, 4096 101.5 / 93.7.  The main
+// kernel over 3 x 777 rows of 1001 in fp32, too few for that: 11.2 at 16, 12 at
+// 24, 13 at 32.  Sized for vector loads: it sizes a workspace too, which must
+// not depend on the current device or on strides.
 //
 // Packed sequences count for the rows they can have.  Their workgroups' sums
 // are numbered through the pieces that the sequences are cut into where that
@@ -435,7 +437,7 @@ hipError_t launch_k(const ConvArgs& a, hipStream_t s) {
 // seven prompts in 6000 rows, 156 us instead of 161, T not stated 196).
 void conv_bwd_plan(int64_t B, int64_t T, int64_t rows, int64_t C, ConvArgs* a) {
   const int64_t all = B * T < rows ? B * T : rows;
-  int64_t steps = (C + 255) / 256 * all / 32 >= 3200 ? 32 : kConvTile;
+  int64_t steps = (C + 255) / 256 * all / 32 >= 2048 ? 32 : kConvTile;
   // the grid's x dimension holds (tiles / 4) x (channel blocks, at most one
   // per 64 channels)
   while (conv_groups(T, steps) * ((C + 63) / 64) > kMaxGrid) steps *= 2;
