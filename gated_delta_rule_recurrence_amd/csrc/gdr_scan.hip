@@ -680,7 +680,8 @@ SCAN_WAVES((NPL <= 8 ? 4 : 3)) void scan_adjoint_kernel(ScanArgs a, int ctiles) 
 // runs back over them.  One barrier a tile: the tile's B and C and its
 // waves' parts of dB, dC sit in two buffers in turn, and a tile's parts are
 // summed behind the next tile's barrier.
-template <typename T, int NPL>
+// WHOLE: every sequence ends with a tile.
+template <typename T, int NPL, bool WHOLE>
 __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void scan_bwd_kernel(
     ScanArgs a, int ctiles) {
   constexpr int TT = save_steps<NPL>();
@@ -830,11 +831,10 @@ __global__ __launch_bounds__(kThreads, (NPL <= 4 ? 3 : NPL <= 8 ? 2 : 1)) void s
           sB[e] = sA[e] = 0.f;
           // A step past the end passes E on and adds nothing.  It is skipped:
           // its delta and slope of 0 times an infinite rate, state or product
-          // would be NaN in dA and ddt_bias.  (A branch the whole wave takes:
-          // 4 x 4096 x 4096 985 -> 1005 us a backward pass, N = 64 at 2048 x
-          // 4096 630 -> 602; masks, or a form of their own for last tiles,
-          // push the kernel past its registers: 1480.)
-          if (s > 0 && s >= left) return;
+          // would be NaN in dA and ddt_bias.  (A branch the whole wave takes;
+          // masks, or a form of their own for last tiles, push the kernel past
+          // its registers: 1480 us at 4 x 4096 x 4096.)
+          if (!WHOLE && s > 0 && s >= left) return;
 #pragma unroll
           for (int i = 0; i < NPL; ++i) {
             const float prev = s > 0 ? h[s > 0 ? s - 1 : 0][i] : h0[i];
@@ -975,7 +975,14 @@ hipError_t bwd(const ScanArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((scan_adjoint_kernel<T, NPL>), grid, dim3(kThreads), 0, s, a, ct);
     if ((e = noted(s)) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_bwd_kernel<T, NPL>), grid, dim3(kThreads), 0, s, a, ct);
+  // the branch around padding steps costs the whole pass 4 x 4096 x 4096 985 ->
+  // 1005 us (16 states) and 2048 x 4096 250 -> 255 (32), nothing below; 64 states
+  // gain by it, 630 -> 602 (fewer registers alive)
+  if ((NPL == 4 || NPL == 8) && a.spans == nullptr && a.T % save_steps<NPL>() == 0)
+    hipLaunchKernelGGL((scan_bwd_kernel<T, NPL, NPL == 4 || NPL == 8>), grid, dim3(kThreads), 0, s,
+                       a, ct);
+  else
+    hipLaunchKernelGGL((scan_bwd_kernel<T, NPL, false>), grid, dim3(kThreads), 0, s, a, ct);
   if ((e = noted(s)) != hipSuccess) return e;
   const int64_t columns = (int64_t)a.C * (np + 2), values = (int64_t)a.T * a.G * a.N;
   const SumGrid g{(int)((columns + kSumCols - 1) / kSumCols), ct / a.G, np};
