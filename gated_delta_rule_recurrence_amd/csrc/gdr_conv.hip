@@ -6,8 +6,9 @@
 //   dw[j] = sum_t ds_t x_{t-(K-1)+j},  dbias = sum_t ds_t.
 // Bound by HBM bytes: x and y once (forward), x, dy and dx once (backward).
 // Measured (bf16, 14336 channels, K = 4; a large copy reaches 4.98 TB/s):
-// forward over 6000 packed rows 76 us, 4.5 TB/s; over 2048 rows 26 us, 4.5
-// TB/s; backward over those 39 us, 4.5 TB/s, and 4.8 us for the sums of dw.
+// forward over 6000 packed rows 76 us, 4.5 TB/s; over 2048 rows 27 us, 4.4
+// TB/s; backward over those 39 to 43 us, 4.1 to 4.5 TB/s, and 5 us for the sums
+// of dw.
 //
 // Mapping: a thread owns 16 bytes of neighbouring channels (8 in the backward;
 // one channel where rows or strides do not divide) and marches over a tile of
@@ -15,7 +16,7 @@
 // per tile plus a halo of K - 1 rows.  A row is a buffer whose bound is its
 // end, or nothing where there is no such row: no load and no store has a
 // branch around it, and the first loads go out together (one token for 64
-// requests: 5.6 us, of which two trips to memory, spans and then the rest,
+// requests: 5.4 us, of which two trips to memory, spans and then the rest,
 // and the launch are most; 14.7 with a wait between each kind).
 #include "gdr_layer.h"
 

@@ -11,9 +11,9 @@
 // Every state and step takes one exponential (two of a vector unit's turns)
 // and 4 (forward) or 12 (backward) products and sums: bound by the vector
 // units, not by HBM.  Measured (bf16, N = 16, at 39 T lane-operations/s): 4 x
-// 4096 x 4096, forward unsplit 444 us, 16 operations' time a state and step
-// (57% busy, one wave a SIMD), backward 201 + 795 us, 7 and 29 (92 and 99%
-// busy).  Of the backward's 29 the formula takes 14, the sums of dB and dC
+// 4096 x 4096, forward unsplit 427 us, 16 operations' time a state and step
+// (57% busy, one wave a SIMD), backward 191 + 754 us, 7 and 28 (93 and 99%
+// busy).  Of the backward's 28 the formula takes 14, the sums of dB and dC
 // over channels 4, preparing the steps 4, sums over states and broadcasts 3.
 //
 // Mapping: the four lanes of a DPP quad share a channel, NPL states each; a

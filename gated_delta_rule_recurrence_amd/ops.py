@@ -209,7 +209,9 @@ def gated_delta_rule(q, k, v, g, beta, S0=None, chunk=DEFAULT_CHUNK, log_decay=F
 #
 # Activations are rows: [B, T, ...] or, with spans, [rows, ...] (any leading
 # dimensions that collapse to one row stride, so slices of a wider projection
-# pass as they are).  spans is int32 [B, 2] on the device, the first row and
+# pass as they are; the first row lies on a 16-byte boundary).  A T given
+# without spans cuts all the rows into sequences of T, whatever their leading
+# dimensions: rows [2, 5, ...] with T = 2 are five sequences.  spans is int32 [B, 2] on the device, the first row and
 # the row past the last of each sequence, ascending and disjoint; T is then
 # the longest sequence's length (by default the number of rows, which sizes
 # grid and workspace for that).  Rows of no sequence are neither read nor

@@ -210,10 +210,11 @@ int gdr_backward(const gdr_shape* shape, const void* q, const void* k,
 /* Measurement hook, for callers that time the library's kernels one by one
  * (a profiler-free per-kernel breakdown; not needed to compute anything).
  * While n > 0, every gdr_forward, gdr_forward_noalloc and gdr_backward call
- * (and every forward and backward of the operators below) records events[i] on its stream right after launching its i-th kernel
- * (counted from 0 in each call; launches past the n-th record nothing) and,
- * when it succeeds, the events past its last launch at its end, so that each
- * event is recorded once per call.  The time between two consecutive events,
+ * (and every forward and backward of the operators below) records events[i]
+ * on its stream right after launching its i-th kernel (counted from 0 in each
+ * call; launches past the n-th record nothing) and, when it succeeds, the
+ * events past its last launch at its end, so that each event is recorded once
+ * per call.  The time between two consecutive events,
  * or between an event the caller records before the call and events[0], is
  * then one kernel's (zero past the call's last kernel).  events holds n
  * hipEvent_t handles that the caller created and owns (with timing for
@@ -242,9 +243,10 @@ int gdr_set_launch_events(void* const* events, int n);
  * Sequences.  spans = NULL: B sequences of T rows each, one after another
  * (rows = B T).  Else spans is a device array int32[B][2]: sequence b owns
  * rows spans[b][0] <= row < spans[b][1], sequences ascending and disjoint
- * (packed prompts, batches padded on either side); T is then the longest
- * sequence's length, and steps past T are not taken.  Rows of no sequence
- * are neither read nor written.  A sequence of no rows keeps its state.
+ * (packed prompts, batches padded on either side; one of no rows may stand
+ * anywhere); T is then the longest sequence's length, and steps past T are not
+ * taken.  Rows of no sequence are neither read nor written.  A sequence of no
+ * rows keeps its state.
  * Spans outside 0 .. rows are cut to that range; ones that overlap, or in
  * another order, give unspecified values.
  * ------------------------------------------------------------------------- */
@@ -295,6 +297,7 @@ int gdr_conv_backward(const gdr_conv_shape* shape, const void* x, const void* we
  *     delta_t = softplus(dt_t[c] + dt_bias[c])   (softplus = 0: the sum itself)
  *     h_t[c][n] = exp(delta_t A[c][n]) h_{t-1}[c][n] + delta_t u_t[c] B_t[g][n]
  *     y_t[c] = (sum_n C_t[g][n] h_t[c][n] + D[c] u_t[c]) * silu(z_t[c])
+ * A step of delta = 0 leaves the state as it is, where A is infinite too.
  * 1 <= N <= GDR_SCAN_MAX_STATES, C a multiple of G, C <= 2^20, B and G at
  * most 65535, T and rows at most 2^30 - 1, strides (and G N) at most 2^25. */
 #define GDR_SCAN_MAX_STATES 64
