@@ -975,9 +975,10 @@ hipError_t bwd(const ScanArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((scan_adjoint_kernel<T, NPL>), grid, dim3(kThreads), 0, s, a, ct);
     if ((e = noted(s)) != hipSuccess) return e;
   }
-  // the branch around padding steps costs the whole pass 4 x 4096 x 4096 985 ->
-  // 1005 us (16 states) and 2048 x 4096 250 -> 255 (32), nothing below; 64 states
-  // gain by it, 630 -> 602 (fewer registers alive)
+  // The branch around padding steps costs a backward pass of 4 x 4096 x 4096
+  // with 16 states 20 us (985 -> 1005), of 2048 x 4096 with 32 states 5 (250 ->
+  // 255), with fewer states nothing; with 64 states it gains (630 -> 602, fewer
+  // registers alive).
   if ((NPL == 4 || NPL == 8) && a.spans == nullptr && a.T % save_steps<NPL>() == 0)
     hipLaunchKernelGGL((scan_bwd_kernel<T, NPL, NPL == 4 || NPL == 8>), grid, dim3(kThreads), 0, s,
                        a, ct);

@@ -35,7 +35,7 @@ def test_infinite_rates_backward(cuda, T):
     assert same(*got)
 
 
-@pytest.mark.parametrize("N", [1, 7, 16, 40])
+@pytest.mark.parametrize("N", [1, 7, 16, 24, 40])
 @pytest.mark.parametrize("T", [1, 3, 21, 24, 150, 152])
 def test_an_infinite_last_input(cuda, N, T):
     """u = inf in the last step makes the last state infinite.  dA, dS0, du
@@ -116,6 +116,32 @@ def test_conv_over_its_input(cuda, dtype, C, T):
     mine = n(17, C)
     with pytest.raises(_lib.GdrError, match="overlap"):
         ops.gdr_conv_forward(mine, w, b, T=17, y=mine)
+
+
+@pytest.mark.parametrize("K", [1, 4, 8])
+@pytest.mark.parametrize("dtype,C", [("bf16", 264), ("f32", 33)])
+def test_conv_gradient_over_its_input(cuda, dtype, C, K):
+    """dx over dy, and over x, as y over x (through the C entry point, as the
+    wrapper allocates dx)."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib, ops
+    B, T = 3, 16
+    g = torch.Generator(device=cuda).manual_seed(K)
+    n = lambda *s: torch.randn(*s, device=cuda, generator=g).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    x, dy, w, b, st = n(B, T, C), n(B, T, C), n(C, K), n(C), n(B, K - 1, C)
+    want = ops.gdr_conv_backward(x, w, b, st, dy, want_dstate=True)
+    dt = _lib.GDR_BF16 if dtype == "bf16" else _lib.GDR_F32
+    shape = _lib.GdrConvShape(B, T, B * T, C, K, 0, dt, dt, _lib.GDR_ACT_SILU, 0)
+    size = _lib.size_of("gdr_conv_backward_workspace_bytes", shape)
+    ws = torch.empty(size, dtype=torch.uint8, device=cuda)
+    for over in (x, dy):
+        mine = over.clone()
+        ins = [mine if t is over else t for t in (x, dy)]
+        dw, db, ds = torch.empty_like(w), torch.empty_like(b), torch.empty_like(st)
+        ptrs = [t.data_ptr() for t in (ins[0], w, b, st)] + [0, ins[1].data_ptr(), 0]
+        ptrs += [t.data_ptr() for t in (mine, dw, db, ds, ws)]
+        assert _lib.layer_raw("gdr_conv_backward", shape, ptrs, torch.cuda.current_stream().cuda_stream, size) == 0
+        assert same([mine, dw, db, ds], want)
 
 
 def test_conv_between_its_rows(cuda):
