@@ -21,6 +21,8 @@ GDR_ACT_SILU = 1
 CONV_MAX_TAPS = 8  # GDR_CONV_MAX_TAPS
 CONV_IN_PLACE_STEPS = 16  # GDR_CONV_IN_PLACE_STEPS
 SCAN_MAX_STATES = 64  # GDR_SCAN_MAX_STATES
+LIN_MAX_DIM = 256  # GDR_LIN_MAX_DIM
+RES_MAX_CHANNELS = 8192  # GDR_RES_MAX_CHANNELS
 
 # entry points declared in include/gdr.h, with their ctypes signatures
 _c_shape_p = None  # set below
@@ -58,6 +60,21 @@ class GdrNormShape(ctypes.Structure):
                                                  "act")])
 
 
+class GdrLinShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "rows", "Hk", "Hv", "Dk", "Dv", "q_stride",
+                                               "k_stride", "v_stride", "g_stride")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int32) for n in ("dtype", "gdtype", "per_head")])
+
+
+class GdrResShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "C", "gate_rows", "x_stride", "r_stride",
+                                               "gate_stride")]
+                + [(n, ctypes.c_float) for n in ("alpha", "eps", "weight_offset")]
+                + [(n, ctypes.c_int32) for n in ("dtype", "rdtype", "wdtype", "gdtype", "post",
+                                                 "pre", "center")])
+
+
 _vp = ctypes.c_void_p
 
 
@@ -93,6 +110,14 @@ _SIGNATURES = {
     "gdr_norm_forward": _call(GdrNormShape, 6),
     "gdr_norm_backward_workspace_bytes": _size_query(GdrNormShape),
     "gdr_norm_backward": _call(GdrNormShape, 11, workspace=True),
+    "gdr_lin_checkpoint_bytes": _size_query(GdrLinShape),
+    "gdr_lin_forward_workspace_bytes": _size_query(GdrLinShape),
+    "gdr_lin_backward_workspace_bytes": _size_query(GdrLinShape),
+    "gdr_lin_forward": _call(GdrLinShape, 10, workspace=True),
+    "gdr_lin_backward": _call(GdrLinShape, 14, workspace=True),
+    "gdr_res_forward": _call(GdrResShape, 10),
+    "gdr_res_backward_workspace_bytes": _size_query(GdrResShape),
+    "gdr_res_backward": _call(GdrResShape, 18, workspace=True),
     "gdr_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "gdr_version": (ctypes.c_char_p, []),
 }
@@ -211,14 +236,14 @@ def backward_raw(shape, q, k, g, beta, ckpt, dy, dS_T, dq, dk, dv, dg, dbeta,
 
 
 def size_of(query: str, shape) -> int:
-    """A size query of the convolution, scan or norm by its name."""
+    """A size query of an operator around the recurrence by its name."""
     out = ctypes.c_size_t()
     check(getattr(load(), query)(ctypes.byref(shape), ctypes.byref(out)), query)
     return out.value
 
 
 def layer_raw(name: str, shape, pointers, stream, workspace_bytes=None) -> int:
-    """A convolution, scan or norm call by its name, with integer device
+    """A call of an operator around the recurrence by its name, with integer device
     addresses (0 = NULL; the workspace last); returns the status."""
     call = getattr(_lib or load(), name)
     if workspace_bytes is None:

@@ -532,15 +532,16 @@ const char* gdr_strerror(int status) {
     case GDR_ERR_WORKSPACE: return "workspace is smaller than the size query returns";
     case GDR_ERR_ALIGNMENT: return "a pointer is not 16-byte aligned";
     case GDR_ERR_HIP: return "the HIP runtime rejected a kernel launch";
-    case GDR_ERR_BAD_DECAY: return "decay must be GDR_DECAY_G or GDR_DECAY_LOG";
+    case GDR_ERR_BAD_DECAY: return "decay must be GDR_DECAY_G or GDR_DECAY_LOG, per_head 0 or 1";
     case GDR_ERR_SCRATCH_LIMIT:
       return "the forward workspace this shape needs exceeds the no-allocation scratch";
     case GDR_ERR_BAD_COUNT:
       return "the launch-event count must be in [0, GDR_MAX_LAUNCH_EVENTS]";
     case GDR_ERR_BAD_DIM:
-      return "a dimension of a convolution, scan or norm is outside its range";
+      return "a dimension of a convolution, scan, norm, linear attention or block is outside its "
+             "range";
     case GDR_ERR_BAD_STRIDE: return "a row stride is below the row's width or above its limit";
-    case GDR_ERR_BAD_ACT: return "act must be GDR_ACT_NONE or GDR_ACT_SILU, softplus 0 or 1";
+    case GDR_ERR_BAD_ACT: return "act must be GDR_ACT_NONE or GDR_ACT_SILU, a flag (softplus, post, pre, center) 0 or 1";
     case GDR_ERR_BAD_EPS: return "eps must be finite and >= 0";
     case GDR_ERR_OVERLAP:
       return "a convolution's output rows overlap its input rows (allowed in place, dense, for at "
@@ -549,7 +550,7 @@ const char* gdr_strerror(int status) {
   return "unknown gdr status";
 }
 
-const char* gdr_version(void) { return "0.8.0"; }
+const char* gdr_version(void) { return "0.9.0"; }
 
 }  // extern "C"
 

@@ -1,6 +1,7 @@
 // Launch interface and shared device helpers of the layer operators beside
 // the gated delta rule: the short causal convolution, the selective state
-// space scan and the group norm (include/gdr.h states their formulas).
+// space scan, the group norm, linear attention and the norms around a block
+// (include/gdr.h states their formulas).
 #pragma once
 
 #include "gdr_device.h"
@@ -124,6 +125,84 @@ int scan_channels();
 int64_t scan_chunk(const ScanArgs& a, int64_t stride, bool bwd);
 hipError_t launch_scan_fwd(const ScanArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs& a, bool bf16, hipStream_t s);
+
+// Linear attention with a decay for each head.
+struct LinArgs {
+  int B, T, Hk, Hv, Dk, Dv;
+  int64_t rows, q_stride, k_stride, v_stride, g_stride;
+  float scale;
+  int g_bf16, per_head;  // log_g: its type; [Hv] instead of [rows][Hv]
+  const int32_t* spans;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* log_g;     // or null (no decay)
+  const float* S0;       // [B][Hv][Dv][Dk] or null
+  void* y;
+  float* S_T;            // or null
+  float* ckpt;           // [B][2][Hv][Dv][Dk]: S0 and S_T, or null
+  // backward
+  const void* dy;
+  const float* dS_T;     // or null
+  void* dq;
+  void* dk;
+  void* dv;
+  void* dlog_g;          // or null
+  float* dS0;            // or null
+  float* dq_part;        // [rows][Hv][Dk], with Hk < Hv
+  float* dk_part;
+  float* flow;           // [2][tiles][rows][Hv]
+  float* head_sums;      // [B][Hv], for a decay per head
+};
+hipError_t launch_lin_fwd(const LinArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_lin_bwd(const LinArgs& a, bool bf16, hipStream_t s);
+// Rows of the state that a workgroup of the step kernel takes.
+constexpr int kLinStepRows = 16;
+
+// The norms before and after a block with its gate and residual sum.
+struct ResArgs {
+  int64_t rows, x_stride, r_stride;
+  int64_t gate_rows;     // rows that one row of the gate serves (1: a gate per row); divides rows
+  int64_t gate_stride;
+  int C;
+  int post, pre, center;
+  float alpha, eps, offset;
+  int w_bf16, gate_bf16;
+  const void* x;
+  const void* r;
+  const void* gate;      // or null
+  const void* post_w;    // [C] or null: ones (the others: zeros)
+  const void* post_b;
+  const void* pre_w;
+  const void* pre_b;
+  void* y;
+  void* h;
+  float* stats;          // [rows][4]: mean, 1/sqrt(..) of x, of h; or null
+  // backward
+  const void* dy;
+  const void* dh;        // or null
+  void* dx;
+  void* dr;
+  void* dgate;           // or null
+  void* dpost_w;         // these four or null
+  void* dpost_b;
+  void* dpre_w;
+  void* dpre_b;
+  float* part;           // [parts][4][C]: post_w, post_b, pre_w, pre_b
+  float* gate_part;      // [parts][C]
+};
+struct ResPlan {
+  int lanes, nv;         // lanes of a row, vectors of a lane
+  bool vec;
+  int64_t step;          // rows of a workgroup, in whole or a part of a gate's rows
+  int64_t per_gate;      // workgroups of one gate row (1: whole gate rows in a workgroup)
+  int64_t parts;         // workgroups
+};
+bool res_plan(const ResArgs& a, bool bf16, ResPlan* p);
+hipError_t launch_res_fwd(const ResArgs& a, const ResPlan& p, bool bf16, bool stream_f32,
+                          hipStream_t s);
+hipError_t launch_res_bwd(const ResArgs& a, const ResPlan& p, bool bf16, bool stream_f32,
+                          hipStream_t s);
 
 // Workgroups of 256 along a grid's x dimension, whose threads have to stay
 // below 2^32.

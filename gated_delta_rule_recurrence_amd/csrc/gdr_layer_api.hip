@@ -1,6 +1,7 @@
 // Host side of the layer operators' C ABI (include/gdr.h): argument
 // validation, size queries and launches of the short causal convolution, the
-// selective state space scan and the group norm.  As in gdr_api.hip, every
+// selective state space scan, the group norm, linear attention and the norms
+// around a block.  As in gdr_api.hip, every
 // check runs on the host before anything is enqueued.
 #include <math.h>
 #include <stdint.h>
@@ -452,6 +453,267 @@ int norm_backward(const gdr_norm_shape* shape, const void* x, const void* w, con
                                          static_cast<hipStream_t>(stream)));
 }
 
+// ---- linear attention --------------------------------------------------------
+int check(const gdr_lin_shape* in, gdr_lin_shape* s) {
+  if (in == nullptr) return GDR_ERR_NULL_ARG;
+  *s = *in;
+  const int st = sequences_ok(s->B, s->T, s->rows);
+  if (st != GDR_OK) return st;
+  if (s->Hk < 1 || s->Hv < 1 || s->Dk < 1 || s->Dv < 1) return GDR_ERR_BAD_DIM;
+  if (s->Hv % s->Hk != 0) return GDR_ERR_HEAD_RATIO;
+  if (s->Dk > GDR_LIN_MAX_DIM || s->Dv > GDR_LIN_MAX_DIM || s->Hv > kMaxBatch)
+    return GDR_ERR_UNSUPPORTED_DIM;
+  if (!dtype_ok(s->dtype) || !dtype_ok(s->gdtype)) return GDR_ERR_BAD_DTYPE;
+  if (s->per_head != 0 && s->per_head != 1) return GDR_ERR_BAD_DECAY;
+  if (!stride_ok(&s->q_stride, s->Hk * s->Dk) || !stride_ok(&s->k_stride, s->Hk * s->Dk) ||
+      !stride_ok(&s->v_stride, s->Hv * s->Dv) || !stride_ok(&s->g_stride, s->Hv))
+    return GDR_ERR_BAD_STRIDE;
+  return GDR_OK;
+}
+
+struct LinSizes {
+  int64_t ckpt, fwd;                         // bytes of the save buffer, of the workspaces
+  int64_t dq, dk, flow, heads, bwd;          // byte offsets of the backward's, its size
+};
+
+int lin_sizes(const gdr_lin_shape& s, LinSizes* z) {
+  int64_t state, rows, x;
+  if (!product_ok(s.Hv * s.Dk * s.Dv * 4, s.B, &state) ||
+      !product_ok(s.Hv * 4, s.rows, &rows))
+    return GDR_ERR_OVERFLOW;
+  z->ckpt = 2 * state;
+  z->fwd = 0;
+  z->bwd = 0;
+  z->dq = z->dk = 0;
+  if (s.Hv > s.Hk) {
+    if (!product_ok(rows, s.Dk, &x)) return GDR_ERR_OVERFLOW;
+    z->dk = round_up256(x);
+    z->bwd = 2 * z->dk;
+  }
+  z->flow = z->bwd;
+  const int64_t tiles = (s.Dk + gdr::kLinStepRows - 1) / gdr::kLinStepRows;
+  if (!product_ok(rows, 2 * tiles, &x)) return GDR_ERR_OVERFLOW;
+  z->bwd += round_up256(x);
+  z->heads = z->bwd;
+  z->bwd += round_up256(s.B * s.Hv * 4);
+  return GDR_OK;
+}
+
+gdr::LinArgs lin_args(const gdr_lin_shape& s, const void* q, const void* k, const void* v,
+                      const void* log_g, const int32_t* spans) {
+  gdr::LinArgs a{};
+  a.B = (int)s.B;
+  a.T = (int)s.T;
+  a.Hk = (int)s.Hk;
+  a.Hv = (int)s.Hv;
+  a.Dk = (int)s.Dk;
+  a.Dv = (int)s.Dv;
+  a.rows = s.rows;
+  a.q_stride = s.q_stride;
+  a.k_stride = s.k_stride;
+  a.v_stride = s.v_stride;
+  a.g_stride = s.g_stride;
+  a.scale = s.scale;
+  a.g_bf16 = s.gdtype == GDR_BF16;
+  a.per_head = s.per_head;
+  a.spans = spans;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.log_g = log_g;
+  return a;
+}
+
+int lin_forward(const gdr_lin_shape* shape, const void* q, const void* k, const void* v,
+                const void* log_g, const float* S0, const int32_t* spans, void* y, float* S_T,
+                void* ckpt, void* workspace, size_t workspace_bytes, void* stream) {
+  gdr_lin_shape s;
+  LinSizes z{};
+  int st = check(shape, &s);
+  if (st == GDR_OK) st = rows_ok(s.B, s.T, s.rows, spans);
+  if (st == GDR_OK) st = lin_sizes(s, &z);
+  const bool has_rows = s.B > 0 && s.T > 0 && s.rows > 0;
+  if (st == GDR_OK) st = pointers_ok({q, k, v, static_cast<const void*>(y)}, has_rows);
+  if (st == GDR_OK)
+    st = alignment_ok({q, k, v, log_g, S0, spans, y, S_T, ckpt,
+                       static_cast<const void*>(workspace)});
+  if (st != GDR_OK) return st;
+  if (s.B == 0 || (!has_rows && S_T == nullptr && ckpt == nullptr)) return GDR_OK;
+  if (z.fwd > 0 && (workspace == nullptr || workspace_bytes < (size_t)z.fwd))
+    return GDR_ERR_WORKSPACE;
+  gdr::LinArgs a = lin_args(s, q, k, v, log_g, spans);
+  if (!has_rows) a.rows = 0, a.T = 0;
+  a.S0 = S0;
+  a.y = y;
+  a.S_T = S_T;
+  a.ckpt = static_cast<float*>(ckpt);
+  return hip_status(gdr::launch_lin_fwd(a, s.dtype == GDR_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const void* v,
+                 const void* log_g, const int32_t* spans, const void* ckpt, const void* dy,
+                 const float* dS_T, void* dq, void* dk, void* dv, void* dlog_g, float* dS0,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  gdr_lin_shape s;
+  LinSizes z{};
+  int st = check(shape, &s);
+  if (st == GDR_OK) st = rows_ok(s.B, s.T, s.rows, spans);
+  if (st == GDR_OK) st = lin_sizes(s, &z);
+  const bool has_rows = s.B > 0 && s.T > 0 && s.rows > 0;
+  if (st == GDR_OK)
+    st = pointers_ok({ckpt, static_cast<const void*>(workspace)}, s.B > 0);
+  if (st == GDR_OK)
+    st = pointers_ok({q, k, v, dy, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                      static_cast<const void*>(dv)},
+                     has_rows);
+  if (st == GDR_OK && dlog_g != nullptr && log_g == nullptr) st = GDR_ERR_NULL_ARG;
+  if (st == GDR_OK)
+    st = alignment_ok({q, k, v, log_g, spans, ckpt, dy, dS_T, dq, dk, dv, dlog_g, dS0,
+                       static_cast<const void*>(workspace)});
+  if (st != GDR_OK) return st;
+  if (s.B == 0) return GDR_OK;
+  if (workspace_bytes < (size_t)z.bwd) return GDR_ERR_WORKSPACE;
+  gdr::LinArgs a = lin_args(s, q, k, v, log_g, spans);
+  if (!has_rows) a.rows = 0, a.T = 0;
+  a.ckpt = static_cast<float*>(const_cast<void*>(ckpt));
+  a.dy = dy;
+  a.dS_T = dS_T;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dlog_g = dlog_g;
+  a.dS0 = dS0;
+  char* const w = static_cast<char*>(workspace);
+  if (s.Hv > s.Hk) {
+    a.dq_part = reinterpret_cast<float*>(w + z.dq);
+    a.dk_part = reinterpret_cast<float*>(w + z.dk);
+  }
+  a.flow = reinterpret_cast<float*>(w + z.flow);
+  a.head_sums = reinterpret_cast<float*>(w + z.heads);
+  return hip_status(gdr::launch_lin_bwd(a, s.dtype == GDR_BF16, static_cast<hipStream_t>(stream)));
+}
+
+// ---- the norms around a block --------------------------------------------------
+int check(const gdr_res_shape* in, gdr_res_shape* s, gdr::ResArgs* a, gdr::ResPlan* p) {
+  if (in == nullptr) return GDR_ERR_NULL_ARG;
+  *s = *in;
+  if (s->rows < 0 || s->rows > kMaxRows || s->C < 1 || s->C > GDR_RES_MAX_CHANNELS ||
+      s->gate_rows < 0)
+    return GDR_ERR_BAD_DIM;
+  if (!dtype_ok(s->dtype) || !dtype_ok(s->rdtype) || !dtype_ok(s->wdtype) || !dtype_ok(s->gdtype))
+    return GDR_ERR_BAD_DTYPE;
+  if (s->dtype == GDR_F32 && s->rdtype == GDR_BF16) return GDR_ERR_BAD_DTYPE;
+  for (const int32_t f : {s->post, s->pre, s->center})
+    if (f != 0 && f != 1) return GDR_ERR_BAD_ACT;
+  if (!(s->eps >= 0.f) || isinf(s->eps)) return GDR_ERR_BAD_EPS;
+  if (!stride_ok(&s->x_stride, s->C) || !stride_ok(&s->r_stride, s->C) ||
+      !stride_ok(&s->gate_stride, s->C))
+    return GDR_ERR_BAD_STRIDE;
+  if (s->gate_rows == 0 || s->gate_rows > s->rows) s->gate_rows = s->rows < 1 ? 1 : s->rows;
+  if (s->rows % s->gate_rows != 0) return GDR_ERR_BAD_DIM;
+  a->rows = s->rows;
+  a->x_stride = s->x_stride;
+  a->r_stride = s->r_stride;
+  a->gate_rows = s->gate_rows;
+  a->gate_stride = s->gate_stride;
+  a->C = (int)s->C;
+  a->post = s->post;
+  a->pre = s->pre;
+  a->center = s->center;
+  a->alpha = s->alpha;
+  a->eps = s->eps;
+  a->offset = s->weight_offset;
+  a->w_bf16 = s->wdtype == GDR_BF16;
+  a->gate_bf16 = s->gdtype == GDR_BF16;
+  if (!gdr::res_plan(*a, s->dtype == GDR_BF16, p)) return GDR_ERR_BAD_DIM;
+  return GDR_OK;
+}
+
+// Bytes of the weights' partial sums, and of them with the gate's behind.
+int64_t res_workspace(const gdr_res_shape& s, const gdr::ResPlan& p, int64_t* gate) {
+  *gate = round_up256(p.parts * 4 * s.C * 4);
+  return *gate + round_up256(p.per_gate > 1 && s.gate_rows > 1 ? p.parts * s.C * 4 : 0);
+}
+
+int res_forward(const gdr_res_shape* shape, const void* x, const void* r, const void* gate,
+                const void* post_w, const void* post_b, const void* pre_w, const void* pre_b,
+                void* y, void* h, float* stats, void* stream) {
+  gdr_res_shape s;
+  gdr::ResArgs a{};
+  gdr::ResPlan p{};
+  int st = check(shape, &s, &a, &p);
+  if (st == GDR_OK) st = pointers_ok({x, r, static_cast<const void*>(h)}, s.rows > 0);
+  if (st == GDR_OK && s.rows > 0 && s.pre && y == nullptr) st = GDR_ERR_NULL_ARG;
+  if (st == GDR_OK)
+    st = alignment_ok({x, r, gate, post_w, post_b, pre_w, pre_b, y, h,
+                       static_cast<const void*>(stats)});
+  if (st != GDR_OK || s.rows == 0) return st;
+  a.x = x;
+  a.r = r;
+  a.gate = gate;
+  a.post_w = post_w;
+  a.post_b = post_b;
+  a.pre_w = pre_w;
+  a.pre_b = pre_b;
+  a.y = y;
+  a.h = h;
+  a.stats = stats;
+  return hip_status(gdr::launch_res_fwd(a, p, s.dtype == GDR_BF16, s.rdtype == GDR_F32,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int res_backward(const gdr_res_shape* shape, const void* x, const void* r, const void* gate,
+                 const void* post_w, const void* post_b, const void* pre_w, const void* pre_b,
+                 const float* stats, const void* dy, const void* dh, void* dx, void* dr,
+                 void* dgate, void* dpost_w, void* dpost_b, void* dpre_w, void* dpre_b,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  gdr_res_shape s;
+  gdr::ResArgs a{};
+  gdr::ResPlan p{};
+  int st = check(shape, &s, &a, &p);
+  if (st == GDR_OK)
+    st = pointers_ok({x, r, static_cast<const void*>(stats), static_cast<const void*>(dx),
+                      static_cast<const void*>(dr)},
+                     s.rows > 0);
+  if (st == GDR_OK && s.rows > 0 && (s.pre ? dy == nullptr : dh == nullptr)) st = GDR_ERR_NULL_ARG;
+  if (st == GDR_OK && dgate != nullptr && gate == nullptr) st = GDR_ERR_NULL_ARG;
+  if (st == GDR_OK)
+    st = alignment_ok({x, r, gate, post_w, post_b, pre_w, pre_b, static_cast<const void*>(stats),
+                       dy, dh, dx, dr, dgate, dpost_w, dpost_b, dpre_w, dpre_b,
+                       static_cast<const void*>(workspace)});
+  if (st != GDR_OK) return st;
+  const bool sums = dpost_w != nullptr || dpost_b != nullptr || dpre_w != nullptr ||
+                    dpre_b != nullptr;
+  int64_t gate_at = 0;
+  const int64_t need = res_workspace(s, p, &gate_at);
+  if (s.rows == 0) return GDR_OK;
+  const bool gates = dgate != nullptr && p.per_gate > 1 && s.gate_rows > 1;
+  if ((sums || gates) && (workspace == nullptr || workspace_bytes < (size_t)need))
+    return GDR_ERR_WORKSPACE;
+  a.x = x;
+  a.r = r;
+  a.gate = gate;
+  a.post_w = post_w;
+  a.post_b = post_b;
+  a.pre_w = pre_w;
+  a.pre_b = pre_b;
+  a.stats = const_cast<float*>(stats);
+  a.dy = dy;
+  a.dh = dh;
+  a.dx = dx;
+  a.dr = dr;
+  a.dgate = dgate;
+  a.dpost_w = dpost_w;
+  a.dpost_b = dpost_b;
+  a.dpre_w = dpre_w;
+  a.dpre_b = dpre_b;
+  if (sums) a.part = static_cast<float*>(workspace);
+  if (gates)
+    a.gate_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + gate_at);
+  return hip_status(gdr::launch_res_bwd(a, p, s.dtype == GDR_BF16, s.rdtype == GDR_F32,
+                                        static_cast<hipStream_t>(stream)));
+}
+
 int store_size(int st, int64_t bytes, size_t* out) {
   if (st != GDR_OK) return st;
   if (out == nullptr) return GDR_ERR_NULL_ARG;
@@ -559,6 +821,82 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
   return gdr::finish_call(norm_backward(shape, x, weight, bias, z, stats, dy, dx, dweight, dbias,
                                         dz, workspace, workspace_bytes, stream),
                           stream);
+}
+
+int gdr_lin_checkpoint_bytes(const gdr_lin_shape* shape, size_t* out) {
+  gdr_lin_shape s;
+  LinSizes z{};
+  int st = check(shape, &s);
+  if (st == GDR_OK) st = lin_sizes(s, &z);
+  return store_size(st, z.ckpt, out);
+}
+
+int gdr_lin_forward_workspace_bytes(const gdr_lin_shape* shape, size_t* out) {
+  gdr_lin_shape s;
+  LinSizes z{};
+  int st = check(shape, &s);
+  if (st == GDR_OK) st = lin_sizes(s, &z);
+  return store_size(st, z.fwd, out);
+}
+
+int gdr_lin_backward_workspace_bytes(const gdr_lin_shape* shape, size_t* out) {
+  gdr_lin_shape s;
+  LinSizes z{};
+  int st = check(shape, &s);
+  if (st == GDR_OK) st = lin_sizes(s, &z);
+  return store_size(st, z.bwd, out);
+}
+
+int gdr_lin_forward(const gdr_lin_shape* shape, const void* q, const void* k, const void* v,
+                    const void* log_g, const float* S0, const int32_t* spans, void* y, float* S_T,
+                    void* ckpt, void* workspace, size_t workspace_bytes, void* stream) {
+  gdr::begin_call();
+  return gdr::finish_call(lin_forward(shape, q, k, v, log_g, S0, spans, y, S_T, ckpt, workspace,
+                                      workspace_bytes, stream),
+                          stream);
+}
+
+int gdr_lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const void* v,
+                     const void* log_g, const int32_t* spans, const void* ckpt, const void* dy,
+                     const float* dS_T, void* dq, void* dk, void* dv, void* dlog_g, float* dS0,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  gdr::begin_call();
+  return gdr::finish_call(lin_backward(shape, q, k, v, log_g, spans, ckpt, dy, dS_T, dq, dk, dv,
+                                       dlog_g, dS0, workspace, workspace_bytes, stream),
+                          stream);
+}
+
+int gdr_res_forward(const gdr_res_shape* shape, const void* x, const void* residual,
+                    const void* gate, const void* post_weight, const void* post_bias,
+                    const void* pre_weight, const void* pre_bias, void* y, void* h, float* stats,
+                    void* stream) {
+  gdr::begin_call();
+  return gdr::finish_call(res_forward(shape, x, residual, gate, post_weight, post_bias, pre_weight,
+                                      pre_bias, y, h, stats, stream),
+                          stream);
+}
+
+int gdr_res_backward_workspace_bytes(const gdr_res_shape* shape, size_t* out) {
+  gdr_res_shape s;
+  gdr::ResArgs a{};
+  gdr::ResPlan p{};
+  int64_t gate = 0;
+  const int st = check(shape, &s, &a, &p);
+  return store_size(st, st == GDR_OK ? res_workspace(s, p, &gate) : 0, out);
+}
+
+int gdr_res_backward(const gdr_res_shape* shape, const void* x, const void* residual,
+                     const void* gate, const void* post_weight, const void* post_bias,
+                     const void* pre_weight, const void* pre_bias, const float* stats,
+                     const void* dy, const void* dh, void* dx, void* dresidual, void* dgate,
+                     void* dpost_weight, void* dpost_bias, void* dpre_weight, void* dpre_bias,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  gdr::begin_call();
+  return gdr::finish_call(
+      res_backward(shape, x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, stats,
+                   dy, dh, dx, dresidual, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias,
+                   workspace, workspace_bytes, stream),
+      stream);
 }
 
 }  // extern "C"

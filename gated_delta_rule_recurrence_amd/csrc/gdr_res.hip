@@ -1,0 +1,509 @@
+// The norms before and after a block with its gate and residual sum, on
+// gfx950.  Per row, N(a; w, b) = (a - mu) r (w + offset) + b with
+// r = 1 / sqrt(mean((a - mu)^2) + eps) (mu = 0: a root mean square norm):
+//   n = N(x; post), or x;  h = residual + alpha gate n;  y = N(h; pre).
+// Backward, with both norms' mu and r from the forward and h formed again
+// (in fp32, as the forward had it, so h need not be kept):
+//   e = dy (w + offset),  dh' = dh + r (e - mean(e) - hh mean(e hh)),  dr = dh'
+//   dgate = alpha dh' n,  dn = alpha gate dh',  dx from dn as dh' from dy.
+// Bound by HBM bytes: every tensor once.
+//
+// Mapping: LANES lanes own one row, each NV vectors of V channels, in registers
+// from the loads to the stores; rows of up to 64 vectors take a wave, wider ones
+// a workgroup.  A workgroup walks neighbouring rows, which lie inside one row
+// of the gate or are whole gate rows, so that it holds weights, gate and the
+// backward's sums over rows in registers.
+#include "gdr_layer.h"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sums of two values over the LANES lanes of a row, the same bits in every lane.
+template <int LANES>
+__device__ __forceinline__ void row_sums(float& x, float& y, float (*red)[2]) {
+  x = rowsum16(x);
+  y = rowsum16(y);
+  x = swap16_sum(x, x);
+  y = swap16_sum(y, y);
+  x = swap32_sum(x, x);
+  y = swap32_sum(y, y);
+  if constexpr (LANES > 64) {
+    __syncthreads();  // the last sums have been read
+    if ((threadIdx.x & 63) == 0) {
+      red[threadIdx.x >> 6][0] = x;
+      red[threadIdx.x >> 6][1] = y;
+    }
+    __syncthreads();
+    x = red[0][0];
+    y = red[0][1];
+#pragma unroll
+    for (int i = 1; i < LANES / 64; ++i) {
+      x += red[i][0];
+      y += red[i][1];
+    }
+  }
+}
+
+template <int LANES>
+struct Res {
+  static constexpr int kBlock = LANES > 64 ? LANES : kThreads;
+  static constexpr int kWalkers = LANES > 64 ? 1 : kThreads / 64;  // rows at a time
+};
+
+// N consecutive channels of a parameter, or `other` where it is absent.
+template <int V>
+__device__ __forceinline__ void parameter(const void* p, int c, int C, int is_bf16, float offset,
+                                          float other, float (&w)[V]) {
+  Weights<V, (V > 1)> raw;
+  raw.load(p, c, C, is_bf16);
+  raw.get(is_bf16, w);
+#pragma unroll
+  for (int v = 0; v < V; ++v) w[v] = p != nullptr ? w[v] + offset : other;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void get_row(const void* p, int64_t off, bool ok, float (&f)[V]) {
+  const Pack<T, V> x = ok ? load_pack<T, V>(static_cast<const T*>(p) + off) : zero_pack<T, V>();
+  unpack(x, f);
+}
+template <typename R, int V>
+__device__ __forceinline__ void get_stream(const void* p, int64_t off, bool ok, float (&f)[V]) {
+  constexpr int VR = V == 1 ? 1 : (V * (int)sizeof(R) <= 16 ? V : 16 / (int)sizeof(R));
+#pragma unroll
+  for (int k = 0; k < V / VR; ++k) {
+    float g[VR];
+    get_row<R, VR>(p, off + k * VR, ok, g);
+#pragma unroll
+    for (int v = 0; v < VR; ++v) f[k * VR + v] = g[v];
+  }
+}
+template <typename R, int V>
+__device__ __forceinline__ void put_stream(void* p, int64_t off, const float (&f)[V]) {
+  constexpr int VR = V == 1 ? 1 : (V * (int)sizeof(R) <= 16 ? V : 16 / (int)sizeof(R));
+#pragma unroll
+  for (int k = 0; k < V / VR; ++k) {
+    float g[VR];
+#pragma unroll
+    for (int v = 0; v < VR; ++v) g[v] = f[k * VR + v];
+    store_pack(static_cast<R*>(p) + off + k * VR, g);
+  }
+}
+
+// Rows of a workgroup: [first, last) of the gate rows [gate, gate_end).
+struct Walk {
+  int64_t first, last;
+};
+__device__ __forceinline__ Walk walk_of(const ResArgs& a, const ResPlan& p) {
+  const int64_t per = a.gate_rows > 1 ? a.gate_rows : a.rows;  // of one gate row
+  int64_t first, last;
+  if (p.per_gate > 1) {
+    const int64_t g = blockIdx.x / p.per_gate;
+    first = g * per + blockIdx.x % p.per_gate * p.step;
+    last = first + p.step;
+    last = last < (g + 1) * per ? last : (g + 1) * per;
+  } else {
+    first = blockIdx.x * p.step;
+    last = first + p.step;
+  }
+  return Walk{first, last < a.rows ? last : a.rows};
+}
+
+template <typename T, typename R, int LANES, int NV, int V>
+__global__ __launch_bounds__((Res<LANES>::kBlock)) void res_fwd_kernel(ResArgs a,
+                                                                               ResPlan p) {
+  using P = Res<LANES>;
+  __shared__ float red[LANES > 64 ? LANES / 64 : 1][2];
+  const int lane = threadIdx.x % LANES, wave = LANES > 64 ? 0 : threadIdx.x >> 6;
+  const Walk k = walk_of(a, p);
+  const float inv = 1.f / (float)a.C;
+  float pw[NV][V], pb[NV][V], w[NV][V], wb[NV][V], gate[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * LANES + lane) * V, at = c < a.C ? c : a.C;
+    parameter(a.post_w, at, a.C, a.w_bf16, a.offset, 1.f, pw[i]);
+    parameter(a.post_b, at, a.C, a.w_bf16, 0.f, 0.f, pb[i]);
+    parameter(a.pre_w, at, a.C, a.w_bf16, a.offset, 1.f, w[i]);
+    parameter(a.pre_b, at, a.C, a.w_bf16, 0.f, 0.f, wb[i]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) gate[i][v] = 1.f;
+  }
+  int64_t held = -1;  // the gate's row in registers
+  for (int64_t row = k.first + wave; row < k.last; row += P::kWalkers) {
+    float x[NV][V], h[NV][V], s = 0.f, mu = 0.f, zero = 0.f;
+    const int64_t g = a.gate_rows > 1 ? row / a.gate_rows : row;
+    if (a.gate != nullptr && g != held) {
+      held = g;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LANES + lane) * V;
+        if (a.gate_bf16)
+          get_row<bf16, V>(a.gate, g * a.gate_stride + c, c < a.C, gate[i]);
+        else
+          get_stream<float, V>(a.gate, g * a.gate_stride + c, c < a.C, gate[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * LANES + lane) * V;
+      get_row<T, V>(a.x, row * a.x_stride + c, c < a.C, x[i]);
+      get_stream<R, V>(a.r, row * a.r_stride + c, c < a.C, h[i]);
+    }
+    float mu1 = 0.f, r1 = 0.f, r2 = 0.f;
+    if (a.post) {
+      if (a.center) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) s += x[i][v];
+        row_sums<LANES>(s, zero, red);
+        mu1 = s * inv;
+      }
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[i][v] = (i * LANES + lane) * V < a.C ? x[i][v] - mu1 : 0.f;
+          s = fmaf(x[i][v], x[i][v], s);
+        }
+      row_sums<LANES>(s, zero, red);
+      r1 = 1.f / sqrtf(fmaf(s, inv, a.eps));
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i][v] = fmaf(x[i][v] * r1, pw[i][v], pb[i][v]);
+    }
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * LANES + lane) * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[i][v] = fmaf(a.alpha * gate[i][v], x[i][v], h[i][v]);
+        h[i][v] = c < a.C ? h[i][v] : 0.f;
+        s += h[i][v];
+      }
+      if (c < a.C) put_stream<R, V>(a.h, row * a.C + c, h[i]);
+    }
+    if (a.pre) {
+      if (a.center) {
+        row_sums<LANES>(s, zero, red);
+        mu = s * inv;
+      }
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[i][v] = (i * LANES + lane) * V < a.C ? h[i][v] - mu : 0.f;
+          s = fmaf(h[i][v], h[i][v], s);
+        }
+      row_sums<LANES>(s, zero, red);
+      r2 = 1.f / sqrtf(fmaf(s, inv, a.eps));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LANES + lane) * V;
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = fmaf(h[i][v] * r2, w[i][v], wb[i][v]);
+        if (c < a.C) store_pack(static_cast<T*>(a.y) + row * a.C + c, o);
+      }
+    }
+    if (a.stats != nullptr && lane == 0)
+      *reinterpret_cast<float4*>(a.stats + 4 * row) = float4{mu1, r1, mu, r2};
+  }
+}
+
+template <typename T, typename R, int LANES, int NV, int V>
+__global__ __launch_bounds__((Res<LANES>::kBlock)) void res_bwd_kernel(ResArgs a,
+                                                                               ResPlan p) {
+  using P = Res<LANES>;
+  __shared__ float red[LANES > 64 ? LANES / 64 : 1][2];
+  __shared__ float sum[LANES > 64 ? 1 : kThreads / 64][64];
+  const int lane = threadIdx.x % LANES, wave = LANES > 64 ? 0 : threadIdx.x >> 6;
+  const Walk k = walk_of(a, p);
+  const float inv = 1.f / (float)a.C;
+  float pw[NV][V], pb[NV][V], w[NV][V], gate[NV][V];
+  float dpw[NV][V], dpb[NV][V], dw[NV][V], db[NV][V], dg[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * LANES + lane) * V, at = c < a.C ? c : a.C;
+    parameter(a.post_w, at, a.C, a.w_bf16, a.offset, 1.f, pw[i]);
+    parameter(a.post_b, at, a.C, a.w_bf16, 0.f, 0.f, pb[i]);
+    parameter(a.pre_w, at, a.C, a.w_bf16, a.offset, 1.f, w[i]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      gate[i][v] = 1.f;
+      dpw[i][v] = dpb[i][v] = dw[i][v] = db[i][v] = dg[i][v] = 0.f;
+    }
+  }
+  // The workgroup's sum of one value a lane, in the first wave (or, where the
+  // workgroup walks as one, in every lane's own).
+  auto over_waves = [&](float x) __attribute__((always_inline)) {
+    if constexpr (LANES <= 64) {
+      __syncthreads();
+      sum[wave][lane] = x;
+      __syncthreads();
+      x = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+    }
+    return x;
+  };
+  const bool row_gate = a.gate_rows == 1;
+  const int64_t per = row_gate ? a.rows : a.gate_rows;
+  // one gate row at a time (all of them, where the gate has a row of its own
+  // for every row)
+  for (int64_t start = k.first; start < k.last;) {
+    const int64_t g = start / per;
+    const int64_t stop = (g + 1) * per < k.last ? (g + 1) * per : k.last;
+    if (a.gate != nullptr && !row_gate) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LANES + lane) * V;
+        if (a.gate_bf16)
+          get_row<bf16, V>(a.gate, g * a.gate_stride + c, c < a.C, gate[i]);
+        else
+          get_stream<float, V>(a.gate, g * a.gate_stride + c, c < a.C, gate[i]);
+      }
+    }
+    for (int64_t row = start + wave; row < stop; row += P::kWalkers) {
+      float n[NV][V], h[NV][V], xh[NV][V], dy[NV][V], d[NV][V];
+      const float4 st4 = *reinterpret_cast<const float4*>(a.stats + 4 * row);
+      const float mu1 = st4.x, r1 = st4.y, mu2 = st4.z, r2 = st4.w;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LANES + lane) * V;
+        const bool ok = c < a.C;
+        get_row<T, V>(a.x, row * a.x_stride + c, ok, xh[i]);
+        if (a.pre) {
+          get_stream<R, V>(a.r, row * a.r_stride + c, ok, h[i]);
+          get_row<T, V>(a.dy, row * a.C + c, ok, dy[i]);
+        }
+        get_stream<R, V>(a.dh, row * a.C + c, ok && a.dh != nullptr, d[i]);
+        if (row_gate && a.gate != nullptr) {
+          if (a.gate_bf16)
+            get_row<bf16, V>(a.gate, row * a.gate_stride + c, ok, gate[i]);
+          else
+            get_stream<float, V>(a.gate, row * a.gate_stride + c, ok, gate[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool ok = (i * LANES + lane) * V < a.C;
+          if (a.post) {
+            xh[i][v] = ok ? (xh[i][v] - mu1) * r1 : 0.f;
+            n[i][v] = fmaf(xh[i][v], pw[i][v], pb[i][v]);
+          } else {
+            n[i][v] = xh[i][v];
+          }
+        }
+      if (a.pre) {
+        float se = 0.f, sx = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const bool ok = (i * LANES + lane) * V < a.C;
+            h[i][v] = fmaf(a.alpha * gate[i][v], n[i][v], h[i][v]);
+            h[i][v] = ok ? (h[i][v] - mu2) * r2 : 0.f;
+            dw[i][v] = fmaf(dy[i][v], h[i][v], dw[i][v]);
+            db[i][v] += dy[i][v];
+            dy[i][v] *= w[i][v];
+            se += dy[i][v];
+            sx = fmaf(dy[i][v], h[i][v], sx);
+          }
+        row_sums<LANES>(se, sx, red);
+        se = a.center ? se * inv : 0.f;
+        sx *= inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            d[i][v] = fmaf(r2, dy[i][v] - se - h[i][v] * sx, d[i][v]);
+      }
+      float se = 0.f, sx = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LANES + lane) * V;
+        if (c < a.C) put_stream<R, V>(a.dr, row * a.C + c, d[i]);
+        float og[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float ad = c < a.C ? a.alpha * d[i][v] : 0.f;
+          og[v] = ad * n[i][v];
+          dg[i][v] += og[v];
+          d[i][v] = ad * gate[i][v];
+          if (a.post) {
+            dpw[i][v] = fmaf(d[i][v], xh[i][v], dpw[i][v]);
+            dpb[i][v] += d[i][v];
+            d[i][v] *= pw[i][v];
+            se += d[i][v];
+            sx = fmaf(d[i][v], xh[i][v], sx);
+          }
+        }
+        if (row_gate && a.dgate != nullptr && c < a.C) {
+          if (a.gate_bf16)
+            store_pack(static_cast<bf16*>(a.dgate) + row * a.C + c, og);
+          else
+            put_stream<float, V>(a.dgate, row * a.C + c, og);
+        }
+      }
+      if (a.post) {
+        row_sums<LANES>(se, sx, red);
+        se = a.center ? se * inv : 0.f;
+        sx *= inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) d[i][v] = r1 * (d[i][v] - se - xh[i][v] * sx);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LANES + lane) * V;
+        if (c < a.C) store_pack(static_cast<T*>(a.dx) + row * a.C + c, d[i]);
+      }
+    }
+    if (a.dgate != nullptr && !row_gate) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float s = over_waves(dg[i][v]);
+          dg[i][v] = 0.f;
+          const int c = (i * LANES + lane) * V + v;
+          if (wave == 0 && c < a.C) {
+            if (p.per_gate > 1)
+              a.gate_part[(int64_t)blockIdx.x * a.C + c] = s;
+            else
+              st_weight(a.dgate, g * a.C + c, s, a.gate_bf16);
+          }
+        }
+    }
+    start = stop;
+  }
+  if (a.part == nullptr) return;
+  float* const part = a.part + (int64_t)blockIdx.x * 4 * a.C;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (i * LANES + lane) * V + v;
+      const float s[4] = {over_waves(dpw[i][v]), over_waves(dpb[i][v]), over_waves(dw[i][v]),
+                          over_waves(db[i][v])};
+      if (wave == 0 && c < a.C)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[(int64_t)j * a.C + c] = s[j];
+    }
+}
+
+// Sums of the partial rows: blockIdx.y 0 .. 3 the weights', then the gate rows'.
+__global__ __launch_bounds__(kThreads) void res_sums(ResArgs a, ResPlan p, int gates_from) {
+  const int tc = threadIdx.x % kSumCols;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + tc;
+  const int64_t j = blockIdx.y;
+  if (j < gates_from) {
+    void* const to[4] = {a.dpost_w, a.dpost_b, a.dpre_w, a.dpre_b};
+    if (to[j] == nullptr) return;  // the whole workgroup
+    // rows of part are 4 C apart; columns j C ..
+    const float s = column_sum(a.part + j * a.C, p.parts, 4 * (int64_t)a.C,
+                               c < a.C ? c : 4 * (int64_t)a.C);
+    if (threadIdx.x < kSumCols && c < a.C) st_weight(to[j], c, s, a.w_bf16);
+  } else {
+    const int64_t g = j - gates_from;
+    const float s = column_sum(a.gate_part + g * p.per_gate * a.C, p.per_gate, a.C, c);
+    if (threadIdx.x < kSumCols && c < a.C) st_weight(a.dgate, g * a.C + c, s, a.gate_bf16);
+  }
+}
+
+template <typename T, typename R, bool BWD, int LANES, int NV, int V>
+hipError_t go(const ResArgs& a, const ResPlan& p, hipStream_t s) {
+  using P = Res<LANES>;
+  if constexpr (!BWD) {
+    hipLaunchKernelGGL((res_fwd_kernel<T, R, LANES, NV, V>), dim3((unsigned)p.parts),
+                       dim3(P::kBlock), 0, s, a, p);
+    const hipError_t e = hipGetLastError();
+    note_launch(s);
+    return e;
+  } else {
+    hipLaunchKernelGGL((res_bwd_kernel<T, R, LANES, NV, V>), dim3((unsigned)p.parts),
+                       dim3(P::kBlock), 0, s, a, p);
+    hipError_t e = hipGetLastError();
+    note_launch(s);
+    const int64_t per = a.gate_rows > 1 ? a.gate_rows : a.rows;
+    const int weights = a.part != nullptr ? 4 : 0;
+    const int64_t gates = a.gate_part != nullptr ? a.rows / per : 0;
+    if (e != hipSuccess || weights + gates == 0) return e;
+    hipLaunchKernelGGL(res_sums, dim3((a.C + kSumCols - 1) / kSumCols, (unsigned)(weights + gates)),
+                       dim3(kThreads), 0, s, a, p, weights);
+    e = hipGetLastError();
+    note_launch(s);
+    return e;
+  }
+}
+
+template <typename T, typename R, bool BWD, int V>
+hipError_t launch_v(const ResArgs& a, const ResPlan& p, hipStream_t s) {
+  constexpr int NV = 8 / V;  // 8 channels a lane
+  switch (p.lanes) {
+    case 64: return go<T, R, BWD, 64, NV, V>(a, p, s);
+    case 256: return go<T, R, BWD, 256, NV, V>(a, p, s);
+    case 512: return go<T, R, BWD, 512, NV, V>(a, p, s);
+    case 1024: return go<T, R, BWD, 1024, NV, V>(a, p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <bool BWD>
+hipError_t launch(const ResArgs& a, const ResPlan& p, bool is_bf16, bool stream_f32,
+                  hipStream_t s) {
+  if (!is_bf16)
+    return p.vec ? launch_v<float, float, BWD, 4>(a, p, s)
+                 : launch_v<float, float, BWD, 1>(a, p, s);
+  if (stream_f32)
+    return p.vec ? launch_v<bf16, float, BWD, 8>(a, p, s) : launch_v<bf16, float, BWD, 1>(a, p, s);
+  return p.vec ? launch_v<bf16, bf16, BWD, 8>(a, p, s) : launch_v<bf16, bf16, BWD, 1>(a, p, s);
+}
+
+}  // namespace
+
+// Lanes of a row (8 channels each) and the workgroups' rows.
+bool res_plan(const ResArgs& a, bool is_bf16, ResPlan* p) {
+  const int64_t V = is_bf16 ? 8 : 4;
+  p->vec = a.C % V == 0 && a.x_stride % V == 0 && a.r_stride % V == 0 && a.gate_stride % V == 0;
+  const int64_t lanes = (a.C + 7) / 8;
+  if (lanes > 1024) return false;
+  p->lanes = lanes <= 64 ? 64 : lanes <= 256 ? 256 : lanes <= 512 ? 512 : 1024;
+  p->nv = 8 / (p->vec ? (int)V : 1);
+  const int64_t walkers = p->lanes > 64 ? 1 : kThreads / 64;
+  const int64_t per = a.gate_rows > 1 ? a.gate_rows : (a.rows < 1 ? 1 : a.rows);
+  const int64_t want = p->lanes > 64 ? 262144 / p->lanes : 1024;
+  int64_t step = (a.rows + want - 1) / want;
+  if (step < walkers) step = walkers;
+  if (step < per) {  // parts of a gate row
+    p->per_gate = per / step;
+    if (p->per_gate < 1) p->per_gate = 1;
+    p->step = (per + p->per_gate - 1) / p->per_gate;
+    p->per_gate = (per + p->step - 1) / p->step;  // none of them empty
+    p->parts = p->per_gate * (a.rows / per);
+  } else {  // whole gate rows
+    p->step = step / per * per;
+    p->per_gate = 1;
+    p->parts = (a.rows + p->step - 1) / p->step;
+  }
+  if (p->parts < 1) p->parts = 1;
+  return true;
+}
+
+hipError_t launch_res_fwd(const ResArgs& a, const ResPlan& p, bool is_bf16, bool stream_f32,
+                          hipStream_t s) {
+  return launch<false>(a, p, is_bf16, stream_f32, s);
+}
+hipError_t launch_res_bwd(const ResArgs& a, const ResPlan& p, bool is_bf16, bool stream_f32,
+                          hipStream_t s) {
+  return launch<true>(a, p, is_bf16, stream_f32, s);
+}
+
+}  // namespace gdr

@@ -412,6 +412,20 @@ def _norm_plan(*sizes):
     return shape, _lib.size_of("gdr_norm_backward_workspace_bytes", shape)
 
 
+@functools.lru_cache(maxsize=1024)
+def _lin_plan(*sizes):
+    shape = _lib.GdrLinShape(*sizes)
+    return (shape, _lib.size_of("gdr_lin_checkpoint_bytes", shape),
+            _lib.size_of("gdr_lin_forward_workspace_bytes", shape),
+            _lib.size_of("gdr_lin_backward_workspace_bytes", shape))
+
+
+@functools.lru_cache(maxsize=1024)
+def _res_plan(*sizes):
+    shape = _lib.GdrResShape(*sizes)
+    return shape, _lib.size_of("gdr_res_backward_workspace_bytes", shape)
+
+
 def _conv_sizes(x, weight, bias, state, spans, T, act):
     dev, dt = _gpu(x)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
@@ -615,6 +629,189 @@ def gdr_norm_backward(x, weight, bias, z, stats, dy, *, groups, center=False, ac
     return dx, dweight, dbias, dz
 
 
+@dataclass
+class LinSaved:
+    """What gdr_lin_forward leaves for gdr_lin_backward (opaque fp32 buffer),
+    with the settings the backward must repeat."""
+
+    ckpt: torch.Tensor
+    spans: Optional[torch.Tensor]
+    T: int
+    scale: float
+
+
+def _lin_sizes(q, k, v, log_g, scale, spans, T):
+    dev, ty = _gpu(q)
+    if q.dim() < 3:
+        raise ValueError("q must be a tensor [.., Hk, Dk]")
+    if not isinstance(v, torch.Tensor) or v.dim() < 3:
+        raise ValueError("v must be a tensor [.., Hv, Dv]")
+    heads, wide = tuple(q.shape[-2:]), tuple(v.shape[-2:])
+    rows, qs = _row_stride("q", q, heads, ty, dev)
+    ks = _row_stride_as("k", k, q, qs, heads, ty, dev, rows)
+    _, vs = _row_stride("v", v, wide, ty, dev, rows)
+    Hv = wide[0]
+    gs, gt, per_head = Hv, torch.float32, 0
+    if log_g is not None:
+        if not isinstance(log_g, torch.Tensor):
+            raise TypeError("log_g must be a torch.Tensor")
+        gt = _weight_dtype("log_g", log_g)
+        if log_g.dim() == 1:
+            _dense("log_g", log_g, (Hv,), gt, dev)
+            per_head = 1
+        else:
+            _, gs = _row_stride("log_g", log_g, (Hv,), gt, dev, rows)
+    B, T = _sequences(q, rows, heads, spans, T, dev)
+    return _lin_plan(B, T, rows, heads[0], Hv, heads[1], wide[1], qs, ks, vs, gs, float(scale),
+                     _DTYPES[ty], _DTYPES[gt], per_head)
+
+
+def gdr_lin_forward(q, k, v, log_g=None, S0=None, *, scale=1.0, spans=None, T=None, save=True,
+                    out_state=True, y=None, S_T=None, ckpt=None, workspace=None):
+    """Linear attention with a decay for each head.  Returns (y, S_T or None,
+    LinSaved or None).
+
+    q, k [B,T,Hk,Dk], v [B,T,Hv,Dv] (or rows, see above); log_g [B,T,Hv], or
+    [Hv] for one decay per head, of either type, or None (no decay); S0
+    [B,Hv,Dv,Dk] fp32 or None.  S_T may be S0 (in place)."""
+    shape, save_bytes, nbytes, _ = _lin_sizes(q, k, v, log_g, scale, spans, T)
+    dev = q.device
+    states = (shape.B, shape.Hv, shape.Dv, shape.Dk)
+    if S0 is not None:
+        _dense("S0", S0, states, torch.float32, dev)
+    y = _rows_out(y, "y", v, spans)
+    S_T = _out(S_T, "S_T", states, torch.float32, dev) if out_state else None
+    saved = None
+    if save:
+        ckpt = _scratch(ckpt, max(save_bytes, 1), q, "ckpt")
+        saved = LinSaved(ckpt, spans, shape.T, float(scale))
+    workspace = _scratch(workspace, nbytes, q)
+    _launch("gdr_lin_forward", shape, (q, k, v, log_g, S0, spans, y, S_T, ckpt if save else None),
+            dev, workspace, nbytes)
+    return y, S_T, saved
+
+
+def gdr_lin_backward(q, k, v, log_g, saved: LinSaved, dy, dS_T=None, *, want_dlog_g=True,
+                     want_dS0=True, workspace=None):
+    """Returns (dq, dk, dv, dlog_g, dS0); dlog_g and dS0 None where not
+    wanted, dlog_g also where the forward had no log_g."""
+    spans = saved.spans
+    shape, save_bytes, _, nbytes = _lin_sizes(q, k, v, log_g, saved.scale, spans, saved.T)
+    dev, ty = q.device, q.dtype
+    states = (shape.B, shape.Hv, shape.Dv, shape.Dk)
+    # (the kernel reads the states of as many rows as the inputs have)
+    if not isinstance(saved.ckpt, torch.Tensor):
+        raise TypeError("saved.ckpt must be a torch.Tensor")
+    _scratch(saved.ckpt, save_bytes, q, "saved.ckpt")
+    _dense("dy", dy, v.shape, ty, dev)
+    if dS_T is not None:
+        _dense("dS_T", dS_T, states, torch.float32, dev)
+    dq, dk, dv = [_dense_like(t, spans) for t in (q, k, v)]
+    dlog_g = None
+    if log_g is not None and want_dlog_g:
+        dlog_g = _dense_like(log_g, spans if shape.B > 0 else True)
+    dS0 = torch.empty(states, dtype=torch.float32, device=dev) if want_dS0 else None
+    workspace = _scratch(workspace, nbytes, q)
+    _launch("gdr_lin_backward", shape, (q, k, v, log_g, spans, saved.ckpt, dy, dS_T, dq, dk, dv,
+                                        dlog_g, dS0), dev, workspace, nbytes)
+    return dq, dk, dv, dlog_g, dS0
+
+
+def _res_sizes(x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, post,
+               pre, center, weight_offset):
+    dev, dt = _gpu(x)
+    if x.dim() < 2:
+        raise ValueError("x must be a tensor [.., C]")
+    C = x.shape[-1]
+    if not isinstance(residual, torch.Tensor):
+        raise TypeError("residual must be a torch.Tensor")
+    rdt = _weight_dtype("residual", residual)
+    if residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+    rows, xs = _row_stride("x", x, (C,), dt, dev)
+    _, rs = _row_stride("residual", residual, (C,), rdt, dev, rows)
+    wdt = None
+    for name, w, used in (("post_weight", post_weight, post), ("post_bias", post_bias, post),
+                          ("pre_weight", pre_weight, pre), ("pre_bias", pre_bias, pre)):
+        if w is None:
+            continue
+        if not used:
+            raise ValueError(f"{name} is given for a norm that is not taken")
+        if not isinstance(w, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        wdt = _weight_dtype(name, w) if wdt is None else wdt  # they have one type
+        _dense(name, w, (C,), wdt, dev)
+    gate_rows, gdt, gs = 0, dt, C
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        gdt = _weight_dtype("gate", gate)
+        lead = x.shape[:-1]
+        if gate.dim() == 1:
+            _dense("gate", gate, (C,), gdt, dev)
+        elif gate.shape == x.shape:
+            gate_rows, gs = 1, _row_stride("gate", gate, (C,), gdt, dev, rows)[1]
+        elif gate.shape in ((*lead[:-1], C), (*lead[:-1], 1, C)):
+            gate_rows = lead[-1]
+            _, gs = _row_stride("gate", gate, (C,), gdt, dev)
+        else:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected (C,), that of x, or "
+                             f"one row for each sequence [B, C]")
+        gate_rows = max(gate_rows, 0)
+    return _res_plan(rows, C, gate_rows, xs, rs, gs, float(alpha), float(eps),
+                     float(weight_offset), _DTYPES[dt], _DTYPES[rdt], _DTYPES[wdt or dt],
+                     _DTYPES[gdt], 1 if post else 0, 1 if pre else 0, 1 if center else 0)
+
+
+def gdr_res_forward(x, residual, gate=None, post_weight=None, post_bias=None, pre_weight=None,
+                    pre_bias=None, *, alpha=1.0, eps=1e-6, post=True, pre=True, center=False,
+                    weight_offset=0.0, save=True, y=None, h=None, stats=None):
+    """The norms around a block: h = residual + alpha gate N(x; post), y =
+    N(h; pre).  Returns (y or None, h, stats or None).
+
+    x [..., C] is what the block made, residual the sum so far (x's shape; fp32
+    or x's type).  gate is [C], of x's shape, or [B, C] with one row for each
+    sequence of x [B, T, C]; of either type.  The weights [C] are used as
+    weight + weight_offset; post and pre say which of the norms are taken.
+    h may be residual (in place)."""
+    shape, _ = _res_sizes(x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, alpha,
+                          eps, post, pre, center, weight_offset)
+    dev = x.device
+    y = _rows_out(y, "y", x) if pre else None
+    h = _rows_out(h, "h", residual)
+    stats = _out(stats, "stats", (shape.rows, 4), torch.float32, dev) if save else None
+    _launch("gdr_res_forward", shape, (x, residual, gate, post_weight, post_bias, pre_weight,
+                                       pre_bias, y, h, stats), dev)
+    return y, h, stats
+
+
+def gdr_res_backward(x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, stats, dy,
+                     dh=None, *, alpha=1.0, eps=1e-6, post=True, pre=True, center=False,
+                     weight_offset=0.0, workspace=None):
+    """Returns (dx, dresidual, dgate, dpost_weight, dpost_bias, dpre_weight,
+    dpre_bias); None where the forward had no such input.  residual is the
+    forward's input, not h; dy is None without the pre norm."""
+    shape, nbytes = _res_sizes(x, residual, gate, post_weight, post_bias, pre_weight, pre_bias,
+                               alpha, eps, post, pre, center, weight_offset)
+    dev = x.device
+    if pre:
+        _dense("dy", dy, x.shape, x.dtype, dev)
+    if dh is not None:
+        _dense("dh", dh, residual.shape, residual.dtype, dev)
+    elif not pre:
+        raise ValueError("dh is needed without the pre norm")
+    _dense("stats", stats, (shape.rows, 4), torch.float32, dev)
+    dx, dr = _dense_like(x), _dense_like(residual)
+    make = torch.empty_like if shape.rows > 0 else torch.zeros_like
+    dgate = None if gate is None else make(gate, memory_format=torch.contiguous_format)
+    dw = [None if w is None else make(w) for w in (post_weight, post_bias, pre_weight, pre_bias)]
+    workspace = _scratch(workspace, nbytes, x)
+    _launch("gdr_res_backward", shape, (x, residual, gate, post_weight, post_bias, pre_weight,
+                                        pre_bias, stats, dy if pre else None, dh, dx, dr, dgate,
+                                        *dw), dev, workspace, nbytes)
+    return (dx, dr, dgate, *dw)
+
+
 def _wanted(args):
     """Whether a gradient of any of them will be asked for."""
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args)
@@ -697,3 +894,63 @@ def group_norm(x, weight=None, bias=None, z=None, *, groups, eps=1e-6, center=Fa
     gdr_norm_forward): returns y."""
     return GroupNorm.apply(x, weight, bias, z, groups, eps, center, act,
                            _wanted((x, weight, bias, z)))
+
+
+class LinearAttention(torch.autograd.Function):
+    """y, S_T = linear_attention(...) with the library VJP."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_g, S0, scale, spans, T, save):
+        y, S_T, ctx.saved = gdr_lin_forward(q, k, v, log_g, S0, scale=scale, spans=spans, T=T,
+                                            save=save)
+        ctx.has_S0 = S0 is not None
+        # (spans too, so that a change of theirs in between is noticed)
+        ctx.save_for_backward(q, k, v, log_g, spans)
+        return y, S_T
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dS_T):
+        q, k, v, log_g, _ = ctx.saved_tensors
+        grads = gdr_lin_backward(q, k, v, log_g, ctx.saved, _gradient(dy), _gradient(dS_T),
+                                 want_dlog_g=ctx.needs_input_grad[3], want_dS0=ctx.has_S0)
+        return (*grads, None, None, None, None)
+
+
+def linear_attention(q, k, v, log_g=None, S0=None, *, scale=1.0, spans=None, T=None):
+    """Autograd-enabled linear attention with a decay for each head (see
+    gdr_lin_forward): returns (y, S_T).  The states for the backward are saved
+    only where a gradient is wanted."""
+    return LinearAttention.apply(q, k, v, log_g, S0, scale, spans, T,
+                                 _wanted((q, k, v, log_g, S0)))
+
+
+class ResidualNorm(torch.autograd.Function):
+    """y, h = residual_norm(...) with the library VJP."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gate, post_weight, post_bias, pre_weight, pre_bias, how, save):
+        y, h, stats = gdr_res_forward(x, residual, gate, post_weight, post_bias, pre_weight,
+                                      pre_bias, save=save, **how)
+        ctx.how = how
+        ctx.save_for_backward(x, residual, gate, post_weight, post_bias, pre_weight, pre_bias,
+                              stats)
+        return y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh):
+        dy = None if dy is None else _gradient(dy)
+        grads = gdr_res_backward(*ctx.saved_tensors, dy, _gradient(dh), **ctx.how)
+        return (*grads, None, None)
+
+
+def residual_norm(x, residual, gate=None, post_weight=None, post_bias=None, pre_weight=None,
+                  pre_bias=None, *, alpha=1.0, eps=1e-6, post=True, pre=True, center=False,
+                  weight_offset=0.0):
+    """Autograd-enabled norms around a block (see gdr_res_forward): returns
+    (y or None, h)."""
+    args = (x, residual, gate, post_weight, post_bias, pre_weight, pre_bias)
+    how = dict(alpha=alpha, eps=eps, post=post, pre=pre, center=center,
+               weight_offset=weight_offset)
+    return ResidualNorm.apply(*args, how, _wanted(args))

@@ -57,17 +57,19 @@ typedef enum {
   GDR_ERR_WORKSPACE = -8,       /* workspace smaller than the size query says  */
   GDR_ERR_ALIGNMENT = -9,       /* a pointer is not 16-byte aligned             */
   GDR_ERR_HIP = -10,            /* the HIP runtime rejected a launch            */
-  GDR_ERR_BAD_DECAY = -11,      /* decay is not GDR_DECAY_G or GDR_DECAY_LOG    */
+  GDR_ERR_BAD_DECAY = -11,      /* decay is not GDR_DECAY_G or GDR_DECAY_LOG,
+                                   or per_head not 0 or 1                   */
   GDR_ERR_SCRATCH_LIMIT = -12,  /* gdr_forward_noalloc: the shape's forward
                                    workspace exceeds GDR_NOALLOC_SCRATCH_BYTES */
   GDR_ERR_BAD_COUNT = -13,      /* gdr_set_launch_events: n outside
                                    0 .. GDR_MAX_LAUNCH_EVENTS               */
-  GDR_ERR_BAD_DIM = -14,        /* a dimension of a gdr_conv_shape,
-                                   gdr_scan_shape or gdr_norm_shape outside
-                                   the range stated there                   */
+  GDR_ERR_BAD_DIM = -14,        /* a dimension of the shape of an operator
+                                   below gdr_set_launch_events outside the
+                                   range stated there                       */
   GDR_ERR_BAD_STRIDE = -15,     /* a row stride below the row's width or
                                    above 2^31 - 1 (2^25 for a scan)         */
-  GDR_ERR_BAD_ACT = -16,        /* act is not a gdr_act, or softplus not 0, 1 */
+  GDR_ERR_BAD_ACT = -16,        /* act is not a gdr_act, or a flag (softplus,
+                                   post, pre, center) not 0 or 1            */
   GDR_ERR_BAD_EPS = -17,        /* eps negative, infinite or NaN             */
   GDR_ERR_OVERLAP = -18         /* a convolution's output rows overlap its
                                    input rows in a way not allowed there    */
@@ -231,8 +233,9 @@ int gdr_set_launch_events(void* const* events, int n);
 /* ---------------------------------------------------------------------------
  * The operators around the recurrence in a layer: the short causal
  * convolution that makes its q, k, v, the selective state space scan (the
- * sibling recurrence, with a diagonal state per channel) and the group norm
- * with a gate behind it.  Ownership, streams, errors and determinism as
+ * sibling recurrence, with a diagonal state per channel), the group norm
+ * with a gate behind it, linear attention (the sibling without the correction)
+ * and the norms around a block with its residual sum.  Ownership, streams, errors and determinism as
  * above; every data pointer is 16-byte aligned.  Outputs and workspaces overlap
  * no input and no other output except where it says so.
  *
@@ -372,6 +375,103 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
                       const void* bias, const void* z, const float* stats, const void* dy,
                       void* dx, void* dweight, void* dbias, void* dz, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* Linear attention with a decay for each head: per sequence and value head h,
+ * reading key head h / (Hv/Hk), with an fp32 state S[Dv][Dk]
+ *     S_t = exp(log_g_t[h]) S_{t-1} + outer(v_t[h], k_t);   y_t[h] = scale S_t q_t
+ * (the gated delta rule without the delta rule's correction).  log_g is rows
+ * [rows][Hv], or [Hv]: one decay per head (per_head).  A log_g of -inf forgets
+ * the state; positive ones are taken as they are.
+ * 1 <= Dk, Dv <= GDR_LIN_MAX_DIM, Hv a multiple of Hk and at most 65535, B at
+ * most 65535, T and rows at most 2^30 - 1.  A value that is not finite in a row
+ * makes the outputs of its sequence that the formula reaches from it not
+ * finite, and may do so to those of up to 63 earlier rows of that sequence
+ * (later ones, for the gradients), which are computed with it in one tile. */
+#define GDR_LIN_MAX_DIM 256
+typedef struct {
+  int64_t B, T, rows, Hk, Hv, Dk, Dv;
+  int64_t q_stride, k_stride; /* 0 = Hk Dk */
+  int64_t v_stride;           /* 0 = Hv Dv */
+  int64_t g_stride;           /* 0 = Hv (rows of log_g) */
+  float scale;
+  int32_t dtype;    /* gdr_dtype of q, k, v, y and their gradients */
+  int32_t gdtype;   /* of log_g and dlog_g */
+  int32_t per_head; /* 0: log_g [rows][Hv], 1: log_g [Hv] */
+} gdr_lin_shape;
+
+int gdr_lin_checkpoint_bytes(const gdr_lin_shape* shape, size_t* out);
+int gdr_lin_forward_workspace_bytes(const gdr_lin_shape* shape, size_t* out);
+int gdr_lin_backward_workspace_bytes(const gdr_lin_shape* shape, size_t* out);
+
+/*   in : q, k [rows][Hk][Dk]; v [rows][Hv][Dv]; log_g (NULL: no decay);
+ *        S0 [B][Hv][Dv][Dk] fp32 (NULL: 0); spans (NULL: dense)
+ *   out: y [rows][Hv][Dv]; S_T [B][Hv][Dv][Dk] fp32 (NULL: not written; may be
+ *        S0); ckpt: gdr_lin_checkpoint_bytes bytes (NULL: inference).
+ *   workspace: gdr_lin_forward_workspace_bytes bytes (NULL if 0).
+ * Single tokens are calls with T = 1 and S_T = S0. */
+int gdr_lin_forward(const gdr_lin_shape* shape, const void* q, const void* k, const void* v,
+                    const void* log_g, const float* S0, const int32_t* spans, void* y, float* S_T,
+                    void* ckpt, void* workspace, size_t workspace_bytes, void* stream);
+
+/* VJP of gdr_lin_forward for <dy, y> + <dS_T, S_T> (dS_T NULL: 0), from the
+ * same inputs and the ckpt that call wrote (S0 is in it).  dq, dk
+ * [rows][Hk][Dk], summed over the Hv/Hk value heads in a fixed order; dv
+ * [rows][Hv][Dv]; dlog_g dense, in gdtype, of log_g's shape (NULL: not
+ * written); dS0 [B][Hv][Dv][Dk] fp32 (NULL: not written; not the dS_T
+ * buffer). */
+int gdr_lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const void* v,
+                     const void* log_g, const int32_t* spans, const void* ckpt, const void* dy,
+                     const float* dS_T, void* dq, void* dk, void* dv, void* dlog_g, float* dS0,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norms before and after a block, with its gate and the residual sum.
+ * x [rows][C] is what the block made, residual [rows][C] the sum so far:
+ *     n = N(x; post_weight, post_bias)   (post = 0: x itself)
+ *     h = residual + alpha gate n        (the next residual)
+ *     y = N(h; pre_weight, pre_bias)     (pre = 0: none; the next block's input)
+ *     N(a; w, b) = (a - mu) / sqrt(mean((a - mu)^2) + eps) (w + weight_offset) + b
+ * over the C channels, mu = the mean (center = 1) or 0; y is the norm of h
+ * before h is rounded.  gate is [rows / gate_rows][C]: each of its rows serves
+ * gate_rows rows, one after another (gate_rows = 1: a gate for every row, T:
+ * one for each sequence of T rows, 0 or at least rows: one for all rows).
+ * 1 <= C <= GDR_RES_MAX_CHANNELS, rows a multiple of gate_rows.  The residual
+ * stream may be fp32 where the rows are bf16. */
+#define GDR_RES_MAX_CHANNELS 8192
+typedef struct {
+  int64_t rows, C, gate_rows;
+  int64_t x_stride, r_stride, gate_stride; /* 0 = C */
+  float alpha, eps, weight_offset;
+  int32_t dtype;  /* gdr_dtype of x, y, dx, dy */
+  int32_t rdtype; /* of residual, h, dh, dresidual */
+  int32_t wdtype; /* of the weights, biases and their gradients */
+  int32_t gdtype; /* of gate and dgate */
+  int32_t post, pre, center;
+} gdr_res_shape;
+
+/* Weights NULL: 1 (and no weight_offset); biases NULL: 0; gate NULL: 1; stats:
+ * fp32 [rows][4], the mean and 1/sqrt(..) of x and of h for the backward (NULL:
+ * not written).  y is not written with pre = 0.  h may be residual and y may be
+ * x, or h x (of one type), where those are dense (each row is read before it
+ * is written). */
+int gdr_res_forward(const gdr_res_shape* shape, const void* x, const void* residual,
+                    const void* gate, const void* post_weight, const void* post_bias,
+                    const void* pre_weight, const void* pre_bias, void* y, void* h, float* stats,
+                    void* stream);
+
+int gdr_res_backward_workspace_bytes(const gdr_res_shape* shape, size_t* out);
+
+/* VJP of gdr_res_forward for <dy, y> + <dh, h> from the same inputs (residual,
+ * not h) and its stats; dh NULL: 0 (with pre = 0, where dy is not read, it is
+ * required).  dx, dresidual [rows][C]; dgate [rows / gate_rows][C] dense;
+ * dgate and the weights' and biases' gradients NULL: not formed (with all of
+ * them NULL no workspace is needed).  Sums over rows in fp32 in a fixed
+ * order. */
+int gdr_res_backward(const gdr_res_shape* shape, const void* x, const void* residual,
+                     const void* gate, const void* post_weight, const void* post_bias,
+                     const void* pre_weight, const void* pre_bias, const float* stats,
+                     const void* dy, const void* dh, void* dx, void* dresidual, void* dgate,
+                     void* dpost_weight, void* dpost_bias, void* dpre_weight, void* dpre_bias,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static, human-readable text for a gdr_status value. */
 const char* gdr_strerror(int status);
