@@ -140,7 +140,12 @@ struct LinArgs {
   const float* S0;       // [B][Hv][Dv][Dk] or null
   void* y;
   float* S_T;            // or null
-  float* ckpt;           // [B][2][Hv][Dv][Dk]: S0 and S_T, or null
+  float* ckpt;           // [slots][Hv][Dv][Dk]: the states around the segments, or null
+  // sequences cut into segments (segs > 1 of the longest)
+  int seg;               // steps, a multiple of 64 (or at least T)
+  int segs;
+  float* states;         // [slots][Hv][Dv][Dk]: ckpt, or the forward's own; backward: adjoints
+  float* decay;          // [slots][Hv]
   // backward
   const void* dy;
   const float* dS_T;     // or null
@@ -152,12 +157,17 @@ struct LinArgs {
   float* dq_part;        // [rows][Hv][Dk], with Hk < Hv
   float* dk_part;
   float* flow;           // [2][tiles][rows][Hv]
-  float* head_sums;      // [B][Hv], for a decay per head
+  double* head_sums;     // [B][segs][Hv], for a decay per head
 };
+// Steps of a segment, segments of the longest sequence, slots of all.
+struct LinPlan {
+  int64_t seg, segs, slots;
+};
+LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv);
+// Workgroups over an output's width.
+int lin_tiles(int64_t width);
 hipError_t launch_lin_fwd(const LinArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_lin_bwd(const LinArgs& a, bool bf16, hipStream_t s);
-// Rows of the state that a workgroup of the step kernel takes.
-constexpr int kLinStepRows = 16;
 
 // The norms before and after a block with its gate and residual sum.
 struct ResArgs {

@@ -472,30 +472,36 @@ int check(const gdr_lin_shape* in, gdr_lin_shape* s) {
 }
 
 struct LinSizes {
-  int64_t ckpt, fwd;                         // bytes of the save buffer, of the workspaces
-  int64_t dq, dk, flow, heads, bwd;          // byte offsets of the backward's, its size
+  gdr::LinPlan plan;
+  int64_t ckpt;                                  // bytes of the save buffer
+  int64_t fwd_decay, fwd;                        // byte offsets of the workspaces, their sizes
+  int64_t bwd_decay, dq, dk, flow, heads, bwd;
 };
 
 int lin_sizes(const gdr_lin_shape& s, LinSizes* z) {
-  int64_t state, rows, x;
-  if (!product_ok(s.Hv * s.Dk * s.Dv * 4, s.B, &state) ||
+  z->plan = gdr::lin_plan(s.B, s.T, s.rows, s.Hv, s.Dk, s.Dv);
+  int64_t states, rows, x;
+  if (!product_ok(s.Hv * s.Dk * s.Dv * 4, z->plan.slots, &states) ||
       !product_ok(s.Hv * 4, s.rows, &rows))
     return GDR_ERR_OVERFLOW;
-  z->ckpt = 2 * state;
-  z->fwd = 0;
-  z->bwd = 0;
-  z->dq = z->dk = 0;
+  z->ckpt = states;
+  const int64_t split = z->plan.segs > 1 ? round_up256(states) : 0;
+  const int64_t decays = z->plan.segs > 1 ? round_up256(z->plan.slots * s.Hv * 4) : 0;
+  z->fwd_decay = z->bwd_decay = split;
+  z->fwd = z->dq = split + decays;
+  z->dk = z->flow = z->dq;
   if (s.Hv > s.Hk) {
     if (!product_ok(rows, s.Dk, &x)) return GDR_ERR_OVERFLOW;
-    z->dk = round_up256(x);
-    z->bwd = 2 * z->dk;
+    z->dk = z->dq + round_up256(x);
+    z->flow = z->dk + round_up256(x);
   }
-  z->flow = z->bwd;
-  const int64_t tiles = (s.Dk + gdr::kLinStepRows - 1) / gdr::kLinStepRows;
-  if (!product_ok(rows, 2 * tiles, &x)) return GDR_ERR_OVERFLOW;
-  z->bwd += round_up256(x);
-  z->heads = z->bwd;
-  z->bwd += round_up256(s.B * s.Hv * 4);
+  if (!product_ok(rows, 2 * gdr::lin_tiles(s.Dk), &x)) return GDR_ERR_OVERFLOW;
+  z->heads = z->flow + round_up256(x);
+  z->bwd = z->heads;
+  if (s.per_head) {
+    if (!product_ok(s.B * s.Hv * 8, z->plan.segs, &x)) return GDR_ERR_OVERFLOW;
+    z->bwd += round_up256(x);
+  }
   return GDR_OK;
 }
 
@@ -547,6 +553,10 @@ int lin_forward(const gdr_lin_shape* shape, const void* q, const void* k, const 
   a.y = y;
   a.S_T = S_T;
   a.ckpt = static_cast<float*>(ckpt);
+  a.seg = (int)z.plan.seg;
+  a.segs = has_rows ? (int)z.plan.segs : 1;
+  a.states = ckpt != nullptr ? a.ckpt : static_cast<float*>(workspace);
+  a.decay = reinterpret_cast<float*>(static_cast<char*>(workspace) + z.fwd_decay);
   return hip_status(gdr::launch_lin_fwd(a, s.dtype == GDR_BF16, static_cast<hipStream_t>(stream)));
 }
 
@@ -584,12 +594,16 @@ int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const
   a.dlog_g = dlog_g;
   a.dS0 = dS0;
   char* const w = static_cast<char*>(workspace);
+  a.seg = (int)z.plan.seg;
+  a.segs = has_rows ? (int)z.plan.segs : 1;
+  a.states = reinterpret_cast<float*>(w);
+  a.decay = reinterpret_cast<float*>(w + z.bwd_decay);
   if (s.Hv > s.Hk) {
     a.dq_part = reinterpret_cast<float*>(w + z.dq);
     a.dk_part = reinterpret_cast<float*>(w + z.dk);
   }
   a.flow = reinterpret_cast<float*>(w + z.flow);
-  a.head_sums = reinterpret_cast<float*>(w + z.heads);
+  a.head_sums = reinterpret_cast<double*>(w + z.heads);
   return hip_status(gdr::launch_lin_bwd(a, s.dtype == GDR_BF16, static_cast<hipStream_t>(stream)));
 }
 

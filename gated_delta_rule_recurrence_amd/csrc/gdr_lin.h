@@ -1,0 +1,560 @@
+// The chunked form of linear attention (formulas in gdr_lin.hip): tiles of L
+// steps of one head, their products on matrix cores.
+//
+// With H_r the summed log decays up to row r of a tile (its own included; for
+// dk and dv, whose tiles hold the steps in reverse, only those of the rows
+// before), P_ij = scale exp(H_i - H_j) Q_i.K_j for j <= i:
+//   out_i = sum_j P_ij V_j + cf_i S Q_i,          cf_i = exp(H_i)
+//   S <- exp(total) S + sum_j uf_j V_j K_j^T,     uf_j = exp(total - H_j)
+// H is summed and subtracted in 64 bits: a difference of two of them keeps the
+// accuracy of the few steps between, however much the tile has decayed.  A log
+// decay below kLeastLog (of which exp is 0 in fp32) counts as that, so that
+// -inf forgets without a difference of infinities.
+//
+// Precision.  bf16 rows are matrix operands as they are.  What is fp32 (P, S,
+// uf V) is held in two bf16 pieces, x = hi + lo within 2^-18: one piece would
+// add a rounding of 2^-9 a term to outputs that round by as much themselves,
+// and would leave the fp32 states with bf16's accuracy.  fp32 rows are three
+// pieces, and so is what they are multiplied with; of the nine products the
+// six above 2^-24 are formed.
+//
+// Mapping.  A workgroup of four waves runs through a segment of one sequence
+// for one head and NT 64 columns of its output.  P is formed by all waves, in
+// LDS; each wave then owns 16 NT columns of out and of the state, which stays
+// in its registers: an accumulator's layout (lane l: row 4 (l / 16) + v, column
+// l % 16) is an operand's (lane l: index l % 16, k = 8 (l / 16) + e) where two
+// accumulators' rows are dealt to the lanes in turn, so the update's left
+// operand is read from LDS in that order and the state needs no exchange.  Out
+// is formed transposed, so that a lane holds four neighbouring columns of one
+// row.
+#pragma once
+
+#include "gdr_layer.h"
+
+namespace gdr {
+
+constexpr double kLeastLog = -200.0;
+
+// One of the four products (gdr_lin.hip).
+struct LinRole {
+  const void* Q;
+  const void* K;
+  const void* V;
+  const void* R;       // with flow: rows that out's earlier part is multiplied with
+  int64_t sq, sk, sv, sr;
+  int dq, dk, dv, dr;  // value heads per head of each
+  int Ni, No, tiles;   // contracted width, output width, workgroups over it
+  float ps, cs, us;    // factors of P, of cf and of uf
+  int reverse;         // time runs backwards
+  int transposed;      // states lie [Ni][No] instead of [No][Ni]
+  int vec;             // widths and strides are whole vectors
+  const float* first;  // states before each segment, or null (zeros)
+  int slots;           // they lie in segments' slots, not [B][Hv]
+  float* last;         // [B][Hv] states behind the sequences (one segment), or null
+  float* save;         // slots of the state before and behind (one segment), or null
+  float* local;        // states only: slots of the segments' own ends
+  float* decay;        // states only: [slots][Hv] exp(total) of the segments
+  void* out;           // [rows][Hv][No], or null
+  float* part;         // the same in fp32
+  float* flow;         // [tiles][rows][Hv]: R out, without the step's own term
+};
+
+enum LinMode { kLinOut = 0, kLinFlow = 1, kLinState = 2 };
+
+// Slot of segment s of sequence b: sequences own more slots than segments, for
+// the state behind the last.
+__device__ __forceinline__ int64_t lin_slot(const LinArgs& a, Span sp, int b, int s) {
+  return sp.first / a.seg + 2 * (int64_t)b + s;
+}
+
+__device__ __forceinline__ float lin_log_decay(const LinArgs& a, int64_t row, int h) {
+  if (a.log_g == nullptr) return 0.f;
+  const int64_t at = a.per_head ? h : row * a.g_stride + h;
+  return a.g_bf16 ? to_f32(static_cast<const bf16*>(a.log_g)[at])
+                  : static_cast<const float*>(a.log_g)[at];
+}
+
+template <typename T>
+struct LinTypes;
+template <>
+struct LinTypes<bf16> {
+  static constexpr int L = 64, NP = 1, NS = 2;
+};
+template <>
+struct LinTypes<float> {
+  static constexpr int L = 32, NP = 3, NS = 3;
+};
+
+// A tile [rows][W] of bf16 in LDS whose 16-byte blocks are exchanged inside a
+// row so that the rows of an operand fall on different banks, read by rows
+// (16 rows, one block each) and transposed (4 rows, 4 blocks).
+template <int W>
+__device__ __forceinline__ int lin_swz(int r) {
+  if constexpr (W % 128 == 0) return ((r & 3) << 2) | ((r >> 2) & 3);
+  if constexpr (W == 32) return (r >> 2) & 3;
+  return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
+template <int W>
+__device__ __forceinline__ int lin_at(int r, int c) {
+  return r * W + (((c >> 3) ^ lin_swz<W>(r)) << 3) + (c & 7);
+}
+// Lane l: row r0 + l % 16, columns c0 + 8 (l / 16) ..
+template <int W>
+__device__ __forceinline__ uint4 lin_rows(const uint16_t* t, int r0, int c0, int lane) {
+  return *reinterpret_cast<const uint4*>(t + lin_at<W>(r0 + (lane & 15), c0 + 8 * (lane >> 4)));
+}
+// Lane l: column c0 + l % 16 (STATE: columns c0 + 8 (l % 16 / 4) + l % 4),
+// rows r0 + 8 (l / 16) ..
+template <int W, bool STATE>
+__device__ __forceinline__ uint4 lin_columns(const uint16_t* t, int r0, int c0, int lane) {
+  const int r = r0 + 8 * (lane >> 4) + ((lane >> 2) & 3), c = c0 + (STATE ? 8 : 4) * (lane & 3);
+  const uint2 lo = lds_read_tr16(t + lin_at<W>(r, c)), hi = lds_read_tr16(t + lin_at<W>(r + 4, c));
+  return uint4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// NS bf16 pieces of eight values, as operands.
+template <int NS>
+__device__ __forceinline__ void lin_split(f4 a, f4 b, uint4 (&p)[NS]) {
+  uint2 x[3], y[3];
+  if constexpr (NS == 3) {
+    split3_quad(a, x[0], x[1], x[2]);
+    split3_quad(b, y[0], y[1], y[2]);
+  } else {
+    x[0] = uint2{cvt_pk_bf16(a[0], a[1]), cvt_pk_bf16(a[2], a[3])};
+    y[0] = uint2{cvt_pk_bf16(b[0], b[1]), cvt_pk_bf16(b[2], b[3])};
+    x[1] = uint2{cvt_pk_bf16(minus_bf16_lo(x[0].x, a[0]), minus_bf16_hi(x[0].x, a[1])),
+                 cvt_pk_bf16(minus_bf16_lo(x[0].y, a[2]), minus_bf16_hi(x[0].y, a[3]))};
+    y[1] = uint2{cvt_pk_bf16(minus_bf16_lo(y[0].x, b[0]), minus_bf16_hi(y[0].x, b[1])),
+                 cvt_pk_bf16(minus_bf16_lo(y[0].y, b[2]), minus_bf16_hi(y[0].y, b[3]))};
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) p[i] = uint4{x[i].x, x[i].y, y[i].x, y[i].y};
+}
+
+// c + a b over the pieces' products that fp32 sees.
+template <int NA, int NB>
+__device__ __forceinline__ f4 lin_mfma(const uint4 (&a)[NA], const uint4 (&b)[NB], f4 c) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j < 3) c = mfma_bf16(a[i], b[j], c);
+  return c;
+}
+
+// Eight elements of a row as loaded.
+template <typename T>
+struct LinRaw;
+template <>
+struct LinRaw<bf16> {
+  uint4 v;
+  __device__ __forceinline__ void put(uint16_t* const (&t)[1], int at) const {
+    *reinterpret_cast<uint4*>(t[0] + at) = v;
+  }
+};
+template <>
+struct LinRaw<float> {
+  f4 lo, hi;
+  __device__ __forceinline__ void put(uint16_t* const (&t)[3], int at) const {
+    uint4 p[3];
+    lin_split<3>(lo, hi, p);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(t[i] + at) = p[i];
+  }
+};
+__device__ __forceinline__ void lin_get(const bf16* p, int n, bool vec, LinRaw<bf16>& r) {
+  r.v = uint4{0, 0, 0, 0};
+  if (n <= 0) return;
+  if (vec) {
+    r.v = *reinterpret_cast<const uint4*>(p);
+    return;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i / 2] |= (uint32_t)p[i].bits << (16 * (i & 1));
+  r.v = uint4{w[0], w[1], w[2], w[3]};
+}
+__device__ __forceinline__ void lin_get(const float* p, int n, bool vec, LinRaw<float>& r) {
+  r.lo = r.hi = f4{0.f, 0.f, 0.f, 0.f};
+  if (n <= 0) return;
+  if (vec) {
+    r.lo = *reinterpret_cast<const f4*>(p);
+    r.hi = *reinterpret_cast<const f4*>(p + 4);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < n) r.lo[i] = p[i];
+    if (i + 4 < n) r.hi[i] = p[i + 4];
+  }
+}
+// Four elements of a row in fp32.
+template <typename T>
+__device__ __forceinline__ f4 lin_quad(const T* p, int n, bool vec) {
+  f4 x = {0.f, 0.f, 0.f, 0.f};
+  if (n <= 0) return x;
+  if (vec) {
+    float f[4];
+    unpack(load_pack<T, 4>(p), f);
+    return f4{f[0], f[1], f[2], f[3]};
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) x[i] = to_f32(p[i]);
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ void lin_put(T* p, f4 x, int n, bool vec) {
+  if (n <= 0) return;
+  if (vec) {
+    const float f[4] = {x[0], x[1], x[2], x[3]};
+    store_pack(p, f);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) st(p, i, x[i]);
+}
+
+// Sums over lanes 0 .. l.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lin_dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF,
+                                                  false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lin_prefix_sum(double x) {
+  x += lin_dpp<0x111, 0xF>(x);  // row_shr:1
+  x += lin_dpp<0x112, 0xF>(x);
+  x += lin_dpp<0x114, 0xF>(x);
+  x += lin_dpp<0x118, 0xF>(x);
+  x += lin_dpp<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+  x += lin_dpp<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
+__device__ __forceinline__ float lin_exp(double x) { return exp2_hw(kLog2e * (float)x); }
+
+// Units of eight elements of a tile [L][W] that a thread stages.
+template <int L, int W>
+constexpr int kLinUnits = (L * W / 8 + 255) / 256;
+
+template <typename T, int W>
+struct LinStage {
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, N = kLinUnits<L, W>;
+  LinRaw<T> raw[N];
+  // rows first + step r, r < len, of which columns c0 .. c0 + n are read
+  __device__ __forceinline__ void load(const T* p, int64_t stride, int step, int from, int len,
+                                       int n, bool vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = threadIdx.x + 256 * i, r = u / (W / 8), c = u % (W / 8) * 8;
+      const bool in = r >= from && r < len && (L * W / 8 % 256 == 0 || u < L * W / 8);
+      lin_get(p + (int64_t)(step * r) * stride + c, in ? n - c : 0, vec, raw[i]);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* const (&t)[NP]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = threadIdx.x + 256 * i, r = u / (W / 8), c = u % (W / 8) * 8;
+      if (L * W / 8 % 256 == 0 || u < L * W / 8) raw[i].put(t, lin_at<W>(r, c));
+    }
+  }
+};
+
+template <typename T, int KI, int NT, int MODE>
+struct LinTiles {
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = LinTypes<T>::NS;
+  static constexpr int WO = 64 * NT;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + (MODE == kLinState ? 0 : NP * L * KI);
+  static constexpr int kV = kK + NP * L * KI;
+  static constexpr int kP = kV + NP * L * WO;
+  static constexpr int kEnd = kP + (MODE == kLinState ? 0 : NS * L * L);  // of uint16_t
+};
+
+template <typename T, int KI, int NT, int MODE>
+__global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk_kernel(LinArgs a,
+                                                                                     LinRole r) {
+  using Z = LinTiles<T, KI, NT, MODE>;
+  constexpr int L = Z::L, NP = Z::NP, NS = Z::NS, WO = Z::WO, IT = L / 16, KS = KI / 32;
+  constexpr bool OUT = MODE != kLinState, FLOW = MODE == kLinFlow;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[Z::kEnd];
+  __shared__ double Hs[L];
+  __shared__ __attribute__((aligned(16))) float cf[L], uf[L], pd[L];
+  __shared__ float total_s, red[4][L];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, lr = lane & 15;
+  const int tile = blockIdx.x % r.tiles, sg = blockIdx.x / r.tiles, h = blockIdx.y, b = blockIdx.z;
+  const Span sp = span_of(a.spans, b, a.T, a.rows);
+  const int begin = sg * a.seg;
+  if (sg > 0 && begin >= sp.len) return;
+  const int len = sp.len - begin < a.seg ? sp.len - begin : a.seg;  // of this segment
+  const int chunks = (len + L - 1) / L;
+  const int64_t size = (int64_t)r.Ni * r.No, slot = lin_slot(a, sp, b, sg);
+  const int o0 = tile * WO, wo = o0 + wave * 16 * NT;  // the wave's columns
+  const int no = r.No - o0;
+
+  uint16_t *Qt[NP], *Kt[NP], *Vt[NP], *Pt[NS];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    Qt[i] = lds + Z::kQ + i * L * KI;
+    Kt[i] = lds + Z::kK + i * L * KI;
+    Vt[i] = lds + Z::kV + i * L * WO;
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) Pt[i] = lds + Z::kP + i * L * L;
+
+  // The state: tile pair s (columns 32 s + 8 q + 4 k + v of Ni), columns lr.
+  f4 S[2 * KS][NT];
+  auto element = [&](int s2, int nt, int v, int64_t* at) __attribute__((always_inline)) {
+    const int i = 32 * (s2 >> 1) + 8 * q + 4 * (s2 & 1) + v, o = wo + 16 * nt + lr;
+    *at = r.transposed ? (int64_t)i * r.No + o : (int64_t)o * r.Ni + i;
+    return i < r.Ni && o < r.No;
+  };
+  const float* first = nullptr;
+  if (r.first != nullptr)
+    first = r.first + ((r.slots ? slot : (int64_t)b) * a.Hv + h) * size;
+#pragma unroll
+  for (int s = 0; s < 2 * KS; ++s)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        int64_t at;
+        const bool in = element(s, nt, v, &at);
+        S[s][nt][v] = first != nullptr && in ? first[at] : 0.f;
+      }
+  auto put_state = [&](float* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2 * KS; ++s)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          int64_t at;
+          if (element(s, nt, v, &at)) to[at] = S[s][nt][v];
+        }
+  };
+  if (r.save != nullptr) put_state(r.save + (slot * a.Hv + h) * size);
+
+  LinStage<T, KI> qs, ks;
+  LinStage<T, WO> vs;
+  float lg = 0.f;
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    // row x of the tile is step t0 + x, or t0 + L - 1 - x
+    const int t0 = (r.reverse ? chunks - 1 - c : c) * L, n = len - t0 < L ? len - t0 : L;
+    const int64_t row = sp.first + begin + t0 + (r.reverse ? L - 1 : 0);
+    const int step = r.reverse ? -1 : 1, from = r.reverse ? L - n : 0, to = r.reverse ? L : n;
+    if constexpr (OUT)
+      qs.load(static_cast<const T*>(r.Q) + row * r.sq + (int64_t)(h / r.dq) * r.Ni, r.sq, step,
+              from, to, r.Ni, r.vec);
+    ks.load(static_cast<const T*>(r.K) + row * r.sk + (int64_t)(h / r.dk) * r.Ni, r.sk, step, from,
+            to, r.Ni, r.vec);
+    vs.load(static_cast<const T*>(r.V) + row * r.sv + (int64_t)(h / r.dv) * r.No + o0, r.sv, step,
+            from, to, no, r.vec);
+    if (threadIdx.x < L)
+      lg = (int)threadIdx.x >= from && (int)threadIdx.x < to
+               ? lin_log_decay(a, row + step * (int)threadIdx.x, h)
+               : 0.f;
+  };
+  if (chunks > 0) fetch(0);
+  if constexpr (OUT) {  // tiles above the diagonal stay zero
+    for (int i = threadIdx.x; i < NS * L * L / 8; i += 256)
+      reinterpret_cast<uint4*>(lds + Z::kP)[i] = uint4{0, 0, 0, 0};
+  }
+  double all = 0.0;  // the segment's summed log decays (first L threads)
+
+  for (int c = 0; c < chunks; ++c) {
+    __syncthreads();  // the last tile has been read
+    if constexpr (OUT) qs.store(Qt);
+    ks.store(Kt);
+    vs.store(Vt);
+    if (threadIdx.x < 64) {
+      double x = threadIdx.x < L ? (double)lg : 0.0;
+      x = x < kLeastLog ? kLeastLog : x;  // (NaN stays)
+      const double sum = lin_prefix_sum(x);
+      const double end = __shfl(sum, 63, 64);
+      all += end;
+      if (threadIdx.x < L) {
+        const double H = r.reverse ? sum - x : sum;
+        Hs[threadIdx.x] = H;
+        cf[threadIdx.x] = r.cs * lin_exp(H);
+        uf[threadIdx.x] = r.us * lin_exp(end - H);
+        if (threadIdx.x == 0) total_s = lin_exp(end);
+      }
+    }
+    if (c + 1 < chunks) fetch(c + 1);
+    __syncthreads();
+    const int t0 = (r.reverse ? chunks - 1 - c : c) * L;
+
+    f4 acc[IT][NT];
+    if constexpr (OUT) {
+      // P: IT (IT + 1) / 2 tiles of 16 x 16 on and below the diagonal
+#pragma unroll
+      for (int k = 0; k < (IT * (IT + 1) / 2 + 3) / 4; ++k) {
+        const int t = 4 * k + wave;
+        if (t < IT * (IT + 1) / 2) {
+          const int it = (t >= 1) + (t >= 3) + (t >= 6), jt = t - it * (it + 1) / 2;
+          f4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            uint4 ka[NP], qb[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              ka[i] = lin_rows<KI>(Kt[i], 16 * jt, 32 * s, lane);
+              qb[i] = lin_rows<KI>(Qt[i], 16 * it, 32 * s, lane);
+            }
+            p = lin_mfma(ka, qb, p);
+          }
+          const int i = 16 * it + lr, j = 16 * jt + 4 * q;
+          const double Hi = Hs[i];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (FLOW && i == j + v) pd[i] = r.ps * p[v];
+            const bool in = FLOW ? j + v < i : j + v <= i;
+            p[v] = in ? p[v] * (r.ps * lin_exp(Hi - Hs[j + v])) : 0.f;
+          }
+          uint4 pieces[NS];
+          lin_split<NS>(p, f4{0.f, 0.f, 0.f, 0.f}, pieces);
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+            *reinterpret_cast<uint2*>(Pt[n] + lin_at<L>(i, j)) = uint2{pieces[n].x, pieces[n].y};
+        }
+      }
+      // out <- S Q, scaled by cf
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[it][nt] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 sa[NT][NS];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) lin_split<NS>(S[2 * s][nt], S[2 * s + 1][nt], sa[nt]);
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          uint4 qb[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) qb[i] = lin_rows<KI>(Qt[i], 16 * it, 32 * s, lane);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(sa[nt], qb, acc[it][nt]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const float x = cf[16 * it + lr];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= x;
+      }
+      __syncthreads();  // P is whole
+    }
+    {
+      const float x = total_s;
+#pragma unroll
+      for (int s = 0; s < 2 * KS; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[s][nt] *= x;
+    }
+#pragma unroll
+    for (int k = 0; k < L / 32; ++k) {
+      uint4 vo[NT][NP], vu[NT][NS];
+      const f4 u0 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q);
+      const f4 u1 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q + 4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+#pragma unroll
+        for (int i = NP - 1; i >= 0; --i) {
+          vo[nt][i] = lin_columns<WO, false>(Vt[i], 32 * k, 16 * (NT * wave + nt), lane);
+          const uint4 w = vo[nt][i];
+          x += f4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                  __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+          y += f4{__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
+                  __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u)};
+        }
+        lin_split<NS>(x * u0, y * u1, vu[nt]);
+      }
+      if constexpr (OUT) {
+#pragma unroll
+        for (int it = 2 * k; it < IT; ++it) {
+          uint4 pb[NS];
+#pragma unroll
+          for (int n = 0; n < NS; ++n) pb[n] = lin_rows<L>(Pt[n], 16 * it, 32 * k, lane);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(vo[nt], pb, acc[it][nt]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2 * KS; ++s) {
+        uint4 ka[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          ka[i] = lin_columns<KI, true>(Kt[i], 32 * k, 32 * (s >> 1) + 4 * (s & 1), lane);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[s][nt] = lin_mfma(ka, vu[nt], S[s][nt]);
+      }
+    }
+    if constexpr (OUT) {
+      const int n = len - t0 < L ? len - t0 : L;
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int x = 16 * it + lr, t = r.reverse ? L - 1 - x : x;
+        const bool live = t < n;
+        const int64_t row = sp.first + begin + t0 + t;
+        float flow = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int o = wo + 16 * nt + 4 * q, left = live ? r.No - o : 0;
+          if constexpr (FLOW) {
+            const f4 w = lin_quad(static_cast<const T*>(r.R) + row * r.sr +
+                                      (int64_t)(h / r.dr) * r.No + o,
+                                  left, r.vec);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) flow = fmaf(w[v], acc[it][nt][v], flow);
+            // the step's own term
+            f4 own = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = NP - 1; i >= 0; --i) {
+              const uint2 y = *reinterpret_cast<const uint2*>(Vt[i] + lin_at<WO>(x, o - o0));
+              own += f4{__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
+                        __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u)};
+            }
+            acc[it][nt] += own * pd[x];
+          }
+          const int64_t at = (row * a.Hv + h) * r.No + o;
+          if (r.out != nullptr)
+            lin_put(static_cast<T*>(r.out) + at, acc[it][nt], left, r.vec);
+          else
+            lin_put(r.part + at, acc[it][nt], left, r.vec);
+        }
+        if constexpr (FLOW) {
+          flow = swap16_sum(flow, flow);
+          flow = swap32_sum(flow, flow);
+          if (q == 0) red[wave][x] = flow;
+        }
+      }
+      if constexpr (FLOW) {
+        __syncthreads();
+        const int x = threadIdx.x, t = r.reverse ? L - 1 - x : x;
+        if (x < L && t < n)
+          r.flow[((int64_t)tile * a.rows + sp.first + begin + t0 + t) * a.Hv + h] =
+              (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
+      }
+    }
+  }
+  if constexpr (MODE == kLinState) {
+    put_state(r.local + ((slot + (r.reverse ? 0 : 1)) * a.Hv + h) * size);
+    if (threadIdx.x == 0 && tile == 0) r.decay[slot * a.Hv + h] = lin_exp(all);
+  }
+  if (r.last != nullptr) put_state(r.last + ((int64_t)b * a.Hv + h) * size);
+  if (r.save != nullptr) put_state(r.save + ((slot + 1) * a.Hv + h) * size);
+}
+
+// The instances: widths of 64 to 256 contracted, 64 or 128 columns of output.
+template <typename T>
+hipError_t lin_chunk(const LinArgs& a, LinRole r, int mode, hipStream_t s);
+
+}  // namespace gdr

@@ -2,23 +2,33 @@
 //   S_t = g_t S_{t-1} + v_t k_t^T,  y_t = scale S_t q_t,  g_t = exp(log_g_t).
 // The adjoint D_t = scale dy_t q_t^T + g_{t+1} D_{t+1} gives dq = scale S^T dy,
 // dk = D^T v, dv = D k: the forward's form with the roles of the tensors
-// turned (and, for dk and dv, with time reversed), so one kernel serves all:
-//   state[o][i] <- g state + u V[o] K[i];  out[o] = s sum_i state[o][i] Q[i]
+// turned (and, for dk and dv, with time reversed), so one kernel serves all
+// (gdr_lin.h):
+//   state[o][i] <- g state + V[o] K[i];  out[o] = sum_i state[o][i] Q[i]
 //   y: (Q, K, V) = (q, k, v);  dq: (dy, v, k);  dk: (v, dy, q);  dv: (k, q, dy).
+// Where sequences times heads are too few for the device, sequences are cut
+// into segments: one pass forms the segments' own ends (of k and v, or q and
+// dy), a second joins them, and the main pass starts each segment from its
+// state.  The forward's states around the segments are what it saves.
 //
 // dlog_g_t is what flows through the decay of step t: the sum of
 //   A_ij = scale exp(..) (q_i k_j) (dy_i v_j) over i >= t > j,
-// which is sum_{i >= t} (a_i - b_i) + <dS_T, S_T> with a_i the sum of A_ij over
-// j < i (q_i times the part of dq_i that comes from earlier steps) and b_j that
-// over i > j.  The term i = j, which both would hold, is left out of both, so
-// that strong decays do not leave a small difference of large sums.
-#include "gdr_layer.h"
+// which is sum_{i >= t} (a_i - b_i) + <adjoint, state> behind the segment, with
+// a_i the sum of A_ij over j < i (q_i times the part of dq_i that comes from
+// earlier steps) and b_j that over i > j.  The term i = j, which both would
+// hold, is left out of both, so that strong decays do not leave a small
+// difference of large sums.
+#include "gdr_lin.h"
 
 namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaveRows = kLinStepRows / (kThreads / 64);
+// Steps up to which a forward call goes one step at a time.
+constexpr int kFewSteps = 8;
+// Rows of the state of a workgroup of that kernel.
+constexpr int kStepRows = 16;
+constexpr int kWaveRows = kStepRows / (kThreads / 64);
 
 __device__ __forceinline__ float wave_sum(float x) {
   x = rowsum16(x);
@@ -26,54 +36,24 @@ __device__ __forceinline__ float wave_sum(float x) {
   return swap32_sum(x, x);
 }
 
-__device__ __forceinline__ float log_decay(const LinArgs& a, int64_t row, int h) {
-  if (a.log_g == nullptr) return 0.f;
-  const int64_t at = a.per_head ? h : row * a.g_stride + h;
-  return a.g_bf16 ? to_f32(static_cast<const bf16*>(a.log_g)[at])
-                  : static_cast<const float*>(a.log_g)[at];
-}
-
-// One of the four products (see above).
-struct Role {
-  const void* Q;
-  const void* K;
-  const void* V;
-  const void* R;       // rows that out's earlier part is multiplied with, or null
-  int64_t sq, sk, sv, sr;
-  int dq, dk, dv, dr;  // value heads per head of each
-  int Ni, No;
-  float u, s;          // factors of the update and of the output
-  int reverse;
-  int transposed;      // the state lies [i][o]
-  const float* first;  // [B][first_per][Hv] states, of which each first one, or null
-  int first_per;
-  float* last;         // [B][Hv] states or null
-  float* save;         // [B][2][Hv] states, the first and the last, or null
-  void* out;           // [rows][Hv][No], or null
-  float* part;         // the same in fp32, or null
-  float* flow;         // [tiles][rows][Hv]: R out, without the step's own term
-};
-
 // A step at a time: a wave holds kWaveRows rows of the state, a lane every
 // 64th column.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a, Role r) {
+__global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int o0 = blockIdx.x * kLinStepRows + wave * kWaveRows;
+  const int h = blockIdx.y, b = blockIdx.z, reps = a.Hv / a.Hk;
+  const int o0 = blockIdx.x * kStepRows + wave * kWaveRows;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
-  const int64_t size = (int64_t)r.Ni * r.No;
+  const int size = a.Dk * a.Dv;
   const float* const first =
-      r.first != nullptr ? r.first + ((int64_t)b * r.first_per * a.Hv + h) * size : nullptr;
+      a.S0 != nullptr ? a.S0 + ((int64_t)b * a.Hv + h) * size : nullptr;
   float S[kWaveRows][4];
 #pragma unroll
   for (int j = 0; j < kWaveRows; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int o = o0 + j, i = lane + 64 * e;
-      S[j][e] = first != nullptr && o < r.No && i < r.Ni
-                    ? first[r.transposed ? i * r.No + o : o * r.Ni + i]
-                    : 0.f;
+      S[j][e] = first != nullptr && o < a.Dv && i < a.Dk ? first[o * a.Dk + i] : 0.f;
     }
   auto store = [&](float* to) __attribute__((always_inline)) {
 #pragma unroll
@@ -81,63 +61,81 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a, Role r) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int o = o0 + j, i = lane + 64 * e;
-        if (o < r.No && i < r.Ni) to[r.transposed ? i * r.No + o : o * r.Ni + i] = S[j][e];
+        if (o < a.Dv && i < a.Dk) to[o * a.Dk + i] = S[j][e];
       }
   };
-  if (r.save != nullptr) store(r.save + ((int64_t)b * 2 * a.Hv + h) * size);
-  __shared__ float red[kThreads / 64];
+  const int64_t slot = lin_slot(a, sp, b, 0);
+  if (a.ckpt != nullptr) store(a.ckpt + (slot * a.Hv + h) * size);
   for (int t = 0; t < sp.len; ++t) {
-    const int64_t row = sp.first + (r.reverse ? sp.len - 1 - t : t);
-    const T* const Q = static_cast<const T*>(r.Q) + row * r.sq + (int64_t)(h / r.dq) * r.Ni;
-    const T* const K = static_cast<const T*>(r.K) + row * r.sk + (int64_t)(h / r.dk) * r.Ni;
-    const T* const V = static_cast<const T*>(r.V) + row * r.sv + (int64_t)(h / r.dv) * r.No;
-    const float g = expf(log_decay(a, row, h));
-    float q[4], k[4], own = 0.f;
+    const int64_t row = sp.first + t;
+    const T* const Q = static_cast<const T*>(a.q) + row * a.q_stride + (int64_t)(h / reps) * a.Dk;
+    const T* const K = static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)(h / reps) * a.Dk;
+    const T* const V = static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)h * a.Dv;
+    const float g = expf(lin_log_decay(a, row, h));
+    float q[4], k[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = lane + 64 * e;
-      q[e] = i < r.Ni ? to_f32(Q[i]) : 0.f;
-      k[e] = i < r.Ni ? to_f32(K[i]) * r.u : 0.f;
-      own = fmaf(q[e], k[e], own);
+      q[e] = i < a.Dk ? to_f32(Q[i]) : 0.f;
+      k[e] = i < a.Dk ? to_f32(K[i]) : 0.f;
     }
-    own = wave_sum(own);
-    float flow = 0.f;
 #pragma unroll
     for (int j = 0; j < kWaveRows; ++j) {
       const int o = o0 + j;
-      const bool in = o < r.No;
+      const bool in = o < a.Dv;
       const float v = in ? to_f32(V[o]) : 0.f;
       float x = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (!r.reverse) S[j][e] *= g;
+        S[j][e] = fmaf(v, k[e], S[j][e] * g);
         x = fmaf(S[j][e], q[e], x);
-        S[j][e] = fmaf(v, k[e], S[j][e]);
-        if (r.reverse) S[j][e] *= g;
       }
-      x = wave_sum(x);
-      if (r.flow != nullptr && in) {
-        const T* const R = static_cast<const T*>(r.R) + row * r.sr + (int64_t)(h / r.dr) * r.No;
-        flow = fmaf(to_f32(R[o]), r.s * x, flow);
-      }
-      x = r.s * fmaf(v, own, x);
-      if (lane == 0 && in) {
-        const int64_t at = (row * a.Hv + h) * r.No + o;
-        if (r.out != nullptr) st(static_cast<T*>(r.out), at, x);
-        if (r.part != nullptr) r.part[at] = x;
-      }
-    }
-    if (r.flow != nullptr) {
-      __syncthreads();
-      if (lane == 0) red[wave] = flow;
-      __syncthreads();
-      if (threadIdx.x == 0)
-        r.flow[((int64_t)blockIdx.x * a.rows + row) * a.Hv + h] =
-            (red[0] + red[1]) + (red[2] + red[3]);
+      x = a.scale * wave_sum(x);
+      if (lane == 0 && in) st(static_cast<T*>(a.y), (row * a.Hv + h) * a.Dv + o, x);
     }
   }
-  if (r.last != nullptr) store(r.last + ((int64_t)b * a.Hv + h) * size);
-  if (r.save != nullptr) store(r.save + (((int64_t)b * 2 + 1) * a.Hv + h) * size);
+  if (a.S_T != nullptr) store(a.S_T + ((int64_t)b * a.Hv + h) * size);
+  if (a.ckpt != nullptr) store(a.ckpt + ((slot + 1) * a.Hv + h) * size);
+}
+
+// The states around the segments from their own ends, in place: forward slot
+// s + 1 holds segment s's end, backward slot s holds segment s's adjoint at its
+// begin and receives the one behind it.
+template <int V>
+__global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int reverse) {
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int size = a.Dk * a.Dv, at = (blockIdx.x * kThreads + threadIdx.x) * V;
+  if (at >= size) return;
+  const Span sp = span_of(a.spans, b, a.T, a.rows);
+  const int n = (sp.len + a.seg - 1) / a.seg;
+  const int64_t slot = lin_slot(a, sp, b, 0);
+  const int64_t whole = ((int64_t)b * a.Hv + h) * size + at, step = (int64_t)a.Hv * size;
+  float* const p = a.states + (slot * a.Hv + h) * size + at;
+  const float* const d = a.decay + slot * a.Hv + h;
+  const float* const first = reverse ? a.dS_T : a.S0;
+  float S[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) S[v] = 0.f;
+  if (first != nullptr) unpack(load_pack<float, V>(first + whole), S);
+  float next[V];
+  auto fetch = [&](int s) __attribute__((always_inline)) {
+    unpack(load_pack<float, V>(p + (reverse ? n - 1 - s : s + 1) * step), next);
+  };
+  if (n > 0) fetch(0);
+  for (int s = 0; s < n; ++s) {
+    float x[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = next[v];
+    if (s + 1 < n) fetch(s + 1);
+    const int m = reverse ? n - 1 - s : s;
+    store_pack(p + m * step, S);
+    const float g = d[(int64_t)m * a.Hv];
+#pragma unroll
+    for (int v = 0; v < V; ++v) S[v] = fmaf(g, S[v], x[v]);
+  }
+  if (!reverse) store_pack(p + n * step, S);
+  float* const last = reverse ? a.dS0 : a.S_T;
+  if (last != nullptr) store_pack(last + whole, S);
 }
 
 // Sums of the fp32 parts over a key head's value heads.
@@ -160,39 +158,66 @@ __global__ __launch_bounds__(kThreads) void lin_heads_sum(LinArgs a) {
   }
 }
 
-// dlog_g from the flows: one wave a sequence and head walks the steps from the
-// end, 64 at a time, sums in 64 bits.
-__global__ __launch_bounds__(64) void lin_flow_kernel(LinArgs a, int tiles_q, int tiles_k) {
-  const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x;
-  const Span sp = span_of(a.spans, b, a.T, a.rows);
-  double carry = 0.0;
-  if (a.dS_T != nullptr) {
-    const int64_t n = (int64_t)a.Dk * a.Dv;
-    const float* const d = a.dS_T + ((int64_t)b * a.Hv + h) * n;
-    const float* const S = a.ckpt + (((int64_t)b * 2 + 1) * a.Hv + h) * n;
-    for (int64_t i = lane; i < n; i += 64) carry += (double)d[i] * (double)S[i];
+// Sum over a workgroup, in every thread.
+__device__ __forceinline__ double block_sum(double x, double* red) {
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) carry += __shfl_xor(carry, m, 64);
+  for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// dlog_g from the flows: a workgroup a segment and head walks the steps from
+// the end, 256 at a time, sums in 64 bits.
+__global__ __launch_bounds__(kThreads) void lin_flow_kernel(LinArgs a, int tiles) {
+  __shared__ double red[kThreads / 64];
+  const int sg = blockIdx.x, h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 63,
+            wave = threadIdx.x >> 6;
+  const Span sp = span_of(a.spans, b, a.T, a.rows);
+  const int begin = sg * a.seg;
+  const int len = sp.len - begin < a.seg ? sp.len - begin : a.seg;
+  if (len <= 0) {  // (the whole workgroup)
+    if (a.per_head && threadIdx.x == 0)
+      a.head_sums[((int64_t)b * a.segs + sg) * a.Hv + h] = 0.0;
+    return;
+  }
+  const int64_t slot = lin_slot(a, sp, b, sg), n = (int64_t)a.Dk * a.Dv;
+  const float* const S = a.ckpt + ((slot + 1) * a.Hv + h) * n;
+  const float* const D = a.segs > 1          ? a.states + (slot * a.Hv + h) * n
+                         : a.dS_T != nullptr ? a.dS_T + ((int64_t)b * a.Hv + h) * n
+                                             : nullptr;
+  double carry = 0.0, head = 0.0;
+  if (D != nullptr) {
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) carry += (double)D[i] * (double)S[i];
+    carry = block_sum(carry, red);
   }
   const float* const fa = a.flow;
-  const float* const fb = a.flow + (int64_t)tiles_q * a.rows * a.Hv;
-  double head = 0.0;
-  for (int t0 = (sp.len - 1) & ~63; t0 >= 0; t0 -= 64) {
-    const int t = t0 + lane;
+  const float* const fb = a.flow + (int64_t)tiles * a.rows * a.Hv;
+  for (int t0 = (len - 1) & ~(kThreads - 1); t0 >= 0; t0 -= kThreads) {
+    const int t = t0 + threadIdx.x;
+    const int64_t row = sp.first + begin + t;
     double x = 0.0;
-    const int64_t row = sp.first + t;
-    if (t < sp.len) {
-      for (int i = 0; i < tiles_q; ++i) x += (double)fa[((int64_t)i * a.rows + row) * a.Hv + h];
-      for (int i = 0; i < tiles_k; ++i) x -= (double)fb[((int64_t)i * a.rows + row) * a.Hv + h];
-    }
+    if (t < len)
+      for (int i = 0; i < tiles; ++i) {
+        const int64_t at = ((int64_t)i * a.rows + row) * a.Hv + h;
+        x += (double)fa[at] - (double)fb[at];
+      }
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {  // sums over the lanes from here on
+    for (int m = 1; m < 64; m <<= 1) {  // sums over the wave's lanes from here on
       const double y = __shfl_down(x, m, 64);
       x += lane + m < 64 ? y : 0.0;
     }
+    __syncthreads();
+    if (lane == 0) red[wave] = x;
+    __syncthreads();
+    for (int w = wave + 1; w < kThreads / 64; ++w) x += red[w];
     x += carry;
-    carry = __shfl(x, 0, 64);
-    if (t < sp.len) {
+    carry += (red[0] + red[1]) + (red[2] + red[3]);
+    if (t < len) {
+      // (a step that forgets everything: nothing flows through it)
+      const bool cut = lin_log_decay(a, row, h) == -__builtin_inff();
+      if (cut) x = 0.0;
       head += x;
       if (!a.per_head) {
         const int64_t at = row * a.Hv + h;
@@ -204,77 +229,201 @@ __global__ __launch_bounds__(64) void lin_flow_kernel(LinArgs a, int tiles_q, in
     }
   }
   if (!a.per_head) return;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) head += __shfl_xor(head, m, 64);
-  if (lane == 0) a.head_sums[(int64_t)b * a.Hv + h] = (float)head;
+  head = block_sum(head, red);
+  if (threadIdx.x == 0) a.head_sums[((int64_t)b * a.segs + sg) * a.Hv + h] = head;
 }
 
 __global__ __launch_bounds__(kThreads) void lin_head_kernel(LinArgs a) {
   const int h = blockIdx.x * kThreads + threadIdx.x;
   if (h >= a.Hv) return;
   double s = 0.0;
-  for (int b = 0; b < a.B; ++b) s += (double)a.head_sums[(int64_t)b * a.Hv + h];
+  for (int64_t i = 0; i < (int64_t)a.B * a.segs; ++i) s += a.head_sums[i * a.Hv + h];
   st_weight(a.dlog_g, h, (float)s, a.g_bf16);
 }
 
-template <typename T>
-hipError_t step(const LinArgs& a, const Role& r, hipStream_t s) {
-  const unsigned tiles = (r.No + kLinStepRows - 1) / kLinStepRows;
-  hipLaunchKernelGGL(lin_step_kernel<T>, dim3(tiles, a.Hv, a.B), dim3(kThreads), 0, s, a, r);
+hipError_t noted(hipStream_t s) {
   const hipError_t e = hipGetLastError();
   note_launch(s);
   return e;
 }
 
+hipError_t join(const LinArgs& a, int reverse, hipStream_t s) {
+  const int size = a.Dk * a.Dv, V = size % 4 == 0 ? 4 : 1;
+  const dim3 grid((size / V + kThreads - 1) / kThreads, a.Hv, a.B);
+  if (V == 4)
+    hipLaunchKernelGGL(lin_join_kernel<4>, grid, dim3(kThreads), 0, s, a, reverse);
+  else
+    hipLaunchKernelGGL(lin_join_kernel<1>, grid, dim3(kThreads), 0, s, a, reverse);
+  return noted(s);
+}
+
+// Whether widths and strides let rows be read in whole vectors.
+bool whole_vectors(const LinArgs& a, bool bf16) {
+  const int64_t v = bf16 ? 8 : 4;
+  return a.Dk % 8 == 0 && a.Dv % 8 == 0 && a.q_stride % v == 0 && a.k_stride % v == 0 &&
+         a.v_stride % v == 0;
+}
+
 template <typename T>
 hipError_t fwd(const LinArgs& a, hipStream_t s) {
+  if (a.T <= kFewSteps) {
+    hipLaunchKernelGGL(lin_step_kernel<T>, dim3((a.Dv + kStepRows - 1) / kStepRows, a.Hv, a.B),
+                       dim3(kThreads), 0, s, a);
+    return noted(s);
+  }
   const int reps = a.Hv / a.Hk;
-  return step<T>(a, Role{a.q, a.k, a.v, nullptr, a.q_stride, a.k_stride, a.v_stride, 0, reps, reps,
-                         1, 1, a.Dk, a.Dv, 1.f, a.scale, 0, 0, a.S0, 1, a.S_T, a.ckpt, a.y,
-                         nullptr, nullptr},
-                 s);
+  LinRole r{};
+  r.Q = a.q;
+  r.K = a.k;
+  r.V = a.v;
+  r.sq = a.q_stride;
+  r.sk = a.k_stride;
+  r.sv = a.v_stride;
+  r.dq = r.dk = reps;
+  r.dv = 1;
+  r.Ni = a.Dk;
+  r.No = a.Dv;
+  r.tiles = lin_tiles(r.No);
+  r.ps = r.cs = a.scale;
+  r.us = 1.f;
+  r.vec = whole_vectors(a, sizeof(T) == 2);
+  r.out = a.y;
+  if (a.segs == 1) {
+    r.first = a.S0;
+    r.last = a.S_T;
+    r.save = a.ckpt;
+    return lin_chunk<T>(a, r, kLinOut, s);
+  }
+  r.local = a.states;
+  r.decay = a.decay;
+  hipError_t e = lin_chunk<T>(a, r, kLinState, s);
+  if (e == hipSuccess) e = join(a, 0, s);
+  r.first = a.states;
+  r.slots = 1;
+  return e == hipSuccess ? lin_chunk<T>(a, r, kLinOut, s) : e;
 }
 
 template <typename T>
 hipError_t bwd(const LinArgs& a, hipStream_t s) {
   const int reps = a.Hv / a.Hk;
   const int64_t wide = (int64_t)a.Hv * a.Dv;
-  const int tiles = (a.Dk + kLinStepRows - 1) / kLinStepRows;
-  const bool flows = a.dlog_g != nullptr;
-  Role q{a.dy, a.v, a.k, a.q, wide, a.v_stride, a.k_stride, a.q_stride, 1, 1, reps, reps, a.Dv,
-         a.Dk, 1.f, a.scale, 0, 1, a.ckpt, 2, nullptr, nullptr, reps > 1 ? nullptr : a.dq, a.dq_part,
-         flows ? a.flow : nullptr};
-  Role k{a.v, a.dy, a.q, a.k, a.v_stride, wide, a.q_stride, a.k_stride, 1, 1, reps, reps, a.Dv,
-         a.Dk, a.scale, 1.f, 1, 1, a.dS_T, 1, nullptr, nullptr, reps > 1 ? nullptr : a.dk, a.dk_part,
-         flows ? a.flow + (int64_t)tiles * a.rows * a.Hv : nullptr};
-  Role v{a.k, a.q, a.dy, nullptr, a.k_stride, a.q_stride, wide, 0, reps, reps, 1, 1, a.Dk, a.Dv,
-         a.scale, 1.f, 1, 0, a.dS_T, 1, a.dS0, nullptr, a.dv, nullptr, nullptr};
-  hipError_t e = step<T>(a, q, s);
-  if (e == hipSuccess) e = step<T>(a, k, s);
-  if (e == hipSuccess) e = step<T>(a, v, s);
+  const int tiles = lin_tiles(a.Dk);
+  const int mode = a.dlog_g != nullptr ? kLinFlow : kLinOut;
+  hipError_t e = hipSuccess;
+  LinRole r{};
+  r.vec = whole_vectors(a, sizeof(T) == 2);
+  r.dq = 1;
+  r.dk = 1;
+  r.dv = r.dr = reps;
+  // dq: (dy, v, k)
+  r.Q = a.dy;
+  r.K = a.v;
+  r.V = a.k;
+  r.R = a.q;
+  r.sq = wide;
+  r.sk = a.v_stride;
+  r.sv = a.k_stride;
+  r.sr = a.q_stride;
+  r.Ni = a.Dv;
+  r.No = a.Dk;
+  r.tiles = tiles;
+  r.ps = r.cs = a.scale;
+  r.us = 1.f;
+  r.transposed = 1;
+  r.first = a.ckpt;
+  r.slots = 1;
+  r.out = reps > 1 ? nullptr : a.dq;
+  r.part = a.dq_part;
+  r.flow = a.flow;
+  LinRole d = r;
+  // dv: (k, q, dy)
+  LinRole v = r;
+  v.Q = a.k;
+  v.K = a.q;
+  v.V = a.dy;
+  v.sq = a.k_stride;
+  v.sk = a.q_stride;
+  v.sv = wide;
+  v.dq = v.dk = reps;
+  v.dv = 1;
+  v.Ni = a.Dk;
+  v.No = a.Dv;
+  v.tiles = lin_tiles(a.Dv);
+  v.ps = v.us = a.scale;
+  v.cs = 1.f;
+  v.reverse = 1;
+  v.transposed = 0;
+  v.out = a.dv;
+  v.part = nullptr;
+  if (a.segs > 1) {
+    v.first = nullptr;
+    v.local = a.states;
+    v.decay = a.decay;
+    e = lin_chunk<T>(a, v, kLinState, s);
+    if (e == hipSuccess) e = join(a, 1, s);
+    v.first = a.states;
+  } else {
+    v.first = a.dS_T;
+    v.slots = 0;
+    v.last = a.dS0;
+  }
+  if (e == hipSuccess) e = lin_chunk<T>(a, r, mode, s);
+  // dk: (v, dy, q)
+  d.Q = a.v;
+  d.K = a.dy;
+  d.V = a.q;
+  d.R = a.k;
+  d.sq = a.v_stride;
+  d.sk = wide;
+  d.sv = a.q_stride;
+  d.sr = a.k_stride;
+  d.ps = d.us = a.scale;
+  d.cs = 1.f;
+  d.reverse = 1;
+  d.first = v.first;
+  d.slots = v.slots;
+  d.out = reps > 1 ? nullptr : a.dk;
+  d.part = a.dk_part;
+  d.flow = a.flow + (int64_t)tiles * a.rows * a.Hv;
+  if (e == hipSuccess) e = lin_chunk<T>(a, d, mode, s);
+  if (e == hipSuccess) e = lin_chunk<T>(a, v, kLinOut, s);
   if (e == hipSuccess && reps > 1) {
     const int64_t blocks = ((int64_t)a.T * a.Hk * a.Dk + kThreads - 1) / kThreads;
     hipLaunchKernelGGL(lin_heads_sum<T>,
                        dim3((unsigned)(blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks), a.B, 2),
                        dim3(kThreads), 0, s, a);
-    e = hipGetLastError();
-    note_launch(s);
+    e = noted(s);
   }
-  if (e == hipSuccess && flows) {
-    hipLaunchKernelGGL(lin_flow_kernel, dim3(a.Hv, a.B), dim3(64), 0, s, a, tiles, tiles);
-    e = hipGetLastError();
-    note_launch(s);
+  if (e == hipSuccess && mode == kLinFlow) {
+    hipLaunchKernelGGL(lin_flow_kernel, dim3(a.segs, a.Hv, a.B), dim3(kThreads), 0, s, a, tiles);
+    e = noted(s);
     if (e == hipSuccess && a.per_head) {
       hipLaunchKernelGGL(lin_head_kernel, dim3((a.Hv + kThreads - 1) / kThreads), dim3(kThreads),
                          0, s, a);
-      e = hipGetLastError();
-      note_launch(s);
+      e = noted(s);
     }
   }
   return e;
 }
 
 }  // namespace
+
+int lin_tiles(int64_t width) { return (int)((width + 127) / 128); }
+
+// Segments for 512 workgroups, two a compute unit, of 128 steps at least.
+LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv) {
+  LinPlan p{};
+  const int64_t per = Hv * lin_tiles(Dv);  // workgroups of one cut through all rows
+  const int64_t want = (512 + per - 1) / per;
+  int64_t seg = (rows + want - 1) / want;
+  seg = (seg + 63) / 64 * 64;
+  if (seg < 128) seg = 128;
+  if (T <= seg) seg = rows < T ? (T < 1 ? 1 : T) : (rows < 1 ? 1 : rows);  // one
+  p.seg = seg;
+  p.segs = T > seg ? (T + seg - 1) / seg : 1;
+  p.slots = rows / seg + 2 * B + 1;
+  return p;
+}
 
 hipError_t launch_lin_fwd(const LinArgs& a, bool is_bf16, hipStream_t s) {
   return is_bf16 ? fwd<bf16>(a, s) : fwd<float>(a, s);

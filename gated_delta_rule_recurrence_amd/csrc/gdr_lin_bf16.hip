@@ -1,0 +1,6 @@
+// The chunked linear attention's instances for bf16 rows (see gdr_lin.h).
+#include "gdr_lin_launch.h"
+
+namespace gdr {
+template hipError_t lin_chunk<bf16>(const LinArgs& a, LinRole r, int mode, hipStream_t s);
+}  // namespace gdr
