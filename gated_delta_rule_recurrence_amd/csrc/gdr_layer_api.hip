@@ -15,6 +15,7 @@ constexpr int64_t kMaxChannels = INT64_C(1) << 20;
 constexpr int64_t kMaxRows = INT32_MAX / 2;  // rows and steps; twice it still is an int
 constexpr int64_t kMaxStride = INT32_MAX;
 constexpr int64_t kMaxScanStride = INT64_C(1) << 25;  // 16 rows of 4 bytes in 32 bits
+constexpr int64_t kMaxLinStride = INT64_C(1) << 23;   // 64 rows of 4 bytes in 31 bits
 constexpr int64_t kMaxBatch = 65535;  // sequences index grid y, groups z
 constexpr int64_t kMaxIndex = INT64_C(1) << 61;
 
@@ -465,8 +466,10 @@ int check(const gdr_lin_shape* in, gdr_lin_shape* s) {
     return GDR_ERR_UNSUPPORTED_DIM;
   if (!dtype_ok(s->dtype) || !dtype_ok(s->gdtype)) return GDR_ERR_BAD_DTYPE;
   if (s->per_head != 0 && s->per_head != 1) return GDR_ERR_BAD_DECAY;
-  if (!stride_ok(&s->q_stride, s->Hk * s->Dk) || !stride_ok(&s->k_stride, s->Hk * s->Dk) ||
-      !stride_ok(&s->v_stride, s->Hv * s->Dv) || !stride_ok(&s->g_stride, s->Hv))
+  const int64_t most = kMaxLinStride;
+  if (!stride_ok(&s->q_stride, s->Hk * s->Dk, most) ||
+      !stride_ok(&s->k_stride, s->Hk * s->Dk, most) ||
+      !stride_ok(&s->v_stride, s->Hv * s->Dv, most) || !stride_ok(&s->g_stride, s->Hv))
     return GDR_ERR_BAD_STRIDE;
   return GDR_OK;
 }

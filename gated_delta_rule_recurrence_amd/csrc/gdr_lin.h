@@ -34,6 +34,8 @@
 namespace gdr {
 
 constexpr double kLeastLog = -200.0;
+// An offset past the end of every buffer (64 rows of at most 2^23 elements).
+constexpr uint32_t kLinPast = 0xf0000000u;
 
 // One of the four products (gdr_lin.hip).
 struct LinRole {
@@ -142,7 +144,8 @@ __device__ __forceinline__ f4 lin_mfma(const uint4 (&a)[NA], const uint4 (&b)[NB
   return c;
 }
 
-// Eight elements of a row as loaded.
+// Eight elements of a row as loaded: whole vectors, or elements of which only
+// the first n are in the row.
 template <typename T>
 struct LinRaw;
 template <>
@@ -151,44 +154,37 @@ struct LinRaw<bf16> {
   __device__ __forceinline__ void put(uint16_t* const (&t)[1], int at) const {
     *reinterpret_cast<uint4*>(t[0] + at) = v;
   }
+  __device__ __forceinline__ void load(Buffer p, uint32_t at) {
+    v = get_pack<bf16, 8>(p, at).v;
+  }
+  __device__ __forceinline__ void load(Buffer p, uint32_t at, int n) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = get_pack<bf16, 1>(p, i < n ? at + 2 * i : kLinPast).v[0].bits;
+    v = uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+  }
 };
 template <>
 struct LinRaw<float> {
-  f4 lo, hi;
+  float4 lo, hi;
   __device__ __forceinline__ void put(uint16_t* const (&t)[3], int at) const {
     uint4 p[3];
-    lin_split<3>(lo, hi, p);
+    lin_split<3>(f4{lo.x, lo.y, lo.z, lo.w}, f4{hi.x, hi.y, hi.z, hi.w}, p);
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(t[i] + at) = p[i];
   }
+  __device__ __forceinline__ void load(Buffer p, uint32_t at) {
+    lo = get_pack<float, 4>(p, at).v;
+    hi = get_pack<float, 4>(p, at + 16).v;
+  }
+  __device__ __forceinline__ void load(Buffer p, uint32_t at, int n) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = get_pack<float, 1>(p, i < n ? at + 4 * i : kLinPast).v[0];
+    lo = float4{w[0], w[1], w[2], w[3]};
+    hi = float4{w[4], w[5], w[6], w[7]};
+  }
 };
-__device__ __forceinline__ void lin_get(const bf16* p, int n, bool vec, LinRaw<bf16>& r) {
-  r.v = uint4{0, 0, 0, 0};
-  if (n <= 0) return;
-  if (vec) {
-    r.v = *reinterpret_cast<const uint4*>(p);
-    return;
-  }
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) w[i / 2] |= (uint32_t)p[i].bits << (16 * (i & 1));
-  r.v = uint4{w[0], w[1], w[2], w[3]};
-}
-__device__ __forceinline__ void lin_get(const float* p, int n, bool vec, LinRaw<float>& r) {
-  r.lo = r.hi = f4{0.f, 0.f, 0.f, 0.f};
-  if (n <= 0) return;
-  if (vec) {
-    r.lo = *reinterpret_cast<const f4*>(p);
-    r.hi = *reinterpret_cast<const f4*>(p + 4);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < n) r.lo[i] = p[i];
-    if (i + 4 < n) r.hi[i] = p[i + 4];
-  }
-}
 // Four elements of a row in fp32.
 template <typename T>
 __device__ __forceinline__ f4 lin_quad(const T* p, int n, bool vec) {
@@ -238,30 +234,38 @@ __device__ __forceinline__ double lin_prefix_sum(double x) {
 
 __device__ __forceinline__ float lin_exp(double x) { return exp2_hw(kLog2e * (float)x); }
 
-// Units of eight elements of a tile [L][W] that a thread stages.
-template <int L, int W>
-constexpr int kLinUnits = (L * W / 8 + 255) / 256;
-
+// A tile [L][W] on its way through a thread's registers: 8 threads a row,
+// eight elements in each 64 columns, 32 rows at a time.
 template <typename T, int W>
 struct LinStage {
-  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, N = kLinUnits<L, W>;
-  LinRaw<T> raw[N];
-  // rows first + step r, r < len, of which columns c0 .. c0 + n are read
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int step, int from, int len,
-                                       int n, bool vec) {
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NR = L / 32, NC = W / 64;
+  LinRaw<T> raw[NR][NC];
+  // `rows` rows of n columns, `stride` apart, from p on; zeros outside
+  __device__ __forceinline__ void load(const T* p, int64_t stride, int rows, int n, bool vec,
+                                       int thread) {
+    const Buffer buf = buffer_of(p, 0, (((int64_t)rows - 1) * stride + n) * sizeof(T));
+    const int c = (thread & 7) * 8;
+    const uint32_t at = ((thread >> 3) * (uint32_t)stride + c) * sizeof(T);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = threadIdx.x + 256 * i, r = u / (W / 8), c = u % (W / 8) * 8;
-      const bool in = r >= from && r < len && (L * W / 8 % 256 == 0 || u < L * W / 8);
-      lin_get(p + (int64_t)(step * r) * stride + c, in ? n - c : 0, vec, raw[i]);
-    }
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const uint32_t to = at + (32 * i * (uint32_t)stride + 64 * k) * sizeof(T);
+        if (vec)
+          raw[i][k].load(buf, c + 64 * k < n ? to : kLinPast);
+        else
+          raw[i][k].load(buf, to, n - c - 64 * k);
+      }
   }
-  __device__ __forceinline__ void store(uint16_t* const (&t)[NP]) const {
+  // reverse: the last row first
+  __device__ __forceinline__ void store(uint16_t* const (&t)[NP], bool reverse, int thread) const {
+    const int x = reverse ? L - 1 - (thread >> 3) : thread >> 3;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = threadIdx.x + 256 * i, r = u / (W / 8), c = u % (W / 8) * 8;
-      if (L * W / 8 % 256 == 0 || u < L * W / 8) raw[i].put(t, lin_at<W>(r, c));
-    }
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        raw[i][k].put(t, lin_at<W>(reverse ? x - 32 * i : x + 32 * i,
+                                   (thread & 7) * 8 + 64 * k));
   }
 };
 
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
   __shared__ double Hs[L];
   __shared__ __attribute__((aligned(16))) float cf[L], uf[L], pd[L];
   __shared__ float total_s, red[4][L];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, lr = lane & 15;
+  const int wave = threadIdx.x >> 6;
   const int tile = blockIdx.x % r.tiles, sg = blockIdx.x / r.tiles, h = blockIdx.y, b = blockIdx.z;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
   const int begin = sg * a.seg;
@@ -309,58 +313,59 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
 
   // The state: tile pair s (columns 32 s + 8 q + 4 k + v of Ni), columns lr.
   f4 S[2 * KS][NT];
-  auto element = [&](int s2, int nt, int v, int64_t* at) __attribute__((always_inline)) {
-    const int i = 32 * (s2 >> 1) + 8 * q + 4 * (s2 & 1) + v, o = wo + 16 * nt + lr;
-    *at = r.transposed ? (int64_t)i * r.No + o : (int64_t)o * r.Ni + i;
-    return i < r.Ni && o < r.No;
-  };
-  const float* first = nullptr;
-  if (r.first != nullptr)
-    first = r.first + ((r.slots ? slot : (int64_t)b) * a.Hv + h) * size;
-#pragma unroll
-  for (int s = 0; s < 2 * KS; ++s)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        int64_t at;
-        const bool in = element(s, nt, v, &at);
-        S[s][nt][v] = first != nullptr && in ? first[at] : 0.f;
-      }
-  auto put_state = [&](float* to) __attribute__((always_inline)) {
+  // (the lane is made opaque, so that no addresses stay in registers between
+  // the loads and the stores: they would be as many as the state)
+  auto each = [&](auto f) __attribute__((always_inline)) {
+    int l = threadIdx.x & 63;
+    asm volatile("" : "+v"(l));
+    const int i0 = 8 * (l >> 4), o = wo + (l & 15);
+    const int step_i = r.transposed ? r.No : 1, step_o = r.transposed ? 1 : r.Ni;
+    const int at = i0 * step_i + o * step_o;
 #pragma unroll
     for (int s = 0; s < 2 * KS; ++s)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          int64_t at;
-          if (element(s, nt, v, &at)) to[at] = S[s][nt][v];
+          const int i = 32 * (s >> 1) + 4 * (s & 1) + v;
+          S[s][nt][v] = f(S[s][nt][v], at + i * step_i + 16 * nt * step_o,
+                          i0 + i < r.Ni && o + 16 * nt < r.No);
         }
+  };
+  const float* first = nullptr;
+  if (r.first != nullptr)
+    first = r.first + ((r.slots ? slot : (int64_t)b) * a.Hv + h) * size;
+  each([&](float, int at, bool in) __attribute__((always_inline)) {
+    return first != nullptr && in ? first[at] : 0.f;
+  });
+  auto put_state = [&](float* to) __attribute__((always_inline)) {
+    each([&](float x, int at, bool in) __attribute__((always_inline)) {
+      if (in) to[at] = x;
+      return x;
+    });
   };
   if (r.save != nullptr) put_state(r.save + (slot * a.Hv + h) * size);
 
   LinStage<T, KI> qs, ks;
   LinStage<T, WO> vs;
   float lg = 0.f;
-  auto fetch = [&](int c) __attribute__((always_inline)) {
+  auto fetch = [&](int c, int thread) __attribute__((always_inline)) {
     // row x of the tile is step t0 + x, or t0 + L - 1 - x
     const int t0 = (r.reverse ? chunks - 1 - c : c) * L, n = len - t0 < L ? len - t0 : L;
-    const int64_t row = sp.first + begin + t0 + (r.reverse ? L - 1 : 0);
-    const int step = r.reverse ? -1 : 1, from = r.reverse ? L - n : 0, to = r.reverse ? L : n;
+    const int64_t row = sp.first + begin + t0;
     if constexpr (OUT)
-      qs.load(static_cast<const T*>(r.Q) + row * r.sq + (int64_t)(h / r.dq) * r.Ni, r.sq, step,
-              from, to, r.Ni, r.vec);
-    ks.load(static_cast<const T*>(r.K) + row * r.sk + (int64_t)(h / r.dk) * r.Ni, r.sk, step, from,
-            to, r.Ni, r.vec);
-    vs.load(static_cast<const T*>(r.V) + row * r.sv + (int64_t)(h / r.dv) * r.No + o0, r.sv, step,
-            from, to, no, r.vec);
-    if (threadIdx.x < L)
-      lg = (int)threadIdx.x >= from && (int)threadIdx.x < to
-               ? lin_log_decay(a, row + step * (int)threadIdx.x, h)
-               : 0.f;
+      qs.load(static_cast<const T*>(r.Q) + row * r.sq + (int64_t)(h / r.dq) * r.Ni, r.sq, n,
+              r.Ni, r.vec, thread);
+    ks.load(static_cast<const T*>(r.K) + row * r.sk + (int64_t)(h / r.dk) * r.Ni, r.sk, n, r.Ni,
+            r.vec, thread);
+    vs.load(static_cast<const T*>(r.V) + row * r.sv + (int64_t)(h / r.dv) * r.No + o0, r.sv, n,
+            no < WO ? no : WO, r.vec, thread);
+    if (threadIdx.x < L) {
+      const int t = r.reverse ? L - 1 - (int)threadIdx.x : (int)threadIdx.x;
+      lg = t < n ? lin_log_decay(a, row + t, h) : 0.f;
+    }
   };
-  if (chunks > 0) fetch(0);
+  if (chunks > 0) fetch(0, threadIdx.x);
   if constexpr (OUT) {  // tiles above the diagonal stay zero
     for (int i = threadIdx.x; i < NS * L * L / 8; i += 256)
       reinterpret_cast<uint4*>(lds + Z::kP)[i] = uint4{0, 0, 0, 0};
@@ -368,10 +373,15 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
   double all = 0.0;  // the segment's summed log decays (first L threads)
 
   for (int c = 0; c < chunks; ++c) {
+    // (opaque, so that addresses are formed where they are used and do not
+    // fill the registers through the loop)
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
+    const int lane = thread & 63, q = lane >> 4, lr = lane & 15;
     __syncthreads();  // the last tile has been read
-    if constexpr (OUT) qs.store(Qt);
-    ks.store(Kt);
-    vs.store(Vt);
+    if constexpr (OUT) qs.store(Qt, r.reverse, thread);
+    ks.store(Kt, r.reverse, thread);
+    vs.store(Vt, r.reverse, thread);
     if (threadIdx.x < 64) {
       double x = threadIdx.x < L ? (double)lg : 0.0;
       x = x < kLeastLog ? kLeastLog : x;  // (NaN stays)
@@ -386,7 +396,7 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
         if (threadIdx.x == 0) total_s = lin_exp(end);
       }
     }
-    if (c + 1 < chunks) fetch(c + 1);
+    if (c + 1 < chunks) fetch(c + 1, thread);
     __syncthreads();
     const int t0 = (r.reverse ? chunks - 1 - c : c) * L;
 

@@ -67,7 +67,8 @@ typedef enum {
                                    below gdr_set_launch_events outside the
                                    range stated there                       */
   GDR_ERR_BAD_STRIDE = -15,     /* a row stride below the row's width or
-                                   above 2^31 - 1 (2^25 for a scan)         */
+                                   above 2^31 - 1 (2^25 for a scan, 2^23 for
+                                   linear attention)         */
   GDR_ERR_BAD_ACT = -16,        /* act is not a gdr_act, or a flag (softplus,
                                    post, pre, center) not 0 or 1            */
   GDR_ERR_BAD_EPS = -17,        /* eps negative, infinite or NaN             */
@@ -383,7 +384,8 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
  * [rows][Hv], or [Hv]: one decay per head (per_head).  A log_g of -inf forgets
  * the state; positive ones are taken as they are.
  * 1 <= Dk, Dv <= GDR_LIN_MAX_DIM, Hv a multiple of Hk and at most 65535, B at
- * most 65535, T and rows at most 2^30 - 1.  A value that is not finite in a row
+ * most 65535, T and rows at most 2^30 - 1, strides (and Hk Dk, Hv Dv) at most
+ * 2^23.  A value that is not finite in a row
  * makes the outputs of its sequence that the formula reaches from it not
  * finite, and may do so to those of up to 63 earlier rows of that sequence
  * (later ones, for the gradients), which are computed with it in one tile. */
