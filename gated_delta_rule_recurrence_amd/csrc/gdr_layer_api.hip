@@ -469,7 +469,8 @@ int check(const gdr_lin_shape* in, gdr_lin_shape* s) {
   const int64_t most = kMaxLinStride;
   if (!stride_ok(&s->q_stride, s->Hk * s->Dk, most) ||
       !stride_ok(&s->k_stride, s->Hk * s->Dk, most) ||
-      !stride_ok(&s->v_stride, s->Hv * s->Dv, most) || !stride_ok(&s->g_stride, s->Hv))
+      !stride_ok(&s->v_stride, s->Hv * s->Dv, most) || !stride_ok(&s->g_stride, s->Hv) ||
+      s->Hv * s->Dk > most)
     return GDR_ERR_BAD_STRIDE;
   return GDR_OK;
 }

@@ -49,7 +49,7 @@ struct LinRole {
   float ps, cs, us;    // factors of P, of cf and of uf
   int reverse;         // time runs backwards
   int transposed;      // states lie [Ni][No] instead of [No][Ni]
-  int vec;             // widths and strides are whole vectors
+  int vec;             // widths and strides are whole vectors (VEC)
   const float* first;  // states before each segment, or null (zeros)
   int slots;           // they lie in segments' slots, not [B][Hv]
   float* last;         // [B][Hv] states behind the sequences (one segment), or null
@@ -185,32 +185,44 @@ struct LinRaw<float> {
     hi = float4{w[4], w[5], w[6], w[7]};
   }
 };
-// Four elements of a row in fp32.
-template <typename T>
-__device__ __forceinline__ f4 lin_quad(const T* p, int n, bool vec) {
-  f4 x = {0.f, 0.f, 0.f, 0.f};
-  if (n <= 0) return x;
-  if (vec) {
-    float f[4];
-    unpack(load_pack<T, 4>(p), f);
-    return f4{f[0], f[1], f[2], f[3]};
-  }
+// Four elements of a row, of which n are in it, `at` + `more` bytes into p (the
+// sum in the offset that the bound is checked with).
+template <bool VEC, typename T>
+__device__ __forceinline__ f4 lin_quad(Buffer p, uint32_t at, uint32_t more, int n) {
+  float f[4];
+  if constexpr (VEC) {
+    unpack(get_pack<T, 4>(p, n > 0 ? at + more : kLinPast), f);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) x[i] = to_f32(p[i]);
-  return x;
+    for (int i = 0; i < 4; ++i)
+      f[i] = to_f32(get_pack<T, 1>(p, i < n ? at + more + i * sizeof(T) : kLinPast).v[0]);
+  }
+  return f4{f[0], f[1], f[2], f[3]};
 }
-template <typename T>
-__device__ __forceinline__ void lin_put(T* p, f4 x, int n, bool vec) {
-  if (n <= 0) return;
-  if (vec) {
-    const float f[4] = {x[0], x[1], x[2], x[3]};
-    store_pack(p, f);
-    return;
-  }
+template <bool VEC, typename T>
+__device__ __forceinline__ void lin_put(Buffer p, uint32_t at, uint32_t more, f4 x, int n) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  if constexpr (VEC) {
+    const int to = n > 0 ? at + more : kLinPast;
+    if constexpr (sizeof(T) == 2)
+      __builtin_amdgcn_raw_buffer_store_b64(
+          u32x2{cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])}, p.resource(), to, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), p.resource(), to,
+                                             0, 0);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) st(p, i, x[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int to = i < n ? at + more + i * sizeof(T) : kLinPast;
+      if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)cvt_pk_bf16(x[i], x[i]), p.resource(), to,
+                                              0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[i]), p.resource(), to,
+                                              0, 0);
+    }
+  }
 }
 
 // Sums over lanes 0 .. l.
@@ -241,8 +253,8 @@ struct LinStage {
   static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NR = L / 32, NC = W / 64;
   LinRaw<T> raw[NR][NC];
   // `rows` rows of n columns, `stride` apart, from p on; zeros outside
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int rows, int n, bool vec,
-                                       int thread) {
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T* p, int64_t stride, int rows, int n, int thread) {
     const Buffer buf = buffer_of(p, 0, (((int64_t)rows - 1) * stride + n) * sizeof(T));
     const int c = (thread & 7) * 8;
     const uint32_t at = ((thread >> 3) * (uint32_t)stride + c) * sizeof(T);
@@ -251,7 +263,7 @@ struct LinStage {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         const uint32_t to = at + (32 * i * (uint32_t)stride + 64 * k) * sizeof(T);
-        if (vec)
+        if constexpr (VEC)
           raw[i][k].load(buf, c + 64 * k < n ? to : kLinPast);
         else
           raw[i][k].load(buf, to, n - c - 64 * k);
@@ -269,6 +281,15 @@ struct LinStage {
   }
 };
 
+// A barrier for what lies in LDS: loads and stores of global memory stay in
+// flight across it (__syncthreads waits for them: 4.8 of a tile's 17.5
+// thousand cycles).
+__device__ __forceinline__ void lin_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 template <typename T, int KI, int NT, int MODE>
 struct LinTiles {
   static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = LinTypes<T>::NS;
@@ -280,14 +301,14 @@ struct LinTiles {
   static constexpr int kEnd = kP + (MODE == kLinState ? 0 : NS * L * L);  // of uint16_t
 };
 
-template <typename T, int KI, int NT, int MODE>
+template <typename T, int KI, int NT, int MODE, bool VEC>
 __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk_kernel(LinArgs a,
                                                                                      LinRole r) {
   using Z = LinTiles<T, KI, NT, MODE>;
   constexpr int L = Z::L, NP = Z::NP, NS = Z::NS, WO = Z::WO, IT = L / 16, KS = KI / 32;
   constexpr bool OUT = MODE != kLinState, FLOW = MODE == kLinFlow;
   __shared__ __attribute__((aligned(16))) uint16_t lds[Z::kEnd];
-  __shared__ double Hs[L];
+  __shared__ __attribute__((aligned(16))) float2 Hs[L];  // in units of ln 2, hi + lo
   __shared__ __attribute__((aligned(16))) float cf[L], uf[L], pd[L];
   __shared__ float total_s, red[4][L];
   const int wave = threadIdx.x >> 6;
@@ -349,23 +370,36 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
   LinStage<T, KI> qs, ks;
   LinStage<T, WO> vs;
   float lg = 0.f;
-  auto fetch = [&](int c, int thread) __attribute__((always_inline)) {
-    // row x of the tile is step t0 + x, or t0 + L - 1 - x
-    const int t0 = (r.reverse ? chunks - 1 - c : c) * L, n = len - t0 < L ? len - t0 : L;
+  // Rows of the next tile, one tensor at a time, so that the requests do not
+  // queue up: row x of a tile is step t0 + x, or t0 + L - 1 - x.
+  const T* const Q = static_cast<const T*>(r.Q) + (int64_t)(h / r.dq) * r.Ni;
+  const T* const K = static_cast<const T*>(r.K) + (int64_t)(h / r.dk) * r.Ni;
+  const T* const V = static_cast<const T*>(r.V) + (int64_t)(h / r.dv) * r.No + o0;
+  auto start = [&](int c) { return (r.reverse ? chunks - 1 - c : c) * L; };
+  auto count = [&](int t0) { return len - t0 < L ? len - t0 : L; };
+  auto fetch_q = [&](int c, int thread) __attribute__((always_inline)) {
+    const int t0 = start(c), n = count(t0);
     const int64_t row = sp.first + begin + t0;
-    if constexpr (OUT)
-      qs.load(static_cast<const T*>(r.Q) + row * r.sq + (int64_t)(h / r.dq) * r.Ni, r.sq, n,
-              r.Ni, r.vec, thread);
-    ks.load(static_cast<const T*>(r.K) + row * r.sk + (int64_t)(h / r.dk) * r.Ni, r.sk, n, r.Ni,
-            r.vec, thread);
-    vs.load(static_cast<const T*>(r.V) + row * r.sv + (int64_t)(h / r.dv) * r.No + o0, r.sv, n,
-            no < WO ? no : WO, r.vec, thread);
-    if (threadIdx.x < L) {
-      const int t = r.reverse ? L - 1 - (int)threadIdx.x : (int)threadIdx.x;
+    if constexpr (OUT) qs.template load<VEC>(Q + row * r.sq, r.sq, n, r.Ni, thread);
+    if (thread < L) {
+      const int t = r.reverse ? L - 1 - thread : thread;
       lg = t < n ? lin_log_decay(a, row + t, h) : 0.f;
     }
   };
-  if (chunks > 0) fetch(0, threadIdx.x);
+  auto fetch_k = [&](int c, int thread) __attribute__((always_inline)) {
+    const int t0 = start(c);
+    ks.template load<VEC>(K + (sp.first + begin + t0) * r.sk, r.sk, count(t0), r.Ni, thread);
+  };
+  auto fetch_v = [&](int c, int thread) __attribute__((always_inline)) {
+    const int t0 = start(c);
+    vs.template load<VEC>(V + (sp.first + begin + t0) * r.sv, r.sv, count(t0), no < WO ? no : WO,
+                          thread);
+  };
+  if (chunks > 0) {
+    fetch_q(0, threadIdx.x);
+    fetch_k(0, threadIdx.x);
+    fetch_v(0, threadIdx.x);
+  }
   if constexpr (OUT) {  // tiles above the diagonal stay zero
     for (int i = threadIdx.x; i < NS * L * L / 8; i += 256)
       reinterpret_cast<uint4*>(lds + Z::kP)[i] = uint4{0, 0, 0, 0};
@@ -378,7 +412,7 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
     int thread = threadIdx.x;
     asm volatile("" : "+v"(thread));
     const int lane = thread & 63, q = lane >> 4, lr = lane & 15;
-    __syncthreads();  // the last tile has been read
+    lin_barrier();  // the last tile has been read
     if constexpr (OUT) qs.store(Qt, r.reverse, thread);
     ks.store(Kt, r.reverse, thread);
     vs.store(Vt, r.reverse, thread);
@@ -390,50 +424,43 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
       all += end;
       if (threadIdx.x < L) {
         const double H = r.reverse ? sum - x : sum;
-        Hs[threadIdx.x] = H;
+        const double H2 = H * 1.4426950408889634;
+        const float hi = (float)H2;
+        Hs[threadIdx.x] = float2{hi, (float)(H2 - (double)hi)};
         cf[threadIdx.x] = r.cs * lin_exp(H);
         uf[threadIdx.x] = r.us * lin_exp(end - H);
         if (threadIdx.x == 0) total_s = lin_exp(end);
       }
     }
-    if (c + 1 < chunks) fetch(c + 1, thread);
-    __syncthreads();
-    const int t0 = (r.reverse ? chunks - 1 - c : c) * L;
+    lin_barrier();
+    const int t0 = start(c);
+    const bool more = c + 1 < chunks;
+    if (more) fetch_q(c + 1, thread);
 
     f4 acc[IT][NT];
     if constexpr (OUT) {
-      // P: IT (IT + 1) / 2 tiles of 16 x 16 on and below the diagonal
+      // P: tiles of 16 x 16 on and below the diagonal (past the last: that one
+      // again, so that no branch stands here), their products first and
+      // their decays behind S Q, which leaves the matrix cores time for them
+      constexpr int PT = IT * (IT + 1) / 2, PW = (PT + 3) / 4;
+      f4 p[PW];
 #pragma unroll
-      for (int k = 0; k < (IT * (IT + 1) / 2 + 3) / 4; ++k) {
-        const int t = 4 * k + wave;
-        if (t < IT * (IT + 1) / 2) {
-          const int it = (t >= 1) + (t >= 3) + (t >= 6), jt = t - it * (it + 1) / 2;
-          f4 p = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < PW; ++k) {
+        const int t = 4 * k + wave < PT ? 4 * k + wave : PT - 1;
+        const int it = (t >= 1) + (t >= 3) + (t >= 6), jt = t - it * (it + 1) / 2;
+        p[k] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            uint4 ka[NP], qb[NP];
+        for (int s = 0; s < KS; ++s) {
+          uint4 ka[NP], qb[NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              ka[i] = lin_rows<KI>(Kt[i], 16 * jt, 32 * s, lane);
-              qb[i] = lin_rows<KI>(Qt[i], 16 * it, 32 * s, lane);
-            }
-            p = lin_mfma(ka, qb, p);
+          for (int i = 0; i < NP; ++i) {
+            ka[i] = lin_rows<KI>(Kt[i], 16 * jt, 32 * s, lane);
+            qb[i] = lin_rows<KI>(Qt[i], 16 * it, 32 * s, lane);
           }
-          const int i = 16 * it + lr, j = 16 * jt + 4 * q;
-          const double Hi = Hs[i];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            if (FLOW && i == j + v) pd[i] = r.ps * p[v];
-            const bool in = FLOW ? j + v < i : j + v <= i;
-            p[v] = in ? p[v] * (r.ps * lin_exp(Hi - Hs[j + v])) : 0.f;
-          }
-          uint4 pieces[NS];
-          lin_split<NS>(p, f4{0.f, 0.f, 0.f, 0.f}, pieces);
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-            *reinterpret_cast<uint2*>(Pt[n] + lin_at<L>(i, j)) = uint2{pieces[n].x, pieces[n].y};
+          p[k] = lin_mfma(ka, qb, p[k]);
         }
       }
+      if (more) fetch_k(c + 1, thread);
       // out <- S Q, scaled by cf
 #pragma unroll
       for (int it = 0; it < IT; ++it)
@@ -454,13 +481,38 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
         }
       }
 #pragma unroll
+      for (int k = 0; k < PW; ++k) {
+        const int t = 4 * k + wave < PT ? 4 * k + wave : PT - 1;
+        const int it = (t >= 1) + (t >= 3) + (t >= 6), jt = t - it * (it + 1) / 2;
+        const int i = 16 * it + lr, j = 16 * jt + 4 * q;
+        const float2 Hi = Hs[i];
+        const float4 H01 = *reinterpret_cast<const float4*>(Hs + j);
+        const float4 H23 = *reinterpret_cast<const float4*>(Hs + j + 2);
+        const float hi[4] = {H01.x, H01.z, H23.x, H23.z}, lo[4] = {H01.y, H01.w, H23.y, H23.w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float x = r.ps * p[k][v];
+          if (FLOW && i == j + v) pd[i] = x;
+          const bool in = FLOW ? j + v < i : j + v <= i;
+          p[k][v] = in ? x * exp2_hw((Hi.x - hi[v]) + (Hi.y - lo[v])) : 0.f;
+        }
+        uint4 pieces[NS];
+        lin_split<NS>(p[k], f4{0.f, 0.f, 0.f, 0.f}, pieces);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+          *reinterpret_cast<uint2*>(Pt[n] + lin_at<L>(i, j)) = uint2{pieces[n].x, pieces[n].y};
+      }
+#pragma unroll
       for (int it = 0; it < IT; ++it) {
         const float x = cf[16 * it + lr];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= x;
       }
-      __syncthreads();  // P is whole
+      lin_barrier();  // P is whole
+    } else {
+      if (more) fetch_k(c + 1, thread);
     }
+    if (more) fetch_v(c + 1, thread);
     {
       const float x = total_s;
 #pragma unroll
@@ -508,37 +560,48 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
       }
     }
     if constexpr (OUT) {
-      const int n = len - t0 < L ? len - t0 : L;
+      const int n = count(t0), wide = a.Hv * r.No;
+      const int64_t row = sp.first + begin + t0;
+      // rows past the sequence's end are past the buffers'
+      const int es = r.out != nullptr ? (int)sizeof(T) : 4;
+      const Buffer out = buffer_of(r.out != nullptr ? r.out : r.part,
+                                   (row * wide + (int64_t)h * r.No) * es,
+                                   ((int64_t)(n - 1) * wide + r.No) * es);
+      Buffer R{nullptr, 0};
+      if constexpr (FLOW)
+        R = buffer_of(r.R, (row * r.sr + (int64_t)(h / r.dr) * r.No) * sizeof(T),
+                      ((int64_t)(n - 1) * r.sr + r.No) * sizeof(T));
+      const int lane_row = r.reverse ? 15 - lr : lr, o = wo + 4 * q;
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int x = 16 * it + lr, t = r.reverse ? L - 1 - x : x;
-        const bool live = t < n;
-        const int64_t row = sp.first + begin + t0 + t;
+        const int x = 16 * it + lr, t = r.reverse ? L - 16 - 16 * it : 16 * it;
         float flow = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int o = wo + 16 * nt + 4 * q, left = live ? r.No - o : 0;
+          const int left = r.No - o - 16 * nt;
           if constexpr (FLOW) {
-            const f4 w = lin_quad(static_cast<const T*>(r.R) + row * r.sr +
-                                      (int64_t)(h / r.dr) * r.No + o,
-                                  left, r.vec);
+            const f4 w = lin_quad<VEC, T>(
+                R, (uint32_t)(lane_row * (uint32_t)r.sr + o) * sizeof(T),
+                (uint32_t)(t * (uint32_t)r.sr + 16 * nt) * sizeof(T), left);
 #pragma unroll
             for (int v = 0; v < 4; ++v) flow = fmaf(w[v], acc[it][nt][v], flow);
             // the step's own term
             f4 own = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = NP - 1; i >= 0; --i) {
-              const uint2 y = *reinterpret_cast<const uint2*>(Vt[i] + lin_at<WO>(x, o - o0));
+              const uint2 y = *reinterpret_cast<const uint2*>(
+                  Vt[i] + lin_at<WO>(x, o - o0 + 16 * nt));
               own += f4{__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
                         __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u)};
             }
             acc[it][nt] += own * pd[x];
           }
-          const int64_t at = (row * a.Hv + h) * r.No + o;
           if (r.out != nullptr)
-            lin_put(static_cast<T*>(r.out) + at, acc[it][nt], left, r.vec);
+            lin_put<VEC, T>(out, (uint32_t)(lane_row * wide + o) * sizeof(T),
+                            (uint32_t)(t * wide + 16 * nt) * sizeof(T), acc[it][nt], left);
           else
-            lin_put(r.part + at, acc[it][nt], left, r.vec);
+            lin_put<VEC, float>(out, (uint32_t)(lane_row * wide + o) * 4,
+                                (uint32_t)(t * wide + 16 * nt) * 4, acc[it][nt], left);
         }
         if constexpr (FLOW) {
           flow = swap16_sum(flow, flow);
@@ -547,10 +610,10 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
         }
       }
       if constexpr (FLOW) {
-        __syncthreads();
-        const int x = threadIdx.x, t = r.reverse ? L - 1 - x : x;
+        lin_barrier();
+        const int x = thread, t = r.reverse ? L - 1 - x : x;
         if (x < L && t < n)
-          r.flow[((int64_t)tile * a.rows + sp.first + begin + t0 + t) * a.Hv + h] =
+          r.flow[((int64_t)tile * a.rows + row + t) * a.Hv + h] =
               (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
       }
     }
@@ -564,7 +627,7 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
 }
 
 // The instances: widths of 64 to 256 contracted, 64 or 128 columns of output.
-template <typename T>
+template <typename T, bool VEC>
 hipError_t lin_chunk(const LinArgs& a, LinRole r, int mode, hipStream_t s);
 
 }  // namespace gdr

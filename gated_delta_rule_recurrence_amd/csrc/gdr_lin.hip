@@ -265,6 +265,11 @@ bool whole_vectors(const LinArgs& a, bool bf16) {
 }
 
 template <typename T>
+hipError_t chunked(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {
+  return r.vec ? lin_chunk<T, true>(a, r, mode, s) : lin_chunk<T, false>(a, r, mode, s);
+}
+
+template <typename T>
 hipError_t fwd(const LinArgs& a, hipStream_t s) {
   if (a.T <= kFewSteps) {
     hipLaunchKernelGGL(lin_step_kernel<T>, dim3((a.Dv + kStepRows - 1) / kStepRows, a.Hv, a.B),
@@ -292,15 +297,15 @@ hipError_t fwd(const LinArgs& a, hipStream_t s) {
     r.first = a.S0;
     r.last = a.S_T;
     r.save = a.ckpt;
-    return lin_chunk<T>(a, r, kLinOut, s);
+    return chunked<T>(a, r, kLinOut, s);
   }
   r.local = a.states;
   r.decay = a.decay;
-  hipError_t e = lin_chunk<T>(a, r, kLinState, s);
+  hipError_t e = chunked<T>(a, r, kLinState, s);
   if (e == hipSuccess) e = join(a, 0, s);
   r.first = a.states;
   r.slots = 1;
-  return e == hipSuccess ? lin_chunk<T>(a, r, kLinOut, s) : e;
+  return e == hipSuccess ? chunked<T>(a, r, kLinOut, s) : e;
 }
 
 template <typename T>
@@ -359,7 +364,7 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
     v.first = nullptr;
     v.local = a.states;
     v.decay = a.decay;
-    e = lin_chunk<T>(a, v, kLinState, s);
+    e = chunked<T>(a, v, kLinState, s);
     if (e == hipSuccess) e = join(a, 1, s);
     v.first = a.states;
   } else {
@@ -367,7 +372,7 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
     v.slots = 0;
     v.last = a.dS0;
   }
-  if (e == hipSuccess) e = lin_chunk<T>(a, r, mode, s);
+  if (e == hipSuccess) e = chunked<T>(a, r, mode, s);
   // dk: (v, dy, q)
   d.Q = a.v;
   d.K = a.dy;
@@ -385,8 +390,8 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
   d.out = reps > 1 ? nullptr : a.dk;
   d.part = a.dk_part;
   d.flow = a.flow + (int64_t)tiles * a.rows * a.Hv;
-  if (e == hipSuccess) e = lin_chunk<T>(a, d, mode, s);
-  if (e == hipSuccess) e = lin_chunk<T>(a, v, kLinOut, s);
+  if (e == hipSuccess) e = chunked<T>(a, d, mode, s);
+  if (e == hipSuccess) e = chunked<T>(a, v, kLinOut, s);
   if (e == hipSuccess && reps > 1) {
     const int64_t blocks = ((int64_t)a.T * a.Hk * a.Dk + kThreads - 1) / kThreads;
     hipLaunchKernelGGL(lin_heads_sum<T>,

@@ -5,30 +5,30 @@
 
 namespace gdr {
 
-template <typename T, int KI, int NT, int MODE>
+template <typename T, int KI, int NT, int MODE, bool VEC>
 hipError_t lin_launch(const LinArgs& a, const LinRole& r, hipStream_t s) {
-  hipLaunchKernelGGL((lin_chunk_kernel<T, KI, NT, MODE>),
+  hipLaunchKernelGGL((lin_chunk_kernel<T, KI, NT, MODE, VEC>),
                      dim3((unsigned)r.tiles * a.segs, a.Hv, a.B), dim3(256), 0, s, a, r);
   const hipError_t e = hipGetLastError();
   note_launch(s);
   return e;
 }
-template <typename T, int KI, int NT>
+template <typename T, int KI, int NT, bool VEC>
 hipError_t lin_mode(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {
-  if (mode == kLinOut) return lin_launch<T, KI, NT, kLinOut>(a, r, s);
-  if (mode == kLinFlow) return lin_launch<T, KI, NT, kLinFlow>(a, r, s);
-  return lin_launch<T, KI, NT, kLinState>(a, r, s);
+  if (mode == kLinOut) return lin_launch<T, KI, NT, kLinOut, VEC>(a, r, s);
+  if (mode == kLinFlow) return lin_launch<T, KI, NT, kLinFlow, VEC>(a, r, s);
+  return lin_launch<T, KI, NT, kLinState, VEC>(a, r, s);
 }
-template <typename T, int KI>
+template <typename T, int KI, bool VEC>
 hipError_t lin_width(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {
-  return r.No <= 64 ? lin_mode<T, KI, 1>(a, r, mode, s) : lin_mode<T, KI, 2>(a, r, mode, s);
+  return r.No <= 64 ? lin_mode<T, KI, 1, VEC>(a, r, mode, s) : lin_mode<T, KI, 2, VEC>(a, r, mode, s);
 }
-template <typename T>
+template <typename T, bool VEC>
 hipError_t lin_chunk(const LinArgs& a, LinRole r, int mode, hipStream_t s) {
-  if (r.Ni <= 64) return lin_width<T, 64>(a, r, mode, s);
-  if (r.Ni <= 128) return lin_width<T, 128>(a, r, mode, s);
-  if (r.Ni <= 192) return lin_width<T, 192>(a, r, mode, s);
-  return lin_width<T, 256>(a, r, mode, s);
+  if (r.Ni <= 64) return lin_width<T, 64, VEC>(a, r, mode, s);
+  if (r.Ni <= 128) return lin_width<T, 128, VEC>(a, r, mode, s);
+  if (r.Ni <= 192) return lin_width<T, 192, VEC>(a, r, mode, s);
+  return lin_width<T, 256, VEC>(a, r, mode, s);
 }
 
 }  // namespace gdr

@@ -384,7 +384,7 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
  * [rows][Hv], or [Hv]: one decay per head (per_head).  A log_g of -inf forgets
  * the state; positive ones are taken as they are.
  * 1 <= Dk, Dv <= GDR_LIN_MAX_DIM, Hv a multiple of Hk and at most 65535, B at
- * most 65535, T and rows at most 2^30 - 1, strides (and Hk Dk, Hv Dv) at most
+ * most 65535, T and rows at most 2^30 - 1, strides (and Hv Dk, Hv Dv) at most
  * 2^23.  A value that is not finite in a row
  * makes the outputs of its sequence that the formula reaches from it not
  * finite, and may do so to those of up to 63 earlier rows of that sequence
