@@ -156,7 +156,7 @@ struct LinArgs {
   float* dS0;            // or null
   float* dq_part;        // [rows][Hv][Dk], with Hk < Hv
   float* dk_part;
-  float* flow;           // [2][tiles][rows][Hv]
+  float* flow;           // [2][tiles][Hv][rows]
   double* head_sums;     // [B][segs][Hv], for a decay per head
 };
 // Steps of a segment, segments of the longest sequence, slots of all.
@@ -164,8 +164,10 @@ struct LinPlan {
   int64_t seg, segs, slots;
 };
 LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv);
-// Workgroups over an output's width.
-int lin_tiles(int64_t width);
+// Columns of a workgroup's output, of width No, for the contracted width Ni, and
+// the workgroups over it.
+int lin_width(int64_t Ni, int64_t No);
+int lin_tiles(int64_t Ni, int64_t No);
 hipError_t launch_lin_fwd(const LinArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_lin_bwd(const LinArgs& a, bool bf16, hipStream_t s);
 

@@ -499,7 +499,7 @@ int lin_sizes(const gdr_lin_shape& s, LinSizes* z) {
     z->dk = z->dq + round_up256(x);
     z->flow = z->dk + round_up256(x);
   }
-  if (!product_ok(rows, 2 * gdr::lin_tiles(s.Dk), &x)) return GDR_ERR_OVERFLOW;
+  if (!product_ok(rows, 2 * gdr::lin_tiles(s.Dv, s.Dk), &x)) return GDR_ERR_OVERFLOW;
   z->heads = z->flow + round_up256(x);
   z->bwd = z->heads;
   if (s.per_head) {

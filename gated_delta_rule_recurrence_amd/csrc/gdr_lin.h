@@ -58,7 +58,7 @@ struct LinRole {
   float* decay;        // states only: [slots][Hv] exp(total) of the segments
   void* out;           // [rows][Hv][No], or null
   float* part;         // the same in fp32
-  float* flow;         // [tiles][rows][Hv]: R out, without the step's own term
+  float* flow;         // [tiles][Hv][rows]: R out, without the step's own term
 };
 
 enum LinMode { kLinOut = 0, kLinFlow = 1, kLinState = 2 };
@@ -89,10 +89,12 @@ struct LinTypes<float> {
 
 // A tile [rows][W] of bf16 in LDS whose 16-byte blocks are exchanged inside a
 // row so that the rows of an operand fall on different banks, read by rows
-// (16 rows, one block each) and transposed (4 rows, 4 blocks).
+// (16 rows, one block each) and transposed (4 rows, 4 blocks), and so that two
+// rows written at once (8 blocks each) do.
 template <int W>
 __device__ __forceinline__ int lin_swz(int r) {
-  if constexpr (W % 128 == 0) return ((r & 3) << 2) | ((r >> 2) & 3);
+  if constexpr (W % 128 == 0)
+    return ((r & 1) << 3) | ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
   if constexpr (W == 32) return (r >> 2) & 3;
   return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
 }
@@ -114,6 +116,11 @@ __device__ __forceinline__ uint4 lin_columns(const uint16_t* t, int r0, int c0, 
   return uint4{lo.x, lo.y, hi.x, hi.y};
 }
 
+__device__ __forceinline__ f4 lin_unpack(uint2 w) {
+  return f4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+}
+
 // NS bf16 pieces of eight values, as operands.
 template <int NS>
 __device__ __forceinline__ void lin_split(f4 a, f4 b, uint4 (&p)[NS]) {
@@ -124,10 +131,11 @@ __device__ __forceinline__ void lin_split(f4 a, f4 b, uint4 (&p)[NS]) {
   } else {
     x[0] = uint2{cvt_pk_bf16(a[0], a[1]), cvt_pk_bf16(a[2], a[3])};
     y[0] = uint2{cvt_pk_bf16(b[0], b[1]), cvt_pk_bf16(b[2], b[3])};
-    x[1] = uint2{cvt_pk_bf16(minus_bf16_lo(x[0].x, a[0]), minus_bf16_hi(x[0].x, a[1])),
-                 cvt_pk_bf16(minus_bf16_lo(x[0].y, a[2]), minus_bf16_hi(x[0].y, a[3]))};
-    y[1] = uint2{cvt_pk_bf16(minus_bf16_lo(y[0].x, b[0]), minus_bf16_hi(y[0].x, b[1])),
-                 cvt_pk_bf16(minus_bf16_lo(y[0].y, b[2]), minus_bf16_hi(y[0].y, b[3]))};
+    // (v_dot2 would form x - hi at once, but needs a move for its sum or wait
+    // states behind it)
+    const f4 ra = a - lin_unpack(x[0]), rb = b - lin_unpack(y[0]);
+    x[1] = uint2{cvt_pk_bf16(ra[0], ra[1]), cvt_pk_bf16(ra[2], ra[3])};
+    y[1] = uint2{cvt_pk_bf16(rb[0], rb[1]), cvt_pk_bf16(rb[2], rb[3])};
   }
 #pragma unroll
   for (int i = 0; i < NS; ++i) p[i] = uint4{x[i].x, x[i].y, y[i].x, y[i].y};
@@ -290,19 +298,26 @@ __device__ __forceinline__ void lin_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Workgroups of a compute unit that the registers are cut to.
+constexpr int lin_waves(int KI, int NT, int mode) {
+  return KI <= 128 && NT == 1 ? 3 : KI * NT <= 256 || (mode == kLinState && KI * NT <= 384) ? 2 : 1;
+}
+
+// What lies in LDS, in elements of 16 bits.  P takes the place of Q, which has
+// been read by then.
 template <typename T, int KI, int NT, int MODE>
 struct LinTiles {
   static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = LinTypes<T>::NS;
   static constexpr int WO = 64 * NT;
-  static constexpr int kQ = 0;
-  static constexpr int kK = kQ + (MODE == kLinState ? 0 : NP * L * KI);
+  static constexpr int kQ = 0, kP = 0;
+  static constexpr int kQP = NP * L * KI > NS * L * L ? NP * L * KI : NS * L * L;
+  static constexpr int kK = MODE == kLinState ? 0 : kQP;
   static constexpr int kV = kK + NP * L * KI;
-  static constexpr int kP = kV + NP * L * WO;
-  static constexpr int kEnd = kP + (MODE == kLinState ? 0 : NS * L * L);  // of uint16_t
+  static constexpr int kEnd = kV + NP * L * WO;
 };
 
 template <typename T, int KI, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk_kernel(LinArgs a,
+__global__ __launch_bounds__(256, (lin_waves(KI, NT, MODE))) void lin_chunk_kernel(LinArgs a,
                                                                                      LinRole r) {
   using Z = LinTiles<T, KI, NT, MODE>;
   constexpr int L = Z::L, NP = Z::NP, NS = Z::NS, WO = Z::WO, IT = L / 16, KS = KI / 32;
@@ -400,10 +415,6 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
     fetch_k(0, threadIdx.x);
     fetch_v(0, threadIdx.x);
   }
-  if constexpr (OUT) {  // tiles above the diagonal stay zero
-    for (int i = threadIdx.x; i < NS * L * L / 8; i += 256)
-      reinterpret_cast<uint4*>(lds + Z::kP)[i] = uint4{0, 0, 0, 0};
-  }
   double all = 0.0;  // the segment's summed log decays (first L threads)
 
   for (int c = 0; c < chunks; ++c) {
@@ -439,23 +450,29 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
 
     f4 acc[IT][NT];
     if constexpr (OUT) {
-      // P: tiles of 16 x 16 on and below the diagonal (past the last: that one
-      // again, so that no branch stands here), their products first and
-      // their decays behind S Q, which leaves the matrix cores time for them
-      constexpr int PT = IT * (IT + 1) / 2, PW = (PT + 3) / 4;
+      // P: the tiles of 16 x 16 that its products below read (row it, columns
+      // up to 16 (it | 1) + 15), three a wave (one in tiles of 32), their
+      // products first and their decays behind S Q, which leaves the matrix
+      // cores time for them
+      constexpr int PW = IT == 4 ? 3 : 1;
       f4 p[PW];
+      int pi[PW], pj[PW];
 #pragma unroll
       for (int k = 0; k < PW; ++k) {
-        const int t = 4 * k + wave < PT ? 4 * k + wave : PT - 1;
-        const int it = (t >= 1) + (t >= 3) + (t >= 6), jt = t - it * (it + 1) / 2;
+        const int t = PW * wave + k;
+        pi[k] = IT == 4 ? (t >= 2) + (t >= 4) + (t >= 8) : t >> 1;
+        pj[k] = t < 4 ? t & 1 : t & 3;
         p[k] = f4{0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
+      for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int k = 0; k < PW; ++k) {
           uint4 ka[NP], qb[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            ka[i] = lin_rows<KI>(Kt[i], 16 * jt, 32 * s, lane);
-            qb[i] = lin_rows<KI>(Qt[i], 16 * it, 32 * s, lane);
+            ka[i] = lin_rows<KI>(Kt[i], 16 * pj[k], 32 * s, lane);
+            qb[i] = lin_rows<KI>(Qt[i], 16 * pi[k], 32 * s, lane);
           }
           p[k] = lin_mfma(ka, qb, p[k]);
         }
@@ -480,11 +497,10 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
           for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(sa[nt], qb, acc[it][nt]);
         }
       }
+      lin_barrier();  // Q has been read
 #pragma unroll
       for (int k = 0; k < PW; ++k) {
-        const int t = 4 * k + wave < PT ? 4 * k + wave : PT - 1;
-        const int it = (t >= 1) + (t >= 3) + (t >= 6), jt = t - it * (it + 1) / 2;
-        const int i = 16 * it + lr, j = 16 * jt + 4 * q;
+        const int i = 16 * pi[k] + lr, j = 16 * pj[k] + 4 * q;
         const float2 Hi = Hs[i];
         const float4 H01 = *reinterpret_cast<const float4*>(Hs + j);
         const float4 H23 = *reinterpret_cast<const float4*>(Hs + j + 2);
@@ -493,8 +509,10 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
         for (int v = 0; v < 4; ++v) {
           const float x = r.ps * p[k][v];
           if (FLOW && i == j + v) pd[i] = x;
-          const bool in = FLOW ? j + v < i : j + v <= i;
-          p[k][v] = in ? x * exp2_hw((Hi.x - hi[v]) + (Hi.y - lo[v])) : 0.f;
+          // (a mask, as a choice becomes a branch around the exponential)
+          const int below = i - (FLOW ? 1 : 0) - (j + v);
+          p[k][v] = __uint_as_float(
+              __float_as_uint(x * exp2_hw((Hi.x - hi[v]) + (Hi.y - lo[v]))) & ~(below >> 31));
         }
         uint4 pieces[NS];
         lin_split<NS>(p[k], f4{0.f, 0.f, 0.f, 0.f}, pieces);
@@ -527,15 +545,14 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
       const f4 u1 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q + 4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        f4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+        f4 x, y;
 #pragma unroll
         for (int i = NP - 1; i >= 0; --i) {
-          vo[nt][i] = lin_columns<WO, false>(Vt[i], 32 * k, 16 * (NT * wave + nt), lane);
-          const uint4 w = vo[nt][i];
-          x += f4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                  __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
-          y += f4{__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
-                  __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u)};
+          const uint4 w = vo[nt][i] =
+              lin_columns<WO, false>(Vt[i], 32 * k, 16 * (NT * wave + nt), lane);
+          const f4 wx = lin_unpack(uint2{w.x, w.y}), wy = lin_unpack(uint2{w.z, w.w});
+          x = i == NP - 1 ? wx : x + wx;
+          y = i == NP - 1 ? wy : y + wy;
         }
         lin_split<NS>(x * u0, y * u1, vu[nt]);
       }
@@ -586,22 +603,15 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
 #pragma unroll
             for (int v = 0; v < 4; ++v) flow = fmaf(w[v], acc[it][nt][v], flow);
             // the step's own term
-            f4 own = {0.f, 0.f, 0.f, 0.f};
+            f4 own;
 #pragma unroll
             for (int i = NP - 1; i >= 0; --i) {
-              const uint2 y = *reinterpret_cast<const uint2*>(
-                  Vt[i] + lin_at<WO>(x, o - o0 + 16 * nt));
-              own += f4{__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u),
-                        __uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u)};
+              const f4 y = lin_unpack(*reinterpret_cast<const uint2*>(
+                  Vt[i] + lin_at<WO>(x, o - o0 + 16 * nt)));
+              own = i == NP - 1 ? y : own + y;
             }
             acc[it][nt] += own * pd[x];
           }
-          if (r.out != nullptr)
-            lin_put<VEC, T>(out, (uint32_t)(lane_row * wide + o) * sizeof(T),
-                            (uint32_t)(t * wide + 16 * nt) * sizeof(T), acc[it][nt], left);
-          else
-            lin_put<VEC, float>(out, (uint32_t)(lane_row * wide + o) * 4,
-                                (uint32_t)(t * wide + 16 * nt) * 4, acc[it][nt], left);
         }
         if constexpr (FLOW) {
           flow = swap16_sum(flow, flow);
@@ -609,11 +619,27 @@ __global__ __launch_bounds__(256, (KI <= 128 && NT <= 2 ? 2 : 1)) void lin_chunk
           if (q == 0) red[wave][x] = flow;
         }
       }
+      auto put = [&](auto type) __attribute__((always_inline)) {
+        using O = decltype(type);
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int t = r.reverse ? L - 16 - 16 * it : 16 * it;
+            lin_put<VEC, O>(out, (uint32_t)(lane_row * wide + o) * sizeof(O),
+                            (uint32_t)(t * wide + 16 * nt) * sizeof(O), acc[it][nt],
+                            r.No - o - 16 * nt);
+          }
+      };
+      if (r.out != nullptr)
+        put(T{});
+      else
+        put(float{});
       if constexpr (FLOW) {
         lin_barrier();
         const int x = thread, t = r.reverse ? L - 1 - x : x;
         if (x < L && t < n)
-          r.flow[((int64_t)tile * a.rows + row + t) * a.Hv + h] =
+          r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] =
               (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
       }
     }

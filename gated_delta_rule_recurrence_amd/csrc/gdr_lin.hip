@@ -138,23 +138,43 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int rever
   if (last != nullptr) store_pack(last + whole, S);
 }
 
-// Sums of the fp32 parts over a key head's value heads.
-template <typename T>
+// Sums of the fp32 parts over a key head's value heads, V columns a thread.
+template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void lin_heads_sum(LinArgs a) {
   const int reps = a.Hv / a.Hk, b = blockIdx.y;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
-  const int64_t n = (int64_t)sp.len * a.Hk * a.Dk, start = sp.first * a.Hk * a.Dk;
+  const uint32_t units = a.Hk * a.Dk / V;  // of a row
+  const int64_t n = (int64_t)sp.len * units;
   const float* const part = blockIdx.z == 0 ? a.dq_part : a.dk_part;
   T* const out = static_cast<T*>(blockIdx.z == 0 ? a.dq : a.dk);
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * kThreads) {
-    const int64_t at = start + i;
-    const int d = at % a.Dk;
-    const int64_t rh = at / a.Dk;  // row and key head
-    const float* const p = part + (rh / a.Hk * a.Hv + rh % a.Hk * reps) * a.Dk + d;
-    float s = 0.f;
-    for (int j = 0; j < reps; ++j) s += p[(int64_t)j * a.Dk];
-    st(out, at, s);
+    const int64_t row = sp.first + i / units;
+    const int c = (int)(i % units) * V, kh = c / a.Dk, d = c - kh * a.Dk;
+    const float* const p = part + (row * a.Hv + kh * reps) * a.Dk + d;
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = 0.f;
+    int j = 0;
+    for (; j + 4 <= reps; j += 4) {
+      Pack<float, V> x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = load_pack<float, V>(p + (int64_t)(j + u) * a.Dk);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float f[V];
+        unpack(x[u], f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] += f[v];
+      }
+    }
+    for (; j < reps; ++j) {
+      float f[V];
+      unpack(load_pack<float, V>(p + (int64_t)j * a.Dk), f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[v] += f[v];
+    }
+    store_pack(out + row * a.Hk * a.Dk + c, s);
   }
 }
 
@@ -192,15 +212,15 @@ __global__ __launch_bounds__(kThreads) void lin_flow_kernel(LinArgs a, int tiles
     for (int64_t i = threadIdx.x; i < n; i += kThreads) carry += (double)D[i] * (double)S[i];
     carry = block_sum(carry, red);
   }
-  const float* const fa = a.flow;
-  const float* const fb = a.flow + (int64_t)tiles * a.rows * a.Hv;
+  const float* const fa = a.flow + h * a.rows;
+  const float* const fb = fa + (int64_t)tiles * a.rows * a.Hv;
   for (int t0 = (len - 1) & ~(kThreads - 1); t0 >= 0; t0 -= kThreads) {
     const int t = t0 + threadIdx.x;
     const int64_t row = sp.first + begin + t;
     double x = 0.0;
     if (t < len)
       for (int i = 0; i < tiles; ++i) {
-        const int64_t at = ((int64_t)i * a.rows + row) * a.Hv + h;
+        const int64_t at = (int64_t)i * a.rows * a.Hv + row;
         x += (double)fa[at] - (double)fb[at];
       }
 #pragma unroll
@@ -288,7 +308,7 @@ hipError_t fwd(const LinArgs& a, hipStream_t s) {
   r.dv = 1;
   r.Ni = a.Dk;
   r.No = a.Dv;
-  r.tiles = lin_tiles(r.No);
+  r.tiles = lin_tiles(r.Ni, r.No);
   r.ps = r.cs = a.scale;
   r.us = 1.f;
   r.vec = whole_vectors(a, sizeof(T) == 2);
@@ -312,7 +332,7 @@ template <typename T>
 hipError_t bwd(const LinArgs& a, hipStream_t s) {
   const int reps = a.Hv / a.Hk;
   const int64_t wide = (int64_t)a.Hv * a.Dv;
-  const int tiles = lin_tiles(a.Dk);
+  const int tiles = lin_tiles(a.Dv, a.Dk);
   const int mode = a.dlog_g != nullptr ? kLinFlow : kLinOut;
   hipError_t e = hipSuccess;
   LinRole r{};
@@ -353,7 +373,7 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
   v.dv = 1;
   v.Ni = a.Dk;
   v.No = a.Dv;
-  v.tiles = lin_tiles(a.Dv);
+  v.tiles = lin_tiles(a.Dk, a.Dv);
   v.ps = v.us = a.scale;
   v.cs = 1.f;
   v.reverse = 1;
@@ -393,10 +413,13 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
   if (e == hipSuccess) e = chunked<T>(a, d, mode, s);
   if (e == hipSuccess) e = chunked<T>(a, v, kLinOut, s);
   if (e == hipSuccess && reps > 1) {
-    const int64_t blocks = ((int64_t)a.T * a.Hk * a.Dk + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(lin_heads_sum<T>,
-                       dim3((unsigned)(blocks < 1 ? 1 : blocks > 1024 ? 1024 : blocks), a.B, 2),
-                       dim3(kThreads), 0, s, a);
+    const int V = a.Dk % 4 == 0 ? 4 : 1;
+    const int64_t blocks = ((int64_t)a.T * a.Hk * a.Dk / V + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)(blocks < 1 ? 1 : blocks > 2048 ? 2048 : blocks), a.B, 2);
+    if (V == 4)
+      hipLaunchKernelGGL((lin_heads_sum<T, 4>), grid, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((lin_heads_sum<T, 1>), grid, dim3(kThreads), 0, s, a);
     e = noted(s);
   }
   if (e == hipSuccess && mode == kLinFlow) {
@@ -413,12 +436,24 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int lin_tiles(int64_t width) { return (int)((width + 127) / 128); }
+// 128 columns a workgroup, which form P once for them, where the state leaves
+// registers for two workgroups a compute unit (up to 128 contracted columns);
+// 64 where it does not, and where 128 would leave a quarter of them empty.
+// Training of 2048 steps, heads 16/64 of 192/128: 514 us; 128 columns for all
+// widths 646, 64 only where 192 are contracted 520.  4 x 4096 steps of 32 heads
+// of 128/128: 757 us, with 64 columns 903.
+int lin_width(int64_t Ni, int64_t No) {
+  return No <= 64 || Ni > 128 || (No > 128 && No <= 192) ? 64 : 128;
+}
+int lin_tiles(int64_t Ni, int64_t No) {
+  const int w = lin_width(Ni, No);
+  return (int)((No + w - 1) / w);
+}
 
 // Segments for 512 workgroups, two a compute unit, of 128 steps at least.
 LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv) {
   LinPlan p{};
-  const int64_t per = Hv * lin_tiles(Dv);  // workgroups of one cut through all rows
+  const int64_t per = Hv * lin_tiles(Dk, Dv);  // workgroups of one cut through all rows
   const int64_t want = (512 + per - 1) / per;
   int64_t seg = (rows + want - 1) / want;
   seg = (seg + 63) / 64 * 64;

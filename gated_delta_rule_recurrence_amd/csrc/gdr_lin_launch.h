@@ -20,15 +20,15 @@ hipError_t lin_mode(const LinArgs& a, const LinRole& r, int mode, hipStream_t s)
   return lin_launch<T, KI, NT, kLinState, VEC>(a, r, s);
 }
 template <typename T, int KI, bool VEC>
-hipError_t lin_width(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {
-  return r.No <= 64 ? lin_mode<T, KI, 1, VEC>(a, r, mode, s) : lin_mode<T, KI, 2, VEC>(a, r, mode, s);
+hipError_t lin_wide(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {
+  return lin_width(r.Ni, r.No) == 64 ? lin_mode<T, KI, 1, VEC>(a, r, mode, s) : lin_mode<T, KI, 2, VEC>(a, r, mode, s);
 }
 template <typename T, bool VEC>
 hipError_t lin_chunk(const LinArgs& a, LinRole r, int mode, hipStream_t s) {
-  if (r.Ni <= 64) return lin_width<T, 64, VEC>(a, r, mode, s);
-  if (r.Ni <= 128) return lin_width<T, 128, VEC>(a, r, mode, s);
-  if (r.Ni <= 192) return lin_width<T, 192, VEC>(a, r, mode, s);
-  return lin_width<T, 256, VEC>(a, r, mode, s);
+  if (r.Ni <= 64) return lin_wide<T, 64, VEC>(a, r, mode, s);
+  if (r.Ni <= 128) return lin_wide<T, 128, VEC>(a, r, mode, s);
+  if (r.Ni <= 192) return lin_wide<T, 192, VEC>(a, r, mode, s);
+  return lin_wide<T, 256, VEC>(a, r, mode, s);
 }
 
 }  // namespace gdr
