@@ -255,10 +255,12 @@ __device__ __forceinline__ double lin_prefix_sum(double x) {
 __device__ __forceinline__ float lin_exp(double x) { return exp2_hw(kLog2e * (float)x); }
 
 // A tile [L][W] on its way through a thread's registers: 8 threads a row,
-// eight elements in each 64 columns, 32 rows at a time.
-template <typename T, int W>
+// eight elements in each 64 columns, 8 NW rows at a time.
+template <typename T, int W, int NW>
 struct LinStage {
-  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NR = L / 32, NC = W / 64;
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, R = 8 * NW;
+  static constexpr int NR = L / R, NC = W / 64;
+  static_assert(NR * R == L, "whole passes of the threads");
   LinRaw<T> raw[NR][NC];
   // `rows` rows of n columns, `stride` apart, from p on; zeros outside
   template <bool VEC>
@@ -270,7 +272,7 @@ struct LinStage {
     for (int i = 0; i < NR; ++i)
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        const uint32_t to = at + (32 * i * (uint32_t)stride + 64 * k) * sizeof(T);
+        const uint32_t to = at + (R * i * (uint32_t)stride + 64 * k) * sizeof(T);
         if constexpr (VEC)
           raw[i][k].load(buf, c + 64 * k < n ? to : kLinPast);
         else
@@ -284,7 +286,7 @@ struct LinStage {
     for (int i = 0; i < NR; ++i)
 #pragma unroll
       for (int k = 0; k < NC; ++k)
-        raw[i][k].put(t, lin_at<W>(reverse ? x - 32 * i : x + 32 * i,
+        raw[i][k].put(t, lin_at<W>(reverse ? x - R * i : x + R * i,
                                    (thread & 7) * 8 + 64 * k));
   }
 };
@@ -298,17 +300,25 @@ __device__ __forceinline__ void lin_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Workgroups of a compute unit that the registers are cut to.
-constexpr int lin_waves(int KI, int NT, int mode) {
+// Waves of a SIMD that the registers are cut to.
+constexpr int lin_waves(int KI, int NT, int NW, int mode) {
+  if (NW == 8) return KI <= 192 ? 4 : 2;
   return KI <= 128 && NT == 1 ? 3 : KI * NT <= 256 || (mode == kLinState && KI * NT <= 384) ? 2 : 1;
+}
+// Sum of the waves' values of row x.
+template <int NW, int L>
+__device__ __forceinline__ float lin_sum(const float (&red)[NW][L], int x) {
+  float s = red[0][x];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) s += red[w][x];
+  return s;
 }
 
 // What lies in LDS, in elements of 16 bits.  P takes the place of Q, which has
 // been read by then.
-template <typename T, int KI, int NT, int MODE>
+template <typename T, int KI, int WO, int MODE>
 struct LinTiles {
   static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = LinTypes<T>::NS;
-  static constexpr int WO = 64 * NT;
   static constexpr int kQ = 0, kP = 0;
   static constexpr int kQP = NP * L * KI > NS * L * L ? NP * L * KI : NS * L * L;
   static constexpr int kK = MODE == kLinState ? 0 : kQP;
@@ -316,18 +326,42 @@ struct LinTiles {
   static constexpr int kEnd = kV + NP * L * WO;
 };
 
-template <typename T, int KI, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(256, (lin_waves(KI, NT, MODE))) void lin_chunk_kernel(LinArgs a,
-                                                                                     LinRole r) {
-  using Z = LinTiles<T, KI, NT, MODE>;
-  constexpr int L = Z::L, NP = Z::NP, NS = Z::NS, WO = Z::WO, IT = L / 16, KS = KI / 32;
+// Which workgroup this is: `each` of them (roles, tiles) to a head and segment.
+// Neighbouring ones lie on different XCDs, each with an L2 of its own: they
+// are renumbered so that an XCD takes runs of them, the roles and tiles of up to
+// eight heads of one key head, and what those read twice comes from its L2.
+// (Longer runs leave XCDs idle where sequences differ in length: seven prompts
+// in 6000 rows 274 us with one run an XCD, 176 without any.)
+struct LinBlock {
+  uint32_t each, sg, h, b;
+};
+__device__ __forceinline__ LinBlock lin_block(const LinArgs& a, uint32_t each) {
+  const uint64_t all = (uint64_t)gridDim.x * gridDim.y * gridDim.z;
+  uint32_t id = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  if (all >= (uint64_t)1 << 32)
+    return LinBlock{blockIdx.x % each, blockIdx.x / each, blockIdx.y, blockIdx.z};
+  const uint32_t reps = a.Hv / a.Hk, run = each * (reps < 8 ? reps : 8);
+  const uint32_t block = id / (8 * run) * (8 * run);
+  if (block + 8 * run <= (uint32_t)all) {
+    const uint32_t in = id - block;
+    id = block + in % 8 * run + in / 8;
+  }
+  const uint32_t rest = id / each, h = rest % a.Hv, at = rest / a.Hv;
+  return LinBlock{id - rest * each, at % a.segs, h, at / a.segs};
+}
+
+template <typename T, int KI, int NT, int NW, int MODE, bool VEC>
+__device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r, LinBlock at,
+                                              uint16_t* lds) {
+  constexpr int WO = 16 * NT * NW;
+  using Z = LinTiles<T, KI, WO, MODE>;
+  constexpr int L = Z::L, NP = Z::NP, NS = Z::NS, IT = L / 16, KS = KI / 32;
   constexpr bool OUT = MODE != kLinState, FLOW = MODE == kLinFlow;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[Z::kEnd];
   __shared__ __attribute__((aligned(16))) float2 Hs[L];  // in units of ln 2, hi + lo
   __shared__ __attribute__((aligned(16))) float cf[L], uf[L], pd[L];
-  __shared__ float total_s, red[4][L];
+  __shared__ float total_s, red[NW][L];
   const int wave = threadIdx.x >> 6;
-  const int tile = blockIdx.x % r.tiles, sg = blockIdx.x / r.tiles, h = blockIdx.y, b = blockIdx.z;
+  const int tile = at.each, sg = at.sg, h = at.h, b = at.b;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
   const int begin = sg * a.seg;
   if (sg > 0 && begin >= sp.len) return;
@@ -382,8 +416,8 @@ __global__ __launch_bounds__(256, (lin_waves(KI, NT, MODE))) void lin_chunk_kern
   };
   if (r.save != nullptr) put_state(r.save + (slot * a.Hv + h) * size);
 
-  LinStage<T, KI> qs, ks;
-  LinStage<T, WO> vs;
+  LinStage<T, KI, NW> qs, ks;
+  LinStage<T, WO, NW> vs;
   float lg = 0.f;
   // Rows of the next tile, one tensor at a time, so that the requests do not
   // queue up: row x of a tile is step t0 + x, or t0 + L - 1 - x.
@@ -451,15 +485,15 @@ __global__ __launch_bounds__(256, (lin_waves(KI, NT, MODE))) void lin_chunk_kern
     f4 acc[IT][NT];
     if constexpr (OUT) {
       // P: the tiles of 16 x 16 that its products below read (row it, columns
-      // up to 16 (it | 1) + 15), three a wave (one in tiles of 32), their
-      // products first and their decays behind S Q, which leaves the matrix
+      // up to 16 (it | 1) + 15) dealt to the waves, their products first and their decays behind S Q, which leaves the matrix
       // cores time for them
-      constexpr int PW = IT == 4 ? 3 : 1;
+      constexpr int PT = IT == 4 ? 12 : 4, PW = (PT + NW - 1) / NW;
       f4 p[PW];
       int pi[PW], pj[PW];
 #pragma unroll
       for (int k = 0; k < PW; ++k) {
-        const int t = PW * wave + k;
+        // (past the last: that one again)
+        const int t = PW * wave + k < PT ? PW * wave + k : PT - 1;
         pi[k] = IT == 4 ? (t >= 2) + (t >= 4) + (t >= 8) : t >> 1;
         pj[k] = t < 4 ? t & 1 : t & 3;
         p[k] = f4{0.f, 0.f, 0.f, 0.f};
@@ -640,7 +674,7 @@ __global__ __launch_bounds__(256, (lin_waves(KI, NT, MODE))) void lin_chunk_kern
         const int x = thread, t = r.reverse ? L - 1 - x : x;
         if (x < L && t < n)
           r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] =
-              (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
+              lin_sum<NW, L>(red, x);
       }
     }
   }
@@ -652,8 +686,37 @@ __global__ __launch_bounds__(256, (lin_waves(KI, NT, MODE))) void lin_chunk_kern
   if (r.save != nullptr) put_state(r.save + ((slot + 1) * a.Hv + h) * size);
 }
 
+template <typename T, int KI, int NT, int NW, int MODE, bool VEC>
+__global__ __launch_bounds__(64 * NW, (lin_waves(KI, NT, NW, MODE))) void lin_chunk_kernel(
+    LinArgs a, LinRole r) {
+  __shared__ __attribute__((aligned(16))) uint16_t
+      lds[LinTiles<T, KI, 16 * NT * NW, MODE>::kEnd];
+  lin_chunk_run<T, KI, NT, NW, MODE, VEC>(a, r, lin_block(a, r.tiles), lds);
+}
+
+// dq, dk and dv in one launch, where their widths take the same instance.
+struct LinRoles {
+  LinRole r[3];
+};
+template <typename T, int KI, int NT, int NW, int MODE, bool VEC>
+__global__ __launch_bounds__(64 * NW, (lin_waves(KI, NT, NW, MODE))) void lin_chunks_kernel(
+    LinArgs a, LinRoles roles) {
+  __shared__ __attribute__((aligned(16))) uint16_t
+      lds[LinTiles<T, KI, 16 * NT * NW, MODE>::kEnd];
+  LinBlock at = lin_block(a, 3 * roles.r[0].tiles);
+  const uint32_t role = at.each % 3;
+  at.each /= 3;
+  if (MODE == kLinFlow && role == 2)
+    lin_chunk_run<T, KI, NT, NW, kLinOut, VEC>(a, roles.r[2], at, lds);
+  else
+    lin_chunk_run<T, KI, NT, NW, MODE, VEC>(a, roles.r[role], at, lds);
+}
+
 // The instances: widths of 64 to 256 contracted, 64 or 128 columns of output.
 template <typename T, bool VEC>
-hipError_t lin_chunk(const LinArgs& a, LinRole r, int mode, hipStream_t s);
+hipError_t lin_chunk(const LinArgs& a, const LinRole& r, int mode, hipStream_t s);
+// dq, dk and dv (whose mode is kLinOut) of one call.
+template <typename T, bool VEC>
+hipError_t lin_chunks(const LinArgs& a, const LinRoles& r, int mode, hipStream_t s);
 
 }  // namespace gdr

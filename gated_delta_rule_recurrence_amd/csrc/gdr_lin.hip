@@ -26,42 +26,38 @@ namespace {
 constexpr int kThreads = 256;
 // Steps up to which a forward call goes one step at a time.
 constexpr int kFewSteps = 8;
-// Rows of the state of a workgroup of that kernel.
-constexpr int kStepRows = 16;
-constexpr int kWaveRows = kStepRows / (kThreads / 64);
+constexpr int kStepRows = 4;  // of the state, of a group of lanes
 
-__device__ __forceinline__ float wave_sum(float x) {
-  x = rowsum16(x);
-  x = swap16_sum(x, x);
-  return swap32_sum(x, x);
-}
-
-// A step at a time: a wave holds kWaveRows rows of the state, a lane every
-// 64th column.
-template <typename T>
+// A step at a time.  LANES lanes own kStepRows rows of the state, each lane
+// NV vectors of V neighbouring columns of every row, so that a row is read and
+// written in whole cache lines.  Bound by the states, read and written once: 48
+// requests of 32 heads of 128 x 128 (201 MB) take TIME.
+template <typename T, int LANES, int NV, int V>
 __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const int h = blockIdx.y, b = blockIdx.z, reps = a.Hv / a.Hk;
-  const int o0 = blockIdx.x * kStepRows + wave * kWaveRows;
+  const int o0 = (blockIdx.x * (kThreads / LANES) + group) * kStepRows;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
   const int size = a.Dk * a.Dv;
-  const float* const first =
-      a.S0 != nullptr ? a.S0 + ((int64_t)b * a.Hv + h) * size : nullptr;
-  float S[kWaveRows][4];
+  const int64_t whole = ((int64_t)b * a.Hv + h) * size;
+  float S[kStepRows][NV][V];
 #pragma unroll
-  for (int j = 0; j < kWaveRows; ++j)
+  for (int j = 0; j < kStepRows; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int o = o0 + j, i = lane + 64 * e;
-      S[j][e] = first != nullptr && o < a.Dv && i < a.Dk ? first[o * a.Dk + i] : 0.f;
+    for (int n = 0; n < NV; ++n) {
+      const int o = o0 + j, i = (n * LANES + lane) * V;
+      const bool in = a.S0 != nullptr && o < a.Dv && i < a.Dk;
+      const Pack<float, V> x = in ? load_pack<float, V>(a.S0 + whole + o * a.Dk + i)
+                                  : zero_pack<float, V>();
+      unpack(x, S[j][n]);
     }
   auto store = [&](float* to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < kWaveRows; ++j)
+    for (int j = 0; j < kStepRows; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int o = o0 + j, i = lane + 64 * e;
-        if (o < a.Dv && i < a.Dk) to[o * a.Dk + i] = S[j][e];
+      for (int n = 0; n < NV; ++n) {
+        const int o = o0 + j, i = (n * LANES + lane) * V;
+        if (o < a.Dv && i < a.Dk) store_pack(to + o * a.Dk + i, S[j][n]);
       }
   };
   const int64_t slot = lin_slot(a, sp, b, 0);
@@ -70,31 +66,40 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
     const int64_t row = sp.first + t;
     const T* const Q = static_cast<const T*>(a.q) + row * a.q_stride + (int64_t)(h / reps) * a.Dk;
     const T* const K = static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)(h / reps) * a.Dk;
-    const T* const V = static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)h * a.Dv;
+    const T* const W = static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)h * a.Dv;
+    float q[NV][V], k[NV][V], v[kStepRows];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int i = (n * LANES + lane) * V;
+      const bool in = i < a.Dk;
+      unpack(in ? load_pack<T, V>(Q + i) : zero_pack<T, V>(), q[n]);
+      unpack(in ? load_pack<T, V>(K + i) : zero_pack<T, V>(), k[n]);
+    }
+#pragma unroll
+    for (int j = 0; j < kStepRows; ++j) v[j] = o0 + j < a.Dv ? to_f32(W[o0 + j]) : 0.f;
     const float g = expf(lin_log_decay(a, row, h));
-    float q[4], k[4];
+    float x[kStepRows];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = lane + 64 * e;
-      q[e] = i < a.Dk ? to_f32(Q[i]) : 0.f;
-      k[e] = i < a.Dk ? to_f32(K[i]) : 0.f;
+    for (int j = 0; j < kStepRows; ++j) {
+      x[j] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          S[j][n][e] = fmaf(v[j], k[n][e], S[j][n][e] * g);
+          x[j] = fmaf(S[j][n][e], q[n][e], x[j]);
+        }
+      x[j] = rowsum16(x[j]);
+      if constexpr (LANES >= 32) x[j] = swap16_sum(x[j], x[j]);
+      if constexpr (LANES >= 64) x[j] = swap32_sum(x[j], x[j]);
     }
+    if (lane == 0)
 #pragma unroll
-    for (int j = 0; j < kWaveRows; ++j) {
-      const int o = o0 + j;
-      const bool in = o < a.Dv;
-      const float v = in ? to_f32(V[o]) : 0.f;
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        S[j][e] = fmaf(v, k[e], S[j][e] * g);
-        x = fmaf(S[j][e], q[e], x);
-      }
-      x = a.scale * wave_sum(x);
-      if (lane == 0 && in) st(static_cast<T*>(a.y), (row * a.Hv + h) * a.Dv + o, x);
-    }
+      for (int j = 0; j < kStepRows; ++j)
+        if (o0 + j < a.Dv)
+          st(static_cast<T*>(a.y), (row * a.Hv + h) * a.Dv + o0 + j, a.scale * x[j]);
   }
-  if (a.S_T != nullptr) store(a.S_T + ((int64_t)b * a.Hv + h) * size);
+  if (a.S_T != nullptr) store(a.S_T + whole);
   if (a.ckpt != nullptr) store(a.ckpt + ((slot + 1) * a.Hv + h) * size);
 }
 
@@ -209,7 +214,23 @@ __global__ __launch_bounds__(kThreads) void lin_flow_kernel(LinArgs a, int tiles
                                              : nullptr;
   double carry = 0.0, head = 0.0;
   if (D != nullptr) {
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) carry += (double)D[i] * (double)S[i];
+    // (16-byte loads where the states are whole vectors, four in flight)
+    const int64_t whole = n % 4 == 0 ? n / 4 : 0;
+    int64_t i = threadIdx.x;
+    for (; i + 3 * kThreads < whole; i += 4 * kThreads) {
+      float4 x[4], y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        x[u] = reinterpret_cast<const float4*>(D)[i + u * kThreads];
+        y[u] = reinterpret_cast<const float4*>(S)[i + u * kThreads];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        carry += ((double)x[u].x * (double)y[u].x + (double)x[u].y * (double)y[u].y) +
+                 ((double)x[u].z * (double)y[u].z + (double)x[u].w * (double)y[u].w);
+    }
+    for (i = whole > 0 ? 4 * (i - threadIdx.x) + threadIdx.x : threadIdx.x; i < n; i += kThreads)
+      carry += (double)D[i] * (double)S[i];
     carry = block_sum(carry, red);
   }
   const float* const fa = a.flow + h * a.rows;
@@ -289,12 +310,22 @@ hipError_t chunked(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) 
   return r.vec ? lin_chunk<T, true>(a, r, mode, s) : lin_chunk<T, false>(a, r, mode, s);
 }
 
+template <typename T, int LANES, int NV, int V>
+hipError_t step(const LinArgs& a, hipStream_t s) {
+  constexpr int kRows = kThreads / LANES * kStepRows;
+  hipLaunchKernelGGL((lin_step_kernel<T, LANES, NV, V>), dim3((a.Dv + kRows - 1) / kRows, a.Hv, a.B),
+                     dim3(kThreads), 0, s, a);
+  return noted(s);
+}
+
 template <typename T>
 hipError_t fwd(const LinArgs& a, hipStream_t s) {
   if (a.T <= kFewSteps) {
-    hipLaunchKernelGGL(lin_step_kernel<T>, dim3((a.Dv + kStepRows - 1) / kStepRows, a.Hv, a.B),
-                       dim3(kThreads), 0, s, a);
-    return noted(s);
+    // (vectors of 16 bytes of the state, of 8 or 16 of the rows)
+    const bool vec = a.Dk % 4 == 0 && a.q_stride % 4 == 0 && a.k_stride % 4 == 0;
+    if (!vec) return step<T, 64, 4, 1>(a, s);
+    return a.Dk <= 64 ? step<T, 16, 1, 4>(a, s)
+                      : a.Dk <= 128 ? step<T, 32, 1, 4>(a, s) : step<T, 64, 1, 4>(a, s);
   }
   const int reps = a.Hv / a.Hk;
   LinRole r{};
@@ -392,7 +423,6 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
     v.slots = 0;
     v.last = a.dS0;
   }
-  if (e == hipSuccess) e = chunked<T>(a, r, mode, s);
   // dk: (v, dy, q)
   d.Q = a.v;
   d.K = a.dy;
@@ -410,8 +440,10 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
   d.out = reps > 1 ? nullptr : a.dk;
   d.part = a.dk_part;
   d.flow = a.flow + (int64_t)tiles * a.rows * a.Hv;
-  if (e == hipSuccess) e = chunked<T>(a, d, mode, s);
-  if (e == hipSuccess) e = chunked<T>(a, v, kLinOut, s);
+  if (e == hipSuccess) {
+    const LinRoles roles{{r, d, v}};
+    e = r.vec ? lin_chunks<T, true>(a, roles, mode, s) : lin_chunks<T, false>(a, roles, mode, s);
+  }
   if (e == hipSuccess && reps > 1) {
     const int V = a.Dk % 4 == 0 ? 4 : 1;
     const int64_t blocks = ((int64_t)a.T * a.Hk * a.Dk / V + kThreads - 1) / kThreads;
