@@ -33,6 +33,7 @@
 
 namespace gdr {
 
+constexpr int kLinWaves = 4;  // waves of a workgroup
 constexpr double kLeastLog = -200.0;
 // An offset past the end of every buffer (64 rows of at most 2^23 elements).
 constexpr uint32_t kLinPast = 0xf0000000u;
@@ -88,31 +89,57 @@ struct LinTypes<float> {
 };
 
 // A tile [rows][W] of bf16 in LDS whose 16-byte blocks are exchanged inside a
-// row so that the rows of an operand fall on different banks, read by rows
-// (16 rows, one block each) and transposed (4 rows, 4 blocks), and so that two
-// rows written at once (8 blocks each) do.
+// row, block ^ lin_swz(row).  The 64 banks hold 16 blocks; what reads them at
+// once, as measured: a read by rows 16 lanes, rows 0 .. 3 and 12 .. 15 of one
+// block and rows 4 .. 11 of its neighbour (or the others); a transposed read 32
+// lanes, rows 0 .. 3 and 8 .. 11 (or the others), two blocks each.  So the bits
+// of r but r2 choose the pair of blocks, and r2 and r3 together, which keep
+// those two groups of rows apart, the one of it.  (The state's order reads
+// halves of four blocks: two cycles for one.)  Conflicts were 42% of the LDS
+// cycles with an order that served consecutive rows only.
 template <int W>
 __device__ __forceinline__ int lin_swz(int r) {
-  if constexpr (W % 128 == 0)
-    return ((r & 1) << 3) | ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
-  if constexpr (W == 32) return (r >> 2) & 3;
-  return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  const int low = ((r & 2) << 1) | (((r >> 2) ^ (r >> 1)) & 2) | ((r >> 2) & 1);
+  if constexpr (W % 128 == 0) return ((r & 1) << 3) | low;  // (else r0 is half of the banks)
+  if constexpr (W == 32) return low & 3;
+  return low;
 }
+// Element c of row r, where c is a whole block's first for a lane's own `at`
+// of another column of the same row: blocks of one row differ by an exclusive
+// or, so that a lane forms one place for all reads of a tile and each costs at
+// most one more instruction (formed one by one, they were a sixth of all).
+template <int W>
+__device__ __forceinline__ int lin_move(int at, int c) {
+  constexpr int kMask = W % 128 == 0 ? 127 : W == 32 ? 31 : 63;
+  return (at ^ (c & kMask)) + (c & ~kMask);
+}
+// Row r, column c.
 template <int W>
 __device__ __forceinline__ int lin_at(int r, int c) {
-  return r * W + (((c >> 3) ^ lin_swz<W>(r)) << 3) + (c & 7);
+  return lin_move<W>(r * W + (lin_swz<W>(r) << 3), c);
 }
-// Lane l: row r0 + l % 16, columns c0 + 8 (l / 16) ..
+// Lane l: row l % 16, columns 8 (l / 16) ..; an operand is read r0 rows (a
+// multiple of 16) and c0 columns (of 32) on.
 template <int W>
-__device__ __forceinline__ uint4 lin_rows(const uint16_t* t, int r0, int c0, int lane) {
-  return *reinterpret_cast<const uint4*>(t + lin_at<W>(r0 + (lane & 15), c0 + 8 * (lane >> 4)));
+__device__ __forceinline__ int lin_row_place(int lane) {
+  return lin_at<W>(lane & 15, 8 * (lane >> 4));
 }
-// Lane l: column c0 + l % 16 (STATE: columns c0 + 8 (l % 16 / 4) + l % 4),
-// rows r0 + 8 (l / 16) ..
+template <int W>
+__device__ __forceinline__ uint4 lin_rows(const uint16_t* t, int place, int r0, int c0) {
+  return *reinterpret_cast<const uint4*>(t + r0 * W + lin_move<W>(place, c0));
+}
+// Lane l: column l % 16 (STATE: columns 8 (l % 16 / 4) + l % 4), rows
+// 8 (l / 16) ..; read r0 rows (of 32) and c0 columns (of 16; STATE: of 32, or 4
+// more) on.  The upper four rows' blocks are those of the lower ones ^ 3.
 template <int W, bool STATE>
-__device__ __forceinline__ uint4 lin_columns(const uint16_t* t, int r0, int c0, int lane) {
-  const int r = r0 + 8 * (lane >> 4) + ((lane >> 2) & 3), c = c0 + (STATE ? 8 : 4) * (lane & 3);
-  const uint2 lo = lds_read_tr16(t + lin_at<W>(r, c)), hi = lds_read_tr16(t + lin_at<W>(r + 4, c));
+__device__ __forceinline__ int lin_column_place(int lane) {
+  return lin_at<W>(8 * (lane >> 4) + ((lane >> 2) & 3), (STATE ? 8 : 4) * (lane & 3));
+}
+template <int W>
+__device__ __forceinline__ uint4 lin_columns(const uint16_t* t, int place, int r0, int c0) {
+  const int at = lin_move<W>(place, c0);
+  const uint2 lo = lds_read_tr16(t + r0 * W + at);
+  const uint2 hi = lds_read_tr16(t + (r0 + 4) * W + (at ^ 24));
   return uint4{lo.x, lo.y, hi.x, hi.y};
 }
 
@@ -255,10 +282,10 @@ __device__ __forceinline__ double lin_prefix_sum(double x) {
 __device__ __forceinline__ float lin_exp(double x) { return exp2_hw(kLog2e * (float)x); }
 
 // A tile [L][W] on its way through a thread's registers: 8 threads a row,
-// eight elements in each 64 columns, 8 NW rows at a time.
-template <typename T, int W, int NW>
+// eight elements in each 64 columns, 8 kLinWaves rows at a time.
+template <typename T, int W>
 struct LinStage {
-  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, R = 8 * NW;
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, R = 8 * kLinWaves;
   static constexpr int NR = L / R, NC = W / 64;
   static_assert(NR * R == L, "whole passes of the threads");
   LinRaw<T> raw[NR][NC];
@@ -282,12 +309,11 @@ struct LinStage {
   // reverse: the last row first
   __device__ __forceinline__ void store(uint16_t* const (&t)[NP], bool reverse, int thread) const {
     const int x = reverse ? L - 1 - (thread >> 3) : thread >> 3;
+    const int at = lin_at<W>(x, (thread & 7) * 8), step = reverse ? -R * W : R * W;
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
-        raw[i][k].put(t, lin_at<W>(reverse ? x - R * i : x + R * i,
-                                   (thread & 7) * 8 + 64 * k));
+      for (int k = 0; k < NC; ++k) raw[i][k].put(t, step * i + lin_move<W>(at, 64 * k));
   }
 };
 
@@ -301,17 +327,13 @@ __device__ __forceinline__ void lin_barrier() {
 }
 
 // Waves of a SIMD that the registers are cut to.
-constexpr int lin_waves(int KI, int NT, int NW, int mode) {
-  if (NW == 8) return KI <= 192 ? 4 : 2;
+constexpr int lin_waves(int KI, int NT, int mode) {
   return KI <= 128 && NT == 1 ? 3 : KI * NT <= 256 || (mode == kLinState && KI * NT <= 384) ? 2 : 1;
 }
 // Sum of the waves' values of row x.
-template <int NW, int L>
-__device__ __forceinline__ float lin_sum(const float (&red)[NW][L], int x) {
-  float s = red[0][x];
-#pragma unroll
-  for (int w = 1; w < NW; ++w) s += red[w][x];
-  return s;
+template <int L>
+__device__ __forceinline__ float lin_sum(const float (&red)[kLinWaves][L], int x) {
+  return (red[0][x] + red[1][x]) + (red[2][x] + red[3][x]);
 }
 
 // What lies in LDS, in elements of 16 bits.  P takes the place of Q, which has
@@ -350,16 +372,16 @@ __device__ __forceinline__ LinBlock lin_block(const LinArgs& a, uint32_t each) {
   return LinBlock{id - rest * each, at % a.segs, h, at / a.segs};
 }
 
-template <typename T, int KI, int NT, int NW, int MODE, bool VEC>
+template <typename T, int KI, int NT, int MODE, bool VEC>
 __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r, LinBlock at,
                                               uint16_t* lds) {
-  constexpr int WO = 16 * NT * NW;
+  constexpr int WO = 16 * NT * kLinWaves;
   using Z = LinTiles<T, KI, WO, MODE>;
   constexpr int L = Z::L, NP = Z::NP, NS = Z::NS, IT = L / 16, KS = KI / 32;
   constexpr bool OUT = MODE != kLinState, FLOW = MODE == kLinFlow;
   __shared__ __attribute__((aligned(16))) float2 Hs[L];  // in units of ln 2, hi + lo
   __shared__ __attribute__((aligned(16))) float cf[L], uf[L], pd[L];
-  __shared__ float total_s, red[NW][L];
+  __shared__ float total_s, red[kLinWaves][L];
   const int wave = threadIdx.x >> 6;
   const int tile = at.each, sg = at.sg, h = at.h, b = at.b;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
@@ -416,8 +438,8 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
   };
   if (r.save != nullptr) put_state(r.save + (slot * a.Hv + h) * size);
 
-  LinStage<T, KI, NW> qs, ks;
-  LinStage<T, WO, NW> vs;
+  LinStage<T, KI> qs, ks;
+  LinStage<T, WO> vs;
   float lg = 0.f;
   // Rows of the next tile, one tensor at a time, so that the requests do not
   // queue up: row x of a tile is step t0 + x, or t0 + L - 1 - x.
@@ -457,6 +479,9 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     int thread = threadIdx.x;
     asm volatile("" : "+v"(thread));
     const int lane = thread & 63, q = lane >> 4, lr = lane & 15;
+    const int rows = lin_row_place<KI>(lane), prows = lin_row_place<L>(lane);
+    const int kcols = lin_column_place<KI, true>(lane);
+    const int vcols = lin_move<WO>(lin_column_place<WO, false>(lane), 16 * NT * wave);
     lin_barrier();  // the last tile has been read
     if constexpr (OUT) qs.store(Qt, r.reverse, thread);
     ks.store(Kt, r.reverse, thread);
@@ -487,7 +512,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       // P: the tiles of 16 x 16 that its products below read (row it, columns
       // up to 16 (it | 1) + 15) dealt to the waves, their products first and their decays behind S Q, which leaves the matrix
       // cores time for them
-      constexpr int PT = IT == 4 ? 12 : 4, PW = (PT + NW - 1) / NW;
+      constexpr int PT = IT == 4 ? 12 : 4, PW = (PT + kLinWaves - 1) / kLinWaves;
       f4 p[PW];
       int pi[PW], pj[PW];
 #pragma unroll
@@ -505,8 +530,8 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
           uint4 ka[NP], qb[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            ka[i] = lin_rows<KI>(Kt[i], 16 * pj[k], 32 * s, lane);
-            qb[i] = lin_rows<KI>(Qt[i], 16 * pi[k], 32 * s, lane);
+            ka[i] = lin_rows<KI>(Kt[i], rows, 16 * pj[k], 32 * s);
+            qb[i] = lin_rows<KI>(Qt[i], rows, 16 * pi[k], 32 * s);
           }
           p[k] = lin_mfma(ka, qb, p[k]);
         }
@@ -526,12 +551,13 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         for (int it = 0; it < IT; ++it) {
           uint4 qb[NP];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) qb[i] = lin_rows<KI>(Qt[i], 16 * it, 32 * s, lane);
+          for (int i = 0; i < NP; ++i) qb[i] = lin_rows<KI>(Qt[i], rows, 16 * it, 32 * s);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(sa[nt], qb, acc[it][nt]);
         }
       }
       lin_barrier();  // Q has been read
+      const int pput = lin_at<L>(lr, 4 * q);
 #pragma unroll
       for (int k = 0; k < PW; ++k) {
         const int i = 16 * pi[k] + lr, j = 16 * pj[k] + 4 * q;
@@ -552,7 +578,8 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         lin_split<NS>(p[k], f4{0.f, 0.f, 0.f, 0.f}, pieces);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-          *reinterpret_cast<uint2*>(Pt[n] + lin_at<L>(i, j)) = uint2{pieces[n].x, pieces[n].y};
+          *reinterpret_cast<uint2*>(Pt[n] + 16 * L * pi[k] + lin_move<L>(pput, 16 * pj[k])) =
+              uint2{pieces[n].x, pieces[n].y};
       }
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
@@ -583,7 +610,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 #pragma unroll
         for (int i = NP - 1; i >= 0; --i) {
           const uint4 w = vo[nt][i] =
-              lin_columns<WO, false>(Vt[i], 32 * k, 16 * (NT * wave + nt), lane);
+              lin_columns<WO>(Vt[i], vcols, 32 * k, 16 * nt);
           const f4 wx = lin_unpack(uint2{w.x, w.y}), wy = lin_unpack(uint2{w.z, w.w});
           x = i == NP - 1 ? wx : x + wx;
           y = i == NP - 1 ? wy : y + wy;
@@ -595,7 +622,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         for (int it = 2 * k; it < IT; ++it) {
           uint4 pb[NS];
 #pragma unroll
-          for (int n = 0; n < NS; ++n) pb[n] = lin_rows<L>(Pt[n], 16 * it, 32 * k, lane);
+          for (int n = 0; n < NS; ++n) pb[n] = lin_rows<L>(Pt[n], prows, 16 * it, 32 * k);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(vo[nt], pb, acc[it][nt]);
         }
@@ -605,7 +632,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         uint4 ka[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-          ka[i] = lin_columns<KI, true>(Kt[i], 32 * k, 32 * (s >> 1) + 4 * (s & 1), lane);
+          ka[i] = lin_columns<KI>(Kt[i], kcols, 32 * k, 32 * (s >> 1) + 4 * (s & 1));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) S[s][nt] = lin_mfma(ka, vu[nt], S[s][nt]);
       }
@@ -623,6 +650,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         R = buffer_of(r.R, (row * r.sr + (int64_t)(h / r.dr) * r.No) * sizeof(T),
                       ((int64_t)(n - 1) * r.sr + r.No) * sizeof(T));
       const int lane_row = r.reverse ? 15 - lr : lr, o = wo + 4 * q;
+      const int vput = lin_move<WO>(lin_at<WO>(lr, 4 * q), 16 * NT * wave);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         const int x = 16 * it + lr, t = r.reverse ? L - 16 - 16 * it : 16 * it;
@@ -641,7 +669,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 #pragma unroll
             for (int i = NP - 1; i >= 0; --i) {
               const f4 y = lin_unpack(*reinterpret_cast<const uint2*>(
-                  Vt[i] + lin_at<WO>(x, o - o0 + 16 * nt)));
+                  Vt[i] + 16 * WO * it + lin_move<WO>(vput, 16 * nt)));
               own = i == NP - 1 ? y : own + y;
             }
             acc[it][nt] += own * pd[x];
@@ -674,7 +702,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         const int x = thread, t = r.reverse ? L - 1 - x : x;
         if (x < L && t < n)
           r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] =
-              lin_sum<NW, L>(red, x);
+              lin_sum<L>(red, x);
       }
     }
   }
@@ -686,30 +714,30 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
   if (r.save != nullptr) put_state(r.save + ((slot + 1) * a.Hv + h) * size);
 }
 
-template <typename T, int KI, int NT, int NW, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * NW, (lin_waves(KI, NT, NW, MODE))) void lin_chunk_kernel(
+template <typename T, int KI, int NT, int MODE, bool VEC>
+__global__ __launch_bounds__(64 * kLinWaves, (lin_waves(KI, NT, MODE))) void lin_chunk_kernel(
     LinArgs a, LinRole r) {
   __shared__ __attribute__((aligned(16))) uint16_t
-      lds[LinTiles<T, KI, 16 * NT * NW, MODE>::kEnd];
-  lin_chunk_run<T, KI, NT, NW, MODE, VEC>(a, r, lin_block(a, r.tiles), lds);
+      lds[LinTiles<T, KI, 16 * NT * kLinWaves, MODE>::kEnd];
+  lin_chunk_run<T, KI, NT, MODE, VEC>(a, r, lin_block(a, r.tiles), lds);
 }
 
 // dq, dk and dv in one launch, where their widths take the same instance.
 struct LinRoles {
   LinRole r[3];
 };
-template <typename T, int KI, int NT, int NW, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * NW, (lin_waves(KI, NT, NW, MODE))) void lin_chunks_kernel(
+template <typename T, int KI, int NT, int MODE, bool VEC>
+__global__ __launch_bounds__(64 * kLinWaves, (lin_waves(KI, NT, MODE))) void lin_chunks_kernel(
     LinArgs a, LinRoles roles) {
   __shared__ __attribute__((aligned(16))) uint16_t
-      lds[LinTiles<T, KI, 16 * NT * NW, MODE>::kEnd];
+      lds[LinTiles<T, KI, 16 * NT * kLinWaves, MODE>::kEnd];
   LinBlock at = lin_block(a, 3 * roles.r[0].tiles);
   const uint32_t role = at.each % 3;
   at.each /= 3;
   if (MODE == kLinFlow && role == 2)
-    lin_chunk_run<T, KI, NT, NW, kLinOut, VEC>(a, roles.r[2], at, lds);
+    lin_chunk_run<T, KI, NT, kLinOut, VEC>(a, roles.r[2], at, lds);
   else
-    lin_chunk_run<T, KI, NT, NW, MODE, VEC>(a, roles.r[role], at, lds);
+    lin_chunk_run<T, KI, NT, MODE, VEC>(a, roles.r[role], at, lds);
 }
 
 // The instances: widths of 64 to 256 contracted, 64 or 128 columns of output.
