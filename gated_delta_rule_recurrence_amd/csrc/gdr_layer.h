@@ -210,7 +210,7 @@ struct ResPlan {
   int64_t per_gate;      // workgroups of one gate row (1: whole gate rows in a workgroup)
   int64_t parts;         // workgroups
 };
-bool res_plan(const ResArgs& a, bool bf16, ResPlan* p);
+bool res_plan(const ResArgs& a, bool bf16, bool bwd, ResPlan* p);
 hipError_t launch_res_fwd(const ResArgs& a, const ResPlan& p, bool bf16, bool stream_f32,
                           hipStream_t s);
 hipError_t launch_res_bwd(const ResArgs& a, const ResPlan& p, bool bf16, bool stream_f32,
@@ -290,6 +290,15 @@ __device__ __forceinline__ float swap16_sum(float a, float b) {
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
                                                   false);
   return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// A barrier for what lies in LDS: loads and stores of global memory stay in
+// flight across it (__syncthreads waits for them: in a tile of linear attention
+// 4.8 of 17.5 thousand cycles).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // V consecutive elements: one, or a vector of 8 or 16 bytes.

@@ -612,7 +612,8 @@ int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const
 }
 
 // ---- the norms around a block --------------------------------------------------
-int check(const gdr_res_shape* in, gdr_res_shape* s, gdr::ResArgs* a, gdr::ResPlan* p) {
+int check(const gdr_res_shape* in, bool bwd, gdr_res_shape* s, gdr::ResArgs* a,
+          gdr::ResPlan* p) {
   if (in == nullptr) return GDR_ERR_NULL_ARG;
   *s = *in;
   if (s->rows < 0 || s->rows > kMaxRows || s->C < 1 || s->C > GDR_RES_MAX_CHANNELS ||
@@ -643,7 +644,7 @@ int check(const gdr_res_shape* in, gdr_res_shape* s, gdr::ResArgs* a, gdr::ResPl
   a->offset = s->weight_offset;
   a->w_bf16 = s->wdtype == GDR_BF16;
   a->gate_bf16 = s->gdtype == GDR_BF16;
-  if (!gdr::res_plan(*a, s->dtype == GDR_BF16, p)) return GDR_ERR_BAD_DIM;
+  if (!gdr::res_plan(*a, s->dtype == GDR_BF16, bwd, p)) return GDR_ERR_BAD_DIM;
   return GDR_OK;
 }
 
@@ -659,7 +660,7 @@ int res_forward(const gdr_res_shape* shape, const void* x, const void* r, const 
   gdr_res_shape s;
   gdr::ResArgs a{};
   gdr::ResPlan p{};
-  int st = check(shape, &s, &a, &p);
+  int st = check(shape, false, &s, &a, &p);
   if (st == GDR_OK) st = pointers_ok({x, r, static_cast<const void*>(h)}, s.rows > 0);
   if (st == GDR_OK && s.rows > 0 && s.pre && y == nullptr) st = GDR_ERR_NULL_ARG;
   if (st == GDR_OK)
@@ -688,7 +689,7 @@ int res_backward(const gdr_res_shape* shape, const void* x, const void* r, const
   gdr_res_shape s;
   gdr::ResArgs a{};
   gdr::ResPlan p{};
-  int st = check(shape, &s, &a, &p);
+  int st = check(shape, true, &s, &a, &p);
   if (st == GDR_OK)
     st = pointers_ok({x, r, static_cast<const void*>(stats), static_cast<const void*>(dx),
                       static_cast<const void*>(dr)},
@@ -899,7 +900,7 @@ int gdr_res_backward_workspace_bytes(const gdr_res_shape* shape, size_t* out) {
   gdr::ResArgs a{};
   gdr::ResPlan p{};
   int64_t gate = 0;
-  const int st = check(shape, &s, &a, &p);
+  const int st = check(shape, true, &s, &a, &p);
   return store_size(st, st == GDR_OK ? res_workspace(s, p, &gate) : 0, out);
 }
 

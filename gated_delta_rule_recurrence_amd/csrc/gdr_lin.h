@@ -317,15 +317,6 @@ struct LinStage {
   }
 };
 
-// A barrier for what lies in LDS: loads and stores of global memory stay in
-// flight across it (__syncthreads waits for them: 4.8 of a tile's 17.5
-// thousand cycles).
-__device__ __forceinline__ void lin_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // Waves of a SIMD that the registers are cut to.
 constexpr int lin_waves(int KI, int NT, int mode) {
   return KI <= 128 && NT == 1 ? 3 : KI * NT <= 256 || (mode == kLinState && KI * NT <= 384) ? 2 : 1;
@@ -482,7 +473,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     const int rows = lin_row_place<KI>(lane), prows = lin_row_place<L>(lane);
     const int kcols = lin_column_place<KI, true>(lane);
     const int vcols = lin_move<WO>(lin_column_place<WO, false>(lane), 16 * NT * wave);
-    lin_barrier();  // the last tile has been read
+    lds_barrier();  // the last tile has been read
     if constexpr (OUT) qs.store(Qt, r.reverse, thread);
     ks.store(Kt, r.reverse, thread);
     vs.store(Vt, r.reverse, thread);
@@ -502,7 +493,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         if (threadIdx.x == 0) total_s = lin_exp(end);
       }
     }
-    lin_barrier();
+    lds_barrier();
     const int t0 = start(c);
     const bool more = c + 1 < chunks;
     if (more) fetch_q(c + 1, thread);
@@ -556,7 +547,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
           for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(sa[nt], qb, acc[it][nt]);
         }
       }
-      lin_barrier();  // Q has been read
+      lds_barrier();  // Q has been read
       const int pput = lin_at<L>(lr, 4 * q);
 #pragma unroll
       for (int k = 0; k < PW; ++k) {
@@ -587,7 +578,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[it][nt] *= x;
       }
-      lin_barrier();  // P is whole
+      lds_barrier();  // P is whole
     } else {
       if (more) fetch_k(c + 1, thread);
     }
@@ -698,7 +689,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       else
         put(float{});
       if constexpr (FLOW) {
-        lin_barrier();
+        lds_barrier();
         const int x = thread, t = r.reverse ? L - 1 - x : x;
         if (x < L && t < n)
           r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] =
