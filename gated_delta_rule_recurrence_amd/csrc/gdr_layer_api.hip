@@ -472,6 +472,8 @@ int check(const gdr_lin_shape* in, gdr_lin_shape* s) {
       !stride_ok(&s->v_stride, s->Hv * s->Dv, most) || !stride_ok(&s->g_stride, s->Hv) ||
       s->Hv * s->Dk > most)
     return GDR_ERR_BAD_STRIDE;
+  // (no sequence is longer than the rows: T sizes the grid)
+  if (s->T > s->rows && s->B > 0) s->T = s->rows;
   return GDR_OK;
 }
 
@@ -540,7 +542,7 @@ int lin_forward(const gdr_lin_shape* shape, const void* q, const void* k, const 
   gdr_lin_shape s;
   LinSizes z{};
   int st = check(shape, &s);
-  if (st == GDR_OK) st = rows_ok(s.B, s.T, s.rows, spans);
+  if (st == GDR_OK) st = rows_ok(shape->B, shape->T, shape->rows, spans);
   if (st == GDR_OK) st = lin_sizes(s, &z);
   const bool has_rows = s.B > 0 && s.T > 0 && s.rows > 0;
   if (st == GDR_OK) st = pointers_ok({q, k, v, static_cast<const void*>(y)}, has_rows);
@@ -571,11 +573,11 @@ int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const
   gdr_lin_shape s;
   LinSizes z{};
   int st = check(shape, &s);
-  if (st == GDR_OK) st = rows_ok(s.B, s.T, s.rows, spans);
+  if (st == GDR_OK) st = rows_ok(shape->B, shape->T, shape->rows, spans);
   if (st == GDR_OK) st = lin_sizes(s, &z);
   const bool has_rows = s.B > 0 && s.T > 0 && s.rows > 0;
   if (st == GDR_OK)
-    st = pointers_ok({ckpt, static_cast<const void*>(workspace)}, s.B > 0);
+    st = pointers_ok({ckpt}, s.B > 0);
   if (st == GDR_OK)
     st = pointers_ok({q, k, v, dy, static_cast<const void*>(dq), static_cast<const void*>(dk),
                       static_cast<const void*>(dv)},
@@ -586,7 +588,8 @@ int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const
                        static_cast<const void*>(workspace)});
   if (st != GDR_OK) return st;
   if (s.B == 0) return GDR_OK;
-  if (workspace_bytes < (size_t)z.bwd) return GDR_ERR_WORKSPACE;
+  if (z.bwd > 0 && (workspace == nullptr || workspace_bytes < (size_t)z.bwd))
+    return GDR_ERR_WORKSPACE;
   gdr::LinArgs a = lin_args(s, q, k, v, log_g, spans);
   if (!has_rows) a.rows = 0, a.T = 0;
   a.ckpt = static_cast<float*>(const_cast<void*>(ckpt));
