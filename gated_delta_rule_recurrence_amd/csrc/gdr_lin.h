@@ -11,12 +11,13 @@
 // decay below kLeastLog (of which exp is 0 in fp32) counts as that, so that
 // -inf forgets without a difference of infinities.
 //
-// Precision.  bf16 rows are matrix operands as they are.  What is fp32 (P, S,
-// uf V) is held in two bf16 pieces, x = hi + lo within 2^-18: one piece would
-// add a rounding of 2^-9 a term to outputs that round by as much themselves,
-// and would leave the fp32 states with bf16's accuracy.  fp32 rows are three
-// pieces, and so is what they are multiplied with; of the nine products the
-// six above 2^-24 are formed.
+// Precision.  bf16 rows are matrix operands as they are; what is fp32 (P, S,
+// uf V) is held in bf16 pieces.  Three hold fp32's 24 bits: for whatever
+// becomes an fp32 output, that is the states that are handed on, and the flows
+// of the decay's gradient.  Outputs in bf16 take two, x = hi + lo within 2^-18,
+// far below their own rounding of 2^-9 (one piece would add another one).
+// fp32 rows are three pieces too; of the nine products the six above 2^-24 are
+// formed.
 //
 // Mapping.  A workgroup of four waves runs through a segment of one sequence
 // for one head and NT 64 columns of its output.  P is formed by all waves, in
@@ -51,6 +52,7 @@ struct LinRole {
   int reverse;         // time runs backwards
   int transposed;      // states lie [Ni][No] instead of [No][Ni]
   int vec;             // widths and strides are whole vectors (VEC)
+  int exact;           // the states are an output (see above)
   const float* first;  // states before each segment, or null (zeros)
   int slots;           // they lie in segments' slots, not [B][Hv]
   float* last;         // [B][Hv] states behind the sequences (one segment), or null
@@ -81,12 +83,15 @@ template <typename T>
 struct LinTypes;
 template <>
 struct LinTypes<bf16> {
-  static constexpr int L = 64, NP = 1, NS = 2;
+  static constexpr int L = 64, NP = 1;
 };
 template <>
 struct LinTypes<float> {
-  static constexpr int L = 32, NP = 3, NS = 3;
+  static constexpr int L = 32, NP = 3;
 };
+// Pieces of an fp32 operand.
+template <typename T, int MODE>
+constexpr int kLinPieces = sizeof(T) == 2 && MODE == kLinOut ? 2 : 3;
 
 // A tile [rows][W] of bf16 in LDS whose 16-byte blocks are exchanged inside a
 // row, block ^ lin_swz(row).  The 64 banks hold 16 blocks; what reads them at
@@ -331,7 +336,7 @@ __device__ __forceinline__ float lin_sum(const float (&red)[kLinWaves][L], int x
 // been read by then.
 template <typename T, int KI, int WO, int MODE>
 struct LinTiles {
-  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = LinTypes<T>::NS;
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = kLinPieces<T, MODE>;
   static constexpr int kQ = 0, kP = 0;
   static constexpr int kQP = NP * L * KI > NS * L * L ? NP * L * KI : NS * L * L;
   static constexpr int kK = MODE == kLinState ? 0 : kQP;
@@ -592,7 +597,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     }
 #pragma unroll
     for (int k = 0; k < L / 32; ++k) {
-      uint4 vo[NT][NP], vu[NT][NS];
+      uint4 vo[NT][NP], vu[NT][3];
       const f4 u0 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q);
       const f4 u1 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q + 4);
 #pragma unroll
@@ -606,7 +611,14 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
           x = i == NP - 1 ? wx : x + wx;
           y = i == NP - 1 ? wy : y + wy;
         }
-        lin_split<NS>(x * u0, y * u1, vu[nt]);
+        if (NS == 3 || r.exact) {
+          lin_split<3>(x * u0, y * u1, vu[nt]);
+        } else {
+          uint4 two[2];
+          lin_split<2>(x * u0, y * u1, two);
+          vu[nt][0] = two[0];
+          vu[nt][1] = two[1];
+        }
       }
       if constexpr (OUT) {
 #pragma unroll
@@ -625,7 +637,15 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         for (int i = 0; i < NP; ++i)
           ka[i] = lin_columns<KI>(Kt[i], kcols, 32 * k, 32 * (s >> 1) + 4 * (s & 1));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[s][nt] = lin_mfma(ka, vu[nt], S[s][nt]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (NS == 3) {
+            S[s][nt] = lin_mfma(ka, vu[nt], S[s][nt]);
+          } else {
+            if (r.exact) S[s][nt] = mfma_bf16(ka[0], vu[nt][2], S[s][nt]);
+            S[s][nt] = mfma_bf16(ka[0], vu[nt][1], S[s][nt]);
+            S[s][nt] = mfma_bf16(ka[0], vu[nt][0], S[s][nt]);
+          }
+        }
       }
     }
     if constexpr (OUT) {
