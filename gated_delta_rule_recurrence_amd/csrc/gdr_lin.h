@@ -534,6 +534,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       }
       if (more) fetch_k(c + 1, thread);
       // out <- S Q, scaled by cf
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int it = 0; it < IT; ++it)
 #pragma unroll
@@ -552,6 +553,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
           for (int nt = 0; nt < NT; ++nt) acc[it][nt] = lin_mfma(sa[nt], qb, acc[it][nt]);
         }
       }
+      __builtin_amdgcn_s_setprio(0);
       lds_barrier();  // Q has been read
       const int pput = lin_at<L>(lr, 4 * q);
 #pragma unroll
@@ -595,6 +597,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) S[s][nt] *= x;
     }
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int k = 0; k < L / 32; ++k) {
       uint4 vo[NT][NP], vu[NT][3];
@@ -648,6 +651,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         }
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if constexpr (OUT) {
       const int n = count(t0), wide = a.Hv * r.No;
       const int64_t row = sp.first + begin + t0;
