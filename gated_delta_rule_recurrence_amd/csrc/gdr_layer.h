@@ -204,7 +204,7 @@ struct ResArgs {
   float* gate_part;      // [parts][C]
 };
 struct ResPlan {
-  int lanes, nv;         // lanes of a row, vectors of a lane
+  int lanes;             // of a row, 8 channels each
   bool vec;
   int64_t step;          // rows of a workgroup, in whole or a part of a gate's rows
   int64_t per_gate;      // workgroups of one gate row (1: whole gate rows in a workgroup)

@@ -226,19 +226,26 @@ struct LinRaw<float> {
   }
 };
 // Four elements of a row, of which n are in it, `at` + `more` bytes into p (the
-// sum in the offset that the bound is checked with).
+// sum in the offset that the bound is checked with), as loaded.
 template <bool VEC, typename T>
-__device__ __forceinline__ f4 lin_quad(Buffer p, uint32_t at, uint32_t more, int n) {
-  float f[4];
-  if constexpr (VEC) {
-    unpack(get_pack<T, 4>(p, n > 0 ? at + more : kLinPast), f);
-  } else {
+struct LinQuad {
+  Pack<T, VEC ? 4 : 1> v[VEC ? 1 : 4];
+  __device__ __forceinline__ void load(Buffer p, uint32_t at, uint32_t more, int n) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = to_f32(get_pack<T, 1>(p, i < n ? at + more + i * sizeof(T) : kLinPast).v[0]);
+    for (int i = 0; i < (VEC ? 1 : 4); ++i)
+      v[i] = get_pack<T, VEC ? 4 : 1>(p, i < n ? at + more + i * sizeof(T) : kLinPast);
   }
-  return f4{f[0], f[1], f[2], f[3]};
-}
+  __device__ __forceinline__ f4 get() const {
+    float f[4];
+    if constexpr (VEC) {
+      unpack(v[0], f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = to_f32(v[i].v[0]);
+    }
+    return f4{f[0], f[1], f[2], f[3]};
+  }
+};
 template <bool VEC, typename T>
 __device__ __forceinline__ void lin_put(Buffer p, uint32_t at, uint32_t more, f4 x, int n) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -322,9 +329,12 @@ struct LinStage {
   }
 };
 
-// Waves of a SIMD that the registers are cut to.
-constexpr int lin_waves(int KI, int NT, int mode) {
-  return KI <= 128 && NT == 1 ? 3 : KI * NT <= 256 || (mode == kLinState && KI * NT <= 384) ? 2 : 1;
+// Waves of a SIMD (workgroups of a compute unit) that the registers are cut to,
+// no more than LDS holds.
+template <typename T>
+constexpr int lin_waves(int KI, int NT) {
+  if (sizeof(T) == 4) return KI <= 64 && NT == 1 ? 3 : KI <= 128 ? 2 : 1;
+  return KI <= 128 && NT == 1 ? 3 : 2;
 }
 // Sum of the waves' values of row x.
 template <int L>
@@ -506,8 +516,8 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     f4 acc[IT][NT];
     if constexpr (OUT) {
       // P: the tiles of 16 x 16 that its products below read (row it, columns
-      // up to 16 (it | 1) + 15) dealt to the waves, their products first and their decays behind S Q, which leaves the matrix
-      // cores time for them
+      // up to 16 (it | 1) + 15) dealt to the waves, their products first and
+      // their decays behind S Q, which leaves the matrix cores time for them
       constexpr int PT = IT == 4 ? 12 : 4, PW = (PT + kLinWaves - 1) / kLinWaves;
       f4 p[PW];
       int pi[PW], pj[PW];
@@ -590,6 +600,23 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       if (more) fetch_k(c + 1, thread);
     }
     if (more) fetch_v(c + 1, thread);
+    // the rows that the flows multiply with, in time for the end of the tile
+    const int n = count(t0), lane_row = r.reverse ? 15 - lr : lr, o = wo + 4 * q;
+    const int64_t row = sp.first + begin + t0;
+    LinQuad<VEC, T> with[FLOW ? IT : 1][FLOW ? NT : 1];
+    if constexpr (FLOW) {
+      const Buffer R = buffer_of(r.R, (row * r.sr + (int64_t)(h / r.dr) * r.No) * sizeof(T),
+                                 ((int64_t)(n - 1) * r.sr + r.No) * sizeof(T));
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int t = r.reverse ? L - 16 - 16 * it : 16 * it;
+          with[it][nt].load(R, (uint32_t)(lane_row * (uint32_t)r.sr + o) * sizeof(T),
+                            (uint32_t)(t * (uint32_t)r.sr + 16 * nt) * sizeof(T),
+                            r.No - o - 16 * nt);
+        }
+    }
     {
       const float x = total_s;
 #pragma unroll
@@ -608,8 +635,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         f4 x, y;
 #pragma unroll
         for (int i = NP - 1; i >= 0; --i) {
-          const uint4 w = vo[nt][i] =
-              lin_columns<WO>(Vt[i], vcols, 32 * k, 16 * nt);
+          const uint4 w = vo[nt][i] = lin_columns<WO>(Vt[i], vcols, 32 * k, 16 * nt);
           const f4 wx = lin_unpack(uint2{w.x, w.y}), wy = lin_unpack(uint2{w.z, w.w});
           x = i == NP - 1 ? wx : x + wx;
           y = i == NP - 1 ? wy : y + wy;
@@ -653,30 +679,21 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     }
     __builtin_amdgcn_s_setprio(0);
     if constexpr (OUT) {
-      const int n = count(t0), wide = a.Hv * r.No;
-      const int64_t row = sp.first + begin + t0;
+      const int wide = a.Hv * r.No;
       // rows past the sequence's end are past the buffers'
       const int es = r.out != nullptr ? (int)sizeof(T) : 4;
       const Buffer out = buffer_of(r.out != nullptr ? r.out : r.part,
                                    (row * wide + (int64_t)h * r.No) * es,
                                    ((int64_t)(n - 1) * wide + r.No) * es);
-      Buffer R{nullptr, 0};
-      if constexpr (FLOW)
-        R = buffer_of(r.R, (row * r.sr + (int64_t)(h / r.dr) * r.No) * sizeof(T),
-                      ((int64_t)(n - 1) * r.sr + r.No) * sizeof(T));
-      const int lane_row = r.reverse ? 15 - lr : lr, o = wo + 4 * q;
       const int vput = lin_move<WO>(lin_at<WO>(lr, 4 * q), 16 * NT * wave);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int x = 16 * it + lr, t = r.reverse ? L - 16 - 16 * it : 16 * it;
+        const int x = 16 * it + lr;
         float flow = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int left = r.No - o - 16 * nt;
           if constexpr (FLOW) {
-            const f4 w = lin_quad<VEC, T>(
-                R, (uint32_t)(lane_row * (uint32_t)r.sr + o) * sizeof(T),
-                (uint32_t)(t * (uint32_t)r.sr + 16 * nt) * sizeof(T), left);
+            const f4 w = with[it][nt].get();
 #pragma unroll
             for (int v = 0; v < 4; ++v) flow = fmaf(w[v], acc[it][nt][v], flow);
             // the step's own term
@@ -716,8 +733,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         lds_barrier();
         const int x = thread, t = r.reverse ? L - 1 - x : x;
         if (x < L && t < n)
-          r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] =
-              lin_sum<L>(red, x);
+          r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] = lin_sum<L>(red, x);
       }
     }
   }
@@ -730,7 +746,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 }
 
 template <typename T, int KI, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * kLinWaves, (lin_waves(KI, NT, MODE))) void lin_chunk_kernel(
+__global__ __launch_bounds__(64 * kLinWaves, (lin_waves<T>(KI, NT))) void lin_chunk_kernel(
     LinArgs a, LinRole r) {
   __shared__ __attribute__((aligned(16))) uint16_t
       lds[LinTiles<T, KI, 16 * NT * kLinWaves, MODE>::kEnd];
@@ -742,7 +758,7 @@ struct LinRoles {
   LinRole r[3];
 };
 template <typename T, int KI, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * kLinWaves, (lin_waves(KI, NT, MODE))) void lin_chunks_kernel(
+__global__ __launch_bounds__(64 * kLinWaves, (lin_waves<T>(KI, NT))) void lin_chunks_kernel(
     LinArgs a, LinRoles roles) {
   __shared__ __attribute__((aligned(16))) uint16_t
       lds[LinTiles<T, KI, 16 * NT * kLinWaves, MODE>::kEnd];

@@ -21,8 +21,9 @@ hipError_t lin_mode(const LinArgs& a, const LinRole& r, int mode, hipStream_t s)
 }
 template <typename T, int KI, bool VEC>
 hipError_t lin_wide(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {
-  if (lin_width(r.Ni, r.No) == 64) return lin_mode<T, KI, 1, VEC>(a, r, mode, s);
-  return lin_mode<T, KI, 2, VEC>(a, r, mode, s);
+  if constexpr (KI <= 128)
+    if (lin_width(r.Ni, r.No) == 128) return lin_mode<T, KI, 2, VEC>(a, r, mode, s);
+  return lin_mode<T, KI, 1, VEC>(a, r, mode, s);
 }
 template <typename T, bool VEC>
 hipError_t lin_chunk(const LinArgs& a, const LinRole& r, int mode, hipStream_t s) {

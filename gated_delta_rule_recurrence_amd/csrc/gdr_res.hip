@@ -541,7 +541,6 @@ bool res_plan(const ResArgs& a, bool is_bf16, bool bwd, ResPlan* p) {
   const int64_t lanes = (a.C + 7) / 8;
   if (lanes > 1024) return false;
   p->lanes = lanes <= 64 ? 64 : lanes <= 256 ? 256 : lanes <= 512 ? 512 : 1024;
-  p->nv = 8 / (p->vec ? (int)V : 1);
   const int64_t walkers = p->lanes > 64 ? 1 : kThreads / 64;
   const int64_t per = a.gate_rows > 1 ? a.gate_rows : (a.rows < 1 ? 1 : a.rows);
   int64_t want = p->lanes > 64 ? 131072 / p->lanes : 512;
