@@ -67,7 +67,8 @@ struct LinRole {
 enum LinMode { kLinOut = 0, kLinFlow = 1, kLinState = 2 };
 
 // Slot of segment s of sequence b: sequences own more slots than segments, for
-// the state behind the last.
+// the state behind the last.  One of no rows owns none and writes none: it may
+// stand anywhere, so its slots here may be another's.
 __device__ __forceinline__ int64_t lin_slot(const LinArgs& a, Span sp, int b, int s) {
   return sp.first / a.seg + 2 * (int64_t)b + s;
 }
@@ -392,7 +393,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
   const int tile = at.each, sg = at.sg, h = at.h, b = at.b;
   const Span sp = span_of(a.spans, b, a.T, a.rows);
   const int begin = sg * a.seg;
-  if (sg > 0 && begin >= sp.len) return;
+  if ((sg > 0 || MODE == kLinState) && begin >= sp.len) return;
   const int len = sp.len - begin < a.seg ? sp.len - begin : a.seg;  // of this segment
   const int chunks = (len + L - 1) / L;
   const int64_t size = (int64_t)r.Ni * r.No, slot = lin_slot(a, sp, b, sg);
@@ -442,7 +443,8 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       return x;
     });
   };
-  if (r.save != nullptr) put_state(r.save + (slot * a.Hv + h) * size);
+  const bool save = r.save != nullptr && len > 0;
+  if (save) put_state(r.save + (slot * a.Hv + h) * size);
 
   LinStage<T, KI> qs, ks;
   LinStage<T, WO> vs;
@@ -742,7 +744,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     if (threadIdx.x == 0 && tile == 0) r.decay[slot * a.Hv + h] = lin_exp(all);
   }
   if (r.last != nullptr) put_state(r.last + ((int64_t)b * a.Hv + h) * size);
-  if (r.save != nullptr) put_state(r.save + ((slot + 1) * a.Hv + h) * size);
+  if (save) put_state(r.save + ((slot + 1) * a.Hv + h) * size);
 }
 
 template <typename T, int KI, int NT, int MODE, bool VEC>

@@ -62,7 +62,8 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
       }
   };
   const int64_t slot = lin_slot(a, sp, b, 0);
-  if (a.ckpt != nullptr) store(a.ckpt + (slot * a.Hv + h) * size);
+  const bool save = a.ckpt != nullptr && sp.len > 0;
+  if (save) store(a.ckpt + (slot * a.Hv + h) * size);
   for (int t = 0; t < sp.len; ++t) {
     const int64_t row = sp.first + t;
     const T* const Q = static_cast<const T*>(a.q) + row * a.q_stride + (int64_t)(h / reps) * a.Dk;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
           st(static_cast<T*>(a.y), (row * a.Hv + h) * a.Dv + o0 + j, a.scale * x[j]);
   }
   if (a.S_T != nullptr) store(a.S_T + whole);
-  if (a.ckpt != nullptr) store(a.ckpt + ((slot + 1) * a.Hv + h) * size);
+  if (save) store(a.ckpt + ((slot + 1) * a.Hv + h) * size);
 }
 
 // The states around the segments from their own ends, in place: forward slot
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int rever
 #pragma unroll
     for (int v = 0; v < V; ++v) S[v] = fmaf(g, S[v], x[v]);
   }
-  if (!reverse) store_pack(p + n * step, S);
+  if (!reverse && n > 0) store_pack(p + n * step, S);
   float* const last = reverse ? a.dS0 : a.S_T;
   if (last != nullptr) store_pack(last + whole, S);
 }

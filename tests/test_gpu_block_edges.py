@@ -7,6 +7,7 @@ import pytest
 
 import oracle.block_oracle as K
 import oracle.layer_oracle as L
+from tests.test_gpu_block_ops import lin_case
 from tests.test_gpu_layer_ops import check, dev_of, dev_spans, round_to, same, seqs_of
 
 pytestmark = pytest.mark.gpu
@@ -485,3 +486,14 @@ def test_block_together(cuda):
             served.append(p)
     err = O.rel_l2(torch.cat(served, 1).double().cpu().numpy().reshape(outr.shape), outr)
     assert err <= 1e-4, err
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("spans,rows", (
+    ([(0, 1200), (0, 0), (500, 500), (1203, 1290), (1300, 1300), (7, 7)], 1300),  # cut and joined
+    ([(0, 0), (2, 50), (50, 50), (0, 0), (60, 120), (0, 0)], 120),                # one piece each
+    ([(9, 9), (0, 6), (0, 0), (6, 7), (10, 10), (7, 10), (3, 3)], 10)))           # step by step
+def test_empty_sequences_anywhere(cuda, dtype, spans, rows):
+    """Sequences of no rows whose spans point into others' rows: they keep
+    their states and leave what the others save alone."""
+    lin_case(cuda, dtype, len(spans), 0, 1, 2, 64, 64, spans=spans, rows=rows, rate=0.02)
