@@ -31,8 +31,9 @@ constexpr int kStepRows = 4;  // of the state, of a group of lanes
 // A step at a time.  LANES lanes own kStepRows rows of the state, each lane
 // NV vectors of V neighbouring columns of every row, so that a row is read and
 // written in whole cache lines.  Bound by the states, read and written once: 48
-// requests of 32 heads of 128 x 128 (201 MB) take 35 us, 5.7 TB/s.  (Lanes that
-// own every 64th column, one element at a time: 54.)
+// requests of 32 heads of 128 x 128 (203 MB) take 34 us, 5.9 TB/s, over the same
+// states again, 43 over others in turn (4.7).  (Lanes that own every 64th column,
+// one element at a time: 54 and 61.)
 template <typename T, int LANES, int NV, int V>
 __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -107,7 +108,11 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
 
 // The states around the segments from their own ends, in place: forward slot
 // s + 1 holds segment s's end, backward slot s holds segment s's adjoint at its
-// begin and receives the one behind it.
+// begin and receives the one behind it.  Bound by the states' bytes, read and
+// written: 2048 steps of 64 heads of 128 x 192 in 4 segments 11 us, 4.5 TB/s.
+// (Each main pass joining what lies before its segment instead: no states
+// between and no launch, but up to 64 loads a lane and segment where registers
+// are short: training 494 us against 446, seven prompts 207 against 174.)
 template <int V>
 __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int reverse) {
   const int h = blockIdx.y, b = blockIdx.z;
@@ -146,6 +151,10 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int rever
 }
 
 // Sums of the fp32 parts over a key head's value heads, V columns a thread.
+// Bound by the parts' bytes: 2048 rows of 64 x 192, twice (226 MB with the sums),
+// 50 us, 4.5 TB/s.  (Heads of one key head in a workgroup, which would add them up
+// in LDS: training 482 us against 451, shared by 64 heads 380 to 500 against 394,
+// as too few workgroups are left.)
 template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void lin_heads_sum(LinArgs a) {
   const int reps = a.Hv / a.Hk, b = blockIdx.y;
@@ -475,7 +484,8 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
 // 128 columns a workgroup, which form P once for them, where the state leaves
 // registers for two workgroups a compute unit (up to 128 contracted columns);
 // 64 where it does not, and where 128 would leave a quarter of them empty.
-// Training of 2048 steps, heads 16/64 of 192/128: 514 us; 128 columns for all
+// Measured when this was chosen (each pass has got 4 to 13% faster since):
+// training of 2048 steps, heads 16/64 of 192/128: 514 us; 128 columns for all
 // widths 646, 64 only where 192 are contracted 520.  4 x 4096 steps of 32 heads
 // of 128/128: 757 us, with 64 columns 903.
 int lin_width(int64_t Ni, int64_t No) {
@@ -486,7 +496,9 @@ int lin_tiles(int64_t Ni, int64_t No) {
   return (int)((No + w - 1) / w);
 }
 
-// Segments for 512 workgroups, two a compute unit, of 128 steps at least.
+// Segments for 512 workgroups, two a compute unit, of 128 steps at least.  (256,
+// 384, 768, 1024 and 1536 workgroups were all slower: fewer leave SIMDs with one
+// wave, more repeat the state pass and wait for a second round.)
 LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv) {
   LinPlan p{};
   const int64_t per = Hv * lin_tiles(Dk, Dv);  // workgroups of one cut through all rows
