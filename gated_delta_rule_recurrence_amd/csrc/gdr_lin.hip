@@ -499,13 +499,42 @@ int lin_tiles(int64_t Ni, int64_t No) {
 // Segments for 512 workgroups, two a compute unit, of 128 steps at least.  (256,
 // 384, 768, 1024 and 1536 workgroups were all slower: fewer leave SIMDs with one
 // wave, more repeat the state pass and wait for a second round.)
+//
+// Each sequence has a last segment that is cut off (of packed rows, half of one
+// on average), so that a cut of all rows into 512 may leave a second round.  Where
+// it does, that one of three cuts is taken whose steps are the fewest by this
+// count: a round of workgroups takes its segment's steps and kLinEach more; more
+// workgroups than one round take their share of all steps and half a segment;
+// what is cut is walked again without outputs (0.45 of a pass) and joined (as 128
+// steps).  Seven prompts in 6000 rows, 32 heads of 128/128: 512 steps 146 us, 384
+// (by rows alone) 172; 20 of them: not cut 105, 384 steps 204; 24 sequences in
+// 16384 rows, 16 heads, training: not cut 685, 512 steps (by rows alone) 790, 832
+// (one round) 980.
+constexpr double kLinEach = 96.0;
 LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv) {
   LinPlan p{};
   const int64_t per = Hv * lin_tiles(Dk, Dv);  // workgroups of one cut through all rows
   const int64_t want = (512 + per - 1) / per;
-  int64_t seg = (rows + want - 1) / want;
-  seg = (seg + 63) / 64 * 64;
-  if (seg < 128) seg = 128;
+  auto cut = [](int64_t steps, int64_t n) {
+    const int64_t seg = ((steps + n - 1) / n + 63) / 64 * 64;
+    return seg < 128 ? 128 : seg;
+  };
+  const bool dense = rows >= B * T;
+  auto pieces = [&](int64_t seg) {
+    return dense ? (double)(B * ((T + seg - 1) / seg)) : (double)rows / (double)seg + 0.5 * (double)B;
+  };
+  int64_t seg = cut(rows, want);
+  if (T > seg && pieces(seg) > (double)want) {
+    auto steps = [&](int64_t segment, double n) {
+      const double x = (double)segment + kLinEach;
+      return n <= (double)want ? x : ((double)rows + kLinEach * n) / (double)want + 0.5 * x;
+    };
+    auto split = [&](int64_t segment) { return 1.45 * steps(segment, pieces(segment)) + 128.0; };
+    const int64_t one = dense ? cut(T, want > B ? want / B : 1)
+                              : want > B / 2 ? cut(rows, want - B / 2) : seg;
+    if (split(one) < split(seg)) seg = one;
+    if (steps(T, (double)B) < split(seg)) seg = T;
+  }
   if (T <= seg) seg = rows < T ? (T < 1 ? 1 : T) : (rows < 1 ? 1 : rows);  // one
   p.seg = seg;
   p.segs = T > seg ? (T + seg - 1) / seg : 1;
