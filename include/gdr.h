@@ -385,10 +385,10 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
  * the state; positive ones are taken as they are.
  * 1 <= Dk, Dv <= GDR_LIN_MAX_DIM, Hv a multiple of Hk and at most 65535, B at
  * most 65535, T and rows at most 2^30 - 1, strides (and Hv Dk, Hv Dv) at most
- * 2^23.  A value that is not finite in a row
- * makes the outputs of its sequence that the formula reaches from it not
- * finite, and may do so to those of up to 63 earlier rows of that sequence
- * (later ones, for the gradients), which are computed with it in one tile. */
+ * 2^23.  A value that is not finite makes the outputs that the formula reaches
+ * from it not finite (an infinity may come out as NaN), and no others, but for
+ * dlog_g, which is summed from a sequence's end: it may be NaN at all steps of
+ * that sequence and head. */
 #define GDR_LIN_MAX_DIM 256
 typedef struct {
   int64_t B, T, rows, Hk, Hv, Dk, Dv;

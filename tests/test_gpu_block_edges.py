@@ -497,3 +497,49 @@ def test_empty_sequences_anywhere(cuda, dtype, spans, rows):
     """Sequences of no rows whose spans point into others' rows: they keep
     their states and leave what the others save alone."""
     lin_case(cuda, dtype, len(spans), 0, 1, 2, 64, 64, spans=spans, rows=rows, rate=0.02)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("T", (100, 300))
+@pytest.mark.parametrize("what", (float("nan"), float("inf"), float("-inf")))
+def test_not_finite_rows(cuda, dtype, T, what):
+    """A value that is not finite reaches the outputs that depend on it, and no
+    other: not the earlier steps of its tile, its neighbouring columns or other
+    heads; the gradients likewise."""
+    import torch
+    s = small_state(cuda, dtype, T=T)
+    q, k, v, lg, S0 = s["lin"]
+    at, h, c = 70, 1, 5
+    run = lambda *a: ops().gdr_lin_forward(*a, S0, scale=0.5)
+    y, S, saved = run(q, k, v, lg)
+    grads = ops().gdr_lin_backward(q, k, v, lg, saved, s["dy"], s["dS"])
+
+    def poison(t, head):
+        t = t.clone()
+        t[0, at, head, c] = what
+        return t
+
+    y2, S2, _ = run(q, k, poison(v, h), lg)  # one column of one value head
+    reached = torch.zeros_like(y, dtype=torch.bool)
+    reached[0, at:, h, c] = True
+    assert torch.equal(y2[~reached], y[~reached]) and not torch.isfinite(y2[reached]).any()
+    reached = torch.zeros_like(S, dtype=torch.bool)
+    reached[0, h, c] = True
+    assert torch.equal(S2[~reached], S[~reached]) and not torch.isfinite(S2[reached]).any()
+    y2, S2, _ = run(q, poison(k, 0), v, lg)  # key head 0: value heads 0 and 1
+    assert torch.equal(y2[0, :at], y[0, :at]) and torch.equal(y2[:, :, 2:], y[:, :, 2:]) and torch.equal(y2[1], y[1])
+    assert not torch.isfinite(y2[0, at:, :2]).any()
+    y2, S2, _ = run(poison(q, 0), k, v, lg)
+    reached = torch.zeros_like(y, dtype=torch.bool)
+    reached[0, at, :2] = True
+    assert torch.equal(y2[~reached], y[~reached]) and torch.equal(S2, S) and not torch.isfinite(y2[reached]).any()
+    # dy: dq of its row, dk and dv of its own and earlier ones
+    dq, dk, dv, _, dS0 = ops().gdr_lin_backward(q, k, v, lg, saved, poison(s["dy"], h), s["dS"])
+    for got, want, rows, heads in ((dq, grads[0], slice(at, at + 1), slice(0, 1)), (dk, grads[1], slice(0, at + 1), slice(0, 1)),
+                                   (dv, grads[2], slice(0, at + 1), slice(h, h + 1))):
+        reached = torch.zeros_like(got, dtype=torch.bool)
+        reached[0, rows, heads, c if got is dv else slice(None)] = True
+        assert torch.equal(got[~reached], want[~reached]) and not torch.isfinite(got[reached]).any()
+    reached = torch.zeros_like(dS0, dtype=torch.bool)
+    reached[0, h, c] = True
+    assert torch.equal(dS0[~reached], grads[4][~reached]) and not torch.isfinite(dS0[reached]).any()
