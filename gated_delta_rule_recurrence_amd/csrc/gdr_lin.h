@@ -32,7 +32,7 @@
 // What bounds it: the dependent phases of a tile (P, S Q, P's decays, P V and the
 // update, with three barriers) at the two waves a SIMD that the state leaves
 // registers for.  4 x 4096 steps of 32 heads of 128/128: states alone 85 us,
-// y 160, dq with dk and dv 434; there the vector units are 34, 39 and 45% busy,
+// y 155 to 174, dq with dk and dv 430 to 490; there the vector units are 34, 39 and 45% busy,
 // matrix cores 23, 24 and 27, LDS 14, 20 and 23, HBM at 3.2 to 3.5 TB/s.  Eight
 // waves of 16 columns have more to switch between and 47% more vector
 // instructions, as each forms the same operands: 812 us a pass against 722.
@@ -382,7 +382,9 @@ struct LinStage {
 };
 
 // Waves of a SIMD (workgroups of a compute unit) that the registers are cut to,
-// no more than LDS holds.
+// no more than LDS holds.  (Three where some registers are spilled for it, too:
+// training of 2048 steps, heads 16/64 of 192/128, 465 us, with two for its dq and
+// dk and no spills 485.)
 template <typename T>
 constexpr int lin_waves(int KI, int NT) {
   if (sizeof(T) == 4) return KI <= 64 && NT == 1 ? 3 : KI <= 128 ? 2 : 1;
