@@ -23,12 +23,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sums of two values over the LANES lanes of a row, the same bits in every
-// lane.  Calls that follow each other get buffers of their own in turn, so that
-// one barrier does for each: what a wave still reads is written again only
-// behind the next call's.
+// Waves of a row.
 template <int LANES>
-__device__ __forceinline__ void row_sums(float& x, float& y, float (*red)[2]) {
+constexpr int kRowWaves = LANES > 64 ? LANES / 64 : 1;
+
+// Sums of two values over the LANES lanes of a row, the same bits in every
+// lane.  Every call of a kernel takes the other of two buffers than the call
+// before it, which `turn` counts (a row may make a single call, always from the
+// same place), so one barrier does for each: a wave that writes a buffer again
+// has passed the barrier of the call between, behind every wave's reads of it.
+template <int LANES>
+__device__ __forceinline__ void row_sums(float& x, float& y,
+                                         float (*buffers)[kRowWaves<LANES>][2], int& turn) {
   x = rowsum16(x);
   y = rowsum16(y);
   x = swap16_sum(x, x);
@@ -36,6 +42,8 @@ __device__ __forceinline__ void row_sums(float& x, float& y, float (*red)[2]) {
   x = swap32_sum(x, x);
   y = swap32_sum(y, y);
   if constexpr (LANES > 64) {
+    float (*const red)[2] = buffers[turn];
+    turn ^= 1;
     if ((threadIdx.x & 63) == 0) {
       red[threadIdx.x >> 6][0] = x;
       red[threadIdx.x >> 6][1] = y;
@@ -158,10 +166,11 @@ template <typename T, typename R, int LANES, int NV, int V>
 __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_fwd_kernel(ResArgs a,
                                                                                ResPlan p) {
   using P = Res<LANES>;
-  __shared__ float red[4][LANES > 64 ? LANES / 64 : 1][2];
+  __shared__ float red[2][kRowWaves<LANES>][2];
   const int lane = threadIdx.x % LANES, wave = LANES > 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Walk k = walk_of(a, p);
   const float inv = 1.f / (float)a.C;
+  int turn = 0;  // of row_sums
   Raw<T, V> xn[NV];  // the next row
   Raw<R, V> rn[NV];
   RawGate<V> gn[NV];
@@ -217,7 +226,7 @@ __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_fwd_kernel(ResArgs a
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) s += x[i][v];
-        row_sums<LANES>(s, zero, red[0]);
+        row_sums<LANES>(s, zero, red, turn);
         mu1 = s * inv;
       }
       s = 0.f;
@@ -228,7 +237,7 @@ __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_fwd_kernel(ResArgs a
           x[i][v] = (i * LANES + lane) * V < a.C ? x[i][v] - mu1 : 0.f;
           s = fmaf(x[i][v], x[i][v], s);
         }
-      row_sums<LANES>(s, zero, red[1]);
+      row_sums<LANES>(s, zero, red, turn);
       r1 = 1.f / sqrtf(fmaf(s, inv, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -249,7 +258,7 @@ __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_fwd_kernel(ResArgs a
     }
     if (a.pre) {
       if (a.center) {
-        row_sums<LANES>(s, zero, red[2]);
+        row_sums<LANES>(s, zero, red, turn);
         mu = s * inv;
       }
       s = 0.f;
@@ -260,7 +269,7 @@ __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_fwd_kernel(ResArgs a
           h[i][v] = (i * LANES + lane) * V < a.C ? h[i][v] - mu : 0.f;
           s = fmaf(h[i][v], h[i][v], s);
         }
-      row_sums<LANES>(s, zero, red[3]);
+      row_sums<LANES>(s, zero, red, turn);
       r2 = 1.f / sqrtf(fmaf(s, inv, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -280,11 +289,12 @@ template <typename T, typename R, int LANES, int NV, int V>
 __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_bwd_kernel(ResArgs a,
                                                                                ResPlan p) {
   using P = Res<LANES>;
-  __shared__ float red[2][LANES > 64 ? LANES / 64 : 1][2];
+  __shared__ float red[2][kRowWaves<LANES>][2];
   __shared__ float sum[LANES > 64 ? 1 : kThreads / 64][64];
   const int lane = threadIdx.x % LANES, wave = LANES > 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Walk k = walk_of(a, p);
   const float inv = 1.f / (float)a.C;
+  int turn = 0;  // of row_sums
   const bool row_gate = a.gate != nullptr && a.gate_rows == 1;
   float pw[NV][V], pb[NV][V], w[NV][V], gate[NV][V];
   float dpw[NV][V], dpb[NV][V], dw[NV][V], db[NV][V], dg[NV][V];
@@ -384,7 +394,7 @@ __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_bwd_kernel(ResArgs a
             se += dy[i][v];
             sx = fmaf(dy[i][v], h[i][v], sx);
           }
-        row_sums<LANES>(se, sx, red[0]);
+        row_sums<LANES>(se, sx, red, turn);
         se = a.center ? se * inv : 0.f;
         sx *= inv;
 #pragma unroll
@@ -421,7 +431,7 @@ __global__ __launch_bounds__((Res<LANES>::kBlock)) void res_bwd_kernel(ResArgs a
         }
       }
       if (a.post) {
-        row_sums<LANES>(se, sx, red[1]);
+        row_sums<LANES>(se, sx, red, turn);
         se = a.center ? se * inv : 0.f;
         sx *= inv;
 #pragma unroll
