@@ -12,12 +12,13 @@
 // -inf forgets without a difference of infinities.
 //
 // Precision.  bf16 rows are matrix operands as they are; what is fp32 (P, S,
-// uf V) is held in bf16 pieces.  Three hold fp32's 24 bits: for whatever
-// becomes an fp32 output, that is the states that are handed on, and the flows
-// of the decay's gradient.  Outputs in bf16 take two, x = hi + lo within 2^-18,
-// far below their own rounding of 2^-9 (one piece would add another one).
-// fp32 rows are three pieces too; of the nine products the six above 2^-24 are
-// formed.
+// uf V) enters a product in three bf16 pieces, which hold fp32's 24 bits.  (Two
+// hold 18: enough for a bf16 output by itself, but not where large terms cancel
+// in it.  Seven prompts 154 us with two and 163 with three, training of 2048
+// steps, heads 16/64 of 192/128, 475 and 495, 4 x 4096 steps of 32 heads of
+// 128/128 762 and 846; the bf16 outputs' difference to a plain fp32 form 1.0e-4
+// and 0.4e-4.)  fp32 rows are three pieces too; of the nine products the six
+// above 2^-24 are formed (with the next two the errors are the same).
 //
 // Mapping.  A workgroup of four waves runs through a segment of one sequence
 // for one head and NT 64 columns of its output.  P is formed by all waves, in
@@ -60,7 +61,6 @@ struct LinRole {
   int reverse;         // time runs backwards
   int transposed;      // states lie [Ni][No] instead of [No][Ni]
   int vec;             // widths and strides are whole vectors (VEC)
-  int exact;           // the states are an output (see above)
   const float* first;  // states before each segment, or null (zeros)
   int slots;           // they lie in segments' slots, not [B][Hv]
   float* last;         // [B][Hv] states behind the sequences (one segment), or null
@@ -98,9 +98,7 @@ template <>
 struct LinTypes<float> {
   static constexpr int L = 32, NP = 3;
 };
-// Pieces of an fp32 operand.
-template <typename T, int MODE>
-constexpr int kLinPieces = sizeof(T) == 2 && MODE == kLinOut ? 2 : 3;
+constexpr int kLinPieces = 3;  // of an fp32 operand
 
 // A tile [rows][W] of bf16 in LDS whose 16-byte blocks are exchanged inside a
 // row, block ^ lin_swz(row).  The 64 banks hold 16 blocks; what reads them at
@@ -162,24 +160,13 @@ __device__ __forceinline__ f4 lin_unpack(uint2 w) {
             __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
 }
 
-// NS bf16 pieces of eight values, as operands.
-template <int NS>
-__device__ __forceinline__ void lin_split(f4 a, f4 b, uint4 (&p)[NS]) {
+// The bf16 pieces of eight values, as operands.
+__device__ __forceinline__ void lin_split(f4 a, f4 b, uint4 (&p)[kLinPieces]) {
   uint2 x[3], y[3];
-  if constexpr (NS == 3) {
-    split3_quad(a, x[0], x[1], x[2]);
-    split3_quad(b, y[0], y[1], y[2]);
-  } else {
-    x[0] = uint2{cvt_pk_bf16(a[0], a[1]), cvt_pk_bf16(a[2], a[3])};
-    y[0] = uint2{cvt_pk_bf16(b[0], b[1]), cvt_pk_bf16(b[2], b[3])};
-    // (v_dot2 would form x - hi at once, but needs a move for its sum or wait
-    // states behind it)
-    const f4 ra = a - lin_unpack(x[0]), rb = b - lin_unpack(y[0]);
-    x[1] = uint2{cvt_pk_bf16(ra[0], ra[1]), cvt_pk_bf16(ra[2], ra[3])};
-    y[1] = uint2{cvt_pk_bf16(rb[0], rb[1]), cvt_pk_bf16(rb[2], rb[3])};
-  }
+  split3_quad(a, x[0], x[1], x[2]);
+  split3_quad(b, y[0], y[1], y[2]);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) p[i] = uint4{x[i].x, x[i].y, y[i].x, y[i].y};
+  for (int i = 0; i < kLinPieces; ++i) p[i] = uint4{x[i].x, x[i].y, y[i].x, y[i].y};
 }
 
 // c + a b over the pieces' products that fp32 sees.
@@ -246,7 +233,7 @@ struct LinRaw<float> {
         a[i] = finite(a[i]) ? a[i] : 0.f;
         b[i] = finite(b[i]) ? b[i] : 0.f;
       }
-    lin_split<3>(a, b, p);
+    lin_split(a, b, p);
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(t[i] + at) = p[i];
     if (odd) {  // (the split would spoil a neighbour)
@@ -400,7 +387,7 @@ __device__ __forceinline__ float lin_sum(const float (&red)[kLinWaves][L], int x
 // been read by then.
 template <typename T, int KI, int WO, int MODE>
 struct LinTiles {
-  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = kLinPieces<T, MODE>;
+  static constexpr int L = LinTypes<T>::L, NP = LinTypes<T>::NP, NS = kLinPieces;
   static constexpr int kQ = 0, kP = 0;
   static constexpr int kQP = NP * L * KI > NS * L * L ? NP * L * KI : NS * L * L;
   static constexpr int kK = MODE == kLinState ? 0 : kQP;
@@ -636,7 +623,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       for (int s = 0; s < KS; ++s) {
         uint4 sa[NT][NS];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) lin_split<NS>(S[2 * s][nt], S[2 * s + 1][nt], sa[nt]);
+        for (int nt = 0; nt < NT; ++nt) lin_split(S[2 * s][nt], S[2 * s + 1][nt], sa[nt]);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
           uint4 qb[NP];
@@ -666,7 +653,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
               __float_as_uint(x * exp2_hw((Hi.x - hi[v]) + (Hi.y - lo[v]))) & ~(below >> 31));
         }
         uint4 pieces[NS];
-        lin_split<NS>(p[k], f4{0.f, 0.f, 0.f, 0.f}, pieces);
+        lin_split(p[k], f4{0.f, 0.f, 0.f, 0.f}, pieces);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
           *reinterpret_cast<uint2*>(Pt[n] + 16 * L * pi[k] + lin_move<L>(pput, 16 * pj[k])) =
@@ -710,7 +697,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int k = 0; k < L / 32; ++k) {
-      uint4 vo[NT][NP], vu[NT][3];
+      uint4 vo[NT][NP], vu[NT][NS];
       const f4 u0 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q);
       const f4 u1 = *reinterpret_cast<const f4*>(uf + 32 * k + 8 * q + 4);
 #pragma unroll
@@ -723,14 +710,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
           x = i == NP - 1 ? wx : x + wx;
           y = i == NP - 1 ? wy : y + wy;
         }
-        if (NS == 3 || r.exact) {
-          lin_split<3>(x * u0, y * u1, vu[nt]);
-        } else {
-          uint4 two[2];
-          lin_split<2>(x * u0, y * u1, two);
-          vu[nt][0] = two[0];
-          vu[nt][1] = two[1];
-        }
+        lin_split(x * u0, y * u1, vu[nt]);
       }
       if constexpr (OUT) {
 #pragma unroll
@@ -749,15 +729,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         for (int i = 0; i < NP; ++i)
           ka[i] = lin_columns<KI>(Kt[i], kcols, 32 * k, 32 * (s >> 1) + 4 * (s & 1));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (NS == 3) {
-            S[s][nt] = lin_mfma(ka, vu[nt], S[s][nt]);
-          } else {
-            if (r.exact) S[s][nt] = mfma_bf16(ka[0], vu[nt][2], S[s][nt]);
-            S[s][nt] = mfma_bf16(ka[0], vu[nt][1], S[s][nt]);
-            S[s][nt] = mfma_bf16(ka[0], vu[nt][0], S[s][nt]);
-          }
-        }
+        for (int nt = 0; nt < NT; ++nt) S[s][nt] = lin_mfma(ka, vu[nt], S[s][nt]);
       }
     }
     __builtin_amdgcn_s_setprio(0);

@@ -359,7 +359,6 @@ hipError_t fwd(const LinArgs& a, hipStream_t s) {
     r.first = a.S0;
     r.last = a.S_T;
     r.save = a.ckpt;
-    r.exact = a.S_T != nullptr || a.ckpt != nullptr;
     return chunked<T>(a, r, kLinOut, s);
   }
   r.local = a.states;
@@ -434,7 +433,6 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
     v.first = a.dS_T;
     v.slots = 0;
     v.last = a.dS0;
-    v.exact = a.dS0 != nullptr;
   }
   // dk: (v, dy, q)
   d.Q = a.v;
