@@ -145,7 +145,7 @@ struct LinArgs {
   int seg;               // steps, a multiple of 64 (or at least T)
   int segs;
   float* states;         // [slots][Hv][Dv][Dk]: ckpt, or the forward's own; backward: adjoints
-  float* decay;          // [slots][Hv]
+  double* decay;         // [slots][Hv] their summed log decays
   // backward
   const void* dy;
   const float* dS_T;     // or null

@@ -492,7 +492,7 @@ int lin_sizes(const gdr_lin_shape& s, LinSizes* z) {
     return GDR_ERR_OVERFLOW;
   z->ckpt = states;
   const int64_t split = z->plan.segs > 1 ? round_up256(states) : 0;
-  const int64_t decays = z->plan.segs > 1 ? round_up256(z->plan.slots * s.Hv * 4) : 0;
+  const int64_t decays = z->plan.segs > 1 ? round_up256(z->plan.slots * s.Hv * 8) : 0;
   z->fwd_decay = z->bwd_decay = split;
   z->fwd = z->dq = split + decays;
   z->dk = z->flow = z->dq;
@@ -562,7 +562,7 @@ int lin_forward(const gdr_lin_shape* shape, const void* q, const void* k, const 
   a.seg = (int)z.plan.seg;
   a.segs = has_rows ? (int)z.plan.segs : 1;
   a.states = ckpt != nullptr ? a.ckpt : static_cast<float*>(workspace);
-  a.decay = reinterpret_cast<float*>(static_cast<char*>(workspace) + z.fwd_decay);
+  a.decay = reinterpret_cast<double*>(static_cast<char*>(workspace) + z.fwd_decay);
   return hip_status(gdr::launch_lin_fwd(a, s.dtype == GDR_BF16, static_cast<hipStream_t>(stream)));
 }
 
@@ -604,7 +604,7 @@ int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const
   a.seg = (int)z.plan.seg;
   a.segs = has_rows ? (int)z.plan.segs : 1;
   a.states = reinterpret_cast<float*>(w);
-  a.decay = reinterpret_cast<float*>(w + z.bwd_decay);
+  a.decay = reinterpret_cast<double*>(w + z.bwd_decay);
   if (s.Hv > s.Hk) {
     a.dq_part = reinterpret_cast<float*>(w + z.dq);
     a.dk_part = reinterpret_cast<float*>(w + z.dk);

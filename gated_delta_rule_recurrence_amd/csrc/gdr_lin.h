@@ -8,8 +8,16 @@
 //   S <- exp(total) S + sum_j uf_j V_j K_j^T,     uf_j = exp(total - H_j)
 // H is summed and subtracted in 64 bits: a difference of two of them keeps the
 // accuracy of the few steps between, however much the tile has decayed.  A log
-// decay below kLeastLog (of which exp is 0 in fp32) counts as that, so that
-// -inf forgets without a difference of infinities.
+// decay below kLeastLog counts as that, so that -inf forgets without a
+// difference of infinities; a segment that holds one keeps nothing of its state.
+//
+// Decays that grow.  Where the positive ones of a tile sum to more than kGrows,
+// factors that the recurrence never forms alone (exp(H_i), P_ij) could pass
+// fp32's range while what they multiply is small or 0.  Such a tile is walked in
+// passes, each over the rows [x0, x1) that grow by no more (lin_pass); a step
+// that grows by more alone is a pass of the state only, or several.  (What the
+// other tiles pay for it: 0 to 1% of a pass, shared keys 409 -> 420 us, the small
+// fp32 one 86 -> 91.)
 //
 // Precision.  bf16 rows are matrix operands as they are; what is fp32 (P, S,
 // uf V) enters a product in three bf16 pieces, which hold fp32's 24 bits.  (Two
@@ -44,7 +52,9 @@
 namespace gdr {
 
 constexpr int kLinWaves = 4;  // waves of a workgroup
-constexpr double kLeastLog = -200.0;
+// (what a kLeastLog leaves is 0 after a pass's growth, any value but 0 that grows
+// by kMostLog is past fp32's range)
+constexpr double kLeastLog = -1000.0, kMostLog = 200.0, kGrows = 40.0;
 // An offset past the end of every buffer (64 rows of at most 2^23 elements).
 constexpr uint32_t kLinPast = 0xf0000000u;
 
@@ -66,7 +76,7 @@ struct LinRole {
   float* last;         // [B][Hv] states behind the sequences (one segment), or null
   float* save;         // slots of the state before and behind (one segment), or null
   float* local;        // states only: slots of the segments' own ends
-  float* decay;        // states only: [slots][Hv] exp(total) of the segments
+  double* decay;       // states only: [slots][Hv] summed log decays of the segments
   void* out;           // [rows][Hv][No], or null
   float* part;         // the same in fp32
   float* flow;         // [tiles][Hv][rows]: R out, without the step's own term
@@ -322,6 +332,49 @@ __device__ __forceinline__ double lin_prefix_sum(double x) {
 }
 
 __device__ __forceinline__ float lin_exp(double x) { return exp2_hw(kLog2e * (float)x); }
+// s exp(x) where exp(x) may be past fp32's range: 0 stays 0.
+__device__ __forceinline__ float lin_grow(float s, double x) {
+  const double y = fmin(x * 1.4426950408889634, 1e6);
+  const int n = (int)(y - 100.0);
+  return ldexpf(s * exp2_hw((float)(y - n)), n);
+}
+
+// Where a tile of growing decays is.  Rows behind x1 wait for another pass, and
+// the state still has to grow by `debt` before it (`paid`: it has grown by row
+// x0's decay).
+struct LinPass {
+  float debt;
+  int x0, paid;
+};
+constexpr uint32_t lin_part(int x0, int x1, bool done) { return x0 | x1 << 8 | done << 16; }
+// The next pass over a tile's log decays x, one a lane of the first L: its part,
+// with x as it takes them (0 outside its rows, in lane 0 where the state alone
+// grows).  A big step, above kGrows, grows the state before its row's pass, or
+// behind it in reverse.  `at` lies in LDS, the same for the whole wave.
+template <int L>
+__device__ __forceinline__ uint32_t lin_pass(double& x, LinPass& at, bool reverse) {
+  const int lane = threadIdx.x & 63, x0 = at.x0;
+  x = x > kMostLog ? (x < __builtin_inf() ? kMostLog : __builtin_nan("")) : x;
+  x = lane < x0 || (at.paid && lane == x0) ? 0.0 : x;
+  const uint64_t big = __ballot(x > kGrows);
+  const uint64_t stop = (reverse ? big << 1 : big) |
+                        __ballot(lin_prefix_sum(x > 0.0 && x <= kGrows ? x : 0.0) > kGrows);
+  float debt = at.debt;
+  int x1 = stop != 0 ? __builtin_ctzll(stop) : L;
+  x1 = debt > 0.f ? x0 : x1 < L ? x1 : L;
+  const int last = reverse ? x1 - 1 : x0;  // the row whose big step is met here
+  if (debt == 0.f && (big >> (last & 63) & 1)) debt = __shfl((float)x, last, 64);
+  x = lane >= x1 || x > kGrows ? 0.0 : x;
+  const bool grow = x1 == x0;  // the state alone
+  if (grow) {
+    const float by = fminf(debt, 2 * (float)kGrows);
+    debt -= by;
+    x = lane == 0 ? (double)by : 0.0;
+  }
+  const bool done = x1 == L && debt == 0.f;
+  at = LinPass{debt, done ? 0 : x1, grow && !reverse && debt == 0.f};
+  return lin_part(x0, x1, done);
+}
 
 // A tile [L][W] on its way through a thread's registers: 8 threads a row,
 // eight elements in each 64 columns, 8 kLinWaves rows at a time.
@@ -429,6 +482,8 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
   __shared__ __attribute__((aligned(16))) float2 Hs[L];  // in units of ln 2, hi + lo
   __shared__ __attribute__((aligned(16))) float cf[L], uf[L], pd[L];
   __shared__ float total_s, red[kLinWaves][L];
+  __shared__ uint32_t part_s;  // rows of a pass (lin_part)
+  __shared__ LinPass pass_s;
   __shared__ int odd_s[kLinWaves], odd_row[WO];
   const int wave = threadIdx.x >> 6;
   const int tile = at.each, sg = at.sg, h = at.h, b = at.b;
@@ -520,9 +575,10 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     fetch_k(0, threadIdx.x);
     fetch_v(0, threadIdx.x);
   }
-  double all = 0.0;  // the segment's summed log decays (first L threads)
+  double all = 0.0;  // the segment's summed log decays (first wave)
+  if (threadIdx.x == 0) pass_s = LinPass{0.f, 0, 0};
 
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = 0; c < chunks;) {
     // (opaque, so that addresses are formed where they are used and do not
     // fill the registers through the loop)
     int thread = threadIdx.x;
@@ -542,22 +598,30 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     if (threadIdx.x < 64) {
       double x = threadIdx.x < L ? (double)lg : 0.0;
       x = x < kLeastLog ? kLeastLog : x;  // (NaN stays)
+      uint32_t part = lin_part(0, L, true);
+      if (__builtin_expect(__any(x > 0.0), 0)) part = lin_pass<L>(x, pass_s, r.reverse);
+      if (threadIdx.x == 0) part_s = part;
       const double sum = lin_prefix_sum(x);
       const double end = __shfl(sum, 63, 64);
-      all += end;
+      if constexpr (!OUT) all += __any(x <= kLeastLog) ? end - __builtin_inf() : end;
+      const bool before = threadIdx.x < (part & 255), in = !before && threadIdx.x < (part >> 8 & 255);
       if (threadIdx.x < L) {
         const double H = r.reverse ? sum - x : sum;
         const double H2 = H * 1.4426950408889634;
         const float hi = (float)H2;
-        Hs[threadIdx.x] = float2{hi, (float)(H2 - (double)hi)};
+        // (rows before the pass reach nothing in it, those behind not the state)
+        Hs[threadIdx.x] = before ? float2{1e30f, 0.f} : float2{hi, (float)(H2 - (double)hi)};
         cf[threadIdx.x] = r.cs * lin_exp(H);
-        uf[threadIdx.x] = r.us * lin_exp(end - H);
+        uf[threadIdx.x] = in ? r.us * lin_exp(end - H) : 0.f;
         if (threadIdx.x == 0) total_s = lin_exp(end);
       }
     }
     lds_barrier();
     const int t0 = start(c);
-    const bool more = c + 1 < chunks;
+    const uint32_t part = __builtin_amdgcn_readfirstlane(part_s);
+    const int x0 = part & 255, x1 = part >> 8 & 255;
+    const int next = c + (int)(part >> 16);
+    const bool more = next < chunks;
     // What is not finite in V may reach its own row and later ones only, but a
     // matrix product multiplies it with the zeros of P above the diagonal too.
     // It is taken out, and each column's outputs from its first such row on,
@@ -581,7 +645,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       }
       lds_barrier();
     }
-    if (more) fetch_q(c + 1, thread);
+    if (more) fetch_q(next, thread);
 
     f4 acc[IT][NT];
     if constexpr (OUT) {
@@ -612,7 +676,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
           p[k] = lin_mfma(ka, qb, p[k]);
         }
       }
-      if (more) fetch_k(c + 1, thread);
+      if (more) fetch_k(next, thread);
       // out <- S Q, scaled by cf
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -667,9 +731,9 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       }
       lds_barrier();  // P is whole
     } else {
-      if (more) fetch_k(c + 1, thread);
+      if (more) fetch_k(next, thread);
     }
-    if (more) fetch_v(c + 1, thread);
+    if (more) fetch_v(next, thread);
     // the rows that the flows multiply with, in time for the end of the tile
     const int n = count(t0), lane_row = r.reverse ? 15 - lr : lr, o = wo + 4 * q;
     const int64_t row = sp.first + begin + t0;
@@ -738,7 +802,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int col = 16 * NT * wave + 16 * nt;
-        if (odd_row[col + lr] < L)
+        if (odd_row[col + lr] < x1)
 #pragma unroll
           for (int s = 0; s < 2 * KS; ++s) S[s][nt] = f4{nan, nan, nan, nan};
         if constexpr (OUT) {
@@ -793,10 +857,10 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
         for (int it = 0; it < IT; ++it)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int t = r.reverse ? L - 16 - 16 * it : 16 * it;
+            const int t = r.reverse ? L - 16 - 16 * it : 16 * it, x = 16 * it + lr;
             lin_put<VEC, O>(out, (uint32_t)(lane_row * wide + o) * sizeof(O),
                             (uint32_t)(t * wide + 16 * nt) * sizeof(O), acc[it][nt],
-                            r.No - o - 16 * nt);
+                            x >= x0 && x < x1 ? r.No - o - 16 * nt : 0);
           }
       };
       if (r.out != nullptr)
@@ -806,14 +870,15 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       if constexpr (FLOW) {
         lds_barrier();
         const int x = thread, t = r.reverse ? L - 1 - x : x;
-        if (x < L && t < n)
+        if (x >= x0 && x < x1 && t < n)
           r.flow[((int64_t)tile * a.Hv + h) * a.rows + row + t] = lin_sum<L>(red, x);
       }
     }
+    c = next;
   }
   if constexpr (MODE == kLinState) {
     put_state(r.local + ((slot + (r.reverse ? 0 : 1)) * a.Hv + h) * size);
-    if (threadIdx.x == 0 && tile == 0) r.decay[slot * a.Hv + h] = lin_exp(all);
+    if (threadIdx.x == 0 && tile == 0) r.decay[slot * a.Hv + h] = all;
   }
   if (r.last != nullptr) put_state(r.last + ((int64_t)b * a.Hv + h) * size);
   if (save) put_state(r.save + ((slot + 1) * a.Hv + h) * size);

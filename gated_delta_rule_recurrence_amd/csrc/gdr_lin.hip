@@ -80,7 +80,24 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < kStepRows; ++j) v[j] = o0 + j < a.Dv ? to_f32(W[o0 + j]) : 0.f;
-    const float g = expf(lin_log_decay(a, row, h));
+    const float lg = lin_log_decay(a, row, h);
+    const float g = expf(lg);
+    if (lg > (float)kGrows) {  // (0 stays 0 where exp(lg) is past fp32's range)
+#pragma unroll
+      for (int j = 0; j < kStepRows; ++j)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            S[j][n][e] = lg < __builtin_inff() ? lin_grow(S[j][n][e], lg) : __builtin_nanf("");
+    } else {
+#pragma unroll
+      for (int j = 0; j < kStepRows; ++j)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int e = 0; e < V; ++e) S[j][n][e] *= g;
+    }
     float x[kStepRows];
 #pragma unroll
     for (int j = 0; j < kStepRows; ++j) {
@@ -89,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(LinArgs a) {
       for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          S[j][n][e] = fmaf(v[j], k[n][e], S[j][n][e] * g);
+          S[j][n][e] = fmaf(v[j], k[n][e], S[j][n][e]);
           x[j] = fmaf(S[j][n][e], q[n][e], x[j]);
         }
       x[j] = rowsum16(x[j]);
@@ -123,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int rever
   const int64_t slot = lin_slot(a, sp, b, 0);
   const int64_t whole = ((int64_t)b * a.Hv + h) * size + at, step = (int64_t)a.Hv * size;
   float* const p = a.states + (slot * a.Hv + h) * size + at;
-  const float* const d = a.decay + slot * a.Hv + h;
+  const double* const d = a.decay + slot * a.Hv + h;
   const float* const first = reverse ? a.dS_T : a.S0;
   float S[V];
 #pragma unroll
@@ -141,9 +158,11 @@ __global__ __launch_bounds__(kThreads) void lin_join_kernel(LinArgs a, int rever
     if (s + 1 < n) fetch(s + 1);
     const int m = reverse ? n - 1 - s : s;
     store_pack(p + m * step, S);
-    const float g = d[(int64_t)m * a.Hv];
+    const double log_g = d[(int64_t)m * a.Hv];
+    const float g = lin_exp(log_g);
 #pragma unroll
-    for (int v = 0; v < V; ++v) S[v] = fmaf(g, S[v], x[v]);
+    for (int v = 0; v < V; ++v)
+      S[v] = log_g > kGrows ? lin_grow(S[v], log_g) + x[v] : fmaf(g, S[v], x[v]);
   }
   if (!reverse && n > 0) store_pack(p + n * step, S);
   float* const last = reverse ? a.dS0 : a.S_T;

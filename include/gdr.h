@@ -382,7 +382,8 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
  *     S_t = exp(log_g_t[h]) S_{t-1} + outer(v_t[h], k_t);   y_t[h] = scale S_t q_t
  * (the gated delta rule without the delta rule's correction).  log_g is rows
  * [rows][Hv], or [Hv]: one decay per head (per_head).  A log_g of -inf forgets
- * the state; positive ones are taken as they are.
+ * the state for good; positive ones are taken as they are, and where exp(log_g)
+ * passes fp32's range, what was 0 stays 0.
  * 1 <= Dk, Dv <= GDR_LIN_MAX_DIM, Hv a multiple of Hk and at most 65535, B at
  * most 65535, T and rows at most 2^30 - 1, strides (and Hv Dk, Hv Dv) at most
  * 2^23.  A value that is not finite makes the outputs that the formula reaches

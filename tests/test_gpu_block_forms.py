@@ -212,3 +212,175 @@ def test_lin_outputs_do_not_depend_on_each_other(cuda, dtype, T):
     grads = ops().gdr_lin_backward(q, k, v, lg, saved, dy)
     some = ops().gdr_lin_backward(q, k, v, lg, saved, dy, want_dS0=False)
     assert all(torch.equal(a, b) for a, b in zip(grads[:4], some))
+
+
+# ---- linear attention: decays that grow, decays that forget --------------------------
+
+def lin_zero(d, names, rows):
+    for n in names:
+        d[n][rows] = 0.0
+
+
+def lin_grow_case(cuda, dtype, B, T, H, D, make, S0=None, dS_T=None, outs=("y", "S_T"), skip=0, rate=0.05, seed=0):
+    """One call on inputs that make(r, d, first row of a sequence) edits, against
+    64 bits wherever the result and its terms are far inside fp32's range.  The
+    first `skip` rows of dk and dv are left out: there the adjoint itself passes it."""
+    import torch
+    r = np.random.default_rng(seed)
+    rows = B * T
+    n = lambda *s: round_to(r.normal(size=s), dtype)
+    d = dict(q=n(rows, H, D), k=round_to(r.normal(size=(rows, H, D)) * D ** -0.5, dtype), v=n(rows, H, D), dy=n(rows, H, D),
+             log_g=-r.exponential(rate, size=(rows, H)))
+    for b in range(B):
+        make(r, d, b * T)
+    d["log_g"] = round_to(d["log_g"], "f32")
+    S0, dS_T = (None if f is None else round_to(f(r, (B, H, D, D)), "f32") for f in (S0, dS_T))
+    on = {m: dev_of(a, "f32" if m == "log_g" else dtype, cuda) for m, a in d.items()}
+    got = lin_run(on, dev_of(S0, "f32", cuda), dev_of(dS_T, "f32", cuda), T=T)
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref, mag = lin_ref(d, [(b * T, (b + 1) * T) for b in range(B)], S0, dS_T)
+    for name in outs:
+        a, m = ref[name], mag[name]
+        g = got[name].double().cpu().numpy().reshape(a.shape)
+        inside = m < 1e30
+        if name in ("dk", "dv"):
+            inside &= (np.arange(rows) % T >= skip)[:, None, None]
+        assert inside.mean() > 0.2, name
+        ty = "f32" if name in ("S_T", "dS0", "dlog_g") else dtype
+        check(name, torch.from_numpy(g[inside]), a[inside], m[inside], ty, (256 + 8 * T) * (2 if name == "dlog_g" else 1))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("B,T,H,D", ((2, 130, 2, 64), (1, 1100, 1, 48), (1, 200, 1, 192)))
+@pytest.mark.parametrize("steps,each", ((40, 3.0), (1, 100.0), (2, 700.0), (20, 30.0), (64, 2.0), (5, 80.0)))
+def test_lin_growth_of_an_empty_state(cuda, dtype, B, T, H, D, steps, each):
+    """Decays that grow past fp32's range before there is a state: it stays 0,
+    and what comes behind is as without them."""
+    def make(r, d, at):
+        d["log_g"][at:at + steps] = each
+        lin_zero(d, ("k", "v"), slice(at, at + steps - 1))  # (the last step writes)
+    lin_grow_case(cuda, dtype, B, T, H, D, make, outs=("y", "S_T", "dq", "dv", "dk"), skip=steps, seed=steps)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("B,T,H,D", ((2, 130, 2, 64), (1, 1100, 1, 48)))
+def test_lin_growth_of_an_empty_adjoint(cuda, dtype, B, T, H, D):
+    """The same at the sequence's end, where no gradient comes from."""
+    def make(r, d, at):
+        d["log_g"][at + T - 40:at + T] = 3.0
+        lin_zero(d, ("q", "dy"), slice(at + T - 40, at + T))
+    lin_grow_case(cuda, dtype, B, T, H, D, make, outs=("dk", "dv", "dS0"), S0=lambda r, s: r.normal(size=s), seed=1)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("B,T,H,D,steps", ((2, 130, 2, 64, 50), (1, 1100, 1, 48, 50), (1, 1100, 1, 48, 400), (1, 300, 1, 160, 50)))
+def test_lin_growth_of_a_small_state(cuda, dtype, B, T, H, D, steps):
+    """1e-24 grows by e^100, in one tile or over several segments."""
+    def make(r, d, at):
+        lin_zero(d, ("v",), slice(at, at + T))
+        d["log_g"][at + 3:at + 3 + steps] = 100.0 / steps
+    lin_grow_case(cuda, dtype, B, T, H, D, make, S0=lambda r, s: 1e-24 * r.normal(size=s), outs=("y", "S_T", "dq"), rate=0.0, seed=2)
+
+    def back(r, d, at):
+        lin_zero(d, ("dy",), slice(at, at + T))
+        d["log_g"][at + 3:at + 3 + steps] = 100.0 / steps
+    lin_grow_case(cuda, dtype, B, T, H, D, back, dS_T=lambda r, s: 1e-24 * r.normal(size=s), outs=("dk", "dv", "dS0"), rate=0.0, seed=3)
+
+    def steps_of(r, d, at):  # small steps, no state
+        d["v"][at:at + 3] *= 2.0 ** -80
+        d["v"][at + 3:at + T] = 0.0
+        d["log_g"][at + 3:at + 3 + steps] = 100.0 / steps
+    lin_grow_case(cuda, dtype, B, T, H, D, steps_of, outs=("y", "S_T", "dq"), rate=0.0, seed=4)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("B,T,H,D", ((2, 130, 2, 64), (1, 1100, 1, 48), (3, 8, 2, 64)))
+@pytest.mark.parametrize("each,steps", ((4.0, 60), (0.9, 600)))
+def test_lin_forgotten_states_stay_forgotten(cuda, dtype, B, T, H, D, each, steps):
+    """A log_g of -inf, then growth by more than e^200 with nothing new: what
+    was forgotten does not come back, in the tile or over segments."""
+    def make(r, d, at):
+        on = slice(at + 4, min(at + 4 + steps, at + T))
+        d["log_g"][at + 3] = -np.inf
+        d["log_g"][on] = each
+        lin_zero(d, ("v",), slice(at + 3, on.stop))
+    lin_grow_case(cuda, dtype, B, T, H, D, make, S0=lambda r, s: r.normal(size=s), outs=("y", "S_T", "dq"), seed=5)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+def test_lin_strong_decay_and_growth_meet(cuda, dtype):
+    """A decay of e^-80 and then growth by e^120 leave e^40."""
+    def make(r, d, at):
+        lin_zero(d, ("v",), slice(at, at + 130))
+        d["log_g"][at + 3] = -80.0
+        d["log_g"][at + 4:at + 54] = 2.4
+    lin_grow_case(cuda, dtype, 2, 130, 2, 64, make, S0=lambda r, s: r.normal(size=s), outs=("y", "S_T", "dq"), rate=0.0, seed=6)
+
+
+@pytest.mark.parametrize("T", (1, 5, 8))
+def test_lin_growth_of_single_tokens(cuda, T):
+    """One step of e^100 (past fp32's range) on a state of 0 and on one of 1e-30."""
+    def make(r, d, at):
+        d["log_g"][at] = 100.0
+    lin_grow_case(cuda, "f32", 3, T, 2, 64, make, outs=("y", "S_T"), seed=7)
+    lin_grow_case(cuda, "f32", 3, T, 2, 64, make, S0=lambda r, s: 1e-30 * r.normal(size=s), outs=("y", "S_T"), seed=8)
+
+
+@pytest.mark.parametrize("T", (4, 100))
+def test_lin_infinite_growth_is_not_finite(cuda, T):
+    """A log_g of +inf or NaN: the rows before it as without, those from it on
+    not finite."""
+    import torch
+    g = torch.Generator(device=cuda).manual_seed(1)
+    q, k, v = (torch.randn(1, T, 2, 64, device=cuda, generator=g) for _ in range(3))
+    lg = -torch.rand(1, T, 2, device=cuda, generator=g)
+    y0, _, _ = ops().gdr_lin_forward(q, k, v, lg)
+    for bad in (float("inf"), float("nan")):
+        for at in (T // 2, T - 1):
+            odd = lg.clone()
+            odd[0, at, 1] = bad
+            y, S, _ = ops().gdr_lin_forward(q, k, v, odd)
+            assert torch.equal(y[:, :at], y0[:, :at]) and torch.equal(y[:, :, 0], y0[:, :, 0])
+            assert not torch.isfinite(y[0, at:, 1]).any() and not torch.isfinite(S[0, 1]).any() and torch.isfinite(S[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("B,T,Hk,Hv,D,head", ((2, 130, 2, 4, 64, False), (1, 1100, 1, 2, 48, False), (2, 70, 1, 2, 128, True),
+                                              (1, 90, 1, 1, 192, False)))
+def test_lin_growth_in_earnest(cuda, dtype, B, T, Hk, Hv, D, head):
+    """States and adjoints that grow by e^55 within fp32's range, every output
+    of it: tiles of several passes, their flows and the sums over heads."""
+    from tests.test_gpu_block_ops import lin_case
+    r = np.random.default_rng(T)
+    if head:
+        lg = r.uniform(0.7, 0.78, size=Hv)
+    else:
+        lg = -r.exponential(0.01, size=(B * T, Hv))
+        for b in range(B):
+            lg[b * T + 4:b * T + 59] = r.uniform(0.9, 1.1, size=(55, Hv))
+    lin_case(cuda, dtype, B, T, Hk, Hv, D, D, log_g=round_to(lg, "f32"), decay="head" if head else "step", seed=T)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+def test_lin_values_that_are_not_finite_in_a_growing_tile(cuda, dtype):
+    """Values that are not finite in the second pass over a tile: the rows
+    before them and the other columns as without."""
+    import torch
+    g = torch.Generator(device=cuda).manual_seed(2)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    n = lambda *s: torch.randn(*s, device=cuda, generator=g).to(t)
+    q, k, v = n(1, 90, 1, 64), n(1, 90, 1, 64), n(1, 90, 1, 64)
+    lg = torch.full((1, 90, 1), -0.1, device=cuda)
+    lg[:, 2:40] = 2.0
+    y0, S0, _ = ops().gdr_lin_forward(q, k, v, lg)
+    assert torch.isfinite(y0).all()
+    for at in (0, 25, 39, 70):
+        odd = v.clone()
+        odd[0, at, 0, 7] = float("inf")
+        odd[0, at + 1, 0, 50] = float("nan")
+        y, S, _ = ops().gdr_lin_forward(q, k, odd, lg)
+        for c, i in ((7, at), (50, at + 1)):
+            assert torch.equal(y[0, :i, 0, c], y0[0, :i, 0, c]) and not torch.isfinite(y[0, i:, 0, c]).any()
+            assert not torch.isfinite(S[0, 0, c]).any()
+        rest = [c for c in range(64) if c not in (7, 50)]
+        assert torch.equal(y[..., rest], y0[..., rest]) and torch.equal(S[:, :, rest], S0[:, :, rest])
