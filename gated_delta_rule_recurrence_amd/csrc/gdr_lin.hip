@@ -16,8 +16,10 @@
 // which is sum_{i >= t} (a_i - b_i) + <adjoint, state> behind the segment, with
 // a_i the sum of A_ij over j < i (q_i times the part of dq_i that comes from
 // earlier steps) and b_j that over i > j.  The term i = j, which both would
-// hold, is left out of both, so that strong decays do not leave a small
-// difference of large sums.
+// hold, is left out of both, so that where all decays are strong no small
+// difference of large sums is left.  It is left at a strong decay among weak
+// ones: there dlog_g is off by units of the a_i and b_i behind it, as anywhere,
+// but they are larger than itself.
 #include "gdr_lin.h"
 
 namespace gdr {
@@ -27,6 +29,9 @@ constexpr int kThreads = 256;
 // Steps up to which a forward call goes one step at a time.
 constexpr int kFewSteps = 8;
 constexpr int kStepRows = 4;  // of the state, of a group of lanes
+// A log decay below which exp is 0 in fp32 (2^-150 rounds to 0): nothing flows
+// through such a step.
+constexpr float kNoFlow = -104.f;
 
 // A step at a time.  LANES lanes own kStepRows rows of the state, each lane
 // NV vectors of V neighbouring columns of every row, so that a row is read and
@@ -286,9 +291,7 @@ __global__ __launch_bounds__(kThreads) void lin_flow_kernel(LinArgs a, int tiles
     x += carry;
     carry += (red[0] + red[1]) + (red[2] + red[3]);
     if (t < len) {
-      // (a step that forgets everything: nothing flows through it)
-      const bool cut = lin_log_decay(a, row, h) == -__builtin_inff();
-      if (cut) x = 0.0;
+      if (lin_log_decay(a, row, h) < kNoFlow) x = 0.0;
       head += x;
       if (!a.per_head) {
         const int64_t at = row * a.Hv + h;

@@ -389,7 +389,9 @@ int gdr_norm_backward(const gdr_norm_shape* shape, const void* x, const void* we
  * 2^23.  A value that is not finite makes the outputs that the formula reaches
  * from it not finite (an infinity may come out as NaN), and no others, but for
  * dlog_g, which is summed from a sequence's end: it may be NaN at all steps of
- * that sequence and head. */
+ * that sequence and head.  For the same reason its error is in units of what
+ * enters and leaves the states behind a step, not of itself; where exp(log_g) is
+ * 0 in fp32 it is 0. */
 #define GDR_LIN_MAX_DIM 256
 typedef struct {
   int64_t B, T, rows, Hk, Hv, Dk, Dv;

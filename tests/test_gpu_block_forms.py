@@ -384,3 +384,32 @@ def test_lin_values_that_are_not_finite_in_a_growing_tile(cuda, dtype):
             assert not torch.isfinite(S[0, 0, c]).any()
         rest = [c for c in range(64) if c not in (7, 50)]
         assert torch.equal(y[..., rest], y0[..., rest]) and torch.equal(S[:, :, rest], S0[:, :, rest])
+
+
+# ---- linear attention: the decay's gradient at strong steps ---------------------------
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("B,T,H", ((2, 130, 2), (1, 700, 1)))
+def test_lin_decay_gradient_of_strong_steps(cuda, dtype, B, T, H):
+    """Single steps of -12, -110, -300 and -inf among weak ones.  Where exp is 0
+    in fp32 nothing flows; elsewhere the gradient is off by units of the flows
+    behind the step (the oracle's mag): a flow carries 16 units (as where terms
+    cancel above) and the 64 products of its sum, the suffix sum is in 64 bits,
+    and the result rounds once: n = 84."""
+    import torch
+    r = np.random.default_rng(T)
+    rows, D = B * T, 64
+    n = lambda *s: round_to(r.normal(size=s), dtype)
+    d = dict(q=n(rows, H, D), k=round_to(r.normal(size=(rows, H, D)) * D ** -0.5, dtype), v=n(rows, H, D), dy=n(rows, H, D),
+             log_g=-r.exponential(0.01, size=(rows, H)))
+    strong = r.choice(rows, size=rows // 12, replace=False)
+    d["log_g"][strong] = r.choice((-12.0, -110.0, -300.0, -np.inf), size=(len(strong), H))
+    d["log_g"] = round_to(d["log_g"], "f32")
+    st = lambda: round_to(r.normal(size=(B, H, D, D)), "f32")
+    S0, dS_T = st(), st()
+    on = {m: dev_of(a, "f32" if m == "log_g" else dtype, cuda) for m, a in d.items()}
+    dg = lin_run(on, dev_of(S0, "f32", cuda), dev_of(dS_T, "f32", cuda), T=T)["dlog_g"]
+    ref, mag = lin_ref(d, [(b * T, (b + 1) * T) for b in range(B)], S0, dS_T)
+    check("dlog_g", dg, ref["dlog_g"], mag["dlog_g"], "f32", 84)
+    gone = torch.from_numpy(d["log_g"] < -104).to(cuda)
+    assert gone.any() and not dg.reshape(rows, H)[gone].any()
