@@ -587,7 +587,8 @@ int lin_backward(const gdr_lin_shape* shape, const void* q, const void* k, const
     st = alignment_ok({q, k, v, log_g, spans, ckpt, dy, dS_T, dq, dk, dv, dlog_g, dS0,
                        static_cast<const void*>(workspace)});
   if (st != GDR_OK) return st;
-  if (s.B == 0) return GDR_OK;
+  // (one decay per head of no sequence has a gradient of zeros)
+  if (s.B == 0 && !(s.per_head && dlog_g != nullptr)) return GDR_OK;
   if (z.bwd > 0 && (workspace == nullptr || workspace_bytes < (size_t)z.bwd))
     return GDR_ERR_WORKSPACE;
   gdr::LinArgs a = lin_args(s, q, k, v, log_g, spans);
@@ -708,7 +709,7 @@ int res_backward(const gdr_res_shape* shape, const void* x, const void* r, const
                     dpre_b != nullptr;
   int64_t gate_at = 0;
   const int64_t need = res_workspace(s, p, &gate_at);
-  if (s.rows == 0) return GDR_OK;
+  if (s.rows == 0 && !sums) return GDR_OK;  // (sums over no rows are zeros)
   const bool gates = dgate != nullptr && p.per_gate > 1 && s.gate_rows > 1;
   if ((sums || gates) && (workspace == nullptr || workspace_bytes < (size_t)need))
     return GDR_ERR_WORKSPACE;

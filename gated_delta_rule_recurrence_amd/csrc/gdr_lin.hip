@@ -331,6 +331,12 @@ hipError_t join(const LinArgs& a, int reverse, hipStream_t s) {
   return noted(s);
 }
 
+hipError_t head_sums(const LinArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(lin_head_kernel, dim3((a.Hv + kThreads - 1) / kThreads), dim3(kThreads), 0, s,
+                     a);
+  return noted(s);
+}
+
 // Whether widths and strides let rows be read in whole vectors.
 bool whole_vectors(const LinArgs& a, bool bf16) {
   const int64_t v = bf16 ? 8 : 4;
@@ -399,6 +405,7 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
   const int tiles = lin_tiles(a.Dv, a.Dk);
   const int mode = a.dlog_g != nullptr ? kLinFlow : kLinOut;
   hipError_t e = hipSuccess;
+  if (a.B == 0) return head_sums(a, s);
   LinRole r{};
   r.vec = whole_vectors(a, sizeof(T) == 2);
   r.dq = 1;
@@ -490,11 +497,7 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
   if (e == hipSuccess && mode == kLinFlow) {
     hipLaunchKernelGGL(lin_flow_kernel, dim3(a.segs, a.Hv, a.B), dim3(kThreads), 0, s, a, tiles);
     e = noted(s);
-    if (e == hipSuccess && a.per_head) {
-      hipLaunchKernelGGL(lin_head_kernel, dim3((a.Hv + kThreads - 1) / kThreads), dim3(kThreads),
-                         0, s, a);
-      e = noted(s);
-    }
+    if (e == hipSuccess && a.per_head) e = head_sums(a, s);
   }
   return e;
 }

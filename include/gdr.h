@@ -469,8 +469,8 @@ int gdr_res_backward_workspace_bytes(const gdr_res_shape* shape, size_t* out);
  * not h) and its stats; dh NULL: 0 (with pre = 0, where dy is not read, it is
  * required).  dx, dresidual [rows][C]; dgate [rows / gate_rows][C] dense;
  * dgate and the weights' and biases' gradients NULL: not formed (with all of
- * them NULL no workspace is needed).  Sums over rows in fp32 in a fixed
- * order. */
+ * them NULL no workspace is needed).  Sums over rows (of none: 0) in fp32 in a
+ * fixed order. */
 int gdr_res_backward(const gdr_res_shape* shape, const void* x, const void* residual,
                      const void* gate, const void* post_weight, const void* post_bias,
                      const void* pre_weight, const void* pre_bias, const float* stats,

@@ -413,3 +413,45 @@ def test_lin_decay_gradient_of_strong_steps(cuda, dtype, B, T, H):
     check("dlog_g", dg, ref["dlog_g"], mag["dlog_g"], "f32", 84)
     gone = torch.from_numpy(d["log_g"] < -104).to(cuda)
     assert gone.any() and not dg.reshape(rows, H)[gone].any()
+
+
+# ---- no rows, no sequences --------------------------------------------------------------
+
+@pytest.mark.parametrize("wdtype", ("bf16", "f32"))
+@pytest.mark.parametrize("C", (64, 600, 2304, 8192))
+def test_res_parameters_of_no_rows(cuda, C, wdtype):
+    """The C call writes zeros into the parameters' gradients of no rows."""
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib
+    t = torch.bfloat16 if wdtype == "bf16" else torch.float32
+    shape = _lib.GdrResShape(0, C, 0, 0, 0, 0, 1.0, 1e-6, 0.0, _lib.GDR_BF16, _lib.GDR_BF16,
+                             _lib.GDR_BF16 if wdtype == "bf16" else _lib.GDR_F32, _lib.GDR_BF16, 1, 1, 1)
+    nbytes = _lib.size_of("gdr_res_backward_workspace_bytes", shape)
+    ws = torch.full((max(nbytes, 1),), 255, dtype=torch.uint8, device=cuda)
+    w = torch.ones(C, dtype=t, device=cuda)
+    grads = [torch.full((C,), float("nan"), dtype=t, device=cuda) for _ in range(4)]
+    ptrs = [0, 0, 0] + [w.data_ptr()] * 4 + [0] * 6 + [g.data_ptr() for g in grads] + [ws.data_ptr()]
+    assert _lib.layer_raw("gdr_res_backward", shape, ptrs, torch.cuda.current_stream().cuda_stream, nbytes) == 0
+    assert not any(g.any() for g in grads)
+    x = torch.zeros(0, 5, C, device=cuda, requires_grad=True)
+    ps = [torch.ones(C, device=cuda, requires_grad=True) for _ in range(2)]
+    y, h = ops().residual_norm(x, x, None, ps[0], None, ps[1])
+    (y.sum() + h.sum()).backward()
+    assert not any(p.grad.any() for p in ps)
+
+
+@pytest.mark.parametrize("gdtype", ("bf16", "f32"))
+def test_lin_decay_per_head_of_no_sequences(cuda, gdtype):
+    import torch
+    from gated_delta_rule_recurrence_amd import _lib
+    t = torch.bfloat16 if gdtype == "bf16" else torch.float32
+    Hv = 300
+    shape = _lib.GdrLinShape(0, 0, 0, 1, Hv, 16, 16, 0, 0, 0, 0, 1.0, _lib.GDR_F32,
+                             _lib.GDR_BF16 if gdtype == "bf16" else _lib.GDR_F32, 1)
+    nbytes = _lib.size_of("gdr_lin_backward_workspace_bytes", shape)
+    ws = torch.zeros(max(nbytes, 1), dtype=torch.uint8, device=cuda)
+    lg = torch.zeros(Hv, dtype=t, device=cuda)
+    dg = torch.full((Hv,), float("nan"), dtype=t, device=cuda)
+    ptrs = [0, 0, 0, lg.data_ptr(), 0, 0, 0, 0, 0, 0, 0, dg.data_ptr(), 0, ws.data_ptr()]
+    assert _lib.layer_raw("gdr_lin_backward", shape, ptrs, torch.cuda.current_stream().cuda_stream, nbytes) == 0
+    assert not dg.any()
