@@ -16,15 +16,14 @@
 // fp32's range while what they multiply is small or 0.  Such a tile is walked in
 // passes, each over the rows [x0, x1) that grow by no more (lin_pass); a step
 // that grows by more alone is a pass of the state only, or several.  (What the
-// other tiles pay for it: 0 to 1% of a pass, shared keys 409 -> 420 us, the small
-// fp32 one 86 -> 91.)
+// other tiles pay for it: 0 to 1% of a pass, 5% of the small fp32 one, 86 us.)
 //
 // Precision.  bf16 rows are matrix operands as they are; what is fp32 (P, S,
 // uf V) enters a product in three bf16 pieces, which hold fp32's 24 bits.  (Two
 // hold 18: enough for a bf16 output by itself, but not where large terms cancel
 // in it.  Seven prompts 154 us with two and 163 with three, training of 2048
-// steps, heads 16/64 of 192/128, 475 and 495, 4 x 4096 steps of 32 heads of
-// 128/128 762 and 846; the bf16 outputs' difference to a plain fp32 form 1.0e-4
+// steps, heads 16/64 of 192/128, 468 and 480, 4 x 4096 steps of 32 heads of
+// 128/128 760 and 843; the bf16 outputs' difference to a plain fp32 form 1.0e-4
 // and 0.4e-4.)  fp32 rows are three pieces too; of the nine products the six
 // above 2^-24 are formed (with the next two the errors are the same).
 //
@@ -422,13 +421,14 @@ struct LinStage {
 };
 
 // Waves of a SIMD (workgroups of a compute unit) that the registers are cut to,
-// no more than LDS holds.  (Three where some registers are spilled for it, too:
-// training of 2048 steps, heads 16/64 of 192/128, 465 us, with two for its dq and
-// dk and no spills 485.)
+// no more than LDS holds.  128 contracted columns with 64 of output: three for the
+// flows, though some registers are spilled for it (training of 2048 steps, heads
+// 16/64 of 192/128, 491 us, with two and no spills 524), two for out alone
+// (2 x 2048 steps, heads 1/64 of 128/64, 411 us, with three 422).
 template <typename T>
-constexpr int lin_waves(int KI, int NT) {
+constexpr int lin_waves(int KI, int NT, int MODE) {
   if (sizeof(T) == 4) return KI <= 64 && NT == 1 ? 3 : KI <= 128 ? 2 : 1;
-  return KI <= 128 && NT == 1 ? 3 : 2;
+  return NT == 1 && KI <= (MODE == kLinOut ? 64 : 128) ? 3 : 2;
 }
 // Sum of the waves' values of row x.
 template <int L>
@@ -885,7 +885,7 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
 }
 
 template <typename T, int KI, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * kLinWaves, (lin_waves<T>(KI, NT))) void lin_chunk_kernel(
+__global__ __launch_bounds__(64 * kLinWaves, (lin_waves<T>(KI, NT, MODE))) void lin_chunk_kernel(
     LinArgs a, LinRole r) {
   __shared__ __attribute__((aligned(16))) uint16_t
       lds[LinTiles<T, KI, 16 * NT * kLinWaves, MODE>::kEnd];
@@ -897,7 +897,7 @@ struct LinRoles {
   LinRole r[3];
 };
 template <typename T, int KI, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * kLinWaves, (lin_waves<T>(KI, NT))) void lin_chunks_kernel(
+__global__ __launch_bounds__(64 * kLinWaves, (lin_waves<T>(KI, NT, MODE))) void lin_chunks_kernel(
     LinArgs a, LinRoles roles) {
   __shared__ __attribute__((aligned(16))) uint16_t
       lds[LinTiles<T, KI, 16 * NT * kLinWaves, MODE>::kEnd];
