@@ -602,11 +602,13 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
       if (__builtin_expect(__any(x > 0.0), 0)) part = lin_pass<L>(x, pass_s, r.reverse);
       if (threadIdx.x == 0) part_s = part;
       const double sum = lin_prefix_sum(x);
+      const double earlier = lin_dpp<0x138, 0xF>(sum);  // wave_shr:1
       const double end = __shfl(sum, 63, 64);
       if constexpr (!OUT) all += __any(x <= kLeastLog) ? end - __builtin_inf() : end;
       const bool before = threadIdx.x < (part & 255), in = !before && threadIdx.x < (part >> 8 & 255);
       if (threadIdx.x < L) {
-        const double H = r.reverse ? sum - x : sum;
+        // (a difference to x would carry a NaN x into its own row)
+        const double H = r.reverse ? earlier : sum;
         const double H2 = H * 1.4426950408889634;
         const float hi = (float)H2;
         // (rows before the pass reach nothing in it, those behind not the state)

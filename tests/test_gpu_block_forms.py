@@ -455,3 +455,31 @@ def test_lin_decay_per_head_of_no_sequences(cuda, gdtype):
     ptrs = [0, 0, 0, lg.data_ptr(), 0, 0, 0, 0, 0, 0, 0, dg.data_ptr(), 0, ws.data_ptr()]
     assert _lib.layer_raw("gdr_lin_backward", shape, ptrs, torch.cuda.current_stream().cuda_stream, nbytes) == 0
     assert not dg.any()
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("T", (7, 100, 700))
+@pytest.mark.parametrize("bad", (float("nan"), float("inf")))
+def test_lin_decays_that_are_not_finite_backward(cuda, dtype, T, bad):
+    """A log_g that is not finite at step t reaches dk and dv of the steps before
+    t and dq from t on, in its head, and no others (not t's own dk and dv)."""
+    import torch
+    g = torch.Generator(device=cuda).manual_seed(T)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v, dy = (torch.randn(2, T, 2, 64, device=cuda, generator=g).to(t) for _ in range(4))
+    lg = -torch.rand(2, T, 2, device=cuda, generator=g)
+    grads = lambda lg: ops().gdr_lin_backward(q, k, v, lg, ops().gdr_lin_forward(q, k, v, lg)[2], dy)
+    clean = grads(lg)
+    for at in sorted({0, 1, T // 2, T - 1}):
+        odd = lg.clone()
+        odd[1, at, 0] = bad
+        got = grads(odd)
+        for i, (a, b) in enumerate(zip(got[:3], clean[:3])):  # dq, dk, dv
+            reached = torch.zeros(2, T, 2, dtype=torch.bool, device=cuda)
+            reached[1, at:, 0] = i == 0
+            reached[1, :at, 0] = i > 0
+            assert torch.equal(a[~reached], b[~reached]), (at, i)
+            assert not torch.isfinite(a[reached]).any(), (at, i)
+        assert torch.equal(got[3][0], clean[3][0]) and torch.equal(got[3][1, :, 1], clean[3][1, :, 1])
+        assert torch.equal(got[4][0], clean[4][0]) and torch.equal(got[4][1, 1], clean[4][1, 1])
+        assert not torch.isfinite(got[4][1, 0]).any()
