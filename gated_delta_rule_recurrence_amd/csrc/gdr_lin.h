@@ -39,11 +39,12 @@
 //
 // What bounds it: the dependent phases of a tile (P, S Q, P's decays, P V and the
 // update, with three barriers) at the two waves a SIMD that the state leaves
-// registers for.  4 x 4096 steps of 32 heads of 128/128: states alone 85 us,
-// y 155 to 174, dq with dk and dv 430 to 490; there the vector units are 34, 39 and 45% busy,
-// matrix cores 23, 24 and 27, LDS 14, 20 and 23, HBM at 3.2 to 3.5 TB/s.  Eight
-// waves of 16 columns have more to switch between and 47% more vector
-// instructions, as each forms the same operands: 812 us a pass against 722.
+// registers for.  4 x 4096 steps of 32 heads of 128/128: states alone 92 us, y
+// 195, dq with dk and dv 534 to 549; there the vector units are 37, 41 and 51%
+// busy, matrix cores 23, 30 and 34, LDS 14, 19 and 22, HBM at 2.7 to 3.3 TB/s.
+// Eight waves of 16 columns have more to switch between and 47% more vector
+// instructions, as each forms the same operands (with operands of two pieces 812
+// us a pass against 722).
 #pragma once
 
 #include "gdr_layer.h"
@@ -627,9 +628,9 @@ __device__ __forceinline__ void lin_chunk_run(const LinArgs& a, const LinRole& r
     // What is not finite in V may reach its own row and later ones only, but a
     // matrix product multiplies it with the zeros of P above the diagonal too.
     // It is taken out, and each column's outputs from its first such row on,
-    // and the column's state, are made NaN instead.  (Looking for them costs 0 to
-    // 4% of a pass in bf16, 8% of the small one in fp32: training of 2048 steps,
-    // heads 16/64 of 192/128, 473 us, 456 without.)
+    // and the column's state, are made NaN instead.  (Looking for them cost 0 to
+    // 4% of a pass in bf16, 8% of the small one in fp32, when it was added:
+    // training of 2048 steps, heads 16/64 of 192/128, 473 us, 456 without.)
     const bool odd = __builtin_amdgcn_readfirstlane(odd_s[0] | odd_s[1] | odd_s[2] | odd_s[3]);
     if (__builtin_expect(odd, 0)) {
       if (threadIdx.x < WO) {

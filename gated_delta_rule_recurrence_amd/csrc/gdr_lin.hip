@@ -507,7 +507,7 @@ hipError_t bwd(const LinArgs& a, hipStream_t s) {
 // 128 columns a workgroup, which form P once for them, where the state leaves
 // registers for two workgroups a compute unit (up to 128 contracted columns);
 // 64 where it does not, and where 128 would leave a quarter of them empty.
-// Measured when this was chosen (each pass has got 4 to 13% faster since):
+// Measured when this was chosen, with operands of two pieces:
 // training of 2048 steps, heads 16/64 of 192/128: 514 us; 128 columns for all
 // widths 646, 64 only where 192 are contracted 520.  4 x 4096 steps of 32 heads
 // of 128/128: 757 us, with 64 columns 903.
@@ -529,10 +529,11 @@ int lin_tiles(int64_t Ni, int64_t No) {
 // count: a round of workgroups takes its segment's steps and kLinEach more; more
 // workgroups than one round take their share of all steps and half a segment;
 // what is cut is walked again without outputs (0.45 of a pass) and joined (as 128
-// steps).  Seven prompts in 6000 rows, 32 heads of 128/128: 512 steps 146 us, 384
-// (by rows alone) 172; 20 of them: not cut 105, 384 steps 204; 24 sequences in
-// 16384 rows, 16 heads, training: not cut 685, 512 steps (by rows alone) 790, 832
-// (one round) 980.
+// steps).  Three draws each of 32 heads of 128/128: seven prompts in 6000 rows 159
+// to 167 us, cut by rows alone 177 to 190; 20 of them (not cut) 108 to 120, by rows
+// 213 to 219; 24 sequences in 16384 rows, 16 heads, training (not cut) 769 to 853,
+// by rows 882 to 909, one round 1113 to 1142.  It loses 5% where it cuts to one
+// round five sequences of 12000 rows, 16 heads of 64/64: 233, by rows 221.
 constexpr double kLinEach = 96.0;
 LinPlan lin_plan(int64_t B, int64_t T, int64_t rows, int64_t Hv, int64_t Dk, int64_t Dv) {
   LinPlan p{};

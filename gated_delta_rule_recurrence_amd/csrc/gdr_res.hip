@@ -6,10 +6,10 @@
 // (in fp32, as the forward had it, so h need not be kept):
 //   e = dy (w + offset),  dh' = dh + r (e - mean(e) - hh mean(e hh)),  dr = dh'
 //   dgate = alpha dh' n,  dn = alpha gate dh',  dx from dn as dh' from dy.
-// Bound by HBM bytes: every tensor once.  8192 x 4096 in bf16: forward 47 us (268
-// MB, 5.7 TB/s, part of it from the memory-side cache), backward 94 (403 MB, 4.3
-// TB/s, its vector units half busy), the sums over rows 6; 6000 x 5120 with an
-// fp32 residual, forward 71 us (369 MB, 5.2 TB/s).
+// Bound by HBM bytes: every tensor once.  8192 x 4096 in bf16: forward 47 to 51 us
+// (268 MB, 5.2 to 5.7 TB/s, part of it from the memory-side cache), backward 94 to
+// 97 (403 MB, 4.2 TB/s, its vector units half busy), the sums over rows 6; 6000 x
+// 5120 with an fp32 residual, forward 71 to 76 us (369 MB, 4.9 to 5.2 TB/s).
 //
 // Mapping: LANES lanes own one row, each NV vectors of V channels, in registers
 // from the loads to the stores; rows of up to 64 vectors take a wave, wider ones
